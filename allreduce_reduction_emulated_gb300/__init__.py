@@ -12,6 +12,10 @@ if libar.so is missing or cannot be loaded, every call raises.
 
 ``allreduce(sends, recvs, op="sum", algo="auto", scale=1.0)`` is the same
 call with dtype / count taken from the tensors and a cached communicator.
+
+The operators at the two ends of the data-parallel step (include/ar_train.h)
+are in ``losses`` (token log-probabilities, policy and preference losses with
+the gradient of the logits) and ``clipping`` (global gradient norm, clipping).
 """
 from __future__ import annotations
 
@@ -88,6 +92,19 @@ def library() -> ctypes.CDLL:
                 L.ar_allreduce_ll_noalloc.argtypes = [i, ctypes.POINTER(vp), ctypes.POINTER(vp), sz,
                                                       i, i, ctypes.c_float, vp, ctypes.POINTER(i)]
                 L.ar_allreduce_ll_noalloc.restype = i
+                f = ctypes.c_float
+                matrix = [vp, sz, sz, sz, i, vp, i, vp]      # logits, sizes, type, targets, weights
+                L.ar_token_logprobs.argtypes = matrix + [vp, vp]
+                L.ar_policy_loss.argtypes = matrix + [vp, vp, vp, f, f, f, f, vp, sz, vp, vp, vp, sz, vp]
+                L.ar_preference_loss.argtypes = matrix + [vp, i, sz, vp, f, f, f, vp, sz, vp, vp, vp, vp, sz, vp]
+                L.ar_grad_norm.argtypes = [sz, vp, vp, vp, vp, vp, sz, vp]
+                L.ar_clip_grads.argtypes = [sz, vp, vp, vp, vp, f, f, vp, vp, sz, vp]
+                for fn in (L.ar_token_logprobs, L.ar_policy_loss, L.ar_preference_loss, L.ar_grad_norm,
+                           L.ar_clip_grads):
+                    fn.restype = i
+                for fn, args in ((L.ar_policy_loss_workspace, []), (L.ar_preference_loss_workspace, [sz, sz]),
+                                 (L.ar_grad_norm_workspace, [])):
+                    fn.argtypes, fn.restype = args, sz
                 _lib = L
     return _lib
 

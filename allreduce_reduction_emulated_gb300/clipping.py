@@ -1,0 +1,109 @@
+"""Global norm of many gradient tensors and clipping by it: what happens to the
+gradients between the all-reduce and the update.
+
+    clipper = GradClipper(grads)          # once, like the reducer
+    norm = clipper.clip(1.0)              # every step: 0-dim tensor, no host wait
+
+Argument checks and marshalling only; the formulas are in include/ar_train.h.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import (AR_BFLOAT16, AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED, AR_FLOAT32, AR_SUCCESS, ArError, _stream_handle,
+               library)
+
+_DTYPES = {torch.float32: AR_FLOAT32, torch.bfloat16: AR_BFLOAT16}
+
+
+class GradClipper:
+    """Norm of, and clipping over, a fixed list of gradient tensors.
+
+    grads   contiguous float32 / bfloat16 CUDA tensors on one device, any sizes and
+            alignments; no two may share memory (a tied gradient counts once:
+            pass it once)
+    out     where the clipped gradients go: tensors of the same sizes and types
+            (default: in place)
+
+    The list is checked and its addresses are laid out once; every call reads
+    the gradients anew.  Calls of one clipper share a workspace of 32 KiB: they
+    may be on any stream but must not overlap on the GPU.
+    """
+
+    def __init__(self, grads, out=None):
+        what = "GradClipper"
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.grads) == 0:
+            raise ArError(AR_ERR_INVALID_ARG, f"{what}: no tensors")
+        if len(self.out) != len(self.grads):
+            raise ArError(AR_ERR_INVALID_ARG, f"{what}: {len(self.grads)} gradients, {len(self.out)} outputs")
+        self.device = self.grads[0].device
+        spans = []
+        for name, tensors in (("grads", self.grads), ("out", self.out)):
+            if name == "out" and out is None:
+                continue
+            for i, (t, g) in enumerate(zip(tensors, self.grads)):
+                if t.dtype not in _DTYPES:
+                    raise ArError(AR_ERR_UNSUPPORTED, f"{what}: {name}[{i}] of {t.dtype}: float32 or bfloat16 needed")
+                if not t.is_cuda or not t.is_contiguous():
+                    raise ArError(AR_ERR_INVALID_ARG, f"{what}: {name}[{i}] is not a contiguous CUDA tensor")
+                if t.device != self.device:
+                    raise ArError(AR_ERR_INVALID_ARG, f"{what}: tensors on {self.device} and {t.device}; "
+                                                      "all must be on one GPU")
+                if t.dtype != g.dtype or t.numel() != g.numel():
+                    raise ArError(AR_ERR_INVALID_ARG, f"{what}: out[{i}] is {t.numel()} x {t.dtype}, the gradient is "
+                                                      f"{g.numel()} x {g.dtype}")
+                if name == "out" and t.data_ptr() == g.data_ptr():
+                    continue
+                if t.numel():
+                    spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]"))
+        spans.sort()
+        for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
+            if start < end:
+                raise ArError(AR_ERR_INVALID_ARG, f"{what}: {a} and {b} share memory")
+        n = len(self.grads)
+        self._n = n
+        self._grads = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.grads])
+        self._outs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.out])
+        self._counts = (ctypes.c_size_t * n)(*[t.numel() for t in self.grads])
+        self._dtypes = (ctypes.c_int * n)(*[_DTYPES[t.dtype] for t in self.grads])
+        self._lib = library()
+        self._bytes = self._lib.ar_grad_norm_workspace()
+        with torch.cuda.device(self.device):
+            self._home = torch.cuda.current_stream().cuda_stream
+            self._workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
+
+    def _begin(self, what: str, stream):
+        """(stream handle, a new 0-dim norm): both belong to the call's stream."""
+        if torch.cuda.current_device() != self.device.index:
+            raise ArError(AR_ERR_INVALID_ARG, f"{what}: gradients are on {self.device}, the current device is "
+                                              f"cuda:{torch.cuda.current_device()}")
+        handle = _stream_handle(stream)
+        if handle != self._home or stream is not None:
+            s = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+            self._workspace.record_stream(s)
+            with torch.cuda.stream(s):
+                return handle, torch.empty((), dtype=torch.float32, device=self.device)
+        return handle, torch.empty((), dtype=torch.float32, device=self.device)
+
+    def norm(self, stream=None):
+        """The global norm, a 0-dim float32 tensor."""
+        handle, norm = self._begin("GradClipper.norm", stream)
+        st = self._lib.ar_grad_norm(self._n, self._grads, self._counts, self._dtypes, norm.data_ptr(),
+                                    self._workspace.data_ptr(), self._bytes, handle)
+        if st != AR_SUCCESS:
+            raise ArError(st, "GradClipper.norm")
+        return norm
+
+    def clip(self, max_norm: float, eps: float = 1e-6, stream=None):
+        """Scales every gradient by min(1, max_norm / (norm + eps)) into `out`;
+        returns the norm before clipping, a 0-dim float32 tensor."""
+        handle, norm = self._begin("GradClipper.clip", stream)
+        st = self._lib.ar_clip_grads(self._n, self._grads, self._outs, self._counts, self._dtypes, max_norm, eps,
+                                     norm.data_ptr(), self._workspace.data_ptr(), self._bytes, handle)
+        if st != AR_SUCCESS:
+            raise ArError(st, "GradClipper.clip")
+        return norm

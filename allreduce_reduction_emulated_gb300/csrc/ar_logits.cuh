@@ -1,0 +1,198 @@
+// ar_logits.cuh -- device-side building blocks of the operators on a logits
+// matrix (ar_logits.cu): a row cut into 16-byte slots, softmax statistics and
+// the losses' per-token arithmetic.
+#pragma once
+
+#include <cfloat>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "ar_device.cuh"
+
+namespace ar {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x in one instruction (relative error 2^-22, results below 2^-126 are 0).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// e^(x - m).  The difference is formed before it is scaled: x and m may be the
+// type's lowest value, and lowest * log2(e) is already -infinity.
+__device__ __forceinline__ float exp_diff(float x, float m) { return ex2((x - m) * kLog2e); }
+
+// ----------------------------------------------------------------- rows
+
+// 16-byte load of data that this block reads once or twice: not kept in L1.
+// Volatile, so it stays behind the wait for the kernel before it (pdl_enter).
+__device__ __forceinline__ uint4 ld_row(const uint4* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+template <int DT> struct ElemOf;
+template <> struct ElemOf<kF32> { using T = float; };
+template <> struct ElemOf<kBF16> { using T = uint16_t; };
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(uint16_t x) { return bf16_lo((uint32_t)x); }
+__device__ __forceinline__ void from_float(float* p, float x) { *p = x; }
+__device__ __forceinline__ void from_float(uint16_t* p, float x) { *p = (uint16_t)(pack_bf16x2(x, 0.0f) & 0xffffu); }
+
+// A row (or any run of elements) as slots of 16 aligned bytes.  Its start needs
+// element alignment only: slot 0 is the aligned 16 bytes that hold element 0,
+// so every slot but the first and the last holds N elements of the run, and
+// slot s holds elements [s * N - lead, s * N - lead + N) of it.
+template <int DT>
+struct Slots {
+  using E = typename ElemOf<DT>::T;
+  static constexpr int N = Lanes<DT>::N;
+  E* row;
+  long long len;     // elements
+  int lead;          // elements of slot 0 that lie before the run
+
+  __device__ __forceinline__ Slots(const E* p, long long n)
+      : row(const_cast<E*>(p)), len(n), lead((int)(((uintptr_t)p & 15) / sizeof(E))) {}
+  __device__ __forceinline__ long long count() const { return (len + lead + N - 1) / N; }
+  __device__ __forceinline__ long long first(long long s) const { return s * N - lead; }
+  __device__ __forceinline__ bool whole(long long s) const { return first(s) >= 0 && first(s) + N <= len; }
+
+  // slot s widened to fp32; elements outside the run read as `fill`
+  __device__ __forceinline__ void load(long long s, float (&x)[N], float fill) const {
+    const long long j = first(s);
+    if (j >= 0 && j + N <= len) {
+      const Acc<DT> a = widen<DT>(ld_row(reinterpret_cast<const uint4*>(row + j)));
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = a.v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = (j + i >= 0 && j + i < len) ? to_float(row[j + i]) : fill;
+    }
+  }
+};
+
+// Stores N elements of slot s of `in` at the same element indices of `out`
+// (which may start at another alignment: then element by element).
+template <int DT>
+__device__ __forceinline__ void store_slot(const Slots<DT>& in, typename ElemOf<DT>::T* out, bool same_align,
+                                           long long s, const float (&y)[Lanes<DT>::N]) {
+  constexpr int N = Lanes<DT>::N;
+  const long long j = in.first(s);
+  if (same_align && j >= 0 && j + N <= in.len) {
+    Acc<DT> a;
+#pragma unroll
+    for (int i = 0; i < N; ++i) a.v[i] = y[i];
+    st_stream(reinterpret_cast<uint4*>(out + j), narrow<DT>(a, 1.0f, false));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (j + i >= 0 && j + i < in.len) from_float(out + j + i, y[i]);
+  }
+}
+
+__device__ __forceinline__ long long load_index(const void* p, int bytes, size_t i) {
+  return bytes == 8 ? static_cast<const long long*>(p)[i] : (long long)static_cast<const int*>(p)[i];
+}
+
+// ------------------------------------------------------------ statistics
+
+// Running maximum m and sum s of e^(x - m).  m starts at the lowest finite
+// value, not at -infinity, so that x - m is never -infinity - -infinity.
+struct MaxSum {
+  float m = -FLT_MAX, s = 0.0f;
+  template <int N>
+  __device__ __forceinline__ void add(const float (&x)[N]) {
+    float mv = x[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) mv = fmaxf(mv, x[i]);
+    if (mv > m) {
+      s *= exp_diff(m, mv);
+      m = mv;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) s += exp_diff(x[i], m);
+  }
+  __device__ __forceinline__ void join(float m2, float s2) {
+    const float mm = fmaxf(m, m2);
+    s = s * exp_diff(m, mm) + s2 * exp_diff(m2, mm);
+    m = mm;
+  }
+};
+
+// Over a block of THREADS threads; every thread gets the result.  `sh` holds
+// THREADS / 32 pairs; the block must synchronize before it is written again.
+template <int THREADS>
+__device__ __forceinline__ MaxSum block_join(MaxSum a, float2* sh) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) a.join(__shfl_xor_sync(~0u, a.m, d), __shfl_xor_sync(~0u, a.s, d));
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a.m, a.s);
+  __syncthreads();
+  MaxSum r;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) r.join(sh[w].x, sh[w].y);
+  return r;
+}
+
+// Sum over a block; valid in every thread.  `sh` as above.
+template <int THREADS, class T>
+__device__ __forceinline__ T block_sum(T v, T* sh) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  T r = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) r += sh[w];
+  return r;
+}
+
+// ------------------------------------------------------------ per token
+
+// log-probability of the target; NaN for a target outside the row
+template <class E>
+__device__ __forceinline__ float target_logprob(const E* row, long long vocab, long long y, float m, float s) {
+  if (y < 0 || y >= vocab) return __int_as_float(0x7fffffff);
+  return (to_float(row[y]) - m) - logf(s);
+}
+
+struct PolicyParams {
+  const float* old_logprobs;
+  const float* advantages;
+  const float* ref_logprobs;  // NULL: no KL term
+  float lo, hi;               // 1 - clip_low, 1 + clip_high
+  float kl_coef, scale;
+};
+
+struct PolicySums {
+  float loss = 0.0f, kl = 0.0f, clipped = 0.0f, weight = 0.0f;
+};
+
+// One token's loss into `sum`; returns its derivative by the log-probability,
+// weight and scale included (scale multiplies the sums at the end).
+__device__ __forceinline__ float policy_token(const PolicyParams& p, size_t t, float w, float lp, PolicySums& sum) {
+  const float A = p.advantages[t];
+  const float r = expf(lp - p.old_logprobs[t]);
+  const bool clip = (A > 0.0f && r > p.hi) || (A < 0.0f && r < p.lo);
+  // a NaN ratio is neither clipped nor clamped away
+  float term = -(clip ? (A > 0.0f ? p.hi : p.lo) * A : r * A);
+  float d = clip ? 0.0f : -A * r;
+  if (p.ref_logprobs) {
+    const float q = p.ref_logprobs[t] - lp;
+    const float e = expm1f(q);  // e^q - 1 without cancellation: policies start at their reference
+    const float kl = e - q;
+    term += p.kl_coef * kl;
+    d -= p.kl_coef * e;
+    sum.kl += w * kl;
+  }
+  sum.loss += w * term;
+  sum.clipped += clip ? w : 0.0f;
+  sum.weight += w;
+  return p.scale * w * d;
+}
+
+}  // namespace ar
