@@ -102,7 +102,7 @@ def library() -> ctypes.CDLL:
                 for fn in (L.ar_token_logprobs, L.ar_policy_loss, L.ar_preference_loss, L.ar_grad_norm,
                            L.ar_clip_grads):
                     fn.restype = i
-                for fn, args in ((L.ar_policy_loss_workspace, []), (L.ar_preference_loss_workspace, [sz, sz]),
+                for fn, args in ((L.ar_policy_loss_workspace, [sz]), (L.ar_preference_loss_workspace, [sz, sz]),
                                  (L.ar_grad_norm_workspace, [])):
                     fn.argtypes, fn.restype = args, sz
                 _lib = L

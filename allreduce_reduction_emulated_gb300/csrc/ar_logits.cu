@@ -6,6 +6,7 @@
 // maximum m and the sum of e^(x - m), rescaled when m grows; a block joins the
 // threads' pairs.
 #include <algorithm>
+#include <climits>
 
 #include "ar_logits.cuh"
 #include "ar_train.h"
@@ -16,6 +17,7 @@ namespace ar {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr size_t kMaxPolicySums = 65536;
 
 template <int DT>
 struct Matrix {
@@ -34,29 +36,31 @@ struct Matrix {
         target_bytes(c.target_bytes), weights(c.weights), logprobs(c.logprobs) {}
 };
 
-template <int DT>
+template <int DT, int THREADS>
 __device__ __forceinline__ MaxSum row_stats(const typename ElemOf<DT>::T* row, long long vocab, float2* sh) {
   const Slots<DT> in(row, vocab);
   MaxSum a;
   const long long n = in.count();
-  for (long long s = threadIdx.x; s < n; s += kThreads) {
+  for (long long s = threadIdx.x; s < n; s += THREADS) {
     float x[Lanes<DT>::N];
     in.load(s, x, -INFINITY);
     a.add(x);
   }
-  return block_join<kThreads>(a, sh);
+  return block_join<THREADS>(a, sh);
 }
 
-// grad[j] = c * ([j == y] - p[j]).  The target's 1 - p is -expm1(log p).
+// grad[j] = c * ([j == y] - p[j]) in slots first, first + step, ... below end.  The
+// target's 1 - p is -expm1(log p).
 template <int DT>
 __device__ __forceinline__ void row_grad(const typename ElemOf<DT>::T* row, typename ElemOf<DT>::T* grad,
-                                         long long vocab, long long y, float lp, MaxSum st, float c) {
+                                         long long vocab, long long y, float lp, MaxSum st, float c, long long first,
+                                         long long end, int step) {
   constexpr int N = Lanes<DT>::N;
   const Slots<DT> in(row, vocab);
   const bool same = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
   const float f = -c / st.s;
-  const long long n = in.count();
-  for (long long s = threadIdx.x; s < n; s += kThreads) {
+  const long long n = min(in.count(), end);
+  for (long long s = first; s < n; s += step) {
     float x[N];
     in.load(s, x, -INFINITY);
     const long long j = in.first(s);
@@ -88,7 +92,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, f
       continue;
     }
     const typename ElemOf<DT>::T* row = a.logits + t * a.stride;
-    const MaxSum st = row_stats<DT>(row, (long long)a.vocab, sh);
+    const MaxSum st = row_stats<DT, kThreads>(row, (long long)a.vocab, sh);
     if (threadIdx.x == 0) {
       const long long y = load_index(a.targets, a.target_bytes, t);
       a.logprobs[t] = target_logprob(row, (long long)a.vocab, y, st.m, st.s);
@@ -116,18 +120,330 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, co
     }
     const typename ElemOf<DT>::T* row = a.logits + t * a.stride;
     const long long y = load_index(a.targets, a.target_bytes, t);
-    const MaxSum st = row_stats<DT>(row, (long long)a.vocab, sh);
+    const MaxSum st = row_stats<DT, kThreads>(row, (long long)a.vocab, sh);
     if (threadIdx.x == 0) {
       const float lp = target_logprob(row, (long long)a.vocab, y, st.m, st.s);
       a.logprobs[t] = lp;
-      sh_c[0] = policy_token(p, t, w, lp, sum);
+      sh_c[0] = policy_token(p, p.old_logprobs[t], p.advantages[t], p.ref_logprobs ? p.ref_logprobs[t] : 0.0f, w, lp,
+                             sum);
       sh_c[1] = lp;
     }
     __syncthreads();  // also: the target's logit is read before an in-place gradient is written
-    row_grad<DT>(row, grad, (long long)a.vocab, y, sh_c[1], st, sh_c[0]);
+    row_grad<DT>(row, grad, (long long)a.vocab, y, sh_c[1], st, sh_c[0], threadIdx.x, LLONG_MAX, kThreads);
     __syncthreads();
   }
   if (threadIdx.x == 0) partial[blockIdx.x] = make_float4(sum.loss, sum.kl, sum.clipped, sum.weight);
+}
+
+template <int DT>
+__device__ __forceinline__ float max_of(uint4 r) {
+  const Acc<DT> a = widen<DT>(r);
+  float m = a.v[0];
+#pragma unroll
+  for (int i = 1; i < Lanes<DT>::N; ++i) m = fmaxf(m, a.v[i]);
+  return m;
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));  // a NaN yields to the other operand
+  return r;
+}
+
+// The same with the row kept on the chip: read once, written once.
+//
+// A cluster of C blocks takes `run` rows, one after the other; each block holds
+// a slice of the row in registers, K slots of 16 bytes per thread.  The slice of
+// the next row is on its way into shared memory (cp.async) while a row is worked
+// on; a thread reads only what it copied itself, so the copies need no barrier.
+// Each warp takes its maximum and its sum of exponentials, and sends the pair to
+// every block of the cluster (st.async, counted by an mbarrier); one warp of each
+// block joins them and computes the token's loss, and one block barrier hands the
+// factors to the others, which write the gradient from their registers.
+//
+// Bound by HBM: 2 rows vocab es bytes.  8192 x 131072 bf16: 672 us, 6.39 TB/s; 4096 x 131072
+// fp32: 666 us, 6.45 TB/s; 4096 x 32768 bf16: 96 us, 5.6 TB/s, where the chain of a row
+// (sum, exchange, loss, about 2 us) shows more.
+struct RowPlan {
+  int C;        // blocks per cluster
+  int per;      // slots per block: at most THREADS * K
+  int most;     // slots of a row at its worst alignment
+  int run;      // rows per cluster, at most 32
+};
+
+constexpr int kMaxCluster = 16;
+constexpr float kHuge = 1e38f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t kWaitLimit = 1u << 20;  // polls; a wait that runs out gives NaN
+
+// A row's slice in one block, all the same in every thread: slots lo .. lim - 1
+// of the slice lie wholly in the row (lo is 1 where slot 0 begins before it), slot
+// `tail` (or none, -1) holds the row's last, `left` elements.
+template <int DT>
+struct Slice {
+  static constexpr int N = Lanes<DT>::N;
+  const typename ElemOf<DT>::T* row;
+  int lead, lo, lim, tail, left;
+  __device__ __forceinline__ Slice(const typename ElemOf<DT>::T* r, int V, int s0, int per) : row(r) {
+    lead = (int)(((uintptr_t)r & 15) / sizeof(*r));
+    const int full = (V + lead) / N - s0;
+    left = (V + lead) % N;
+    lo = lead && s0 == 0;
+    lim = min(per, full);
+    tail = left && full >= lo && full < per ? full : -1;
+  }
+};
+
+template <int DT, int THREADS, int K, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS)
+policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, float4* partial) {
+  constexpr int N = Lanes<DT>::N, W = THREADS / 32;
+  using E = typename ElemOf<DT>::T;
+  extern __shared__ uint4 next[];                   // [K][THREADS]: the row that is on its way
+  __shared__ float2 pairs[2][kMaxCluster * W];      // (m, s) of every warp, by parity: a block may be one row ahead
+  __shared__ float4 result;
+  __shared__ float2 shared_c, again_sh[W];
+  __shared__ uint64_t bars[2];
+  pdl_enter();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)cluster_rank();
+  const unsigned long long cluster = blockIdx.x / plan.C, row0 = cluster * plan.run;
+  const int rows = (int)min((unsigned long long)plan.run, a.rows - row0);
+  const int V = (int)a.vocab, s0 = rank * plan.per;
+  const uint32_t mine = (uint32_t)__cvta_generic_to_shared(next) + tid * 16;
+  const uint32_t bars_at = (uint32_t)__cvta_generic_to_shared(bars);
+  // this warp's pair and the barriers in the block that this lane sends to
+  const uint32_t pair_to = cluster_address((uint32_t)__cvta_generic_to_shared(&pairs[0][rank * W + warp]),
+                                           min(lane, plan.C - 1));
+  const uint32_t bars_to = cluster_address(bars_at, min(lane, plan.C - 1));
+  if (tid == 0) {
+    mbar_init(bars_at, 1);
+    mbar_init(bars_at + 8, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+
+  // lane i holds row i's scalars
+  float w_l = 0.0f;
+  if (lane < rows) w_l = a.weights ? a.weights[row0 + lane] : 1.0f;
+  const uint32_t live = __ballot_sync(~0u, w_l != 0.0f);  // bit i: row i is not masked
+
+  const E* const logits = a.logits + row0 * a.stride;
+  const auto issue = [&](int i) {
+    if (i < rows && (live >> i & 1)) {
+      const Slice<DT> in(logits + i * a.stride, V, s0, plan.per);
+      // a slot that begins before the row also brings what lies there, but nothing from before the matrix
+      const bool before = in.lo && in.row - in.lead < a.logits;
+      const char* src = reinterpret_cast<const char*>(in.row - in.lead) + (s0 + tid) * 16ll;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (k * THREADS + tid < in.lim && (k > 0 || tid >= (int)before))
+          cp_async16(mine + k * THREADS * 16, src + k * THREADS * 16, 16);
+      if (in.tail >= 0 && in.tail % THREADS == tid)
+        cp_async16(mine + in.tail / THREADS * (THREADS * 16), src + in.tail / THREADS * (THREADS * 16),
+                   in.left * (int)sizeof(E));
+      if (tid == 0 && before) {
+        E* to = reinterpret_cast<E*>(&next[0]);
+        for (int x = in.lead; x < N && x < in.lead + V; ++x) to[x] = in.row[x - in.lead];
+      } else if (tid == 0 && in.lo && in.lead + V < N) {  // the row begins and ends inside one slot
+        cp_async16(mine, src, (in.lead + V) * (int)sizeof(E));
+      }
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (k * THREADS + tid >= plan.per || s0 + k * THREADS + tid >= plan.most) {
+      const uint32_t none = DT == kBF16 ? 0xff80ff80u : 0xff800000u;  // -infinity
+      st_shared16(mine + k * THREADS * 16, make_uint4(none, none, none, none));
+    }
+  issue(0);
+
+  int y_l = -1;
+  float old_l = 0.0f, adv_l = 0.0f, ref_l = 0.0f, x_l = 0.0f;
+  if (live >> lane & 1) {
+    const unsigned long long t = row0 + lane;
+    const long long y = load_index(a.targets, a.target_bytes, t);
+    y_l = y >= 0 && y < V ? (int)y : -1;
+    if (warp == 0) {
+      old_l = p.old_logprobs[t];
+      adv_l = p.advantages[t];
+      if (p.ref_logprobs) ref_l = p.ref_logprobs[t];
+      x_l = y_l < 0 ? __int_as_float(0x7fffffff) : to_float(a.logits[t * a.stride + y_l]);
+    }
+  }
+  // every block's barriers are set up before another block sends, and its targets' logits are read before another
+  // block may overwrite them (gradient in place)
+  if (plan.C > 1) cluster_sync();
+  else __syncthreads();
+
+  PolicySums sum;
+  int done = 0;
+  for (int i = 0; i < rows; ++i) {
+    E* const grad = a.grad + (row0 + i) * a.grad_stride;
+    if (!(live >> i & 1)) {
+      const Slots<DT> out(grad, V);
+      const int n = (int)out.count();
+      const float zero[N] = {};
+      for (int q = rank * THREADS + tid; q < n; q += plan.C * THREADS) store_slot<DT>(out, grad, true, q, zero);
+      if (rank == 0 && tid == 0) a.logprobs[row0 + i] = 0.0f;
+      issue(i + 1);
+      continue;
+    }
+    const int b = done & 1;
+    if (tid == 0) mbar_expect_tx(bars_at + 8 * b, plan.C * W * 8);
+    const Slice<DT> in(logits + i * a.stride, V, s0, plan.per);
+
+    cp_async_wait<0>();
+    // -infinity into what the slots at the row's ends hold beside the row, and into the slot after them, which
+    // an earlier row of another alignment may have filled
+    if (in.lo && tid == 0) {
+      E* to = reinterpret_cast<E*>(&next[0]);
+      for (int x = 0; x < in.lead; ++x) from_float(to + x, -INFINITY);
+    }
+    const int end = (V + in.lead + N - 1) / N - s0;  // the slot after the row's last
+    if (in.tail >= 0 && in.tail % THREADS == tid) {
+      E* to = reinterpret_cast<E*>(&next[in.tail / THREADS * THREADS + tid]);
+      for (int x = in.left; x < N; ++x) from_float(to + x, -INFINITY);
+    } else if (in.lo && V + in.lead < N && tid == 0) {
+      E* to = reinterpret_cast<E*>(&next[0]);
+      for (int x = V + in.lead; x < N; ++x) from_float(to + x, -INFINITY);
+    }
+    if (end >= 0 && end < plan.per && s0 + end < plan.most && end % THREADS == tid) {
+      E* to = reinterpret_cast<E*>(&next[end / THREADS * THREADS + tid]);
+      for (int x = 0; x < N; ++x) from_float(to + x, -INFINITY);
+    }
+
+    // the slots as they are, kept until the gradient is written
+    uint4 r[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) r[k] = ld_shared16(mine + k * THREADS * 16);
+    float m;
+    if constexpr (DT == kBF16) {
+      uint32_t mm = max_bf16x2(max_bf16x2(r[0].x, r[0].y), max_bf16x2(r[0].z, r[0].w));
+#pragma unroll
+      for (int k = 1; k < K; ++k)
+        mm = max_bf16x2(mm, max_bf16x2(max_bf16x2(r[k].x, r[k].y), max_bf16x2(r[k].z, r[k].w)));
+      m = fmaxf(bf16_lo(mm), bf16_hi(mm));
+    } else {
+      m = max_of<DT>(r[0]);
+#pragma unroll
+      for (int k = 1; k < K; ++k) m = fmaxf(m, max_of<DT>(r[k]));
+    }
+    // in powers of 2: b = m log2 e, e^x / 2^b = 2^(x log2 e - b).  |m| is held to 1e38, so that b is finite; where that
+    // matters the sum ends at 0 or infinity, and the row is done again below.
+    m = warp_max(m);
+    const float base = fminf(fmaxf(m, -kHuge), kHuge) * kLog2e;
+
+    float2 s2 = make_float2(0.0f, 0.0f);
+    const float2 minus_b = make_float2(-base, -base), log2e = make_float2(kLog2e, kLog2e);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const Acc<DT> x = widen<DT>(r[k]);
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        float2 z = fma2(make_float2(x.v[c], x.v[c + 1]), log2e, minus_b);
+        z.x = ex2(z.x);
+        z.y = ex2(z.y);
+        s2 = add2(s2, z);
+        if constexpr (DT == kF32) {  // the exponentials fit where the logits were
+          if (c == 0) { r[k].x = __float_as_uint(z.x); r[k].y = __float_as_uint(z.y); }
+          else { r[k].z = __float_as_uint(z.x); r[k].w = __float_as_uint(z.y); }
+        }
+      }
+    }
+    const float ws = warp_sum(s2.x + s2.y);
+    if (lane < plan.C) st_async(pair_to + b * (kMaxCluster * W * 8), make_float2(base, ws), bars_to + 8 * b);
+    issue(i + 1);
+
+    // by warp 0: the token's loss and what the gradient needs of it
+    const auto token = [&](float lp, float base, float S) {
+      const float c = policy_token(p, __shfl_sync(~0u, old_l, i), __shfl_sync(~0u, adv_l, i),
+                                   __shfl_sync(~0u, ref_l, i), __shfl_sync(~0u, w_l, i), lp, sum);
+      if (lane == 0) {
+        result = make_float4(base, -c / S, -c * expm1f(lp), 0.0f);
+        shared_c = make_float2(c, lp);
+        if (rank == 0) a.logprobs[row0 + i] = lp;
+      }
+    };
+    if (warp == 0) {
+      // the row's base B and sum S
+      const bool ok = mbar_wait(bars_at + 8 * b, done >> 1 & 1, kWaitLimit);
+      float B = -FLT_MAX, S = 0.0f;
+      for (int q = lane; q < plan.C * W; q += 32) B = fmaxf(B, pairs[b][q].x);
+      B = warp_max(B);
+      for (int q = lane; q < plan.C * W; q += 32) S += pairs[b][q].y * ex2(pairs[b][q].x - B);
+      S = warp_sum(S);
+      if (!ok) S = __int_as_float(0x7fffffff);
+      const bool again = ok && !(S > 0.0f && S < INFINITY);
+      if (!again) token((fmaf(__shfl_sync(~0u, x_l, i), kLog2e, -B) - log2f(S)) * kLn2, B, S);
+      else if (lane == 0) result.w = 1.0f;
+    }
+    __syncthreads();
+    const float4 res = result;
+    ++done;
+    if (res.w != 0.0f) {
+      // no finite sum: values beyond 1e38 (masks of the type's lowest value all over the row, say) or a row without
+      // a distribution.  Every block goes over the whole row once more, with differences formed first.
+      const MaxSum st = row_stats<DT, THREADS>(in.row, V, again_sh);
+      if (plan.C > 1) cluster_sync();  // nobody reads the row any more
+      if (warp == 0) token((__shfl_sync(~0u, x_l, i) - st.m) - logf(st.s), st.m, st.s);
+      __syncthreads();
+      row_grad<DT>(in.row, grad, V, __shfl_sync(~0u, y_l, i), shared_c.y, st, shared_c.x, s0 + tid, s0 + plan.per,
+                   THREADS);
+      continue;
+    }
+
+    // fp32: the exponentials, to the warp's base; bf16: the logits, whose exponentials are taken again (half the
+    // registers, so that more rows are on the SM at a time), to the row's base
+    const float f = DT == kF32 ? res.y * ex2(base - res.x) : res.y;
+    const float2 f2 = make_float2(f, f), minus_B = make_float2(-res.x, -res.x);
+    if constexpr (DT == kBF16)  // unpacked again, not kept unpacked
+#pragma unroll
+      for (int k = 0; k < K; ++k) asm volatile("" : "+r"(r[k].x), "+r"(r[k].y), "+r"(r[k].z), "+r"(r[k].w));
+    const auto values = [&](int k) {
+      Acc<DT> g = widen<DT>(r[k]);
+#pragma unroll
+      for (int x = 0; x < N; x += 2) {
+        float2 v = make_float2(g.v[x], g.v[x + 1]);
+        if constexpr (DT == kBF16) {
+          v = fma2(v, log2e, minus_B);
+          v.x = ex2(v.x);
+          v.y = ex2(v.y);
+        }
+        v = mul2(v, f2);
+        g.v[x] = v.x;
+        g.v[x + 1] = v.y;
+      }
+      return g;
+    };
+    const bool same = (((uintptr_t)in.row ^ (uintptr_t)grad) & 15) == 0;
+    if (same) {
+      char* dst = reinterpret_cast<char*>(grad - in.lead) + (s0 + tid) * 16ll;
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (k * THREADS + tid < in.lim && (k > 0 || tid >= in.lo))
+          st_stream(reinterpret_cast<uint4*>(dst + k * THREADS * 16), narrow<DT>(values(k), 1.0f, false));
+    }
+    // slots at the row's ends, or all of them when the gradient's rows start at another alignment: by elements
+    const bool first = in.lo && tid == 0, last = in.tail >= 0 && in.tail % THREADS == tid;
+    if (!same || first || last) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const int q = k * THREADS + tid;
+        if (q < plan.per && (!same || (q == 0 && first) || (q == in.tail && last))) {
+          const int j = (s0 + q) * N - in.lead;
+          const Acc<DT> g = values(k);
+#pragma unroll
+          for (int x = 0; x < N; ++x)
+            if (j + x >= 0 && j + x < V) from_float(grad + j + x, g.v[x]);
+        }
+      }
+    }
+    const int y = __shfl_sync(~0u, y_l, i);
+    const int yq = (y + in.lead) / N - s0;
+    if (y >= 0 && yq >= 0 && yq < plan.per && yq % THREADS == tid) from_float(grad + y, res.z);  // over its own store
+  }
+  if (rank == 0 && tid == 0) partial[cluster] = make_float4(sum.loss, sum.kl, sum.clipped, sum.weight);
+  if (plan.C > 1) cluster_meet();   // no block leaves while another may still send to it
 }
 
 // The blocks' sums in a fixed order.
@@ -237,26 +553,97 @@ __global__ void __launch_bounds__(kThreads) preference_grad_kernel(const Matrix<
     st.m = stats[t].x;
     st.s = stats[t].y;
     row_grad<DT>(a.logits + t * a.stride, grad, (long long)a.vocab, load_index(a.targets, a.target_bytes, t),
-                 a.logprobs[t], st, w * p.side[k]);
+                 a.logprobs[t], st, w * p.side[k], threadIdx.x, LLONG_MAX, kThreads);
   }
 }
 
-inline unsigned grid_of(unsigned long long work, unsigned most) {
-  return (unsigned)std::max(1ull, std::min<unsigned long long>(work, most));
+inline unsigned grid_of(unsigned long long work) {
+  return (unsigned)std::max(1ull, std::min<unsigned long long>(work, kMaxLossBlocks));
 }
 
 template <int DT>
 cudaError_t run_logprobs(const LogitsCall& c) {
-  return launch_kernel(logprob_kernel<DT>, grid_of(c.rows, kMaxLossBlocks), kThreads, 0, c.stream, true,
+  return launch_kernel(logprob_kernel<DT>, grid_of(c.rows), kThreads, 0, c.stream, true,
                        Matrix<DT>(c), (float2*)nullptr);
 }
 
+// Rows per cluster: about four waves of clusters, so that the blocks of an SM
+// are at different points of their rows and the last wave is short, but at most
+// 8 (4096 x 32768 bf16: 1 row 123 us, 2 101, 3 96, 4 96, 8 100; 8192 x 131072: 2
+// 772, 4 708, 8 690, 16 684).  More only to bound the number of partial sums.
+inline int rows_per_cluster(unsigned long long rows, unsigned clusters_per_wave) {
+  const unsigned long long four_waves = rows / (4ull * std::max(1u, clusters_per_wave));
+  const unsigned long long bound = (rows + kMaxPolicySums - 1) / kMaxPolicySums;
+  return (int)std::min(32ull, std::max({1ull, std::min(8ull, four_waves), bound}));
+}
+
+template <int DT, int THREADS, int K, int BLOCKS>
+cudaError_t launch_policy_row(const LogitsCall& c, const PolicyParams& p, unsigned long long slots, int C,
+                              float4* partial, unsigned* sums) {
+  constexpr int smem = K * THREADS * 16;
+  const auto kernel = policy_row_kernel<DT, THREADS, K, BLOCKS>;
+  RowPlan plan;
+  plan.C = C;
+  plan.per = (int)((slots + C - 1) / C);
+  plan.most = (int)slots;
+  plan.run = rows_per_cluster(c.rows, (unsigned)(c.sms * BLOCKS / C));
+  *sums = (unsigned)((c.rows + plan.run - 1) / plan.run);
+  cudaError_t e = cudaSuccess;
+  if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = *sums * C;
+  cfg.blockDim = THREADS;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, Matrix<DT>(c), p, plan, partial);
+}
+
+// The shape by the row's length in 16-byte slots.  Registers hold the row: a
+// slice of 32 KiB in 256 threads leaves room for four blocks on an SM, which was
+// faster than two blocks of 512 threads with a deeper queue (8192 x 131072 bf16
+// 690 against 984 us, before the exponentials were taken twice to halve the
+// registers 826).  From a cluster of more than 4 such blocks on, slices of
+// 64 KiB, two on an SM, in half the blocks (131072 bf16: 672 against 690 us; fp32:
+// 666 against 687; at 65536 they are level).  Short rows take small blocks, many
+// on an SM (8192 x 4096 bf16: 64 threads 35 us, 128 threads 40, 256 threads 52).
 template <int DT>
 cudaError_t run_policy(const LogitsCall& c, const PolicyParams& p, float* stats, float4* partial) {
-  const unsigned grid = grid_of(c.rows, kMaxLossBlocks);
-  cudaError_t e = launch_kernel(policy_kernel<DT>, grid, kThreads, 0, c.stream, true, Matrix<DT>(c), p, partial);
+  constexpr int N = Lanes<DT>::N;
+  const size_t es = sizeof(typename ElemOf<DT>::T);
+  const bool alike = c.rows == 1 || c.row_stride * es % 16 == 0;  // every row starts at the same alignment
+  const unsigned long long lead = alike ? ((uintptr_t)c.logits & 15) / es : N - 1;
+  const unsigned long long n = c.vocab / N + (c.vocab % N + lead + N - 1) / N;
+  unsigned sums = 0;
+  cudaError_t e;
+#define AR_ROW(THREADS, K, BLOCKS) launch_policy_row<DT, THREADS, K, BLOCKS>(c, p, n, C, partial, &sums)
+  if (c.rows == 0 || n > 16 * 4096) {
+    sums = grid_of(c.rows);
+    e = launch_kernel(policy_kernel<DT>, sums, kThreads, 0, c.stream, true, Matrix<DT>(c), p, partial);
+  } else if (n <= 1024) {
+    constexpr int C = 1;
+    e = n <= 512 ? AR_ROW(64, 8, 14) : AR_ROW(128, 8, 7);
+  } else if (n <= 8192) {
+    const int C = n <= 2048 ? 1 : n <= 4096 ? 2 : 4;
+    const unsigned long long k = (n + 256 * C - 1) / (256 * C);  // 5 .. 8
+    e = k <= 5 ? AR_ROW(256, 5, 4) : k == 6 ? AR_ROW(256, 6, 4) : k == 7 ? AR_ROW(256, 7, 4) : AR_ROW(256, 8, 4);
+  } else {
+    const int C = n <= 16384 ? 4 : n <= 32768 ? 8 : 16;
+    const unsigned long long k = (n + 256 * C - 1) / (256 * C);  // 9 .. 16
+    e = k <= 10 ? AR_ROW(256, 10, 2) : k <= 12 ? AR_ROW(256, 12, 2) : k <= 14 ? AR_ROW(256, 14, 2) : AR_ROW(256, 16, 2);
+  }
+#undef AR_ROW
   if (e == cudaSuccess)
-    e = launch_kernel(policy_sum_kernel, 1, kThreads, 0, c.stream, true, (const float4*)partial, (int)grid, p.scale,
+    e = launch_kernel(policy_sum_kernel, 1, kThreads, 0, c.stream, true, (const float4*)partial, (int)sums, p.scale,
                       stats);
   return e;
 }
@@ -265,12 +652,12 @@ template <int DT>
 cudaError_t run_preference(const LogitsCall& c, const PairParams& p, float2* stats) {
   cudaError_t e = cudaSuccess;
   if (c.rows)
-    e = launch_kernel(logprob_kernel<DT>, grid_of(c.rows, kMaxLossBlocks), kThreads, 0, c.stream, true, Matrix<DT>(c),
+    e = launch_kernel(logprob_kernel<DT>, grid_of(c.rows), kThreads, 0, c.stream, true, Matrix<DT>(c),
                       stats);
   if (e == cudaSuccess && p.pairs)
-    e = launch_kernel(pair_kernel, grid_of(p.pairs, kMaxLossBlocks), kThreads, 0, c.stream, true, p);
+    e = launch_kernel(pair_kernel, grid_of(p.pairs), kThreads, 0, c.stream, true, p);
   if (e == cudaSuccess)
-    e = launch_kernel(preference_grad_kernel<DT>, grid_of(c.rows, kMaxLossBlocks), kThreads, 0, c.stream, true,
+    e = launch_kernel(preference_grad_kernel<DT>, grid_of(c.rows), kThreads, 0, c.stream, true,
                       Matrix<DT>(c), p, (const float2*)stats);
   return e;
 }
@@ -285,6 +672,11 @@ cudaError_t launch_policy(const LogitsCall& c, const PolicyCall& q) {
   const PolicyParams p{q.old_logprobs, q.advantages, q.ref_logprobs, q.lo, q.hi, q.kl_coef, q.scale};
   float4* partial = static_cast<float4*>(q.workspace);
   return c.dtype == kF32 ? run_policy<kF32>(c, p, q.stats, partial) : run_policy<kBF16>(c, p, q.stats, partial);
+}
+
+// one partial sum per cluster of rows (rows_per_cluster)
+size_t policy_workspace(size_t rows) {
+  return std::max<size_t>(1, std::max(std::min(rows, kMaxPolicySums), (rows + 31) / 32)) * sizeof(float4);
 }
 
 // workspace: {m, s} per row, then the pairs' losses and the sequences' factors

@@ -119,32 +119,36 @@ extern "C" {
 ar_status_t ar_token_logprobs(const void* logits, size_t rows, size_t vocab, size_t row_stride, ar_dtype_t dtype,
                               const void* targets, int target_bytes, const float* weights, float* logprobs,
                               void* stream) {
-  const ar::LogitsCall c{logits, nullptr, rows, vocab, row_stride, 0, (int)dtype, targets, target_bytes, weights,
-                         logprobs, static_cast<cudaStream_t>(stream)};
+  ar::LogitsCall c{logits, nullptr, rows, vocab, row_stride, 0, (int)dtype, targets, target_bytes, weights,
+                         logprobs, static_cast<cudaStream_t>(stream), 0};
   const ar_status_t st = check_logits(c, false);
   if (st != AR_SUCCESS || rows == 0) return st;
+  if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
   Range range("ar_token_logprobs");
   return finish(ar::launch_logprobs(c), "token_logprobs", rows, vocab);
 }
 
-size_t ar_policy_loss_workspace(void) { return ar::kMaxLossBlocks * 4 * sizeof(float); }
+size_t ar_policy_loss_workspace(size_t rows) {
+  return rows > (size_t)1 << 56 ? SIZE_MAX : ar::policy_workspace(rows);
+}
 
 ar_status_t ar_policy_loss(const void* logits, size_t rows, size_t vocab, size_t row_stride, ar_dtype_t dtype,
                            const void* targets, int target_bytes, const float* weights, const float* old_logprobs,
                            const float* advantages, const float* ref_logprobs, float clip_low, float clip_high,
                            float kl_coef, float scale, void* grad, size_t grad_stride, float* logprobs, float* stats,
                            void* workspace, size_t workspace_bytes, void* stream) {
-  const ar::LogitsCall c{logits, grad, rows, vocab, row_stride, grad_stride, (int)dtype, targets, target_bytes, weights,
-                         logprobs, static_cast<cudaStream_t>(stream)};
+  ar::LogitsCall c{logits, grad, rows, vocab, row_stride, grad_stride, (int)dtype, targets, target_bytes, weights,
+                         logprobs, static_cast<cudaStream_t>(stream), 0};
   const ar_status_t st = check_logits(c, true);
   if (st != AR_SUCCESS) return st;
   if (!(clip_low >= 0.0f) || !(clip_high >= 0.0f) || nan(kl_coef) || nan(scale)) return AR_ERR_INVALID_ARG;
-  if (!aligned(stats, 4) || !aligned(workspace, 16) || workspace_bytes < ar_policy_loss_workspace())
+  if (!aligned(stats, 4) || !aligned(workspace, 16) || workspace_bytes < ar_policy_loss_workspace(rows))
     return AR_ERR_INVALID_ARG;
   if (rows && (!aligned(old_logprobs, 4) || !aligned(advantages, 4) || !aligned_or_null(ref_logprobs, 4)))
     return AR_ERR_INVALID_ARG;
   const ar::PolicyCall p{old_logprobs, advantages, ref_logprobs, (float)(1.0 - (double)clip_low),
                          (float)(1.0 + (double)clip_high), kl_coef, scale, stats, workspace};
+  if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
   Range range("ar_policy_loss");
   return finish(ar::launch_policy(c, p), "policy_loss", rows, vocab);
 }
@@ -159,8 +163,8 @@ ar_status_t ar_preference_loss(const void* logits, size_t rows, size_t vocab, si
                                int offset_bytes, size_t pairs, const float* ref_logprobs, float beta,
                                float label_smoothing, float scale, void* grad, size_t grad_stride, float* logprobs,
                                float* loss, float* margins, void* workspace, size_t workspace_bytes, void* stream) {
-  const ar::LogitsCall c{logits, grad, rows, vocab, row_stride, grad_stride, (int)dtype, targets, target_bytes, weights,
-                         logprobs, static_cast<cudaStream_t>(stream)};
+  ar::LogitsCall c{logits, grad, rows, vocab, row_stride, grad_stride, (int)dtype, targets, target_bytes, weights,
+                         logprobs, static_cast<cudaStream_t>(stream), 0};
   const ar_status_t st = check_logits(c, true);
   if (st != AR_SUCCESS) return st;
   if (nan(beta) || nan(scale) || !(label_smoothing >= 0.0f && label_smoothing <= 1.0f)) return AR_ERR_INVALID_ARG;
@@ -171,6 +175,7 @@ ar_status_t ar_preference_loss(const void* logits, size_t rows, size_t vocab, si
   if (workspace_bytes < need || (need && !aligned(workspace, 16))) return AR_ERR_INVALID_ARG;
   const ar::PreferenceCall p{offsets, offset_bytes, pairs, ref_logprobs, beta, label_smoothing, scale, loss, margins,
                              workspace};
+  if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
   Range range("ar_preference_loss");
   return finish(ar::launch_preference(c, p), "preference_loss", rows, vocab);
 }

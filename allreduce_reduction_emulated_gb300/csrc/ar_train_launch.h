@@ -20,6 +20,7 @@ struct LogitsCall {
   const float* weights;            // NULL: all 1
   float* logprobs;
   cudaStream_t stream;
+  int sms;                         // multiprocessors of the device
 };
 
 struct PolicyCall {
@@ -39,13 +40,13 @@ struct PreferenceCall {
   void* workspace;
 };
 
-// Most blocks a loss kernel launches (its rows are strided over them): the
-// policy loss keeps one partial sum per block.
+// Most blocks of a kernel whose rows are strided over its blocks.
 constexpr unsigned kMaxLossBlocks = 1216;
 
 cudaError_t launch_logprobs(const LogitsCall& c);
 cudaError_t launch_policy(const LogitsCall& c, const PolicyCall& p);
 cudaError_t launch_preference(const LogitsCall& c, const PreferenceCall& p);
+size_t policy_workspace(size_t rows);
 size_t preference_workspace(size_t rows, size_t pairs);
 
 // One call over many gradient tensors (host arrays, read during the call).

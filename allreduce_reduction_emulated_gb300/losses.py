@@ -164,7 +164,7 @@ def policy_loss(logits, targets, old_logprobs, advantages, ref_logprobs=None, we
     if scale is None:
         scale = 1.0 / max(1, rows) if weights is None else 1.0
     lib = library()
-    bytes_ = lib.ar_policy_loss_workspace()
+    bytes_ = lib.ar_policy_loss_workspace(rows)
     context, handle = _on(stream)
     with context:
         grad, grad_stride = _gradient(what, logits, grad, device, rows, vocab)

@@ -73,13 +73,13 @@ ar_status_t ar_token_logprobs(const void* logits, size_t rows, size_t vocab, siz
  *   logprobs      rows floats: lp (0 for masked rows)
  *   stats         4 floats: loss, scale * sum w (exp(d) - 1 - d),
  *                 scale * sum w [clipped], scale * sum w
- *   workspace     at least ar_policy_loss_workspace() bytes, 16-byte aligned;
+ *   workspace     at least ar_policy_loss_workspace(rows) bytes, 16-byte aligned;
  *                 its contents on entry do not matter
  * rows == 0 writes zero stats.  Errors as for ar_token_logprobs;
  * AR_ERR_INVALID_ARG also for a NaN parameter, a negative clip bound, a
  * workspace that is too small or an overlap.
  */
-size_t ar_policy_loss_workspace(void);
+size_t ar_policy_loss_workspace(size_t rows);
 ar_status_t ar_policy_loss(const void* logits, size_t rows, size_t vocab, size_t row_stride,
                            ar_dtype_t dtype, const void* targets, int target_bytes,
                            const float* weights, const float* old_logprobs,

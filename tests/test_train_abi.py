@@ -32,8 +32,9 @@ def test_token_logprobs_arguments(lib):
 
 
 def test_policy_loss_arguments(lib):
-    need = lib.ar_policy_loss_workspace()
+    need = lib.ar_policy_loss_workspace(4)
     assert need > 0
+    assert lib.ar_policy_loss_workspace(1 << 60) == ctypes.c_size_t(-1).value
 
     def call(logits=P, rows=4, vocab=8, stride=8, dtype=ar.AR_FLOAT32, targets=P, size=8, weights=None, old=P, adv=P,
              ref=None, lo=0.2, hi=0.2, kl=0.0, scale=1.0, grad=1 << 20, gstride=8, lp=P, stats=P, ws=P, nbytes=need):
