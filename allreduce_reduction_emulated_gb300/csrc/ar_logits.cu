@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr size_t kMaxPolicySums = 65536;
+constexpr unsigned long long kShortRow = 1024;  // slots: up to here a warp takes a row (log-probabilities)
 
 template <int DT>
 struct Matrix {
@@ -78,27 +79,215 @@ __device__ __forceinline__ void row_zero(typename ElemOf<DT>::T* grad, long long
   for (long long s = threadIdx.x; s < n; s += kThreads) store_slot<DT>(out, grad, true, s, zero);
 }
 
+// ---------------------------------------------------- statistics in powers of 2
+//
+// b = m log2 e and the sum of e^x / 2^b = 2^(x log2 e - b): one fused multiply-add
+// and one exponential per element.  |m| is held to 1e38, so that b is finite (masks
+// of the type's lowest value are beyond it).  Where that matters, the row's sum ends
+// at 0, infinity or NaN, and the row is gone over again with MaxSum, which forms
+// the differences first.
+constexpr float kHuge = 1e38f, kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float base_of(float m) { return fminf(fmaxf(m, -kHuge), kHuge) * kLog2e; }
+__device__ __forceinline__ bool usable(float sum) { return sum > 0.0f && sum < INFINITY; }
+
+template <int DT>
+__device__ __forceinline__ float max_of(uint4 r) {
+  const Acc<DT> a = widen<DT>(r);
+  float m = a.v[0];
+#pragma unroll
+  for (int i = 1; i < Lanes<DT>::N; ++i) m = fmaxf(m, a.v[i]);
+  return m;
+}
+
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));  // a NaN yields to the other operand
+  return r;
+}
+
+template <int DT, int K>
+__device__ __forceinline__ float max_of(const uint4 (&r)[K]) {
+  if constexpr (DT == kBF16) {
+    uint32_t m = max_bf16x2(max_bf16x2(r[0].x, r[0].y), max_bf16x2(r[0].z, r[0].w));
+#pragma unroll
+    for (int k = 1; k < K; ++k)
+      m = max_bf16x2(m, max_bf16x2(max_bf16x2(r[k].x, r[k].y), max_bf16x2(r[k].z, r[k].w)));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+  } else {
+    float m = max_of<DT>(r[0]);
+#pragma unroll
+    for (int k = 1; k < K; ++k) m = fmaxf(m, max_of<DT>(r[k]));
+    return m;
+  }
+}
+
+// 2^(x log2 e - b) of a pair
+__device__ __forceinline__ float2 exp2_pair(float x, float y, float2 minus_b) {
+  float2 z = fma2(make_float2(x, y), make_float2(kLog2e, kLog2e), minus_b);
+  z.x = ex2(z.x);
+  z.y = ex2(z.y);
+  return z;
+}
+
+__device__ __forceinline__ uint4 no_logits(int dtype) {  // a slot of -infinity
+  const uint32_t v = dtype == kBF16 ? 0xff80ff80u : 0xff800000u;
+  return make_uint4(v, v, v, v);
+}
+
+// A row's slice in one block, all the same in every thread: slots lo .. lim - 1
+// of the slice lie wholly in the row (lo is 1 where slot 0 begins before it), slot
+// `tail` (or none, -1) holds the row's last, `left` elements.
+template <int DT>
+struct Slice {
+  static constexpr int N = Lanes<DT>::N;
+  const typename ElemOf<DT>::T* row;
+  int lead, lo, lim, tail, left;
+  __device__ __forceinline__ Slice(const typename ElemOf<DT>::T* r, int V, int s0, int per) : row(r) {
+    lead = (int)(((uintptr_t)r & 15) / sizeof(*r));
+    const int full = (V + lead) / N - s0;
+    left = (V + lead) % N;
+    lo = lead && s0 == 0;
+    lim = min(per, full);
+    tail = left && full >= lo && full < per ? full : -1;
+  }
+};
+
 // ----------------------------------------------------------- log-probabilities
 
-// stats != NULL: {m, s} of every row for the gradient that follows
-template <int DT>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, float2* stats) {
+// What the gradient of a row needs: p = 2^(x log2 e - b) / s, or, s < 0 (a row that
+// was gone over again), e^(x - b) / -s.
+__device__ __forceinline__ float2 pack_stats(float b, float s, bool natural) { return make_float2(b, natural ? -s : s); }
+
+// Log-probability of every row's target; stats != NULL: its statistics too, and 0
+// into factors[t], for the preference loss.
+//
+// One pass with a running base, four slots per thread on the way while four are
+// worked on.  GROUP threads take a row: a warp where a row is short (eight rows in
+// a block), else the block; with few long rows, a cluster of C blocks.
+struct LogprobPlan {
+  int C, per;  // blocks per row; slots per block
+};
+
+template <int DT, int GROUP>
+__global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, const LogprobPlan plan, float2* stats,
+                                                           float* factors) {
+  constexpr int N = Lanes<DT>::N, U = 4, W = kThreads / 32;
+  using E = typename ElemOf<DT>::T;
   pdl_enter();
-  __shared__ float2 sh[kThreads / 32];
-  for (unsigned long long t = blockIdx.x; t < a.rows; t += gridDim.x) {
-    const float w = a.weights ? a.weights[t] : 1.0f;
-    if (w == 0.0f) {
-      if (threadIdx.x == 0) a.logprobs[t] = 0.0f;
-      continue;
+  __shared__ float2 sh[W], mine;
+  const int tid = threadIdx.x % GROUP, lane = threadIdx.x & 31;
+  const unsigned long long t = GROUP == kThreads ? blockIdx.x / plan.C
+                                                 : blockIdx.x * (unsigned long long)(kThreads / GROUP) +
+                                                       threadIdx.x / GROUP;
+  if (t >= a.rows) return;                         // whole warps; never with GROUP == kThreads
+  const int rank = GROUP == kThreads ? (int)cluster_rank() : 0;
+  const bool writer = rank == 0 && tid == 0;
+  if (writer && stats) factors[t] = 0.0f;
+  if (a.weights && a.weights[t] == 0.0f) {         // the same in all blocks of the cluster
+    if (writer) a.logprobs[t] = 0.0f;
+    return;
+  }
+  const int V = (int)a.vocab, s0 = rank * plan.per;
+  const E* row = a.logits + t * a.stride;
+  const Slice<DT> in(row, V, s0, plan.per);
+  const uint4* src = reinterpret_cast<const uint4*>(row - in.lead) + s0 + tid;
+  const long long y = writer ? load_index(a.targets, a.target_bytes, t) : 0;
+
+  const auto load = [&](int at, uint4 (&r)[U]) {
+    if (at + U * GROUP <= in.lim && at >= in.lo) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) r[u] = ld_row(src + at + u * GROUP);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int q = at + u * GROUP + tid;
+        r[u] = no_logits(DT);
+        if (q >= in.lo && q < in.lim) r[u] = ld_row(src + at + u * GROUP);
+      }
     }
-    const typename ElemOf<DT>::T* row = a.logits + t * a.stride;
-    const MaxSum st = row_stats<DT, kThreads>(row, (long long)a.vocab, sh);
-    if (threadIdx.x == 0) {
-      const long long y = load_index(a.targets, a.target_bytes, t);
-      a.logprobs[t] = target_logprob(row, (long long)a.vocab, y, st.m, st.s);
-      if (stats) stats[t] = make_float2(st.m, st.s);
+  };
+  float m = -FLT_MAX, b = base_of(m);
+  float2 s2 = make_float2(0.0f, 0.0f);
+  const auto grow = [&](float top) {
+    m = fmaxf(m, top);
+    const float to = base_of(m), f = ex2(b - to);
+    s2 = mul2(s2, make_float2(f, f));
+    b = to;
+  };
+  uint4 r[U], next[U] = {};
+  load(0, r);
+  // the row's ends by elements: slot 0 where the row begins inside it, the last where it ends inside it
+  for (int e = 0; e < 2; ++e) {
+    const int q = e == 0 ? (in.lo ? 0 : -1) : in.tail;
+    if (q >= 0 && q % GROUP == tid) {
+      const int j = (s0 + q) * N - in.lead;
+      for (int x = max(0, -j); x < N && j + x < V; ++x) {
+        const float v = to_float(row[j + x]);
+        grow(v);
+        s2.x += ex2(fmaf(v, kLog2e, -b));
+      }
     }
+  }
+  for (int at = 0; at < in.lim; at += U * GROUP) {
+    if (at + U * GROUP < in.lim) load(at + U * GROUP, next);
+    grow(max_of<DT>(r));
+    const float2 minus_b = make_float2(-b, -b);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const Acc<DT> x = widen<DT>(r[u]);
+      float2 part = exp2_pair(x.v[0], x.v[1], minus_b);  // a slot is added up first: short chains of roundings
+#pragma unroll
+      for (int c = 2; c < N; c += 2) part = add2(part, exp2_pair(x.v[c], x.v[c + 1], minus_b));
+      s2 = add2(s2, part);
+      r[u] = next[u];
+    }
+  }
+  // joined: warp, block, cluster
+  float B = warp_max(b), S = warp_sum((s2.x + s2.y) * ex2(b - B));
+  if constexpr (GROUP == kThreads) {
+    if (lane == 0) sh[threadIdx.x >> 5] = make_float2(B, S);
     __syncthreads();
+    const float2 v = lane < W ? sh[lane] : make_float2(-FLT_MAX, 0.0f);
+    B = warp_max(v.x);
+    S = warp_sum(v.y * ex2(v.x - B));
+    if (plan.C > 1) {
+      if (threadIdx.x == 0) mine = make_float2(B, S);
+      cluster_sync();
+      const float2 v2 = lane < plan.C ? ld_cluster(cluster_address((uint32_t)__cvta_generic_to_shared(&mine), lane))
+                                      : make_float2(-FLT_MAX, 0.0f);
+      B = warp_max(v2.x);
+      S = warp_sum(v2.y * ex2(v2.x - B));
+      cluster_meet();                              // nobody leaves before the others have read
+    }
+  }
+  float x = 0.0f;
+  if (writer) x = y >= 0 && y < V ? to_float(row[y]) : __int_as_float(0x7fffffff);
+  if (usable(S)) {
+    if (writer) {
+      a.logprobs[t] = (fmaf(x, kLog2e, -B) - log2f(S)) * kLn2;
+      if (stats) stats[t] = pack_stats(B, S, false);
+    }
+    return;
+  }
+  if (rank != 0) return;
+  MaxSum st;
+  const Slots<DT> all(row, V);
+  for (long long s = tid; s < all.count(); s += GROUP) {
+    float v[N];
+    all.load(s, v, -INFINITY);
+    st.add(v);
+  }
+  if constexpr (GROUP == kThreads) {
+    __syncthreads();                               // sh is free again
+    st = block_join<kThreads>(st, sh);
+  } else {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) st.join(__shfl_xor_sync(~0u, st.m, d), __shfl_xor_sync(~0u, st.s, d));
+  }
+  if (writer) {
+    a.logprobs[t] = (x - st.m) - logf(st.s);
+    if (stats) stats[t] = pack_stats(st.m, st.s, true);
   }
 }
 
@@ -135,21 +324,6 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, co
   if (threadIdx.x == 0) partial[blockIdx.x] = make_float4(sum.loss, sum.kl, sum.clipped, sum.weight);
 }
 
-template <int DT>
-__device__ __forceinline__ float max_of(uint4 r) {
-  const Acc<DT> a = widen<DT>(r);
-  float m = a.v[0];
-#pragma unroll
-  for (int i = 1; i < Lanes<DT>::N; ++i) m = fmaxf(m, a.v[i]);
-  return m;
-}
-
-__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));  // a NaN yields to the other operand
-  return r;
-}
-
 // The same with the row kept on the chip: read once, written once.
 //
 // A cluster of C blocks takes `run` rows, one after the other; each block holds
@@ -172,26 +346,7 @@ struct RowPlan {
 };
 
 constexpr int kMaxCluster = 16;
-constexpr float kHuge = 1e38f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls; a wait that runs out gives NaN
-
-// A row's slice in one block, all the same in every thread: slots lo .. lim - 1
-// of the slice lie wholly in the row (lo is 1 where slot 0 begins before it), slot
-// `tail` (or none, -1) holds the row's last, `left` elements.
-template <int DT>
-struct Slice {
-  static constexpr int N = Lanes<DT>::N;
-  const typename ElemOf<DT>::T* row;
-  int lead, lo, lim, tail, left;
-  __device__ __forceinline__ Slice(const typename ElemOf<DT>::T* r, int V, int s0, int per) : row(r) {
-    lead = (int)(((uintptr_t)r & 15) / sizeof(*r));
-    const int full = (V + lead) / N - s0;
-    left = (V + lead) % N;
-    lo = lead && s0 == 0;
-    lim = min(per, full);
-    tail = left && full >= lo && full < per ? full : -1;
-  }
-};
 
 template <int DT, int THREADS, int K, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
@@ -251,10 +406,8 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
   };
 #pragma unroll
   for (int k = 0; k < K; ++k)
-    if (k * THREADS + tid >= plan.per || s0 + k * THREADS + tid >= plan.most) {
-      const uint32_t none = DT == kBF16 ? 0xff80ff80u : 0xff800000u;  // -infinity
-      st_shared16(mine + k * THREADS * 16, make_uint4(none, none, none, none));
-    }
+    if (k * THREADS + tid >= plan.per || s0 + k * THREADS + tid >= plan.most)
+      st_shared16(mine + k * THREADS * 16, no_logits(DT));
   issue(0);
 
   int y_l = -1;
@@ -316,33 +469,16 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     uint4 r[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) r[k] = ld_shared16(mine + k * THREADS * 16);
-    float m;
-    if constexpr (DT == kBF16) {
-      uint32_t mm = max_bf16x2(max_bf16x2(r[0].x, r[0].y), max_bf16x2(r[0].z, r[0].w));
-#pragma unroll
-      for (int k = 1; k < K; ++k)
-        mm = max_bf16x2(mm, max_bf16x2(max_bf16x2(r[k].x, r[k].y), max_bf16x2(r[k].z, r[k].w)));
-      m = fmaxf(bf16_lo(mm), bf16_hi(mm));
-    } else {
-      m = max_of<DT>(r[0]);
-#pragma unroll
-      for (int k = 1; k < K; ++k) m = fmaxf(m, max_of<DT>(r[k]));
-    }
-    // in powers of 2: b = m log2 e, e^x / 2^b = 2^(x log2 e - b).  |m| is held to 1e38, so that b is finite; where that
-    // matters the sum ends at 0 or infinity, and the row is done again below.
-    m = warp_max(m);
-    const float base = fminf(fmaxf(m, -kHuge), kHuge) * kLog2e;
+    const float base = base_of(warp_max(max_of<DT>(r)));
 
     float2 s2 = make_float2(0.0f, 0.0f);
-    const float2 minus_b = make_float2(-base, -base), log2e = make_float2(kLog2e, kLog2e);
+    const float2 minus_b = make_float2(-base, -base);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const Acc<DT> x = widen<DT>(r[k]);
 #pragma unroll
       for (int c = 0; c < N; c += 2) {
-        float2 z = fma2(make_float2(x.v[c], x.v[c + 1]), log2e, minus_b);
-        z.x = ex2(z.x);
-        z.y = ex2(z.y);
+        const float2 z = exp2_pair(x.v[c], x.v[c + 1], minus_b);
         s2 = add2(s2, z);
         if constexpr (DT == kF32) {  // the exponentials fit where the logits were
           if (c == 0) { r[k].x = __float_as_uint(z.x); r[k].y = __float_as_uint(z.y); }
@@ -373,7 +509,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       for (int q = lane; q < plan.C * W; q += 32) S += pairs[b][q].y * ex2(pairs[b][q].x - B);
       S = warp_sum(S);
       if (!ok) S = __int_as_float(0x7fffffff);
-      const bool again = ok && !(S > 0.0f && S < INFINITY);
+      const bool again = ok && !usable(S);
       if (!again) token((fmaf(__shfl_sync(~0u, x_l, i), kLog2e, -B) - log2f(S)) * kLn2, B, S);
       else if (lane == 0) result.w = 1.0f;
     }
@@ -404,11 +540,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
 #pragma unroll
       for (int x = 0; x < N; x += 2) {
         float2 v = make_float2(g.v[x], g.v[x + 1]);
-        if constexpr (DT == kBF16) {
-          v = fma2(v, log2e, minus_B);
-          v.x = ex2(v.x);
-          v.y = ex2(v.y);
-        }
+        if constexpr (DT == kBF16) v = exp2_pair(v.x, v.y, minus_B);
         v = mul2(v, f2);
         g.v[x] = v.x;
         g.v[x + 1] = v.y;
@@ -474,7 +606,7 @@ struct PairParams {
   float beta, ls, scale;
   float* margins;
   float* pair_loss;  // pairs
-  float* side;       // 2 * pairs: d(loss)/d(R_k)
+  float* factors;    // rows: d(loss)/d(lp), 0 on entry
   float* loss;
 };
 
@@ -483,11 +615,11 @@ __device__ __forceinline__ unsigned long long offset_at(const PairParams& p, uns
   return v < 0 ? 0ull : min((unsigned long long)v, p.rows);
 }
 
-// One block per pair: the two sequences' sums, the pair's loss and the two
-// factors of the gradient.
+// One block per pair: the two sequences' sums, the pair's loss and its rows'
+// factors.
 __global__ void __launch_bounds__(kThreads) pair_kernel(const PairParams p) {
   pdl_enter();
-  __shared__ float sh[2][kThreads / 32];
+  __shared__ float sh[2][kThreads / 32], side;
   for (unsigned long long i = blockIdx.x; i < p.pairs; i += gridDim.x) {
     float R[2];
     for (int k = 0; k < 2; ++k) {
@@ -510,29 +642,31 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const PairParams p) {
       const float small = e / (1.0f + e), big = 1.0f / (1.0f + e);
       const float neg = z >= 0.0f ? small : big, pos = z >= 0.0f ? big : small;
       const float dz = z != z ? z : p.ls * pos - (1.0f - p.ls) * neg;
-      p.side[2 * i] = p.scale * p.beta * dz;
-      p.side[2 * i + 1] = -p.scale * p.beta * dz;
+      side = p.scale * p.beta * dz;
+    }
+    __syncthreads();
+    for (int k = 0; k < 2; ++k) {
+      const unsigned long long b = offset_at(p, 2 * i + k), e = offset_at(p, 2 * i + k + 1);
+      const float f = k == 0 ? side : -side;
+      for (unsigned long long t = b + threadIdx.x; t < e; t += kThreads) {
+        const float w = p.weights ? p.weights[t] : 1.0f;
+        if (w != 0.0f) p.factors[t] = w * f;
+      }
     }
     __syncthreads();
   }
 }
 
-// The sequence of row t (offsets are non-decreasing): the last k with
-// offsets[k] <= t, or -1 when t lies in none.
-__device__ __forceinline__ long long sequence_of(const PairParams& p, unsigned long long t) {
-  unsigned long long lo = 0, hi = 2 * p.pairs + 1;  // offsets[lo] <= t < offsets[hi]
-  if (hi == 1 || offset_at(p, 0) > t) return -1;
-  while (hi - lo > 1) {
-    const unsigned long long mid = (lo + hi) / 2;
-    if (offset_at(p, mid) <= t) lo = mid;
-    else hi = mid;
-  }
-  return lo < 2 * p.pairs ? (long long)lo : -1;
-}
+// The gradient of one piece of a row: kGradSlots slots per thread, all loaded
+// before the first is used.  The rows go from the last to the first: what the
+// statistics' pass has read last is still in L2.
+constexpr int kGradSlots = 4, kPiece = kThreads * kGradSlots;
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads) preference_grad_kernel(const Matrix<DT> a, const PairParams p,
-                                                                   const float2* stats) {
+                                                                   const float2* stats, unsigned pieces) {
+  constexpr int N = Lanes<DT>::N;
+  using E = typename ElemOf<DT>::T;
   pdl_enter();
   __shared__ float sh[kThreads / 32];
   if (blockIdx.x == 0) {
@@ -541,19 +675,55 @@ __global__ void __launch_bounds__(kThreads) preference_grad_kernel(const Matrix<
     v = block_sum<kThreads>(v, sh);
     if (threadIdx.x == 0) *p.loss = p.scale * v;
   }
-  for (unsigned long long t = blockIdx.x; t < a.rows; t += gridDim.x) {
-    const float w = a.weights ? a.weights[t] : 1.0f;
-    typename ElemOf<DT>::T* grad = a.grad + t * a.grad_stride;
-    const long long k = w == 0.0f ? -1 : sequence_of(p, t);
-    if (k < 0) {
-      row_zero<DT>(grad, (long long)a.vocab);
-      continue;
+  const unsigned long long back = blockIdx.x / pieces;
+  if (back >= a.rows) return;
+  const unsigned long long t = a.rows - 1 - back;
+  const long long V = (long long)a.vocab, s0 = (long long)(blockIdx.x % pieces) * kPiece + threadIdx.x;
+  E* grad = a.grad + t * a.grad_stride;
+  const float c = p.factors[t];
+  const E* row = a.logits + t * a.stride;
+  if (c == 0.0f) {  // masked, of no sequence, or of a pair whose loss is flat
+    const Slots<DT> out(grad, V);
+    const float zero[N] = {};
+#pragma unroll
+    for (int k = 0; k < kGradSlots; ++k)
+      if (s0 + k * kThreads < out.count()) store_slot<DT>(out, grad, true, s0 + k * kThreads, zero);
+    return;
+  }
+  const Slots<DT> in(row, V);
+  const long long n = in.count();
+  const bool same = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
+  uint4 r[kGradSlots];
+#pragma unroll
+  for (int k = 0; k < kGradSlots; ++k)
+    if (in.whole(s0 + k * kThreads)) r[k] = ld_row(reinterpret_cast<const uint4*>(row + in.first(s0 + k * kThreads)));
+  const float2 st = stats[t];
+  const long long y = load_index(a.targets, a.target_bytes, t);
+  const bool natural = st.y < 0.0f;
+  const float f = -c / fabsf(st.y);
+  const float2 minus_b = make_float2(-st.x, -st.x), f2 = make_float2(f, f);
+#pragma unroll
+  for (int k = 0; k < kGradSlots; ++k) {
+    const long long s = s0 + k * kThreads;
+    if (s >= n) break;
+    const long long j = in.first(s);
+    if (in.whole(s) && same && !natural) {
+      Acc<DT> g = widen<DT>(r[k]);
+#pragma unroll
+      for (int x = 0; x < N; x += 2) {
+        const float2 v = mul2(exp2_pair(g.v[x], g.v[x + 1], minus_b), f2);
+        g.v[x] = v.x;
+        g.v[x + 1] = v.y;
+      }
+      st_stream(reinterpret_cast<uint4*>(grad + j), narrow<DT>(g, 1.0f, false));
+    } else {
+      float x[N];
+      in.load(s, x, -INFINITY);
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = f * (natural ? exp_diff(x[i], st.x) : ex2(fmaf(x[i], kLog2e, -st.x)));
+      store_slot<DT>(in, grad, same, s, x);
     }
-    MaxSum st;
-    st.m = stats[t].x;
-    st.s = stats[t].y;
-    row_grad<DT>(a.logits + t * a.stride, grad, (long long)a.vocab, load_index(a.targets, a.target_bytes, t),
-                 a.logprobs[t], st, w * p.side[k], threadIdx.x, LLONG_MAX, kThreads);
+    if (y >= j && y < j + N) from_float(grad + y, -c * expm1f(a.logprobs[t]));  // over its own store
   }
 }
 
@@ -561,10 +731,47 @@ inline unsigned grid_of(unsigned long long work) {
   return (unsigned)std::max(1ull, std::min<unsigned long long>(work, kMaxLossBlocks));
 }
 
+// Slots of a matrix's row at its worst alignment.
 template <int DT>
-cudaError_t run_logprobs(const LogitsCall& c) {
-  return launch_kernel(logprob_kernel<DT>, grid_of(c.rows), kThreads, 0, c.stream, true,
-                       Matrix<DT>(c), (float2*)nullptr);
+unsigned long long row_slots(const LogitsCall& c, const void* matrix, size_t stride) {
+  constexpr int N = Lanes<DT>::N;
+  const size_t es = sizeof(typename ElemOf<DT>::T);
+  const bool alike = c.rows == 1 || stride * es % 16 == 0;  // every row starts at the same alignment
+  const unsigned long long lead = alike ? ((uintptr_t)matrix & 15) / es : N - 1;
+  return (c.vocab + lead + N - 1) / N;
+}
+
+// cudaLaunchKernelEx with programmatic dependent launch, in clusters of C blocks
+template <class... K, class... A>
+cudaError_t launch_clusters(void (*kernel)(K...), unsigned grid, unsigned threads, int smem, int C, cudaStream_t stream,
+                            A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = threads;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+template <int DT>
+cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
+  const unsigned long long n = row_slots<DT>(c, c.logits, c.row_stride);
+  if (n <= kShortRow)
+    return launch_kernel(logprob_kernel<DT, 32>, (unsigned)((c.rows + 7) / 8), kThreads, 0, c.stream, true,
+                         Matrix<DT>(c), LogprobPlan{1, (int)n}, stats, factors);
+  // a row over several blocks until there are two blocks for every SM, each with 1024 slots at least
+  int C = 1;
+  while (C < 8 && c.rows * C < 2ull * c.sms && n >= 2048ull * C) C *= 2;
+  return launch_clusters(logprob_kernel<DT, kThreads>, (unsigned)c.rows * C, kThreads, 0, C, c.stream, Matrix<DT>(c),
+                         LogprobPlan{C, (int)((n + C - 1) / C)}, stats, factors);
 }
 
 // Rows per cluster: about four waves of clusters, so that the blocks of an SM
@@ -592,20 +799,7 @@ cudaError_t launch_policy_row(const LogitsCall& c, const PolicyParams& p, unsign
   if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = *sums * C;
-  cfg.blockDim = THREADS;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = c.stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, Matrix<DT>(c), p, plan, partial);
+  return launch_clusters(kernel, *sums * C, THREADS, smem, C, c.stream, Matrix<DT>(c), p, plan, partial);
 }
 
 // The shape by the row's length in 16-byte slots.  Registers hold the row: a
@@ -618,11 +812,7 @@ cudaError_t launch_policy_row(const LogitsCall& c, const PolicyParams& p, unsign
 // on an SM (8192 x 4096 bf16: 64 threads 35 us, 128 threads 40, 256 threads 52).
 template <int DT>
 cudaError_t run_policy(const LogitsCall& c, const PolicyParams& p, float* stats, float4* partial) {
-  constexpr int N = Lanes<DT>::N;
-  const size_t es = sizeof(typename ElemOf<DT>::T);
-  const bool alike = c.rows == 1 || c.row_stride * es % 16 == 0;  // every row starts at the same alignment
-  const unsigned long long lead = alike ? ((uintptr_t)c.logits & 15) / es : N - 1;
-  const unsigned long long n = c.vocab / N + (c.vocab % N + lead + N - 1) / N;
+  const unsigned long long n = row_slots<DT>(c, c.logits, c.row_stride);
   unsigned sums = 0;
   cudaError_t e;
 #define AR_ROW(THREADS, K, BLOCKS) launch_policy_row<DT, THREADS, K, BLOCKS>(c, p, n, C, partial, &sums)
@@ -651,21 +841,22 @@ cudaError_t run_policy(const LogitsCall& c, const PolicyParams& p, float* stats,
 template <int DT>
 cudaError_t run_preference(const LogitsCall& c, const PairParams& p, float2* stats) {
   cudaError_t e = cudaSuccess;
-  if (c.rows)
-    e = launch_kernel(logprob_kernel<DT>, grid_of(c.rows), kThreads, 0, c.stream, true, Matrix<DT>(c),
-                      stats);
-  if (e == cudaSuccess && p.pairs)
-    e = launch_kernel(pair_kernel, grid_of(p.pairs), kThreads, 0, c.stream, true, p);
+  if (c.rows) e = run_logprobs<DT>(c, stats, p.factors);
+  if (e == cudaSuccess && p.pairs) e = launch_kernel(pair_kernel, grid_of(p.pairs), kThreads, 0, c.stream, true, p);
+  const unsigned long long slots = std::max(row_slots<DT>(c, c.logits, c.row_stride),
+                                            row_slots<DT>(c, c.grad, c.grad_stride));
+  const unsigned long long pieces = std::max(1ull, (slots + kPiece - 1) / kPiece);
+  if (e == cudaSuccess && c.rows * pieces > 0x7fffffffull) e = cudaErrorInvalidValue;
   if (e == cudaSuccess)
-    e = launch_kernel(preference_grad_kernel<DT>, grid_of(c.rows), kThreads, 0, c.stream, true,
-                      Matrix<DT>(c), p, (const float2*)stats);
+    e = launch_kernel(preference_grad_kernel<DT>, (unsigned)std::max(1ull, c.rows * pieces), kThreads, 0, c.stream,
+                      true, Matrix<DT>(c), p, (const float2*)stats, (unsigned)pieces);
   return e;
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogitsCall& c) {
-  return c.dtype == kF32 ? run_logprobs<kF32>(c) : run_logprobs<kBF16>(c);
+  return c.dtype == kF32 ? run_logprobs<kF32>(c, nullptr, nullptr) : run_logprobs<kBF16>(c, nullptr, nullptr);
 }
 
 cudaError_t launch_policy(const LogitsCall& c, const PolicyCall& q) {
@@ -679,14 +870,16 @@ size_t policy_workspace(size_t rows) {
   return std::max<size_t>(1, std::max(std::min(rows, kMaxPolicySums), (rows + 31) / 32)) * sizeof(float4);
 }
 
-// workspace: {m, s} per row, then the pairs' losses and the sequences' factors
-size_t preference_workspace(size_t rows, size_t pairs) { return rows * sizeof(float2) + 3 * pairs * sizeof(float); }
+// workspace: the rows' statistics and factors, then the pairs' losses
+size_t preference_workspace(size_t rows, size_t pairs) {
+  return rows * (sizeof(float2) + sizeof(float)) + pairs * sizeof(float);
+}
 
 cudaError_t launch_preference(const LogitsCall& c, const PreferenceCall& q) {
   float2* stats = static_cast<float2*>(q.workspace);
-  float* pair_loss = reinterpret_cast<float*>(stats + c.rows);
-  const PairParams p{q.offsets, q.offset_bytes, q.pairs, c.rows, c.weights, c.logprobs, q.ref_logprobs,
-                     q.beta, q.label_smoothing, q.scale, q.margins, pair_loss, pair_loss + q.pairs, q.loss};
+  float* factors = reinterpret_cast<float*>(stats + c.rows);
+  const PairParams p{q.offsets, q.offset_bytes, q.pairs, c.rows, c.weights, c.logprobs, q.ref_logprobs, q.beta,
+                     q.label_smoothing, q.scale, q.margins, factors + c.rows, factors, q.loss};
   return c.dtype == kF32 ? run_preference<kF32>(c, p, stats) : run_preference<kBF16>(c, p, stats);
 }
 

@@ -71,6 +71,7 @@ ar_status_t check_logits(const ar::LogitsCall& c, bool grad) {
   if (c.dtype != AR_FLOAT32 && c.dtype != AR_BFLOAT16) return AR_ERR_INVALID_ARG;
   if (!index_bytes(c.target_bytes)) return AR_ERR_INVALID_ARG;
   if (c.rows == 0) return AR_SUCCESS;
+  if (c.rows > AR_MAX_TOKENS || c.vocab > AR_MAX_VOCAB) return AR_ERR_UNSUPPORTED;
   const size_t es = ar::elem_bytes(c.dtype);
   if (c.vocab == 0 || c.row_stride < c.vocab || !aligned(c.logits, es)) return AR_ERR_INVALID_ARG;
   if (!aligned(c.targets, (size_t)c.target_bytes) || !aligned(c.logprobs, 4) || !aligned_or_null(c.weights, 4))

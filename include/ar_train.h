@@ -42,12 +42,17 @@
 extern "C" {
 #endif
 
+/* Largest matrix of logits: rows and columns. */
+#define AR_MAX_TOKENS ((size_t)1 << 28)
+#define AR_MAX_VOCAB ((size_t)1 << 30)
+
 /*
  * logprobs[t] = x[t, y_t] - log sum_j exp(x[t, j]), fp32, for each row.
  *   logprobs  device array of `rows` floats
  * rows == 0 is a no-op.  Errors: AR_ERR_INVALID_ARG (NULL or misaligned
  * pointer, vocab == 0, row_stride < vocab, enum), AR_ERR_UNSUPPORTED
- * (AR_INT32), AR_ERR_CUDA (launch failed).
+ * (AR_INT32, or more than AR_MAX_TOKENS rows or AR_MAX_VOCAB columns),
+ * AR_ERR_CUDA (launch failed).
  */
 ar_status_t ar_token_logprobs(const void* logits, size_t rows, size_t vocab, size_t row_stride,
                               ar_dtype_t dtype, const void* targets, int target_bytes,

@@ -24,10 +24,11 @@ def test_token_logprobs_arguments(lib):
         return lib.ar_token_logprobs(logits, rows, vocab, stride, dtype, targets, size, weights, out, None)
 
     assert call(rows=0) == ar.AR_SUCCESS
-    assert call(dtype=ar.AR_INT32) == NO
+    for kw in (dict(dtype=ar.AR_INT32), dict(rows=(1 << 28) + 1), dict(vocab=(1 << 30) + 1, stride=1 << 31)):
+        assert call(**kw) == NO, kw
     for kw in (dict(dtype=7), dict(logits=None), dict(logits=P + 2), dict(vocab=0), dict(stride=7), dict(targets=None),
                dict(targets=P + 4), dict(size=2), dict(out=None), dict(out=P + 1), dict(weights=P + 3),
-               dict(rows=1 << 61, stride=1 << 20), dict(dtype=ar.AR_BFLOAT16, logits=P + 1)):
+               dict(rows=1 << 28, stride=1 << 40), dict(dtype=ar.AR_BFLOAT16, logits=P + 1)):
         assert call(**kw) == BAD, kw
 
 
