@@ -70,18 +70,20 @@ class GradClipper:
         self._outs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.out])
         self._counts = (ctypes.c_size_t * n)(*[t.numel() for t in self.grads])
         self._dtypes = (ctypes.c_int * n)(*[_DTYPES[t.dtype] for t in self.grads])
+        self._index = self.device.index
         self._lib = library()
         self._bytes = self._lib.ar_grad_norm_workspace()
         with torch.cuda.device(self.device):
             self._home = torch.cuda.current_stream().cuda_stream
             self._workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
+        self._at = self._workspace.data_ptr()
 
     def _begin(self, what: str, stream):
         """(stream handle, a new 0-dim norm): both belong to the call's stream."""
-        if torch.cuda.current_device() != self.device.index:
+        if torch.cuda.current_device() != self._index:
             raise ArError(AR_ERR_INVALID_ARG, f"{what}: gradients are on {self.device}, the current device is "
                                               f"cuda:{torch.cuda.current_device()}")
-        handle = _stream_handle(stream)
+        handle = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else _stream_handle(stream)
         if handle != self._home or stream is not None:
             s = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
             self._workspace.record_stream(s)
@@ -93,7 +95,7 @@ class GradClipper:
         """The global norm, a 0-dim float32 tensor."""
         handle, norm = self._begin("GradClipper.norm", stream)
         st = self._lib.ar_grad_norm(self._n, self._grads, self._counts, self._dtypes, norm.data_ptr(),
-                                    self._workspace.data_ptr(), self._bytes, handle)
+                                    self._at, self._bytes, handle)
         if st != AR_SUCCESS:
             raise ArError(st, "GradClipper.norm")
         return norm
@@ -103,7 +105,7 @@ class GradClipper:
         returns the norm before clipping, a 0-dim float32 tensor."""
         handle, norm = self._begin("GradClipper.clip", stream)
         st = self._lib.ar_clip_grads(self._n, self._grads, self._outs, self._counts, self._dtypes, max_norm, eps,
-                                     norm.data_ptr(), self._workspace.data_ptr(), self._bytes, handle)
+                                     norm.data_ptr(), self._at, self._bytes, handle)
         if st != AR_SUCCESS:
             raise ArError(st, "GradClipper.clip")
         return norm

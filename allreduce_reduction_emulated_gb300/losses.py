@@ -17,7 +17,8 @@ logits        (tokens, vocab) float32 or bfloat16 CUDA tensor on the current
 targets       (tokens,) int64 or int32
 per-token     (tokens,) contiguous float32: weights, old_logprobs, ...
 grad          where the gradient goes: a tensor of the logits' shape and type, or
-              the logits themselves (in place); None allocates one
+              the logits themselves (in place); None allocates one with the logits'
+              row stride
 stream        a torch stream or a cudaStream_t (default: the current stream)
 
 Nothing waits for the GPU and nothing is kept between calls.
@@ -32,6 +33,7 @@ from . import AR_BFLOAT16, AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED, AR_FLOAT32, A
 
 _DTYPES = {torch.float32: AR_FLOAT32, torch.bfloat16: AR_BFLOAT16}
 _INDEX_BYTES = {torch.int64: 8, torch.int32: 4}
+_HERE = contextlib.nullcontext()
 
 
 def _bad(what: str, why: str, status: int = AR_ERR_INVALID_ARG) -> ArError:
@@ -86,25 +88,40 @@ def _indices(what: str, name: str, x, device: int, count: int):
 
 
 def _gradient(what: str, logits, grad, device: int, rows: int, vocab: int):
+    """(tensor for the gradient, its row stride); None makes one whose rows are
+    laid out like the logits', so that both start at the same alignments."""
     if grad is None:
-        return torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device), vocab
+        return torch.empty_like(logits) if logits.is_contiguous() else _like_rows(logits, rows, vocab)
     if grad is not logits:
         at, r, v, stride = _matrix(what, "grad", grad)
         if (at, r, v) != (device, rows, vocab) or grad.dtype != logits.dtype:
             raise _bad(what, f"grad: {tuple(grad.shape)} {grad.dtype}, the logits are {(rows, vocab)} {logits.dtype}")
-        return grad, stride
-    return grad, logits.stride(0) if rows > 1 else vocab
+    return grad
 
 
-def _on(stream):
+def _like_rows(logits, rows: int, vocab: int):
+    """A new matrix with the logits' row stride (a padded one cut to `vocab`
+    columns), starting at the same alignment within 16 bytes."""
+    stride = logits.stride(0) if rows > 1 else vocab
+    lead = logits.data_ptr() % 16 // logits.element_size()
+    flat = torch.empty(lead + rows * stride, dtype=logits.dtype, device=logits.device)
+    return flat.as_strided((rows, vocab), (stride, 1), lead)
+
+
+def _on(device: int, stream):
     """(the context in which outputs are allocated, the stream's handle).  What
     is allocated for a stream has to come from that stream's memory pool."""
     if stream is None:
-        return contextlib.nullcontext(), torch.cuda.current_stream().cuda_stream
+        return _HERE, torch._C._cuda_getCurrentRawStream(device)
     if isinstance(stream, int):
         s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
         return torch.cuda.stream(s), stream
     return torch.cuda.stream(stream), stream.cuda_stream
+
+
+def _whole(n: int) -> int:
+    """n floats rounded up to whole 16 bytes."""
+    return (n + 3) & ~3
 
 
 def _check(status: int, what: str) -> None:
@@ -119,7 +136,7 @@ def token_logprobs(logits, targets, weights=None, out=None, stream=None):
     device, rows, vocab, stride = _matrix(what, "logits", logits)
     y, size = _indices(what, "targets", targets, device, rows)
     w = None if weights is None else _vector(what, "weights", weights, device, rows)
-    context, handle = _on(stream)
+    context, handle = _on(device, stream)
     if out is None:
         with context:
             out = torch.empty(rows, dtype=torch.float32, device=logits.device)
@@ -130,18 +147,20 @@ def token_logprobs(logits, targets, weights=None, out=None, stream=None):
 
 
 class PolicyLoss:
-    """What policy_loss computes: loss, kl, clipped and weight are 0-dim views of
-    one tensor of statistics, each scaled like the loss; grad and logprobs."""
+    """What policy_loss computes.  grad is a tensor of its own; loss, kl, clipped and
+    weight (0-dim) and logprobs are views of one buffer."""
 
-    __slots__ = ("stats", "grad", "logprobs")
+    __slots__ = ("grad", "_buffer", "_rows")
 
-    def __init__(self, stats, grad, logprobs):
-        self.stats, self.grad, self.logprobs = stats, grad, logprobs
+    def __init__(self, grad, buffer, rows):
+        self.grad, self._buffer, self._rows = grad, buffer, rows
 
-    loss = property(lambda self: self.stats[0], doc="scale * sum of w * term")
-    kl = property(lambda self: self.stats[1], doc="scale * sum of w * (e^d - 1 - d), d = ref - logp")
-    clipped = property(lambda self: self.stats[2], doc="scale * sum of w over the clipped tokens")
-    weight = property(lambda self: self.stats[3], doc="scale * sum of w")
+    loss = property(lambda self: self._buffer[0], doc="scale * sum of w * term")
+    kl = property(lambda self: self._buffer[1], doc="scale * sum of w * (e^d - 1 - d), d = ref - logp")
+    clipped = property(lambda self: self._buffer[2], doc="scale * sum of w over the clipped tokens")
+    weight = property(lambda self: self._buffer[3], doc="scale * sum of w")
+    stats = property(lambda self: self._buffer[:4], doc="loss, kl, clipped, weight")
+    logprobs = property(lambda self: self._buffer[4:4 + self._rows], doc="(tokens,) float32, 0 for masked rows")
 
 
 def policy_loss(logits, targets, old_logprobs, advantages, ref_logprobs=None, weights=None, clip_low: float = 0.2,
@@ -165,25 +184,35 @@ def policy_loss(logits, targets, old_logprobs, advantages, ref_logprobs=None, we
         scale = 1.0 / max(1, rows) if weights is None else 1.0
     lib = library()
     bytes_ = lib.ar_policy_loss_workspace(rows)
-    context, handle = _on(stream)
+    after = 4 + _whole(rows)                       # floats before the workspace: the statistics, logprobs
+    context, handle = _on(device, stream)
     with context:
-        grad, grad_stride = _gradient(what, logits, grad, device, rows, vocab)
-        stats = torch.empty(4, dtype=torch.float32, device=logits.device)
-        logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
-        workspace = torch.empty(bytes_, dtype=torch.uint8, device=logits.device)
+        grad = _gradient(what, logits, grad, device, rows, vocab)
+        buffer = torch.empty(after + bytes_ // 4, dtype=torch.float32, device=logits.device)
+    at = buffer.data_ptr()
     _check(lib.ar_policy_loss(logits.data_ptr(), rows, vocab, stride, _DTYPES[logits.dtype], y, size, w, old, adv, ref,
-                              clip_low, clip_high, kl_coef, scale, grad.data_ptr(), grad_stride, logprobs.data_ptr(),
-                              stats.data_ptr(), workspace.data_ptr(), bytes_, handle), what)
-    return PolicyLoss(stats, grad, logprobs)
+                              clip_low, clip_high, kl_coef, scale, grad.data_ptr(),
+                              grad.stride(0) if rows > 1 else vocab, at + 16, at, at + 4 * after, bytes_, handle), what)
+    return PolicyLoss(grad, buffer, rows)
 
 
 class PreferenceLoss:
-    """What preference_loss computes: loss (0-dim), margins (pairs,), grad, logprobs."""
+    """What preference_loss computes.  grad is a tensor of its own; loss (0-dim),
+    margins and logprobs are views of one buffer."""
 
-    __slots__ = ("loss", "margins", "grad", "logprobs")
+    __slots__ = ("grad", "_buffer", "_pairs", "_rows")
 
-    def __init__(self, loss, margins, grad, logprobs):
-        self.loss, self.margins, self.grad, self.logprobs = loss, margins, grad, logprobs
+    def __init__(self, grad, buffer, pairs, rows):
+        self.grad, self._buffer, self._pairs, self._rows = grad, buffer, pairs, rows
+
+    loss = property(lambda self: self._buffer[0])
+    margins = property(lambda self: self._buffer[4:4 + self._pairs], doc="(pairs,) float32")
+
+    @property
+    def logprobs(self):
+        """(tokens,) float32, 0 for masked rows"""
+        at = 4 + _whole(self._pairs)
+        return self._buffer[at:at + self._rows]
 
 
 def preference_loss(logits, targets, offsets, ref_logprobs=None, weights=None, beta: float = 0.1,
@@ -211,15 +240,15 @@ def preference_loss(logits, targets, offsets, ref_logprobs=None, weights=None, b
         scale = 1.0 / max(1, pairs)
     lib = library()
     bytes_ = lib.ar_preference_loss_workspace(rows, pairs)
-    context, handle = _on(stream)
+    first = 4 + _whole(pairs)                      # floats before logprobs: the loss, the margins
+    after = first + _whole(rows)
+    context, handle = _on(device, stream)
     with context:
-        grad, grad_stride = _gradient(what, logits, grad, device, rows, vocab)
-        loss = torch.empty((), dtype=torch.float32, device=logits.device)
-        margins = torch.empty(pairs, dtype=torch.float32, device=logits.device)
-        logprobs = torch.empty(rows, dtype=torch.float32, device=logits.device)
-        workspace = torch.empty(bytes_, dtype=torch.uint8, device=logits.device)
+        grad = _gradient(what, logits, grad, device, rows, vocab)
+        buffer = torch.empty(after + bytes_ // 4, dtype=torch.float32, device=logits.device)
+    at = buffer.data_ptr()
     _check(lib.ar_preference_loss(logits.data_ptr(), rows, vocab, stride, _DTYPES[logits.dtype], y, size, w, off,
-                                  off_size, pairs, ref, beta, label_smoothing, scale, grad.data_ptr(), grad_stride,
-                                  logprobs.data_ptr(), loss.data_ptr(), margins.data_ptr(), workspace.data_ptr(),
+                                  off_size, pairs, ref, beta, label_smoothing, scale, grad.data_ptr(),
+                                  grad.stride(0) if rows > 1 else vocab, at + 4 * first, at, at + 16, at + 4 * after,
                                   bytes_, handle), what)
-    return PreferenceLoss(loss, margins, grad, logprobs)
+    return PreferenceLoss(grad, buffer, pairs, rows)
