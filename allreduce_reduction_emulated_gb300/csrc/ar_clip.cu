@@ -2,14 +2,16 @@
 // (ar_train.h).
 //
 // norm = sqrt(sum g^2), out = g * min(1, max_norm / (norm + eps)).
-// The tensors are cut into chunks of kChunkSlots 16-byte slots, numbered over
-// all tensors, so that the blocks get equal work whatever the tensors' sizes:
-// block b takes chunks b, b + grid, ...  Each block leaves one partial sum of
-// squares; the clipping kernel's blocks each add all partials, in the same
-// order and in fp64, and scale their chunks.  No atomics: the bits of the
-// norm depend on the sizes and the device alone.
-// The clipping kernel takes the chunks from the last to the first, so that it
-// starts with the data that the norm kernel has left in L2.
+// The tensors are cut into chunks of 32 KiB, numbered over all tensors, and every
+// block takes the same number of runs of consecutive chunks, whatever the tensors'
+// sizes.  Each block leaves one partial sum of squares; the clipping kernel's blocks
+// each add all partials, in the same order, and scale their chunks.  No
+// atomics: the bits of the norm depend on the sizes and the device alone.
+//
+// Bound by HBM: the coefficient needs every element, so a gradient that does not
+// stay in L2 (129 MB) is read twice and written once.  The clipping kernel takes
+// the chunks from the last to the first, so that it starts with what the norm
+// kernel has left in L2.
 #include <algorithm>
 
 #include "ar_logits.cuh"
@@ -21,11 +23,38 @@ namespace ar {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSlotsPerThread = 8;
-constexpr int kChunkSlots = kThreads * kSlotsPerThread;  // 32 KiB
-constexpr int kBlocksPerSm = 8;
+constexpr int kSlots = 8;                            // 16-byte slots per thread in a chunk, all loaded before any is used
+// Blocks per SM: with eight 16-byte loads on the way per thread, four are resident.
+constexpr int kBlocksPerSm = 4;
+constexpr int kMaxBlocks = 640;                      // of one launch
 constexpr int kMaxPartials = 8192;
-constexpr int kSmallTable = 64, kLargeTable = 1000;      // tensors per launch (kernel parameters: 32 bytes each)
+constexpr int kSmallTable = 64, kLargeTable = 768;   // tensors per launch
+// Chunks in a run: a block that walks through consecutive chunks looks its tensor
+// up once, but 608 blocks in 608 far places of 5 GB are slower than all blocks in
+// one moving window (2608 against 2365 us).
+constexpr unsigned int kRun = 16;
+
+// What L2 does with a load's lines.  Up to kHintChunks (512 MB) the norm kernel asks
+// L2 to keep the last kKeptChunks (40 MB; the two halves of L2 may each hold a copy)
+// and to drop the rest first, and the clipping kernel, which begins with the kept
+// ones, drops them as it goes: 160 MB read and written 38.5 -> 34.9 us, 480 MB 118 ->
+// 112.  Above, nothing is gained and a hint of any kind costs 2% (9.7 GB: 2152 us
+// without, 2190 with), so the kernels come without them too.
+constexpr unsigned int kHintChunks = 16384, kKeptChunks = 1250;
+__device__ __forceinline__ uint64_t keep_policy(bool keep) {
+  uint64_t p;
+  if (keep) asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  else asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+template <bool HINTS>
+__device__ __forceinline__ uint4 ld_hint(const uint4* p, uint64_t policy) {
+  if constexpr (!HINTS) return ld_row(p);
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p), "l"(policy));
+  return r;
+}
 
 struct Tensor {
   const void* grad;
@@ -35,129 +64,266 @@ struct Tensor {
   int dtype;
 };
 
+// In the kernel's parameters (at most 26 KiB of the 32 they may have): nothing to
+// copy to the device first, and a captured call keeps its own.
 template <int CAP>
 struct Table {
   Tensor t[CAP];
+  unsigned short start[kMaxBlocks];  // tensor of the first chunk of each block's first run
+  unsigned int chunks, rounds;       // of this launch
+  unsigned int kept;                 // chunks at the end that L2 is to keep for the clipping kernel (0: no hints)
   int n;
-  unsigned int chunks;
 };
 
-// tensor of a chunk: the last one whose first chunk is not after it
-template <int CAP>
-__device__ __forceinline__ int tensor_of(const Table<CAP>& tab, unsigned int chunk) {
-  int lo = 0, hi = tab.n;
-  while (hi - lo > 1) {
+// The launch's chunks are cut into `rounds` equal windows, each window into one
+// run of consecutive chunks for every block.
+struct Run {
+  unsigned int begin, end;
+};
+__host__ __device__ __forceinline__ Run run_of(unsigned int chunks, unsigned int rounds, unsigned int round,
+                                               unsigned int block, unsigned int blocks) {
+  const unsigned long long a = (unsigned long long)chunks * round / rounds;
+  const unsigned long long n = (unsigned long long)chunks * (round + 1) / rounds - a;
+  return Run{(unsigned int)(a + n * block / blocks), (unsigned int)(a + n * (block + 1) / blocks)};
+}
+
+// The tensor of a chunk: the last whose first chunk is not after it.
+__device__ __forceinline__ int tensor_of(const unsigned int* first, int n, unsigned int chunk) {
+  int lo = 0;
+  for (int hi = n; hi - lo > 1;) {
     const int mid = (lo + hi) >> 1;
-    if (tab.t[mid].first_chunk <= chunk) lo = mid;
+    if (first[mid] <= chunk) lo = mid;
     else hi = mid;
   }
   return lo;
 }
 
-// f(slot, whole, x) for this thread's slots of a chunk; partial slots are
-// filled with zeros.  All loads of a full chunk are issued before the first use.
-template <int DT, class F>
-__device__ __forceinline__ void for_chunk(const Tensor& t, unsigned int chunk, F&& f) {
-  constexpr int N = Lanes<DT>::N;
-  const Slots<DT> in(static_cast<const typename ElemOf<DT>::T*>(t.grad), (long long)t.count);
-  const long long s0 = (long long)(chunk - t.first_chunk) * kChunkSlots;
-  const long long n = in.count();
-  if (in.whole(s0) && s0 + kChunkSlots <= n && in.whole(s0 + kChunkSlots - 1)) {
-    uint4 r[kSlotsPerThread];
-    const uint4* p = reinterpret_cast<const uint4*>(in.row + in.first(s0)) + threadIdx.x;
-#pragma unroll
-    for (int k = 0; k < kSlotsPerThread; ++k) r[k] = ld_row(p + k * kThreads);
-#pragma unroll
-    for (int k = 0; k < kSlotsPerThread; ++k) {
-      const Acc<DT> a = widen<DT>(r[k]);
-      f(in, s0 + threadIdx.x + k * kThreads, a.v);
-    }
-  } else {
-    const long long e = min(n, s0 + kChunkSlots);
-    for (long long s = s0 + threadIdx.x; s < e; s += kThreads) {
-      float x[N];
-      in.load(s, x, 0.0f);
-      f(in, s, x);
+// f(tensor, chunk) for this block's chunks; with BACKWARDS they are numbered, and
+// gone through, from the last.
+template <bool BACKWARDS, int CAP, class F>
+__device__ __forceinline__ void for_chunks(const Table<CAP>& tab, F&& f) {
+  __shared__ unsigned int first[CAP];
+  if (tab.rounds > 1) {  // a second run has its tensor to find
+    for (int i = threadIdx.x; i < tab.n; i += kThreads) first[i] = tab.t[i].first_chunk;
+    __syncthreads();
+  }
+  int i = tab.start[blockIdx.x];
+  for (unsigned int round = 0; round < tab.rounds; ++round) {
+    const Run r = run_of(tab.chunks, tab.rounds, round, blockIdx.x, gridDim.x);
+    if (r.begin == r.end) continue;
+    if (round) i = tensor_of(first, tab.n, BACKWARDS ? tab.chunks - 1 - r.begin : r.begin);
+    for (unsigned int k = r.begin; k < r.end; ++k) {
+      const unsigned int c = BACKWARDS ? tab.chunks - 1 - k : k;
+      if (BACKWARDS) {
+        while (tab.t[i].first_chunk > c) --i;
+      } else {
+        while (i + 1 < tab.n && tab.t[i + 1].first_chunk <= c) ++i;
+      }
+      f(tab.t[i], c);
     }
   }
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) square_sum_kernel(const __grid_constant__ Table<CAP> tab, float* partial) {
+// This thread's slots of one chunk of a tensor.  The chunks lie on 128-byte lines,
+// so a tensor may begin up to 127 bytes into its first one.  All whole slots are
+// loaded (zeros for the others) before any is used; a partial slot, where the
+// tensor begins or ends inside it, by elements.
+template <int DT>
+struct Chunk {
+  static constexpr int N = Lanes<DT>::N;
+  using E = typename ElemOf<DT>::T;
+  const E* run;               // the tensor
+  long long count, s0;        // its elements; the chunk's first slot
+  int lead;                   // elements of its first line before it
+  int lo, lim;                // slots lo .. lim - 1 of the chunk are whole
+  int ends[2];                // partial slots: the first, the last (-1: none; the same one only once)
+  uint4 r[kSlots];
+
+  template <bool HINTS>
+  __device__ __forceinline__ void load(const Tensor& t, unsigned int chunk, uint64_t policy) {
+    run = static_cast<const E*>(t.grad);
+    count = (long long)t.count;
+    s0 = (long long)(chunk - t.first_chunk) * (kSlots * kThreads);
+    lead = (int)(((uintptr_t)run & 127) / sizeof(E));
+    const long long full = (count + lead) / N - s0;
+    lo = s0 == 0 ? (lead + N - 1) / N : 0;
+    lim = (int)min((long long)(kSlots * kThreads), full);
+    ends[0] = s0 == 0 && lead % N ? lead / N : -1;
+    ends[1] = (count + lead) % N && full >= lo && full < kSlots * kThreads ? (int)full : -1;
+    const uint4* src = reinterpret_cast<const uint4*>(run - lead) + s0 + threadIdx.x;
+    if (lo == 0 && lim == kSlots * kThreads) {
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k) r[k] = ld_hint<HINTS>(src + k * kThreads, policy);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k) {
+        const int q = k * kThreads + (int)threadIdx.x;
+        r[k] = make_uint4(0, 0, 0, 0);
+        if (q >= lo && q < lim) r[k] = ld_hint<HINTS>(src + k * kThreads, policy);
+      }
+    }
+  }
+  __device__ __forceinline__ long long element(int slot) const { return (s0 + slot) * N - lead; }
+  // f(first index, values) for a partial slot of this thread; zeros outside the tensor
+  template <class F>
+  __device__ __forceinline__ void partial_slots(F&& f) const {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (ends[e] >= 0 && ends[e] % kThreads == (int)threadIdx.x) {
+        const long long j = element(ends[e]);
+        float x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = j + i >= 0 && j + i < count ? to_float(run[j + i]) : 0.0f;
+        f(j, x);
+      }
+  }
+};
+
+struct Squares {
+  float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+  template <int DT, bool HINTS>
+  __device__ __forceinline__ void add(const Tensor& t, unsigned int chunk, uint64_t policy) {
+    Chunk<DT> c;
+    c.template load<HINTS>(t, chunk, policy);
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const Acc<DT> x = widen<DT>(c.r[k]);
+#pragma unroll
+      for (int i = 0; i < Lanes<DT>::N; i += 2) {
+        const float2 v = make_float2(x.v[i], x.v[i + 1]);
+        acc[i >> 1 & 1] = fma2(v, v, acc[i >> 1 & 1]);
+      }
+    }
+    c.partial_slots([&](long long, const auto& x) {
+#pragma unroll
+      for (int i = 0; i < Lanes<DT>::N; ++i) acc[0].x = fmaf(x[i], x[i], acc[0].x);
+    });
+  }
+};
+
+template <int CAP, bool HINTS>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+square_sum_kernel(const __grid_constant__ Table<CAP> tab, float* partial) {
   pdl_enter();
   __shared__ float sh[kThreads / 32];
-  float acc[4] = {};
-  for (unsigned int c = blockIdx.x; c < tab.chunks; c += gridDim.x) {
-    const Tensor& t = tab.t[tensor_of(tab, c)];
-    const auto add = [&](const auto&, long long, const auto& x) {
-      constexpr int N = sizeof(x) / sizeof(float);
-#pragma unroll
-      for (int i = 0; i < N; ++i) acc[i & 3] = fmaf(x[i], x[i], acc[i & 3]);
-    };
-    if (t.dtype == kF32) for_chunk<kF32>(t, c, add);
-    else for_chunk<kBF16>(t, c, add);
-  }
-  const float v = block_sum<kThreads>((acc[0] + acc[1]) + (acc[2] + acc[3]), sh);
+  Squares sum;
+  const uint64_t keep = keep_policy(true), rest = keep_policy(false);
+  for_chunks<false>(tab, [&](const Tensor& t, unsigned int c) {
+    const uint64_t policy = tab.chunks - c <= tab.kept ? keep : rest;
+    if (t.dtype == kF32) sum.add<kF32, HINTS>(t, c, policy);
+    else sum.add<kBF16, HINTS>(t, c, policy);
+  });
+  const float v = block_sum<kThreads>((sum.acc[0].x + sum.acc[0].y) + (sum.acc[1].x + sum.acc[1].y), sh);
   if (threadIdx.x == 0) partial[blockIdx.x] = v;
 }
 
-// The norm from the partial sums, the same in every block.
-__device__ __forceinline__ float norm_of(const float* partial, int nparts, double* sh) {
-  double v = 0.0;
-  for (int i = threadIdx.x; i < nparts; i += kThreads) v += (double)partial[i];
-  return (float)sqrt(block_sum<kThreads>(v, sh));
+// The norm from the partial sums, the same in every block.  In fp32: at most 32
+// sums per thread, then a tree (fp64 additions and the fp64 root took 3 us of
+// every block's start).
+__device__ __forceinline__ float norm_of(const float* partial, int nparts, float* sh) {
+  float v = 0.0f;
+  for (int i = threadIdx.x; i < nparts; i += kThreads) v += partial[i];
+  return sqrtf(block_sum<kThreads>(v, sh));
 }
 
 __global__ void __launch_bounds__(kThreads) norm_kernel(const float* partial, int nparts, float* norm) {
   pdl_enter();
-  __shared__ double sh[kThreads / 32];
+  __shared__ float sh[kThreads / 32];
   const float v = norm_of(partial, nparts, sh);
   if (threadIdx.x == 0) *norm = v;
 }
 
-template <int CAP>
-__global__ void __launch_bounds__(kThreads) scale_kernel(const __grid_constant__ Table<CAP> tab, const float* partial,
-                                                         int nparts, float max_norm, float eps, float* norm) {
+template <int DT, bool HINTS>
+__device__ __forceinline__ void scale_chunk(const Tensor& t, unsigned int chunk, float coef, uint64_t policy) {
+  constexpr int N = Lanes<DT>::N;
+  using E = typename ElemOf<DT>::T;
+  Chunk<DT> c;
+  c.template load<HINTS>(t, chunk, policy);
+  E* const out = static_cast<E*>(t.out);
+  const bool same = (((uintptr_t)t.grad ^ (uintptr_t)t.out) & 15) == 0;
+  const float2 f = make_float2(coef, coef);
+#pragma unroll
+  for (int k = 0; k < kSlots; ++k) {
+    const int q = k * kThreads + (int)threadIdx.x;
+    if (q >= c.lo && q < c.lim) {
+      Acc<DT> y = widen<DT>(c.r[k]);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 v = mul2(make_float2(y.v[i], y.v[i + 1]), f);
+        y.v[i] = v.x;
+        y.v[i + 1] = v.y;
+      }
+      E* to = out + c.element(q);
+      if (same) {
+        st_stream(reinterpret_cast<uint4*>(to), narrow<DT>(y, 1.0f, false));
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) from_float(to + i, y.v[i]);
+      }
+    }
+  }
+  c.partial_slots([&](long long j, const auto& x) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (j + i >= 0 && j + i < c.count) from_float(out + j + i, x[i] * coef);
+  });
+}
+
+template <int CAP, bool HINTS>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+scale_kernel(const __grid_constant__ Table<CAP> tab, const float* partial, int nparts, float max_norm, float eps,
+             float* norm) {
   pdl_enter();
-  __shared__ double sh[kThreads / 32];
+  __shared__ float sh[kThreads / 32];
   const float v = norm_of(partial, nparts, sh);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
   const float q = max_norm / (v + eps);
   const float coef = q > 1.0f ? 1.0f : q;  // NaN stays NaN
-  for (unsigned int b = blockIdx.x; b < tab.chunks; b += gridDim.x) {
-    const unsigned int c = tab.chunks - 1 - b;
-    const Tensor& t = tab.t[tensor_of(tab, c)];
-    if (coef == 1.0f && t.out == t.grad) continue;
-    const bool same = (((uintptr_t)t.grad ^ (uintptr_t)t.out) & 15) == 0;
-    const auto scale = [&](const auto& in, long long s, const auto& x) {
-      constexpr int N = sizeof(x) / sizeof(float);
-      constexpr int DT = N == Lanes<kF32>::N ? kF32 : kBF16;
-      float y[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) y[i] = x[i] * coef;
-      store_slot<DT>(in, static_cast<typename ElemOf<DT>::T*>(t.out), same, s, y);
-    };
-    if (t.dtype == kF32) for_chunk<kF32>(t, c, scale);
-    else for_chunk<kBF16>(t, c, scale);
-  }
+  const uint64_t policy = keep_policy(false);
+  for_chunks<true>(tab, [&](const Tensor& t, unsigned int c) {
+    if (coef == 1.0f && t.out == t.grad) return;  // in place and nothing to scale
+    if (t.dtype == kF32) scale_chunk<kF32, HINTS>(t, c, coef, policy);
+    else scale_chunk<kBF16, HINTS>(t, c, coef, policy);
+  });
 }
 
+// Tensors from i on until the table is full; returns the first that is not in it.
 template <int CAP>
-size_t fill(const GradsCall& c, size_t i, bool outs, Table<CAP>& tab) {
+size_t fill(const GradsCall& c, size_t i, bool clip, Table<CAP>& tab) {
   unsigned long long chunks = 0;
   tab.n = 0;
   for (; i < c.ntensors && tab.n < CAP; ++i) {
     if (c.counts[i] == 0) continue;
-    const size_t es = elem_bytes(c.dtypes[i]), lead = ((uintptr_t)c.grads[i] & 15) / es;
-    const unsigned long long slots = (c.counts[i] + lead + 16 / es - 1) / (16 / es);
-    const unsigned long long n = (slots + kChunkSlots - 1) / kChunkSlots;
-    if (chunks + n > 0xffffffffull) break;
-    tab.t[tab.n++] = Tensor{c.grads[i], !outs ? nullptr : c.outs ? c.outs[i] : const_cast<void*>(c.grads[i]),
+    // chunks of 32 KiB from the 128-byte line that the tensor begins in
+    const unsigned long long bytes = ((uintptr_t)c.grads[i] & 127) + c.counts[i] * elem_bytes(c.dtypes[i]);
+    const unsigned long long n = (bytes + kSlots * kThreads * 16 - 1) / (kSlots * kThreads * 16);
+    if (chunks + n > 0x7fffffffull) break;
+    tab.t[tab.n++] = Tensor{c.grads[i], !clip ? nullptr : c.outs ? c.outs[i] : const_cast<void*>(c.grads[i]),
                             c.counts[i], (unsigned int)chunks, c.dtypes[i]};
     chunks += n;
   }
   tab.chunks = (unsigned int)chunks;
+  tab.kept = 0;
   return i;
+}
+
+// Runs of about kRun chunks; the tensors that the blocks start with.  Returns the
+// number of blocks.
+template <int CAP>
+unsigned plan_runs(Table<CAP>& tab, unsigned most, bool backwards) {
+  const unsigned blocks = std::min(most, tab.chunks);
+  tab.rounds = (unsigned)(((unsigned long long)tab.chunks + blocks * kRun - 1) / (blocks * kRun));
+  int i = backwards ? tab.n - 1 : 0;
+  for (unsigned b = 0; b < blocks; ++b) {
+    const unsigned k = run_of(tab.chunks, tab.rounds, 0, b, blocks).begin, c = backwards ? tab.chunks - 1 - k : k;
+    if (backwards) {
+      while (tab.t[i].first_chunk > c) --i;
+    } else {
+      while (i + 1 < tab.n && tab.t[i + 1].first_chunk <= c) ++i;
+    }
+    tab.start[b] = (unsigned short)i;
+  }
+  return blocks;
 }
 
 template <int CAP>
@@ -165,47 +331,46 @@ cudaError_t run(const GradsCall& c, bool clip) {
   float* partial = static_cast<float*>(c.workspace);
   const size_t launches = std::max<size_t>(1, (c.ntensors + CAP - 1) / CAP);
   if (launches > (size_t)kMaxPartials) return cudaErrorInvalidValue;
-  const unsigned most = std::max(1u, std::min<unsigned>(c.sms * kBlocksPerSm, kMaxPartials / (unsigned)launches));
+  const unsigned most = std::max(1u, std::min<unsigned>(std::min(c.sms * kBlocksPerSm, kMaxBlocks),
+                                                        kMaxPartials / (unsigned)launches));
   Table<CAP> tab;
   int nparts = 0;
-  for (size_t i = 0; i < c.ntensors;) {
-    const size_t next = fill(c, i, false, tab);
-    if (tab.chunks) {
-      const unsigned grid = std::min(tab.chunks, most);
-      if (nparts + (int)grid > kMaxPartials) return cudaErrorInvalidValue;
-      const cudaError_t e = launch_kernel(square_sum_kernel<CAP>, grid, kThreads, 0, c.stream, true, tab,
-                                          partial + nparts);
-      if (e != cudaSuccess) return e;
-      nparts += (int)grid;
-    } else if (next == i) {
-      return cudaErrorInvalidValue;
+  for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {
+    for (size_t i = 0; i < c.ntensors;) {
+      const size_t next = fill(c, i, pass == 1, tab);
+      if (tab.chunks) {
+        const unsigned grid = plan_runs(tab, most, pass == 1);
+        if (clip && launches == 1 && tab.chunks <= kHintChunks) tab.kept = std::min(tab.chunks, kKeptChunks);
+        cudaError_t e;
+        if (pass == 0) {
+          if (nparts + (int)grid > kMaxPartials) return cudaErrorInvalidValue;
+          e = launch_kernel(tab.kept ? square_sum_kernel<CAP, true> : square_sum_kernel<CAP, false>, grid, kThreads, 0,
+                            c.stream, true, tab, partial + nparts);
+          nparts += (int)grid;
+        } else {
+          e = launch_kernel(tab.kept ? scale_kernel<CAP, true> : scale_kernel<CAP, false>, grid, kThreads, 0, c.stream,
+                            true, tab, (const float*)partial, nparts, c.max_norm, c.eps, c.norm);
+        }
+        if (e != cudaSuccess) return e;
+      } else if (next == i) {
+        return cudaErrorInvalidValue;
+      }
+      i = next;
     }
-    i = next;
-  }
-  if (!clip || nparts == 0)
-    return launch_kernel(norm_kernel, 1, kThreads, 0, c.stream, true, (const float*)partial, nparts, c.norm);
-  for (size_t i = 0; i < c.ntensors;) {
-    const size_t next = fill(c, i, true, tab);
-    if (tab.chunks) {
-      const cudaError_t e = launch_kernel(scale_kernel<CAP>, std::min(tab.chunks, most), kThreads, 0, c.stream, true,
-                                          tab, (const float*)partial, nparts, c.max_norm, c.eps, c.norm);
-      if (e != cudaSuccess) return e;
-    }
-    i = next;
+    if (pass == 0 && (!clip || nparts == 0))
+      return launch_kernel(norm_kernel, 1, kThreads, 0, c.stream, true, (const float*)partial, nparts, c.norm);
   }
   return cudaSuccess;
+}
+
+cudaError_t dispatch(const GradsCall& c, bool clip) {
+  return c.ntensors <= kSmallTable ? run<kSmallTable>(c, clip) : run<kLargeTable>(c, clip);
 }
 
 }  // namespace
 
 size_t grad_norm_workspace() { return kMaxPartials * sizeof(float); }
-
-cudaError_t launch_grad_norm(const GradsCall& c) {
-  return c.ntensors <= kSmallTable ? run<kSmallTable>(c, false) : run<kLargeTable>(c, false);
-}
-
-cudaError_t launch_clip_grads(const GradsCall& c) {
-  return c.ntensors <= kSmallTable ? run<kSmallTable>(c, true) : run<kLargeTable>(c, true);
-}
+cudaError_t launch_grad_norm(const GradsCall& c) { return dispatch(c, false); }
+cudaError_t launch_clip_grads(const GradsCall& c) { return dispatch(c, true); }
 
 }  // namespace ar

@@ -18,7 +18,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr size_t kMaxPolicySums = 65536;
-constexpr unsigned long long kShortRow = 1024;  // slots: up to here a warp takes a row (log-probabilities)
 
 template <int DT>
 struct Matrix {
@@ -163,8 +162,10 @@ __device__ __forceinline__ float2 pack_stats(float b, float s, bool natural) { r
 // into factors[t], for the preference loss.
 //
 // One pass with a running base, four slots per thread on the way while four are
-// worked on.  GROUP threads take a row: a warp where a row is short (eight rows in
-// a block), else the block; with few long rows, a cluster of C blocks.
+// worked on.  GROUP threads take a row: a warp (eight rows in a block) where there
+// are many rows, else the block; with few long rows, a cluster of C blocks.
+// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 150 us, 7.2 TB/s (reads alone are
+// faster than the copy).
 struct LogprobPlan {
   int C, per;  // blocks per row; slots per block
 };
@@ -218,15 +219,19 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
   uint4 r[U], next[U] = {};
   load(0, r);
   // the row's ends by elements: slot 0 where the row begins inside it, the last where it ends inside it
+#pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int q = e == 0 ? (in.lo ? 0 : -1) : in.tail;
     if (q >= 0 && q % GROUP == tid) {
       const int j = (s0 + q) * N - in.lead;
-      for (int x = max(0, -j); x < N && j + x < V; ++x) {
-        const float v = to_float(row[j + x]);
-        grow(v);
-        s2.x += ex2(fmaf(v, kLog2e, -b));
-      }
+      float v[N], top = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < N; ++x) v[x] = j + x >= 0 && j + x < V ? to_float(row[j + x]) : -INFINITY;
+#pragma unroll
+      for (int x = 0; x < N; ++x) top = fmaxf(top, v[x]);
+      grow(top);
+#pragma unroll
+      for (int x = 0; x < N; ++x) s2.x += ex2(fmaf(v[x], kLog2e, -b));
     }
   }
   for (int at = 0; at < in.lim; at += U * GROUP) {
@@ -348,32 +353,35 @@ struct RowPlan {
 constexpr int kMaxCluster = 16;
 constexpr uint32_t kWaitLimit = 1u << 20;  // polls; a wait that runs out gives NaN
 
-template <int DT, int THREADS, int K, int BLOCKS>
+template <int DT, int THREADS, int K, int BLOCKS, bool CLUSTER>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
 policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, float4* partial) {
   constexpr int N = Lanes<DT>::N, W = THREADS / 32;
+  constexpr bool kEachWarp = !CLUSTER && W <= 2;  // every warp computes the token's loss for itself
   using E = typename ElemOf<DT>::T;
   extern __shared__ uint4 next[];                   // [K][THREADS]: the row that is on its way
-  __shared__ float2 pairs[2][kMaxCluster * W];      // (m, s) of every warp, by parity: a block may be one row ahead
+  __shared__ float2 pairs[2][(CLUSTER ? kMaxCluster : 1) * W];      // (m, s) of every warp, by parity: a block may be one row ahead
   __shared__ float4 result;
   __shared__ float2 shared_c, again_sh[W];
   __shared__ uint64_t bars[2];
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = (int)cluster_rank();
-  const unsigned long long cluster = blockIdx.x / plan.C, row0 = cluster * plan.run;
+  const int rank = CLUSTER ? (int)cluster_rank() : 0, C = CLUSTER ? plan.C : 1;
+  const unsigned long long cluster = blockIdx.x / C, row0 = cluster * plan.run;
   const int rows = (int)min((unsigned long long)plan.run, a.rows - row0);
   const int V = (int)a.vocab, s0 = rank * plan.per;
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(next) + tid * 16;
   const uint32_t bars_at = (uint32_t)__cvta_generic_to_shared(bars);
   // this warp's pair and the barriers in the block that this lane sends to
-  const uint32_t pair_to = cluster_address((uint32_t)__cvta_generic_to_shared(&pairs[0][rank * W + warp]),
-                                           min(lane, plan.C - 1));
-  const uint32_t bars_to = cluster_address(bars_at, min(lane, plan.C - 1));
-  if (tid == 0) {
-    mbar_init(bars_at, 1);
-    mbar_init(bars_at + 8, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  uint32_t pair_to = 0, bars_to = 0;
+  if constexpr (CLUSTER) {
+    pair_to = cluster_address((uint32_t)__cvta_generic_to_shared(&pairs[0][rank * W + warp]), min(lane, C - 1));
+    bars_to = cluster_address(bars_at, min(lane, C - 1));
+    if (tid == 0) {
+      mbar_init(bars_at, 1);
+      mbar_init(bars_at + 8, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
   }
 
   // lane i holds row i's scalars
@@ -416,7 +424,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     const unsigned long long t = row0 + lane;
     const long long y = load_index(a.targets, a.target_bytes, t);
     y_l = y >= 0 && y < V ? (int)y : -1;
-    if (warp == 0) {
+    if (kEachWarp || warp == 0) {
       old_l = p.old_logprobs[t];
       adv_l = p.advantages[t];
       if (p.ref_logprobs) ref_l = p.ref_logprobs[t];
@@ -425,7 +433,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
   }
   // every block's barriers are set up before another block sends, and its targets' logits are read before another
   // block may overwrite them (gradient in place)
-  if (plan.C > 1) cluster_sync();
+  if constexpr (CLUSTER) cluster_sync();
   else __syncthreads();
 
   PolicySums sum;
@@ -436,13 +444,13 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       const Slots<DT> out(grad, V);
       const int n = (int)out.count();
       const float zero[N] = {};
-      for (int q = rank * THREADS + tid; q < n; q += plan.C * THREADS) store_slot<DT>(out, grad, true, q, zero);
+      for (int q = rank * THREADS + tid; q < n; q += C * THREADS) store_slot<DT>(out, grad, true, q, zero);
       if (rank == 0 && tid == 0) a.logprobs[row0 + i] = 0.0f;
       issue(i + 1);
       continue;
     }
     const int b = done & 1;
-    if (tid == 0) mbar_expect_tx(bars_at + 8 * b, plan.C * W * 8);
+    if (CLUSTER && tid == 0) mbar_expect_tx(bars_at + 8 * b, C * W * 8);
     const Slice<DT> in(logits + i * a.stride, V, s0, plan.per);
 
     cp_async_wait<0>();
@@ -487,41 +495,51 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       }
     }
     const float ws = warp_sum(s2.x + s2.y);
-    if (lane < plan.C) st_async(pair_to + b * (kMaxCluster * W * 8), make_float2(base, ws), bars_to + 8 * b);
+    if constexpr (CLUSTER) {
+      if (lane < C) st_async(pair_to + b * (kMaxCluster * W * 8), make_float2(base, ws), bars_to + 8 * b);
+    } else {
+      if (lane == 0) pairs[b][warp] = make_float2(base, ws);
+    }
     issue(i + 1);
 
-    // by warp 0: the token's loss and what the gradient needs of it
+    // the token's loss and what the gradient needs of it
+    float4 res = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float2 c_lp;
     const auto token = [&](float lp, float base, float S) {
       const float c = policy_token(p, __shfl_sync(~0u, old_l, i), __shfl_sync(~0u, adv_l, i),
                                    __shfl_sync(~0u, ref_l, i), __shfl_sync(~0u, w_l, i), lp, sum);
-      if (lane == 0) {
-        result = make_float4(base, -c / S, -c * expm1f(lp), 0.0f);
-        shared_c = make_float2(c, lp);
-        if (rank == 0) a.logprobs[row0 + i] = lp;
-      }
+      res = make_float4(base, -c / S, -c * expm1f(lp), 0.0f);
+      c_lp = make_float2(c, lp);
+      if (rank == 0 && tid == 0) a.logprobs[row0 + i] = lp;
     };
-    if (warp == 0) {
+    if constexpr (!CLUSTER) __syncthreads();
+    if (kEachWarp || warp == 0) {
       // the row's base B and sum S
-      const bool ok = mbar_wait(bars_at + 8 * b, done >> 1 & 1, kWaitLimit);
+      const bool ok = !CLUSTER || mbar_wait(bars_at + 8 * b, done >> 1 & 1, kWaitLimit);
       float B = -FLT_MAX, S = 0.0f;
-      for (int q = lane; q < plan.C * W; q += 32) B = fmaxf(B, pairs[b][q].x);
+      for (int q = lane; q < C * W; q += 32) B = fmaxf(B, pairs[b][q].x);
       B = warp_max(B);
-      for (int q = lane; q < plan.C * W; q += 32) S += pairs[b][q].y * ex2(pairs[b][q].x - B);
+      for (int q = lane; q < C * W; q += 32) S += pairs[b][q].y * ex2(pairs[b][q].x - B);
       S = warp_sum(S);
       if (!ok) S = __int_as_float(0x7fffffff);
-      const bool again = ok && !usable(S);
-      if (!again) token((fmaf(__shfl_sync(~0u, x_l, i), kLog2e, -B) - log2f(S)) * kLn2, B, S);
-      else if (lane == 0) result.w = 1.0f;
+      if (!ok || usable(S)) token((fmaf(__shfl_sync(~0u, x_l, i), kLog2e, -B) - log2f(S)) * kLn2, B, S);
+      else res.w = 1.0f;
+      if (!kEachWarp && lane == 0) result = res;
     }
-    __syncthreads();
-    const float4 res = result;
+    if constexpr (!kEachWarp) {
+      __syncthreads();
+      res = result;
+    }
     ++done;
     if (res.w != 0.0f) {
       // no finite sum: values beyond 1e38 (masks of the type's lowest value all over the row, say) or a row without
       // a distribution.  Every block goes over the whole row once more, with differences formed first.
       const MaxSum st = row_stats<DT, THREADS>(in.row, V, again_sh);
-      if (plan.C > 1) cluster_sync();  // nobody reads the row any more
-      if (warp == 0) token((__shfl_sync(~0u, x_l, i) - st.m) - logf(st.s), st.m, st.s);
+      if constexpr (CLUSTER) cluster_sync();  // nobody reads the row any more
+      if (kEachWarp || warp == 0) {
+        token((__shfl_sync(~0u, x_l, i) - st.m) - logf(st.s), st.m, st.s);
+        if (lane == 0) shared_c = c_lp;       // the same from every warp
+      }
       __syncthreads();
       row_grad<DT>(in.row, grad, V, __shfl_sync(~0u, y_l, i), shared_c.y, st, shared_c.x, s0 + tid, s0 + plan.per,
                    THREADS);
@@ -575,7 +593,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     if (y >= 0 && yq >= 0 && yq < plan.per && yq % THREADS == tid) from_float(grad + y, res.z);  // over its own store
   }
   if (rank == 0 && tid == 0) partial[cluster] = make_float4(sum.loss, sum.kl, sum.clipped, sum.weight);
-  if (plan.C > 1) cluster_meet();   // no block leaves while another may still send to it
+  if constexpr (CLUSTER) cluster_meet();   // no block leaves while another may still send to it
 }
 
 // The blocks' sums in a fixed order.
@@ -764,7 +782,9 @@ cudaError_t launch_clusters(void (*kernel)(K...), unsigned grid, unsigned thread
 template <int DT>
 cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
   const unsigned long long n = row_slots<DT>(c, c.logits, c.row_stride);
-  if (n <= kShortRow)
+  // a warp per row where that makes 16 warps for every SM (8192 x 9000 bf16: 23 us, a block per row 43; 4096 x 32768
+  // 40 and 44; 4096 x 131072 150 and 150; but 1000 x 32768 23 and 12) or a row has no more for a warp to do
+  if (c.rows >= 16ull * c.sms || n <= 256)
     return launch_kernel(logprob_kernel<DT, 32>, (unsigned)((c.rows + 7) / 8), kThreads, 0, c.stream, true,
                          Matrix<DT>(c), LogprobPlan{1, (int)n}, stats, factors);
   // a row over several blocks until there are two blocks for every SM, each with 1024 slots at least
@@ -774,26 +794,29 @@ cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
                          LogprobPlan{C, (int)((n + C - 1) / C)}, stats, factors);
 }
 
-// Rows per cluster: about four waves of clusters, so that the blocks of an SM
-// are at different points of their rows and the last wave is short, but at most
-// 8 (4096 x 32768 bf16: 1 row 123 us, 2 101, 3 96, 4 96, 8 100; 8192 x 131072: 2
-// 772, 4 708, 8 690, 16 684).  More only to bound the number of partial sums.
-inline int rows_per_cluster(unsigned long long rows, unsigned clusters_per_wave) {
-  const unsigned long long four_waves = rows / (4ull * std::max(1u, clusters_per_wave));
+// Rows per cluster.  One start-up (scalars, first copies, cluster barrier) serves
+// them, but clusters that come and go keep the blocks of an SM at different points
+// of their rows and the end of the kernel short.  At most one wave's share, and at
+// most 4, or 8 where two blocks fill an SM (us at 1 / 2 / 4 / 8 rows: 8192 x 4096 bf16
+// 38 / 35 / 31 / 31, 8192 x 8000 56 / 49 / 48 / 53, 4096 x 32768 123 / 101 / 96 / 100, 8192 x
+// 131072 943 / 782 / 699 / 669; 1000 x 4000, less than a wave, 8.6 / 10.5 / 13 / 21).  More only
+// to bound the number of partial sums.
+inline int rows_per_cluster(unsigned long long rows, unsigned clusters_per_wave, int most) {
+  const unsigned long long wave = std::max(1u, clusters_per_wave), share = (rows + wave / 2) / wave;
   const unsigned long long bound = (rows + kMaxPolicySums - 1) / kMaxPolicySums;
-  return (int)std::min(32ull, std::max({1ull, std::min(8ull, four_waves), bound}));
+  return (int)std::min(32ull, std::max({1ull, std::min<unsigned long long>(most, share), bound}));
 }
 
-template <int DT, int THREADS, int K, int BLOCKS>
+template <int DT, int THREADS, int K, int BLOCKS, bool CLUSTER>
 cudaError_t launch_policy_row(const LogitsCall& c, const PolicyParams& p, unsigned long long slots, int C,
                               float4* partial, unsigned* sums) {
   constexpr int smem = K * THREADS * 16;
-  const auto kernel = policy_row_kernel<DT, THREADS, K, BLOCKS>;
+  const auto kernel = policy_row_kernel<DT, THREADS, K, BLOCKS, CLUSTER>;
   RowPlan plan;
   plan.C = C;
   plan.per = (int)((slots + C - 1) / C);
   plan.most = (int)slots;
-  plan.run = rows_per_cluster(c.rows, (unsigned)(c.sms * BLOCKS / C));
+  plan.run = rows_per_cluster(c.rows, (unsigned)(c.sms * BLOCKS / C), BLOCKS == 2 ? 8 : 4);
   *sums = (unsigned)((c.rows + plan.run - 1) / plan.run);
   cudaError_t e = cudaSuccess;
   if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -815,21 +838,31 @@ cudaError_t run_policy(const LogitsCall& c, const PolicyParams& p, float* stats,
   const unsigned long long n = row_slots<DT>(c, c.logits, c.row_stride);
   unsigned sums = 0;
   cudaError_t e;
-#define AR_ROW(THREADS, K, BLOCKS) launch_policy_row<DT, THREADS, K, BLOCKS>(c, p, n, C, partial, &sums)
+#define AR_ROW(THREADS, K, BLOCKS, CLUSTER) \
+  launch_policy_row<DT, THREADS, K, BLOCKS, CLUSTER>(c, p, n, C, partial, &sums)
   if (c.rows == 0 || n > 16 * 4096) {
     sums = grid_of(c.rows);
     e = launch_kernel(policy_kernel<DT>, sums, kThreads, 0, c.stream, true, Matrix<DT>(c), p, partial);
-  } else if (n <= 1024) {
+  } else if (n <= 2048) {
     constexpr int C = 1;
-    e = n <= 512 ? AR_ROW(64, 8, 14) : AR_ROW(128, 8, 7);
+    e = n <= 512    ? AR_ROW(64, 8, 14, false)
+        : n <= 1024 ? AR_ROW(128, 8, 7, false)
+        : n <= 1536 ? AR_ROW(256, 6, 4, false)
+                    : AR_ROW(256, 8, 4, false);
   } else if (n <= 8192) {
-    const int C = n <= 2048 ? 1 : n <= 4096 ? 2 : 4;
+    const int C = n <= 4096 ? 2 : 4;
     const unsigned long long k = (n + 256 * C - 1) / (256 * C);  // 5 .. 8
-    e = k <= 5 ? AR_ROW(256, 5, 4) : k == 6 ? AR_ROW(256, 6, 4) : k == 7 ? AR_ROW(256, 7, 4) : AR_ROW(256, 8, 4);
+    e = k <= 5   ? AR_ROW(256, 5, 4, true)
+        : k == 6 ? AR_ROW(256, 6, 4, true)
+        : k == 7 ? AR_ROW(256, 7, 4, true)
+                 : AR_ROW(256, 8, 4, true);
   } else {
     const int C = n <= 16384 ? 4 : n <= 32768 ? 8 : 16;
     const unsigned long long k = (n + 256 * C - 1) / (256 * C);  // 9 .. 16
-    e = k <= 10 ? AR_ROW(256, 10, 2) : k <= 12 ? AR_ROW(256, 12, 2) : k <= 14 ? AR_ROW(256, 14, 2) : AR_ROW(256, 16, 2);
+    e = k <= 10   ? AR_ROW(256, 10, 2, true)
+        : k <= 12 ? AR_ROW(256, 12, 2, true)
+        : k <= 14 ? AR_ROW(256, 14, 2, true)
+                  : AR_ROW(256, 16, 2, true);
   }
 #undef AR_ROW
   if (e == cudaSuccess)
