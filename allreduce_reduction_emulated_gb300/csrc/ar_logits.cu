@@ -348,6 +348,7 @@ struct RowPlan {
   int per;      // slots per block: at most THREADS * K
   int most;     // slots of a row at its worst alignment
   int run;      // rows per cluster, at most 32
+  uint32_t zero;  // 0, which the compiler does not know
 };
 
 constexpr int kMaxCluster = 16;
@@ -382,6 +383,8 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       mbar_init(bars_at + 8, 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    __syncwarp();
+    cluster_arrive();  // waited for before the first pair is sent
   }
 
   // lane i holds row i's scalars
@@ -431,16 +434,13 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       x_l = y_l < 0 ? __int_as_float(0x7fffffff) : to_float(a.logits[t * a.stride + y_l]);
     }
   }
-  // every block's barriers are set up before another block sends, and its targets' logits are read before another
-  // block may overwrite them (gradient in place)
-  if constexpr (CLUSTER) cluster_sync();
-  else __syncthreads();
+  if constexpr (CLUSTER) cluster_wait();  // every block's barriers are set up
 
   PolicySums sum;
   int done = 0;
   for (int i = 0; i < rows; ++i) {
-    E* const grad = a.grad + (row0 + i) * a.grad_stride;
     if (!(live >> i & 1)) {
+      E* const grad = a.grad + (row0 + i) * a.grad_stride;
       const Slots<DT> out(grad, V);
       const int n = (int)out.count();
       const float zero[N] = {};
@@ -451,26 +451,28 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     }
     const int b = done & 1;
     if (CLUSTER && tid == 0) mbar_expect_tx(bars_at + 8 * b, C * W * 8);
-    const Slice<DT> in(logits + i * a.stride, V, s0, plan.per);
+    {
+      const Slice<DT> in(logits + i * a.stride, V, s0, plan.per);
 
-    cp_async_wait<0>();
-    // -infinity into what the slots at the row's ends hold beside the row, and into the slot after them, which
-    // an earlier row of another alignment may have filled
-    if (in.lo && tid == 0) {
-      E* to = reinterpret_cast<E*>(&next[0]);
-      for (int x = 0; x < in.lead; ++x) from_float(to + x, -INFINITY);
-    }
-    const int end = (V + in.lead + N - 1) / N - s0;  // the slot after the row's last
-    if (in.tail >= 0 && in.tail % THREADS == tid) {
-      E* to = reinterpret_cast<E*>(&next[in.tail / THREADS * THREADS + tid]);
-      for (int x = in.left; x < N; ++x) from_float(to + x, -INFINITY);
-    } else if (in.lo && V + in.lead < N && tid == 0) {
-      E* to = reinterpret_cast<E*>(&next[0]);
-      for (int x = V + in.lead; x < N; ++x) from_float(to + x, -INFINITY);
-    }
-    if (end >= 0 && end < plan.per && s0 + end < plan.most && end % THREADS == tid) {
-      E* to = reinterpret_cast<E*>(&next[end / THREADS * THREADS + tid]);
-      for (int x = 0; x < N; ++x) from_float(to + x, -INFINITY);
+      cp_async_wait<0>();
+      // -infinity into what the slots at the row's ends hold beside the row, and into the slot after them, which
+      // an earlier row of another alignment may have filled
+      if (in.lo && tid == 0) {
+        E* to = reinterpret_cast<E*>(&next[0]);
+        for (int x = 0; x < in.lead; ++x) from_float(to + x, -INFINITY);
+      }
+      const int end = (V + in.lead + N - 1) / N - s0;  // the slot after the row's last
+      if (in.tail >= 0 && in.tail % THREADS == tid) {
+        E* to = reinterpret_cast<E*>(&next[in.tail / THREADS * THREADS + tid]);
+        for (int x = in.left; x < N; ++x) from_float(to + x, -INFINITY);
+      } else if (in.lo && V + in.lead < N && tid == 0) {
+        E* to = reinterpret_cast<E*>(&next[0]);
+        for (int x = V + in.lead; x < N; ++x) from_float(to + x, -INFINITY);
+      }
+      if (end >= 0 && end < plan.per && s0 + end < plan.most && end % THREADS == tid) {
+        E* to = reinterpret_cast<E*>(&next[end / THREADS * THREADS + tid]);
+        for (int x = 0; x < N; ++x) from_float(to + x, -INFINITY);
+      }
     }
 
     // the slots as they are, kept until the gradient is written
@@ -495,21 +497,22 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       }
     }
     const float ws = warp_sum(s2.x + s2.y);
+    // Once all pairs are there, gradients may overwrite the row (in place): not before this warp's targets' logits
+    // have arrived in their register.
+    const uint32_t zero = __float_as_uint(x_l) & plan.zero;
     if constexpr (CLUSTER) {
-      if (lane < C) st_async(pair_to + b * (kMaxCluster * W * 8), make_float2(base, ws), bars_to + 8 * b);
+      if (lane < C) st_async(pair_to + b * (kMaxCluster * W * 8) + zero, make_float2(base, ws), bars_to + 8 * b);
     } else {
-      if (lane == 0) pairs[b][warp] = make_float2(base, ws);
+      if (lane == 0) pairs[b][warp + zero] = make_float2(base, ws);
     }
     issue(i + 1);
 
     // the token's loss and what the gradient needs of it
     float4 res = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float2 c_lp;
     const auto token = [&](float lp, float base, float S) {
       const float c = policy_token(p, __shfl_sync(~0u, old_l, i), __shfl_sync(~0u, adv_l, i),
                                    __shfl_sync(~0u, ref_l, i), __shfl_sync(~0u, w_l, i), lp, sum);
-      res = make_float4(base, -c / S, -c * expm1f(lp), 0.0f);
-      c_lp = make_float2(c, lp);
+      res = make_float4(base, -c / S, -c, lp);
       if (rank == 0 && tid == 0) a.logprobs[row0 + i] = lp;
     };
     if constexpr (!CLUSTER) __syncthreads();
@@ -523,7 +526,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       S = warp_sum(S);
       if (!ok) S = __int_as_float(0x7fffffff);
       if (!ok || usable(S)) token((fmaf(__shfl_sync(~0u, x_l, i), kLog2e, -B) - log2f(S)) * kLn2, B, S);
-      else res.w = 1.0f;
+      else res.x = INFINITY;
       if (!kEachWarp && lane == 0) result = res;
     }
     if constexpr (!kEachWarp) {
@@ -531,14 +534,20 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       res = result;
     }
     ++done;
-    if (res.w != 0.0f) {
+    // Where registers are short the slice is computed once more, not kept (2000 x 30000 fp32 95 -> 86 us; in bf16
+    // it costs more than it frees, 4096 x 32768 93 -> 98).
+    int again = i;
+    if constexpr (DT == kF32 && CLUSTER) asm volatile("" : "+r"(again));
+    const Slice<DT> in(logits + again * a.stride, V, s0, plan.per);
+    E* const grad = a.grad + (row0 + again) * a.grad_stride;
+    if (res.x == INFINITY) {
       // no finite sum: values beyond 1e38 (masks of the type's lowest value all over the row, say) or a row without
       // a distribution.  Every block goes over the whole row once more, with differences formed first.
       const MaxSum st = row_stats<DT, THREADS>(in.row, V, again_sh);
       if constexpr (CLUSTER) cluster_sync();  // nobody reads the row any more
       if (kEachWarp || warp == 0) {
         token((__shfl_sync(~0u, x_l, i) - st.m) - logf(st.s), st.m, st.s);
-        if (lane == 0) shared_c = c_lp;       // the same from every warp
+        if (lane == 0) shared_c = make_float2(-res.z, res.w);  // the same from every warp
       }
       __syncthreads();
       row_grad<DT>(in.row, grad, V, __shfl_sync(~0u, y_l, i), shared_c.y, st, shared_c.x, s0 + tid, s0 + plan.per,
@@ -590,7 +599,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     }
     const int y = __shfl_sync(~0u, y_l, i);
     const int yq = (y + in.lead) / N - s0;
-    if (y >= 0 && yq >= 0 && yq < plan.per && yq % THREADS == tid) from_float(grad + y, res.z);  // over its own store
+    if (y >= 0 && yq >= 0 && yq < plan.per && yq % THREADS == tid) from_float(grad + y, res.z * expm1f(res.w));  // over its own store
   }
   if (rank == 0 && tid == 0) partial[cluster] = make_float4(sum.loss, sum.kl, sum.clipped, sum.weight);
   if constexpr (CLUSTER) cluster_meet();   // no block leaves while another may still send to it
@@ -782,9 +791,11 @@ cudaError_t launch_clusters(void (*kernel)(K...), unsigned grid, unsigned thread
 template <int DT>
 cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
   const unsigned long long n = row_slots<DT>(c, c.logits, c.row_stride);
-  // a warp per row where that makes 16 warps for every SM (8192 x 9000 bf16: 23 us, a block per row 43; 4096 x 32768
-  // 40 and 44; 4096 x 131072 150 and 150; but 1000 x 32768 23 and 12) or a row has no more for a warp to do
-  if (c.rows >= 16ull * c.sms || n <= 256)
+  // A warp per row where that makes 16 warps for every SM (8192 x 9000 bf16: 23 us, a block per row 43; 4096 x 32768
+  // 40 and 44; 4096 x 131072 150 and 150; but 1000 x 32768 23 and 12) or a row has no more for a warp to do.  Thousands of
+  // warps leave no whole rows in L2, though: where the gradient follows, long rows take a block (preference 4 x 1024
+  // x 131072: 789 us, with a warp per row 828).
+  if (n <= 256 || (c.rows >= 16ull * c.sms && (!stats || n <= 2048)))
     return launch_kernel(logprob_kernel<DT, 32>, (unsigned)((c.rows + 7) / 8), kThreads, 0, c.stream, true,
                          Matrix<DT>(c), LogprobPlan{1, (int)n}, stats, factors);
   // a row over several blocks until there are two blocks for every SM, each with 1024 slots at least
@@ -815,6 +826,7 @@ cudaError_t launch_policy_row(const LogitsCall& c, const PolicyParams& p, unsign
   RowPlan plan;
   plan.C = C;
   plan.per = (int)((slots + C - 1) / C);
+  plan.zero = 0;
   plan.most = (int)slots;
   plan.run = rows_per_cluster(c.rows, (unsigned)(c.sms * BLOCKS / C), BLOCKS == 2 ? 8 : 4);
   *sums = (unsigned)((c.rows + plan.run - 1) / plan.run);
@@ -845,7 +857,7 @@ cudaError_t run_policy(const LogitsCall& c, const PolicyParams& p, float* stats,
     e = launch_kernel(policy_kernel<DT>, sums, kThreads, 0, c.stream, true, Matrix<DT>(c), p, partial);
   } else if (n <= 2048) {
     constexpr int C = 1;
-    e = n <= 512    ? AR_ROW(64, 8, 14, false)
+    e = n <= 512    ? AR_ROW(64, 8, 12, false)
         : n <= 1024 ? AR_ROW(128, 8, 7, false)
         : n <= 1536 ? AR_ROW(256, 6, 4, false)
                     : AR_ROW(256, 8, 4, false);

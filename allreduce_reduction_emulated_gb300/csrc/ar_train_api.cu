@@ -1,6 +1,7 @@
 // ar_train_api.cu -- the C ABI of the training operators (declared in
 // include/ar_train.h): argument checks and dispatch.  Host code only; the
 // kernels live in ar_logits.cu and ar_clip.cu.  Nothing here allocates or throws.
+#include <atomic>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
@@ -104,11 +105,17 @@ ar_status_t check_grads(size_t n, const void* const* grads, void* const* outs, c
   return AR_SUCCESS;
 }
 
+// Of the current device; asked once per device.
 bool multiprocessors(int* sms) {
+  static std::atomic<int> known[64];
   int dev = -1;
-  if (cudaGetDevice(&dev) == cudaSuccess &&
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
-    return true;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0) {
+    if (dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return true;
+    if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess) {
+      if (dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+      return true;
+    }
+  }
   cudaGetLastError();
   return false;
 }
