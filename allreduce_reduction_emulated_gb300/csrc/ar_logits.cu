@@ -690,8 +690,8 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const PairParams p) {
 constexpr int kGradSlots = 4, kPiece = kThreads * kGradSlots;
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) preference_grad_kernel(const Matrix<DT> a, const PairParams p,
-                                                                   const float2* stats, unsigned pieces) {
+__global__ void __launch_bounds__(kThreads, 6) preference_grad_kernel(const Matrix<DT> a, const PairParams p,
+                                                                      const float2* stats, unsigned pieces) {
   constexpr int N = Lanes<DT>::N;
   using E = typename ElemOf<DT>::T;
   pdl_enter();
@@ -702,10 +702,10 @@ __global__ void __launch_bounds__(kThreads) preference_grad_kernel(const Matrix<
     v = block_sum<kThreads>(v, sh);
     if (threadIdx.x == 0) *p.loss = p.scale * v;
   }
-  const unsigned long long back = blockIdx.x / pieces;
+  const unsigned back = blockIdx.x / pieces;
   if (back >= a.rows) return;
   const unsigned long long t = a.rows - 1 - back;
-  const long long V = (long long)a.vocab, s0 = (long long)(blockIdx.x % pieces) * kPiece + threadIdx.x;
+  const int V = (int)a.vocab, s0 = (int)(blockIdx.x % pieces) * kPiece, tid = threadIdx.x;
   E* grad = a.grad + t * a.grad_stride;
   const float c = p.factors[t];
   const E* row = a.logits + t * a.stride;
@@ -714,43 +714,58 @@ __global__ void __launch_bounds__(kThreads) preference_grad_kernel(const Matrix<
     const float zero[N] = {};
 #pragma unroll
     for (int k = 0; k < kGradSlots; ++k)
-      if (s0 + k * kThreads < out.count()) store_slot<DT>(out, grad, true, s0 + k * kThreads, zero);
+      if (s0 + k * kThreads + tid < out.count()) store_slot<DT>(out, grad, true, s0 + k * kThreads + tid, zero);
     return;
   }
-  const Slots<DT> in(row, V);
-  const long long n = in.count();
-  const bool same = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
+  const Slice<DT> in(row, V, s0, kPiece);
+  const uint4* src = reinterpret_cast<const uint4*>(row - in.lead) + s0 + tid;
   uint4 r[kGradSlots];
 #pragma unroll
-  for (int k = 0; k < kGradSlots; ++k)
-    if (in.whole(s0 + k * kThreads)) r[k] = ld_row(reinterpret_cast<const uint4*>(row + in.first(s0 + k * kThreads)));
+  for (int k = 0; k < kGradSlots; ++k) {
+    const int q = k * kThreads + tid;
+    if (q >= in.lo && q < in.lim) r[k] = ld_row(src + k * kThreads);
+  }
   const float2 st = stats[t];
-  const long long y = load_index(a.targets, a.target_bytes, t);
-  const bool natural = st.y < 0.0f;
+  const bool natural = st.y < 0.0f, same = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
   const float f = -c / fabsf(st.y);
   const float2 minus_b = make_float2(-st.x, -st.x), f2 = make_float2(f, f);
+  uint4* dst = reinterpret_cast<uint4*>(grad - in.lead) + s0 + tid;
+  if (same && !natural) {
 #pragma unroll
-  for (int k = 0; k < kGradSlots; ++k) {
-    const long long s = s0 + k * kThreads;
-    if (s >= n) break;
-    const long long j = in.first(s);
-    if (in.whole(s) && same && !natural) {
-      Acc<DT> g = widen<DT>(r[k]);
+    for (int k = 0; k < kGradSlots; ++k) {
+      const int q = k * kThreads + tid;
+      if (q >= in.lo && q < in.lim) {
+        Acc<DT> g = widen<DT>(r[k]);
 #pragma unroll
-      for (int x = 0; x < N; x += 2) {
-        const float2 v = mul2(exp2_pair(g.v[x], g.v[x + 1], minus_b), f2);
-        g.v[x] = v.x;
-        g.v[x + 1] = v.y;
+        for (int x = 0; x < N; x += 2) {
+          const float2 v = mul2(exp2_pair(g.v[x], g.v[x + 1], minus_b), f2);
+          g.v[x] = v.x;
+          g.v[x + 1] = v.y;
+        }
+        st_stream(dst + k * kThreads, narrow<DT>(g, 1.0f, false));
       }
-      st_stream(reinterpret_cast<uint4*>(grad + j), narrow<DT>(g, 1.0f, false));
-    } else {
-      float x[N];
-      in.load(s, x, -INFINITY);
-#pragma unroll
-      for (int i = 0; i < N; ++i) x[i] = f * (natural ? exp_diff(x[i], st.x) : ex2(fmaf(x[i], kLog2e, -st.x)));
-      store_slot<DT>(in, grad, same, s, x);
     }
-    if (y >= j && y < j + N) from_float(grad + y, -c * expm1f(a.logprobs[t]));  // over its own store
+  }
+  // slots at the row's ends, and all of them in the rarer layouts and rows: by elements
+  const int end = (V + in.lead + N - 1) / N - s0;
+#pragma unroll 1
+  for (int q = tid; q < kPiece && q < end; q += kThreads) {
+    if (same && !natural && q >= in.lo && q < in.lim) continue;
+    const int j = (s0 + q) * N - in.lead;
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = j + i >= 0 && j + i < V ? to_float(row[j + i]) : -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float g = f * (natural ? exp_diff(x[i], st.x) : ex2(fmaf(x[i], kLog2e, -st.x)));
+      if (j + i >= 0 && j + i < V) from_float(grad + j + i, g);
+    }
+  }
+  // the target's element, over its thread's own store
+  const long long y = load_index(a.targets, a.target_bytes, t);
+  if (y >= 0 && y < V) {
+    const int q = ((int)y + in.lead) / N - s0;
+    if (q >= 0 && q < kPiece && q % kThreads == tid) from_float(grad + y, -c * expm1f(a.logprobs[t]));
   }
 }
 
