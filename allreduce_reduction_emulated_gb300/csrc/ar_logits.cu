@@ -6,6 +6,7 @@
 // maximum m and the sum of e^(x - m), rescaled when m grows; a block joins the
 // threads' pairs.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "ar_logits.cuh"
@@ -783,16 +784,14 @@ unsigned long long row_slots(const LogitsCall& c, const void* matrix, size_t str
   return (c.vocab + lead + N - 1) / N;
 }
 
-// cudaLaunchKernelEx with programmatic dependent launch, in clusters of C blocks
-template <class... K, class... A>
-cudaError_t launch_clusters(void (*kernel)(K...), unsigned grid, unsigned threads, int smem, int C, cudaStream_t stream,
-                            A&&... args) {
+// Programmatic dependent launch in clusters of C blocks (attr: room for two).
+inline cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, int smem, int C, cudaStream_t stream,
+                                         cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = threads;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -800,7 +799,7 @@ cudaError_t launch_clusters(void (*kernel)(K...), unsigned grid, unsigned thread
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+  return cfg;
 }
 
 template <int DT>
@@ -816,21 +815,60 @@ cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
   // a row over several blocks until there are two blocks for every SM, each with 1024 slots at least
   int C = 1;
   while (C < 8 && c.rows * C < 2ull * c.sms && n >= 2048ull * C) C *= 2;
-  return launch_clusters(logprob_kernel<DT, kThreads>, (unsigned)c.rows * C, kThreads, 0, C, c.stream, Matrix<DT>(c),
-                         LogprobPlan{C, (int)((n + C - 1) / C)}, stats, factors);
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = cluster_config((unsigned)c.rows * C, kThreads, 0, C, c.stream, attr);
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<DT, kThreads>, Matrix<DT>(c),
+                            LogprobPlan{C, (int)((n + C - 1) / C)}, stats, factors);
 }
 
-// Rows per cluster.  One start-up (scalars, first copies, cluster barrier) serves
-// them, but clusters that come and go keep the blocks of an SM at different points
-// of their rows and the end of the kernel short.  At most one wave's share, and at
-// most 4, or 8 where two blocks fill an SM (us at 1 / 2 / 4 / 8 rows: 8192 x 4096 bf16
-// 38 / 35 / 31 / 31, 8192 x 8000 56 / 49 / 48 / 53, 4096 x 32768 123 / 101 / 96 / 100, 8192 x
-// 131072 943 / 782 / 699 / 669; 1000 x 4000, less than a wave, 8.6 / 10.5 / 13 / 21).  More only
-// to bound the number of partial sums.
-inline int rows_per_cluster(unsigned long long rows, unsigned clusters_per_wave, int most) {
-  const unsigned long long wave = std::max(1u, clusters_per_wave), share = (rows + wave / 2) / wave;
+// Rows per cluster, of 1 .. most.  A row takes a resident cluster 3.7 us by itself
+// (2.0 in blocks of 128 threads: copies, sum, exchange, loss, stores); all resident
+// clusters' rows take 2 wave row_bytes / 6.8 TB/s together.
+// Where HBM is the longer by a fifth, the clusters' start-ups hide behind others'
+// transfers and small runs end evenly: one wave's share of the rows, at most 4, or 8
+// where two blocks fill an SM (us at 1 / 2 / 4 / 8 / 16 rows: 4096 x 32768 bf16 109 / 97 / 95 /
+// 99 / 101, 8192 x 131072 804 / 701 / 663 / 657 / 672).
+// Where the row itself is, a wave takes its rows' time and a start-up of about one
+// row whether it is full or not: the least ceil(waves) (rows + 1) (300 x 70000 at 3 / 4 / 5 /
+// 6: 24.1 / 29.3 / 22.8 / 26.6; 700 x 100000 at 4 / 5 / 8 / 10: 59 / 57 / 69 / 55; 2489 x 50001 at
+// 4 / 6 / 8: 102 / 101 / 108).  More only to bound the number of partial sums.
+inline int rows_per_cluster(unsigned long long rows, int wave, double row_bytes, int threads, bool two_blocks) {
+  const double row_us = threads >= 256 ? 3.7 : 2.0, wave_us = 2.0 * wave * row_bytes / 6.8e6;
+  int run = 1;
+  if (wave_us > 1.2 * row_us) {
+    run = (int)std::max(1ull, std::min<unsigned long long>(two_blocks ? 8 : 4, (rows + wave / 2) / wave));
+  } else {
+    unsigned long long least = ~0ull;
+    for (int k = 1; k <= (two_blocks ? 12 : 8); ++k) {
+      const unsigned long long clusters = (rows + k - 1) / k, time = (clusters + wave - 1) / wave * (k + 1);
+      if (time < least) {
+        least = time;
+        run = k;
+      }
+    }
+  }
   const unsigned long long bound = (rows + kMaxPolicySums - 1) / kMaxPolicySums;
-  return (int)std::min(32ull, std::max({1ull, std::min<unsigned long long>(most, share), bound}));
+  return (int)std::min(32ull, std::max((unsigned long long)run, bound));
+}
+
+// Clusters of C of this kernel's blocks that the device holds at a time; asked
+// once per device (a cluster's blocks have to fit one group of SMs).
+template <int DT, int THREADS, int K, int BLOCKS, bool CLUSTER>
+int resident_clusters(const cudaLaunchConfig_t& cfg, int C, int sms) {
+  if (!CLUSTER) return sms * BLOCKS;
+  static std::atomic<int> known[16][5];  // by device, log2 C
+  int dev = -1, log2 = 0;
+  while (1 << log2 < C) ++log2;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) dev = -1;
+  int n = dev < 0 ? 0 : known[dev][log2].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  if (cudaOccupancyMaxActiveClusters(&n, policy_row_kernel<DT, THREADS, K, BLOCKS, CLUSTER>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (n <= 0) n = std::max(1, sms * BLOCKS / C);
+  else if (dev >= 0) known[dev][log2].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 template <int DT, int THREADS, int K, int BLOCKS, bool CLUSTER>
@@ -843,13 +881,17 @@ cudaError_t launch_policy_row(const LogitsCall& c, const PolicyParams& p, unsign
   plan.per = (int)((slots + C - 1) / C);
   plan.zero = 0;
   plan.most = (int)slots;
-  plan.run = rows_per_cluster(c.rows, (unsigned)(c.sms * BLOCKS / C), BLOCKS == 2 ? 8 : 4);
-  *sums = (unsigned)((c.rows + plan.run - 1) / plan.run);
   cudaError_t e = cudaSuccess;
   if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess && C > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  return launch_clusters(kernel, *sums * C, THREADS, smem, C, c.stream, Matrix<DT>(c), p, plan, partial);
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = cluster_config(C, THREADS, smem, C, c.stream, attr);
+  plan.run = rows_per_cluster(c.rows, resident_clusters<DT, THREADS, K, BLOCKS, CLUSTER>(cfg, C, c.sms), 16.0 * slots,
+                              THREADS, BLOCKS == 2);
+  *sums = (unsigned)((c.rows + plan.run - 1) / plan.run);
+  cfg.gridDim = *sums * C;
+  return cudaLaunchKernelEx(&cfg, kernel, Matrix<DT>(c), p, plan, partial);
 }
 
 // The shape by the row's length in 16-byte slots.  Registers hold the row: a
