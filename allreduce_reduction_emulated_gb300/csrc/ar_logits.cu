@@ -806,10 +806,10 @@ template <int DT>
 cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
   const unsigned long long n = row_slots<DT>(c, c.logits, c.row_stride);
   // A warp per row where that makes 16 warps for every SM (8192 x 9000 bf16: 23 us, a block per row 43; 4096 x 32768
-  // 40 and 44; 4096 x 131072 150 and 150; but 1000 x 32768 23 and 12) or a row has no more for a warp to do.  Thousands of
+  // 40 and 44; but 4096 x 131072 159 and 154, 1000 x 32768 23 and 12) or a row has no more for a warp to do.  Thousands of
   // warps leave no whole rows in L2, though: where the gradient follows, long rows take a block (preference 4 x 1024
   // x 131072: 789 us, with a warp per row 828).
-  if (n <= 256 || (c.rows >= 16ull * c.sms && (!stats || n <= 2048)))
+  if (n <= 256 || (c.rows >= 16ull * c.sms && n <= (stats ? 2048 : 8192)))
     return launch_kernel(logprob_kernel<DT, 32>, (unsigned)((c.rows + 7) / 8), kThreads, 0, c.stream, true,
                          Matrix<DT>(c), LogprobPlan{1, (int)n}, stats, factors);
   // a row over several blocks until there are two blocks for every SM, each with 1024 slots at least
