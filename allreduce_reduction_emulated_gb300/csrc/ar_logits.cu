@@ -2,9 +2,13 @@
 // token log-probabilities, the policy loss and the preference loss with the
 // gradient of the logits.
 //
-// softmax statistics in one pass over a row: each thread keeps a running
-// maximum m and the sum of e^(x - m), rescaled when m grows; a block joins the
-// threads' pairs.
+// With M the largest logit of a row and S the sum of e^(x - M), the target's
+// log-probability is (x_y - M) - log S and p_j = e^(x_j - M) / S.  Every kernel takes
+// them in one pass: a running maximum and a sum that is rescaled when it grows, in
+// fp32, joined over threads, warps, blocks and clusters.  All of them are bound by
+// HBM where the matrix is large (a row is 8 to 600 KB); the policy loss keeps the row on
+// the chip between the sum and the gradient, so it reads and writes the matrix once.
+// Comments give times on one GB300 (152 SMs; a copy reaches 6.79 TB/s).
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -165,8 +169,8 @@ __device__ __forceinline__ float2 pack_stats(float b, float s, bool natural) { r
 // One pass with a running base, four slots per thread on the way while four are
 // worked on.  GROUP threads take a row: a warp (eight rows in a block) where there
 // are many rows, else the block; with few long rows, a cluster of C blocks.
-// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 150 us, 7.2 TB/s (reads alone are
-// faster than the copy).
+// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 154 us, 7.0 TB/s (reads alone are
+// faster than the copy); one row of 32768 3.0 us.
 struct LogprobPlan {
   int C, per;  // blocks per row; slots per block
 };
@@ -299,6 +303,9 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
 
 // --------------------------------------------------------------- policy loss
 
+// Rows too long to be held (above 65536 slots, 524,288 bf16 logits): a block per row,
+// which it reads twice, the second time from L2 (its whole range of sizes, before the
+// kernel below was there: 8192 x 131072 bf16 1200 us, 4096 x 32768 154 us).
 template <int DT>
 __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, const PolicyParams p, float4* partial) {
   pdl_enter();
@@ -341,9 +348,10 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, co
 // block joins them and computes the token's loss, and one block barrier hands the
 // factors to the others, which write the gradient from their registers.
 //
-// Bound by HBM: 2 rows vocab es bytes.  8192 x 131072 bf16: 672 us, 6.39 TB/s; 4096 x 131072
-// fp32: 666 us, 6.45 TB/s; 4096 x 32768 bf16: 96 us, 5.6 TB/s, where the chain of a row
-// (sum, exchange, loss, about 2 us) shows more.
+// Bound by HBM: 2 rows vocab es bytes.  8192 x 131072 bf16: 653 us, 6.58 TB/s; 4096 x 131072
+// fp32: 650 us, 6.61 TB/s; 4096 x 32768 bf16: 94 us, 5.73 TB/s.  Below that a row's own
+// chain (copies, sum, exchange, loss, stores: 3.7 us) shows: 2489 x 50001 100 us, 5.0 TB/s;
+// 300 x 70000 23 us, 3.7 TB/s.
 struct RowPlan {
   int C;        // blocks per cluster
   int per;      // slots per block: at most THREADS * K
@@ -362,7 +370,8 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
   constexpr bool kEachWarp = !CLUSTER && W <= 2;  // every warp computes the token's loss for itself
   using E = typename ElemOf<DT>::T;
   extern __shared__ uint4 next[];                   // [K][THREADS]: the row that is on its way
-  __shared__ float2 pairs[2][(CLUSTER ? kMaxCluster : 1) * W];      // (m, s) of every warp, by parity: a block may be one row ahead
+  // (base, sum) of every warp, by parity: a block may be one row ahead
+  __shared__ float2 pairs[2][(CLUSTER ? kMaxCluster : 1) * W];
   __shared__ float4 result;
   __shared__ float2 shared_c, again_sh[W];
   __shared__ uint64_t bars[2];
@@ -661,11 +670,15 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const PairParams p) {
     }
     if (threadIdx.x == 0) {
       const float z = p.beta * (R[0] - R[1]);
-      // softplus(-z) = max(-z, 0) + log1p(e^-|z|); softplus(z) = softplus(-z) + z
+      // softplus(-z) = max(-z, 0) + log1p(e^-|z|)
       const float e = expf(-fabsf(z));
       const float sp = fmaxf(-z, 0.0f) + log1pf(e);
       p.margins[i] = z;
-      p.pair_loss[i] = z != z ? z : (1.0f - p.ls) * sp + p.ls * (sp + z);
+      // (a side of weight 0 is left out: it may be infinite)
+      float l = z != z ? z : 0.0f;
+      if (p.ls < 1.0f) l += (1.0f - p.ls) * sp;
+      if (p.ls > 0.0f) l += p.ls * (fmaxf(z, 0.0f) + log1pf(e));
+      p.pair_loss[i] = l;
       // sigmoid(-z) and sigmoid(z), the smaller one without cancellation
       const float small = e / (1.0f + e), big = 1.0f / (1.0f + e);
       const float neg = z >= 0.0f ? small : big, pos = z >= 0.0f ? big : small;
@@ -688,6 +701,10 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const PairParams p) {
 // The gradient of one piece of a row: kGradSlots slots per thread, all loaded
 // before the first is used.  The rows go from the last to the first: what the
 // statistics' pass has read last is still in L2.
+// Bound by HBM: with the statistics' pass the logits are read twice, since a row's
+// factor needs its whole pair's log-probabilities: 6830 x 131072 bf16 773 us for the whole
+// loss, 6.95 TB/s of two reads and one write; 2489 x 50001 105 us.  2 / 4 / 8 slots: 120 / 114 /
+// 115 us (2400 x 50001).
 constexpr int kGradSlots = 4, kPiece = kThreads * kGradSlots;
 
 template <int DT>
@@ -852,7 +869,8 @@ inline int rows_per_cluster(unsigned long long rows, int wave, double row_bytes,
 }
 
 // Clusters of C of this kernel's blocks that the device holds at a time; asked
-// once per device (a cluster's blocks have to fit one group of SMs).
+// once per device (a cluster's blocks have to fit one group of SMs).  0: clusters
+// of 16, which a device need not offer, do not fit.
 template <int DT, int THREADS, int K, int BLOCKS, bool CLUSTER>
 int resident_clusters(const cudaLaunchConfig_t& cfg, int C, int sms) {
   if (!CLUSTER) return sms * BLOCKS;
@@ -862,12 +880,13 @@ int resident_clusters(const cudaLaunchConfig_t& cfg, int C, int sms) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) dev = -1;
   int n = dev < 0 ? 0 : known[dev][log2].load(std::memory_order_relaxed);
   if (n > 0) return n;
+  n = 0;
   if (cudaOccupancyMaxActiveClusters(&n, policy_row_kernel<DT, THREADS, K, BLOCKS, CLUSTER>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
-  if (n <= 0) n = std::max(1, sms * BLOCKS / C);
-  else if (dev >= 0) known[dev][log2].store(n, std::memory_order_relaxed);
+  if (n <= 0) return C > 8 ? 0 : std::max(1, sms * BLOCKS / C);
+  if (dev >= 0) known[dev][log2].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -887,21 +906,23 @@ cudaError_t launch_policy_row(const LogitsCall& c, const PolicyParams& p, unsign
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = cluster_config(C, THREADS, smem, C, c.stream, attr);
-  plan.run = rows_per_cluster(c.rows, resident_clusters<DT, THREADS, K, BLOCKS, CLUSTER>(cfg, C, c.sms), 16.0 * slots,
-                              THREADS, BLOCKS == 2);
+  const int wave = resident_clusters<DT, THREADS, K, BLOCKS, CLUSTER>(cfg, C, c.sms);
+  if (wave == 0) return cudaErrorNotSupported;
+  plan.run = rows_per_cluster(c.rows, wave, 16.0 * slots, THREADS, BLOCKS == 2);
   *sums = (unsigned)((c.rows + plan.run - 1) / plan.run);
   cfg.gridDim = *sums * C;
   return cudaLaunchKernelEx(&cfg, kernel, Matrix<DT>(c), p, plan, partial);
 }
 
 // The shape by the row's length in 16-byte slots.  Registers hold the row: a
-// slice of 32 KiB in 256 threads leaves room for four blocks on an SM, which was
-// faster than two blocks of 512 threads with a deeper queue (8192 x 131072 bf16
-// 690 against 984 us, before the exponentials were taken twice to halve the
-// registers 826).  From a cluster of more than 4 such blocks on, slices of
-// 64 KiB, two on an SM, in half the blocks (131072 bf16: 672 against 690 us; fp32:
+// slice of up to 32 KiB in 256 threads leaves room for four blocks on an SM, which was
+// faster than two blocks of 512 threads with three rows on the way (8192 x 131072 bf16
+// 690 against 984 us) and than keeping the exponentials instead of the logits in twice
+// the registers (826).  From a cluster of more than 4 such blocks on, slices of
+// up to 64 KiB, two on an SM, in half the blocks (131072 bf16: 672 against 690 us; fp32:
 // 666 against 687; at 65536 they are level).  Short rows take small blocks, many
-// on an SM (8192 x 4096 bf16: 64 threads 35 us, 128 threads 40, 256 threads 52).
+// on an SM, and no cluster (8192 x 4096 bf16: 64 threads 30 us, 128 threads 40, 256 threads
+// 52).
 template <int DT>
 cudaError_t run_policy(const LogitsCall& c, const PolicyParams& p, float* stats, float4* partial) {
   const unsigned long long n = row_slots<DT>(c, c.logits, c.row_stride);
@@ -909,9 +930,12 @@ cudaError_t run_policy(const LogitsCall& c, const PolicyParams& p, float* stats,
   cudaError_t e;
 #define AR_ROW(THREADS, K, BLOCKS, CLUSTER) \
   launch_policy_row<DT, THREADS, K, BLOCKS, CLUSTER>(c, p, n, C, partial, &sums)
-  if (c.rows == 0 || n > 16 * 4096) {
+  const auto streamed = [&] {
     sums = grid_of(c.rows);
-    e = launch_kernel(policy_kernel<DT>, sums, kThreads, 0, c.stream, true, Matrix<DT>(c), p, partial);
+    return launch_kernel(policy_kernel<DT>, sums, kThreads, 0, c.stream, true, Matrix<DT>(c), p, partial);
+  };
+  if (c.rows == 0 || n > 16 * 4096) {
+    e = streamed();
   } else if (n <= 2048) {
     constexpr int C = 1;
     e = n <= 512    ? AR_ROW(64, 8, 12, false)
@@ -932,6 +956,7 @@ cudaError_t run_policy(const LogitsCall& c, const PolicyParams& p, float* stats,
         : k <= 12 ? AR_ROW(256, 12, 2, true)
         : k <= 14 ? AR_ROW(256, 14, 2, true)
                   : AR_ROW(256, 16, 2, true);
+    if (e == cudaErrorNotSupported) e = streamed();
   }
 #undef AR_ROW
   if (e == cudaSuccess)
@@ -942,13 +967,13 @@ cudaError_t run_policy(const LogitsCall& c, const PolicyParams& p, float* stats,
 
 template <int DT>
 cudaError_t run_preference(const LogitsCall& c, const PairParams& p, float2* stats) {
-  cudaError_t e = cudaSuccess;
-  if (c.rows) e = run_logprobs<DT>(c, stats, p.factors);
-  if (e == cudaSuccess && p.pairs) e = launch_kernel(pair_kernel, grid_of(p.pairs), kThreads, 0, c.stream, true, p);
   const unsigned long long slots = std::max(row_slots<DT>(c, c.logits, c.row_stride),
                                             row_slots<DT>(c, c.grad, c.grad_stride));
   const unsigned long long pieces = std::max(1ull, (slots + kPiece - 1) / kPiece);
-  if (e == cudaSuccess && c.rows * pieces > 0x7fffffffull) e = cudaErrorInvalidValue;
+  if (c.rows * pieces > 0x7fffffffull) return cudaErrorInvalidValue;
+  cudaError_t e = cudaSuccess;
+  if (c.rows) e = run_logprobs<DT>(c, stats, p.factors);
+  if (e == cudaSuccess && p.pairs) e = launch_kernel(pair_kernel, grid_of(p.pairs), kThreads, 0, c.stream, true, p);
   if (e == cudaSuccess)
     e = launch_kernel(preference_grad_kernel<DT>, (unsigned)std::max(1ull, c.rows * pieces), kThreads, 0, c.stream,
                       true, Matrix<DT>(c), p, (const float2*)stats, (unsigned)pieces);

@@ -196,7 +196,7 @@ ar_status_t ar_grad_norm(size_t ntensors, const void* const* grads, const size_t
   if (st != AR_SUCCESS) return st;
   if (!aligned(norm, 4) || !aligned(workspace, 16) || workspace_bytes < ar_grad_norm_workspace())
     return AR_ERR_INVALID_ARG;
-  ar::GradsCall c{ntensors, grads, nullptr, counts, reinterpret_cast<const int*>(dtypes), 0.0f, 0.0f, norm, workspace,
+  ar::GradsCall c{ntensors, grads, nullptr, counts, dtypes, 0.0f, 0.0f, norm, workspace,
                   0, static_cast<cudaStream_t>(stream)};
   if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
   Range range("ar_grad_norm");
@@ -211,7 +211,7 @@ ar_status_t ar_clip_grads(size_t ntensors, const void* const* grads, void* const
   if (!(max_norm >= 0.0f) || !(eps >= 0.0f)) return AR_ERR_INVALID_ARG;
   if (!aligned(norm, 4) || !aligned(workspace, 16) || workspace_bytes < ar_grad_norm_workspace())
     return AR_ERR_INVALID_ARG;
-  ar::GradsCall c{ntensors, grads, outs, counts, reinterpret_cast<const int*>(dtypes), max_norm, eps, norm, workspace,
+  ar::GradsCall c{ntensors, grads, outs, counts, dtypes, max_norm, eps, norm, workspace,
                   0, static_cast<cudaStream_t>(stream)};
   if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
   Range range("ar_clip_grads");

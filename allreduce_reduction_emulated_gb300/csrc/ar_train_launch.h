@@ -5,6 +5,7 @@
 #include <cstddef>
 #include <cuda_runtime.h>
 
+#include "../../include/ar.h"
 #include "ar_launch.h"
 
 namespace ar {
@@ -55,7 +56,7 @@ struct GradsCall {
   const void* const* grads;
   void* const* outs;               // NULL: in place
   const size_t* counts;
-  const int* dtypes;               // ar_dtype_t each: fp32 or bf16
+  const ar_dtype_t* dtypes;        // fp32 or bf16 each
   float max_norm, eps;
   float* norm;
   void* workspace;

@@ -271,6 +271,52 @@ def test_preference_extreme_margins(dev, z):
     check_preference(logits, y, torch.tensor([0, 1, 2], device=dev), ref, w)
 
 
+def test_preference_targets_of_probability_zero(dev):
+    """A rejected answer with a token of probability zero: margin infinite, loss and
+    gradient 0; a chosen one: loss infinite, gradient that of the linear branch."""
+    logits, y, _, _, ref, w = inputs(dev, 4, 70, torch.float32, masked=0.0)
+    w[:] = 1.0
+    off = torch.tensor([0, 2, 4], device=dev)
+    for row, loss, dz in ((3, 0.0, 0.0), (0, INF, -1.0)):
+        x, t = logits.clone(), y.clone()
+        t[row] = 69
+        x[:, 69] = -1.0
+        x[row, 69] = -INF
+        r = losses.preference_loss(x, t, off, ref, w, beta=0.1)
+        tu.assert_close(r.loss, loss, 0.0)
+        assert float(r.margins) == (INF if dz == 0 else -INF) and float(r.logprobs[row]) == -INF
+        lp, p = tu.rows64(x, t, w)
+        c = 0.1 * dz * torch.tensor([1.0, 1.0, -1.0, -1.0], device=dev, dtype=torch.float64)
+        want = tu.grad64(p, t, c)
+        assert bool(((r.grad.double() - want).abs() <= 1e-5 * want.abs() + 1e-12).all())
+
+
+# slots of 16 bytes at which the policy loss changes its shape (blocks, clusters, registers per thread)
+SHAPES = [512, 1024, 1536, 2048, 2560, 3584, 4096, 5120, 8192, 10240, 12288, 16384, 20480, 32768, 49152, 65536]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("slots", SHAPES)
+def test_policy_shapes(dev, slots, dtype):
+    """Rows that just fill a shape, begin at an odd element, or need one slot more."""
+    N = 16 // (4 if dtype == torch.float32 else 2)
+    for V, pad, shift in ((slots * N, 0, 0), (slots * N - 2 * N, 1, 3), (slots * N + 1, 0, 0)):
+        check_policy(*inputs(dev, 5, V, dtype, pad, shift, seed=slots))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(5000, 700), (3100, 4099), (2500, 9001), (1300, 20011), (700, 50003)])
+def test_many_rows(dev, T, V, dtype):
+    """Enough rows that a cluster takes several, masked ones among them; in place too."""
+    logits, y, old, adv, ref, w = inputs(dev, T, V, dtype, seed=T)
+    first = check_policy(logits, y, old, adv, ref, w)
+    tu.assert_logprobs(losses.token_logprobs(logits, y, w), tu.rows64(logits, y, w)[0])
+    off = lengths_to_offsets((T // 4, T // 2, 3, T // 8), dev)
+    check_preference(logits, y, off, ref, w, beta=0.001)
+    again = losses.policy_loss(logits, y, old, adv, ref, w, kl_coef=0.05, scale=1.0, grad=logits)
+    assert torch.equal(again.grad, first.grad) and torch.equal(again.stats, first.stats)
+
+
 @pytest.mark.parametrize("op", ["policy", "preference"])
 def test_gradient_against_differences(dev, op):
     """The kernel's gradient against central differences of the 64-bit loss along
