@@ -5,8 +5,9 @@
 // The tensors are cut into chunks of 32 KiB, numbered over all tensors, and every
 // block takes the same number of runs of consecutive chunks, whatever the tensors'
 // sizes.  Each block leaves one partial sum of squares; the clipping kernel's blocks
-// each add all partials, in the same order, and scale their chunks.  No
-// atomics: the bits of the norm depend on the sizes and the device alone.
+// each add all partials, in the same order, and scale their chunks; with many chunks
+// one block adds them and blocks of half a chunk scale.  No atomics: the bits of the
+// norm depend on the sizes and the device alone.
 //
 // Bound by HBM: the coefficient needs every element, so a gradient that does not
 // stay in L2 (129 MB) is read twice and written once.  The clipping kernel takes
@@ -128,7 +129,7 @@ __device__ __forceinline__ void for_chunks(const Table<CAP>& tab, F&& f) {
 // so a tensor may begin up to 127 bytes into its first one.  All whole slots are
 // loaded (zeros for the others) before any is used; a partial slot, where the
 // tensor begins or ends inside it, by elements.
-template <int DT>
+template <int DT, int K = kSlots>
 struct Chunk {
   static constexpr int N = Lanes<DT>::N;
   using E = typename ElemOf<DT>::T;
@@ -137,26 +138,27 @@ struct Chunk {
   int lead;                   // elements of its first line before it
   int lo, lim;                // slots lo .. lim - 1 of the chunk are whole
   int ends[2];                // partial slots: the first, the last (-1: none; the same one only once)
-  uint4 r[kSlots];
+  uint4 r[K];
 
+  // part: which K of a chunk's kSlots slots per thread
   template <bool HINTS>
-  __device__ __forceinline__ void load(const Tensor& t, unsigned int chunk, uint64_t policy) {
+  __device__ __forceinline__ void load(const Tensor& t, unsigned int chunk, uint64_t policy, int part = 0) {
     run = static_cast<const E*>(t.grad);
     count = (long long)t.count;
-    s0 = (long long)(chunk - t.first_chunk) * (kSlots * kThreads);
+    s0 = (long long)(chunk - t.first_chunk) * (kSlots * kThreads) + part * (K * kThreads);
     lead = (int)(((uintptr_t)run & 127) / sizeof(E));
     const long long full = (count + lead) / N - s0;
     lo = s0 == 0 ? (lead + N - 1) / N : 0;
-    lim = (int)min((long long)(kSlots * kThreads), full);
+    lim = (int)min((long long)(K * kThreads), full);
     ends[0] = s0 == 0 && lead % N ? lead / N : -1;
-    ends[1] = (count + lead) % N && full >= lo && full < kSlots * kThreads ? (int)full : -1;
+    ends[1] = (count + lead) % N && full >= lo && full < K * kThreads ? (int)full : -1;
     const uint4* src = reinterpret_cast<const uint4*>(run - lead) + s0 + threadIdx.x;
-    if (lo == 0 && lim == kSlots * kThreads) {
+    if (lo == 0 && lim == K * kThreads) {
 #pragma unroll
-      for (int k = 0; k < kSlots; ++k) r[k] = ld_hint<HINTS>(src + k * kThreads, policy);
+      for (int k = 0; k < K; ++k) r[k] = ld_hint<HINTS>(src + k * kThreads, policy);
     } else {
 #pragma unroll
-      for (int k = 0; k < kSlots; ++k) {
+      for (int k = 0; k < K; ++k) {
         const int q = k * kThreads + (int)threadIdx.x;
         r[k] = make_uint4(0, 0, 0, 0);
         if (q >= lo && q < lim) r[k] = ld_hint<HINTS>(src + k * kThreads, policy);
@@ -233,17 +235,17 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const float* partial, in
   if (threadIdx.x == 0) *norm = v;
 }
 
-template <int DT, bool HINTS>
-__device__ __forceinline__ void scale_chunk(const Tensor& t, unsigned int chunk, float coef, uint64_t policy) {
+template <int DT, bool HINTS, int K>
+__device__ __forceinline__ void scale_chunk(const Tensor& t, unsigned int chunk, float coef, uint64_t policy, int part = 0) {
   constexpr int N = Lanes<DT>::N;
   using E = typename ElemOf<DT>::T;
-  Chunk<DT> c;
-  c.template load<HINTS>(t, chunk, policy);
+  Chunk<DT, K> c;
+  c.template load<HINTS>(t, chunk, policy, part);
   E* const out = static_cast<E*>(t.out);
   const bool same = (((uintptr_t)t.grad ^ (uintptr_t)t.out) & 15) == 0;
   const float2 f = make_float2(coef, coef);
 #pragma unroll
-  for (int k = 0; k < kSlots; ++k) {
+  for (int k = 0; k < K; ++k) {
     const int q = k * kThreads + (int)threadIdx.x;
     if (q >= c.lo && q < c.lim) {
       Acc<DT> y = widen<DT>(c.r[k]);
@@ -282,9 +284,35 @@ scale_kernel(const __grid_constant__ Table<CAP> tab, const float* partial, int n
   const uint64_t policy = keep_policy(false);
   for_chunks<true>(tab, [&](const Tensor& t, unsigned int c) {
     if (coef == 1.0f && t.out == t.grad) return;  // in place and nothing to scale
-    if (t.dtype == kF32) scale_chunk<kF32, HINTS>(t, c, coef, policy);
-    else scale_chunk<kBF16, HINTS>(t, c, coef, policy);
+    if (t.dtype == kF32) scale_chunk<kF32, HINTS, kSlots>(t, c, coef, policy);
+    else scale_chunk<kBF16, HINTS, kSlots>(t, c, coef, policy);
   });
+}
+
+// The same from kPieceChunks (46 MB) on, after a kernel that joins the partial sums:
+// a block takes half a chunk and is gone, and the reads and writes of blocks that come
+// and go overlap better than those of resident ones (9.7 GB: 2191 -> 2034 us; 96 MB
+// 19.0 -> 17.5; 76 MB 17.0, the other way 17.6).
+constexpr unsigned long long kPieceChunks = 1400;
+template <int CAP, bool HINTS>
+__global__ void __launch_bounds__(kThreads, 6)
+scale_piece_kernel(const __grid_constant__ Table<CAP> tab, const float* norm, float max_norm, float eps) {
+  pdl_enter();
+  const float q = max_norm / (*norm + eps);
+  const float coef = q > 1.0f ? 1.0f : q;  // NaN stays NaN
+  const unsigned int c = tab.chunks - 1 - blockIdx.x / 2;
+  int i = 0;
+  for (int hi = tab.n; hi - i > 1;) {
+    const int mid = (i + hi) >> 1;
+    if (tab.t[mid].first_chunk <= c) i = mid;
+    else hi = mid;
+  }
+  const Tensor& t = tab.t[i];
+  if (coef == 1.0f && t.out == t.grad) return;  // in place and nothing to scale
+  const uint64_t policy = keep_policy(false);
+  const int part = 1 - (int)(blockIdx.x & 1);
+  if (t.dtype == kF32) scale_chunk<kF32, HINTS, kSlots / 2>(t, c, coef, policy, part);
+  else scale_chunk<kBF16, HINTS, kSlots / 2>(t, c, coef, policy, part);
 }
 
 // Tensors from i on until the table is full; returns the first that is not in it.
@@ -297,7 +325,7 @@ size_t fill(const GradsCall& c, size_t i, bool clip, Table<CAP>& tab) {
     // chunks of 32 KiB from the 128-byte line that the tensor begins in
     const unsigned long long bytes = ((uintptr_t)c.grads[i] & 127) + c.counts[i] * elem_bytes(c.dtypes[i]);
     const unsigned long long n = (bytes + kSlots * kThreads * 16 - 1) / (kSlots * kThreads * 16);
-    if (chunks + n > 0x7fffffffull) break;
+    if (chunks + n > 0x3fffffffull) break;
     tab.t[tab.n++] = Tensor{c.grads[i], !clip ? nullptr : c.outs ? c.outs[i] : const_cast<void*>(c.grads[i]),
                             c.counts[i], (unsigned int)chunks, c.dtypes[i]};
     chunks += n;
@@ -335,11 +363,14 @@ cudaError_t run(const GradsCall& c, bool clip) {
                                                         kMaxPartials / (unsigned)launches));
   Table<CAP> tab;
   int nparts = 0;
+  unsigned long long all_chunks = 0;
+  bool pieces = false;
   for (int pass = 0; pass < (clip ? 2 : 1); ++pass) {
     for (size_t i = 0; i < c.ntensors;) {
       const size_t next = fill(c, i, pass == 1, tab);
       if (tab.chunks) {
         const unsigned grid = plan_runs(tab, most, pass == 1);
+        if (pass == 0) all_chunks += tab.chunks;
         if (clip && launches == 1 && tab.chunks <= kHintChunks) tab.kept = std::min(tab.chunks, kKeptChunks);
         cudaError_t e;
         if (pass == 0) {
@@ -347,6 +378,9 @@ cudaError_t run(const GradsCall& c, bool clip) {
           e = launch_kernel(tab.kept ? square_sum_kernel<CAP, true> : square_sum_kernel<CAP, false>, grid, kThreads, 0,
                             c.stream, true, tab, partial + nparts);
           nparts += (int)grid;
+        } else if (pieces) {
+          e = launch_kernel(tab.kept ? scale_piece_kernel<CAP, true> : scale_piece_kernel<CAP, false>, 2 * tab.chunks,
+                            kThreads, 0, c.stream, true, tab, (const float*)c.norm, c.max_norm, c.eps);
         } else {
           e = launch_kernel(tab.kept ? scale_kernel<CAP, true> : scale_kernel<CAP, false>, grid, kThreads, 0, c.stream,
                             true, tab, (const float*)partial, nparts, c.max_norm, c.eps, c.norm);
@@ -357,8 +391,12 @@ cudaError_t run(const GradsCall& c, bool clip) {
       }
       i = next;
     }
-    if (pass == 0 && (!clip || nparts == 0))
-      return launch_kernel(norm_kernel, 1, kThreads, 0, c.stream, true, (const float*)partial, nparts, c.norm);
+    pieces = all_chunks >= kPieceChunks;
+    if (pass == 0 && (!clip || pieces || nparts == 0)) {
+      const cudaError_t e = launch_kernel(norm_kernel, 1, kThreads, 0, c.stream, true, (const float*)partial, nparts,
+                                          c.norm);
+      if (e != cudaSuccess || !clip || nparts == 0) return e;
+    }
   }
   return cudaSuccess;
 }
