@@ -11,7 +11,6 @@
 // Comments give times on one GB300 (152 SMs; a copy reaches 6.79 TB/s).
 #include <algorithm>
 #include <atomic>
-#include <climits>
 
 #include "ar_logits.cuh"
 #include "ar_train.h"
@@ -41,31 +40,29 @@ struct Matrix {
         target_bytes(c.target_bytes), weights(c.weights), logprobs(c.logprobs) {}
 };
 
-template <int DT, int THREADS>
+template <int DT>
 __device__ __forceinline__ MaxSum row_stats(const typename ElemOf<DT>::T* row, long long vocab, float2* sh) {
   const Slots<DT> in(row, vocab);
   MaxSum a;
   const long long n = in.count();
-  for (long long s = threadIdx.x; s < n; s += THREADS) {
+  for (long long s = threadIdx.x; s < n; s += kThreads) {
     float x[Lanes<DT>::N];
     in.load(s, x, -INFINITY);
     a.add(x);
   }
-  return block_join<THREADS>(a, sh);
+  return block_join<kThreads>(a, sh);
 }
 
-// grad[j] = c * ([j == y] - p[j]) in slots first, first + step, ... below end.  The
-// target's 1 - p is -expm1(log p).
+// grad[j] = c * ([j == y] - p[j]).  The target's 1 - p is -expm1(log p).
 template <int DT>
 __device__ __forceinline__ void row_grad(const typename ElemOf<DT>::T* row, typename ElemOf<DT>::T* grad,
-                                         long long vocab, long long y, float lp, MaxSum st, float c, long long first,
-                                         long long end, int step) {
+                                         long long vocab, long long y, float lp, MaxSum st, float c) {
   constexpr int N = Lanes<DT>::N;
   const Slots<DT> in(row, vocab);
   const bool same = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
   const float f = -c / st.s;
-  const long long n = min(in.count(), end);
-  for (long long s = first; s < n; s += step) {
+  const long long n = in.count();
+  for (long long s = threadIdx.x; s < n; s += kThreads) {
     float x[N];
     in.load(s, x, -INFINITY);
     const long long j = in.first(s);
@@ -82,18 +79,6 @@ __device__ __forceinline__ void row_zero(typename ElemOf<DT>::T* grad, long long
   const float zero[Lanes<DT>::N] = {};
   for (long long s = threadIdx.x; s < n; s += kThreads) store_slot<DT>(out, grad, true, s, zero);
 }
-
-// ---------------------------------------------------- statistics in powers of 2
-//
-// b = m log2 e and the sum of e^x / 2^b = 2^(x log2 e - b): one fused multiply-add
-// and one exponential per element.  |m| is held to 1e38, so that b is finite (masks
-// of the type's lowest value are beyond it).  Where that matters, the row's sum ends
-// at 0, infinity or NaN, and the row is gone over again with MaxSum, which forms
-// the differences first.
-constexpr float kHuge = 1e38f, kLn2 = 0.6931471805599453f;
-
-__device__ __forceinline__ float base_of(float m) { return fminf(fmaxf(m, -kHuge), kHuge) * kLog2e; }
-__device__ __forceinline__ bool usable(float sum) { return sum > 0.0f && sum < INFINITY; }
 
 template <int DT>
 __device__ __forceinline__ float max_of(uint4 r) {
@@ -126,13 +111,18 @@ __device__ __forceinline__ float max_of(const uint4 (&r)[K]) {
   }
 }
 
-// 2^(x log2 e - b) of a pair
-__device__ __forceinline__ float2 exp2_pair(float x, float y, float2 minus_b) {
-  float2 z = fma2(make_float2(x, y), make_float2(kLog2e, kLog2e), minus_b);
+// e^(x - m) of a pair.  The difference is formed first (for most logits it is
+// exact, and 0 at the maximum), then scaled: a multiply-add would save half an
+// instruction per element, but round the largest terms, and lowest * log2(e) is
+// -infinity.
+__device__ __forceinline__ float2 exp_pair(float x, float y, float2 minus_m) {
+  float2 z = mul2(add2(make_float2(x, y), minus_m), make_float2(kLog2e, kLog2e));
   z.x = ex2(z.x);
   z.y = ex2(z.y);
   return z;
 }
+
+__device__ __forceinline__ float2 minus(float2 a) { return make_float2(-a.x, -a.y); }
 
 __device__ __forceinline__ uint4 no_logits(int dtype) {  // a slot of -infinity
   const uint32_t v = dtype == kBF16 ? 0xff80ff80u : 0xff800000u;
@@ -159,18 +149,22 @@ struct Slice {
 
 // ----------------------------------------------------------- log-probabilities
 
-// What the gradient of a row needs: p = 2^(x log2 e - b) / s, or, s < 0 (a row that
-// was gone over again), e^(x - b) / -s.
-__device__ __forceinline__ float2 pack_stats(float b, float s, bool natural) { return make_float2(b, natural ? -s : s); }
-
-// Log-probability of every row's target; stats != NULL: its statistics too, and 0
-// into factors[t], for the preference loss.
+// Log-probability of every row's target; stats != NULL: {maximum, sum of e^(x -
+// maximum)} too, and 0 into factors[t], for the preference loss.
 //
-// One pass with a running base, four slots per thread on the way while four are
+// One pass with a running maximum, four slots per thread on the way while four are
 // worked on.  GROUP threads take a row: a warp (eight rows in a block) where there
 // are many rows, else the block; with few long rows, a cluster of C blocks.
 // Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 154 us, 7.0 TB/s (reads alone are
 // faster than the copy); one row of 32768 3.0 us.
+// The lanes' pairs (m, rest), each (1 + rest) e^m, as one; in every lane.
+__device__ __forceinline__ float2 warp_rest(float2 v) {
+  const float M = warp_max(v.x);
+  const int first = __ffs(__ballot_sync(~0u, v.x == M)) - 1;  // its 1 is the pair's, all the others are rest
+  const float part = (int)(threadIdx.x & 31) == first ? v.y : (1.0f + v.y) * exp_diff(v.x, M);
+  return make_float2(M, warp_sum(part));
+}
+
 struct LogprobPlan {
   int C, per;  // blocks per row; slots per block
 };
@@ -213,13 +207,13 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
       }
     }
   };
-  float m = -FLT_MAX, b = base_of(m);
-  float2 s2 = make_float2(0.0f, 0.0f);
+  float m = -FLT_MAX;                              // never -infinity: differences from it have to exist
+  float2 s2 = make_float2(0.0f, 0.0f), lost = s2;
   const auto grow = [&](float top) {
-    m = fmaxf(m, top);
-    const float to = base_of(m), f = ex2(b - to);
+    const float to = fmaxf(m, top), f = exp_diff(m, to);
     s2 = mul2(s2, make_float2(f, f));
-    b = to;
+    lost = mul2(lost, make_float2(f, f));
+    m = to;
   };
   uint4 r[U], next[U] = {};
   load(0, r);
@@ -236,68 +230,50 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
       for (int x = 0; x < N; ++x) top = fmaxf(top, v[x]);
       grow(top);
 #pragma unroll
-      for (int x = 0; x < N; ++x) s2.x += ex2(fmaf(v[x], kLog2e, -b));
+      for (int x = 0; x < N; ++x) s2.x += exp_diff(v[x], m);
     }
   }
   for (int at = 0; at < in.lim; at += U * GROUP) {
     if (at + U * GROUP < in.lim) load(at + U * GROUP, next);
     grow(max_of<DT>(r));
-    const float2 minus_b = make_float2(-b, -b);
+    const float2 minus_m = make_float2(-m, -m);
+    float2 part[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const Acc<DT> x = widen<DT>(r[u]);
-      float2 part = exp2_pair(x.v[0], x.v[1], minus_b);  // a slot is added up first: short chains of roundings
+      part[u] = exp_pair(x.v[0], x.v[1], minus_m);
 #pragma unroll
-      for (int c = 2; c < N; c += 2) part = add2(part, exp2_pair(x.v[c], x.v[c + 1], minus_b));
-      s2 = add2(s2, part);
+      for (int c = 2; c < N; c += 2) part[u] = add2(part[u], exp_pair(x.v[c], x.v[c + 1], minus_m));
       r[u] = next[u];
     }
+    // where the maximum is among the terms, every addition to its 1 rounds: four slots are added up first, and what
+    // that addition loses is carried over to the next
+    const float2 add = add2(add2(add2(part[0], part[1]), add2(part[2], part[3])), lost);
+    const float2 sum = add2(s2, add);
+    lost = add2(add, minus(add2(sum, minus(s2))));
+    s2 = sum;
   }
-  // joined: warp, block, cluster
-  float B = warp_max(b), S = warp_sum((s2.x + s2.y) * ex2(b - B));
+  // Joined: threads, warps, blocks, as pairs (m, rest) that stand for (1 + rest) e^m: for a near-certain token the sum
+  // is 1 and a little, and the little is its log-probability.
+  const bool swap = s2.y > s2.x;                   // not fmaxf: a NaN has to stay
+  const float more = swap ? s2.y : s2.x, less = (swap ? s2.x : s2.y) + (lost.x + lost.y);
+  float2 v = make_float2(m, (more - 1.0f) + less);
+  v = warp_rest(v);
   if constexpr (GROUP == kThreads) {
-    if (lane == 0) sh[threadIdx.x >> 5] = make_float2(B, S);
+    if (lane == 0) sh[threadIdx.x >> 5] = v;
     __syncthreads();
-    const float2 v = lane < W ? sh[lane] : make_float2(-FLT_MAX, 0.0f);
-    B = warp_max(v.x);
-    S = warp_sum(v.y * ex2(v.x - B));
+    v = warp_rest(lane < W ? sh[lane] : make_float2(-FLT_MAX, -1.0f));
     if (plan.C > 1) {
-      if (threadIdx.x == 0) mine = make_float2(B, S);
+      if (threadIdx.x == 0) mine = v;
       cluster_sync();
-      const float2 v2 = lane < plan.C ? ld_cluster(cluster_address((uint32_t)__cvta_generic_to_shared(&mine), lane))
-                                      : make_float2(-FLT_MAX, 0.0f);
-      B = warp_max(v2.x);
-      S = warp_sum(v2.y * ex2(v2.x - B));
+      v = warp_rest(lane < plan.C ? ld_cluster(cluster_address((uint32_t)__cvta_generic_to_shared(&mine), lane))
+                                  : make_float2(-FLT_MAX, -1.0f));
       cluster_meet();                              // nobody leaves before the others have read
     }
   }
-  float x = 0.0f;
-  if (writer) x = y >= 0 && y < V ? to_float(row[y]) : __int_as_float(0x7fffffff);
-  if (usable(S)) {
-    if (writer) {
-      a.logprobs[t] = (fmaf(x, kLog2e, -B) - log2f(S)) * kLn2;
-      if (stats) stats[t] = pack_stats(B, S, false);
-    }
-    return;
-  }
-  if (rank != 0) return;
-  MaxSum st;
-  const Slots<DT> all(row, V);
-  for (long long s = tid; s < all.count(); s += GROUP) {
-    float v[N];
-    all.load(s, v, -INFINITY);
-    st.add(v);
-  }
-  if constexpr (GROUP == kThreads) {
-    __syncthreads();                               // sh is free again
-    st = block_join<kThreads>(st, sh);
-  } else {
-#pragma unroll
-    for (int d = 16; d; d >>= 1) st.join(__shfl_xor_sync(~0u, st.m, d), __shfl_xor_sync(~0u, st.s, d));
-  }
   if (writer) {
-    a.logprobs[t] = (x - st.m) - logf(st.s);
-    if (stats) stats[t] = pack_stats(st.m, st.s, true);
+    a.logprobs[t] = y >= 0 && y < V ? (to_float(row[y]) - v.x) - log1pf(v.y) : __int_as_float(0x7fffffff);
+    if (stats) stats[t] = make_float2(v.x, 1.0f + v.y);
   }
 }
 
@@ -322,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, co
     }
     const typename ElemOf<DT>::T* row = a.logits + t * a.stride;
     const long long y = load_index(a.targets, a.target_bytes, t);
-    const MaxSum st = row_stats<DT, kThreads>(row, (long long)a.vocab, sh);
+    const MaxSum st = row_stats<DT>(row, (long long)a.vocab, sh);
     if (threadIdx.x == 0) {
       const float lp = target_logprob(row, (long long)a.vocab, y, st.m, st.s);
       a.logprobs[t] = lp;
@@ -331,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, co
       sh_c[1] = lp;
     }
     __syncthreads();  // also: the target's logit is read before an in-place gradient is written
-    row_grad<DT>(row, grad, (long long)a.vocab, y, sh_c[1], st, sh_c[0], threadIdx.x, LLONG_MAX, kThreads);
+    row_grad<DT>(row, grad, (long long)a.vocab, y, sh_c[1], st, sh_c[0]);
     __syncthreads();
   }
   if (threadIdx.x == 0) partial[blockIdx.x] = make_float4(sum.loss, sum.kl, sum.clipped, sum.weight);
@@ -367,13 +343,12 @@ template <int DT, int THREADS, int K, int BLOCKS, bool CLUSTER>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
 policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, float4* partial) {
   constexpr int N = Lanes<DT>::N, W = THREADS / 32;
-  constexpr bool kEachWarp = !CLUSTER && W <= 2;  // every warp computes the token's loss for itself
+  constexpr bool kEachWarp = !CLUSTER && W <= 4;  // every warp computes the token's loss for itself
   using E = typename ElemOf<DT>::T;
   extern __shared__ uint4 next[];                   // [K][THREADS]: the row that is on its way
-  // (base, sum) of every warp, by parity: a block may be one row ahead
+  // (maximum, sum) of every warp, by parity: a block may be one row ahead
   __shared__ float2 pairs[2][(CLUSTER ? kMaxCluster : 1) * W];
   __shared__ float4 result;
-  __shared__ float2 shared_c, again_sh[W];
   __shared__ uint64_t bars[2];
   pdl_enter();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -489,54 +464,53 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     uint4 r[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) r[k] = ld_shared16(mine + k * THREADS * 16);
-    const float base = base_of(warp_max(max_of<DT>(r)));
+    const float m = fmaxf(warp_max(max_of<DT>(r)), -FLT_MAX);
 
-    float2 s2 = make_float2(0.0f, 0.0f);
-    const float2 minus_b = make_float2(-base, -base);
+    float2 s2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};  // short chains of roundings
+    const float2 minus_m = make_float2(-m, -m);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const Acc<DT> x = widen<DT>(r[k]);
+      float2 part;
 #pragma unroll
       for (int c = 0; c < N; c += 2) {
-        const float2 z = exp2_pair(x.v[c], x.v[c + 1], minus_b);
-        s2 = add2(s2, z);
+        const float2 z = exp_pair(x.v[c], x.v[c + 1], minus_m);
+        part = c == 0 ? z : add2(part, z);
         if constexpr (DT == kF32) {  // the exponentials fit where the logits were
           if (c == 0) { r[k].x = __float_as_uint(z.x); r[k].y = __float_as_uint(z.y); }
           else { r[k].z = __float_as_uint(z.x); r[k].w = __float_as_uint(z.y); }
         }
       }
+      s2[k & 1] = add2(s2[k & 1], part);
     }
-    const float ws = warp_sum(s2.x + s2.y);
+    const float ws = warp_sum((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y));
     // Once all pairs are there, gradients may overwrite the row (in place): not before this warp's targets' logits
     // have arrived in their register.
     const uint32_t zero = __float_as_uint(x_l) & plan.zero;
     if constexpr (CLUSTER) {
-      if (lane < C) st_async(pair_to + b * (kMaxCluster * W * 8) + zero, make_float2(base, ws), bars_to + 8 * b);
+      if (lane < C) st_async(pair_to + b * (kMaxCluster * W * 8) + zero, make_float2(m, ws), bars_to + 8 * b);
     } else {
-      if (lane == 0) pairs[b][warp + zero] = make_float2(base, ws);
+      if (lane == 0) pairs[b][warp + zero] = make_float2(m, ws);
     }
     issue(i + 1);
 
     // the token's loss and what the gradient needs of it
     float4 res = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const auto token = [&](float lp, float base, float S) {
-      const float c = policy_token(p, __shfl_sync(~0u, old_l, i), __shfl_sync(~0u, adv_l, i),
-                                   __shfl_sync(~0u, ref_l, i), __shfl_sync(~0u, w_l, i), lp, sum);
-      res = make_float4(base, -c / S, -c, lp);
-      if (rank == 0 && tid == 0) a.logprobs[row0 + i] = lp;
-    };
     if constexpr (!CLUSTER) __syncthreads();
     if (kEachWarp || warp == 0) {
-      // the row's base B and sum S
+      // the row's maximum M and sum S
       const bool ok = !CLUSTER || mbar_wait(bars_at + 8 * b, done >> 1 & 1, kWaitLimit);
-      float B = -FLT_MAX, S = 0.0f;
-      for (int q = lane; q < C * W; q += 32) B = fmaxf(B, pairs[b][q].x);
-      B = warp_max(B);
-      for (int q = lane; q < C * W; q += 32) S += pairs[b][q].y * ex2(pairs[b][q].x - B);
+      float M = -FLT_MAX, S = 0.0f;
+      for (int q = lane; q < C * W; q += 32) M = fmaxf(M, pairs[b][q].x);
+      M = warp_max(M);
+      for (int q = lane; q < C * W; q += 32) S += pairs[b][q].y * exp_diff(pairs[b][q].x, M);
       S = warp_sum(S);
       if (!ok) S = __int_as_float(0x7fffffff);
-      if (!ok || usable(S)) token((fmaf(__shfl_sync(~0u, x_l, i), kLog2e, -B) - log2f(S)) * kLn2, B, S);
-      else res.x = INFINITY;
+      const float lp = (__shfl_sync(~0u, x_l, i) - M) - logf(S);
+      const float c = policy_token(p, __shfl_sync(~0u, old_l, i), __shfl_sync(~0u, adv_l, i),
+                                   __shfl_sync(~0u, ref_l, i), __shfl_sync(~0u, w_l, i), lp, sum);
+      res = make_float4(M, -c / S, -c, lp);
+      if (rank == 0 && tid == 0) a.logprobs[row0 + i] = lp;
       if (!kEachWarp && lane == 0) result = res;
     }
     if constexpr (!kEachWarp) {
@@ -544,31 +518,16 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       res = result;
     }
     ++done;
-    // Where registers are short the slice is computed once more, not kept (2000 x 30000 fp32 95 -> 86 us; in bf16
-    // it costs more than it frees, 4096 x 32768 93 -> 98).
+    // Where registers are shortest the slice is computed once more, not kept (4096 x 32768 bf16 94 -> 92 us, 2000 x
+    // 30000 fp32 92 -> 85; with 7 slots per thread it costs more than it frees, 2489 x 50001 bf16 101 -> 107).
     int again = i;
-    if constexpr (DT == kF32 && CLUSTER) asm volatile("" : "+r"(again));
+    if constexpr (K == 8 && THREADS == 256) asm volatile("" : "+r"(again));
     const Slice<DT> in(logits + again * a.stride, V, s0, plan.per);
     E* const grad = a.grad + (row0 + again) * a.grad_stride;
-    if (res.x == INFINITY) {
-      // no finite sum: values beyond 1e38 (masks of the type's lowest value all over the row, say) or a row without
-      // a distribution.  Every block goes over the whole row once more, with differences formed first.
-      const MaxSum st = row_stats<DT, THREADS>(in.row, V, again_sh);
-      if constexpr (CLUSTER) cluster_sync();  // nobody reads the row any more
-      if (kEachWarp || warp == 0) {
-        token((__shfl_sync(~0u, x_l, i) - st.m) - logf(st.s), st.m, st.s);
-        if (lane == 0) shared_c = make_float2(-res.z, res.w);  // the same from every warp
-      }
-      __syncthreads();
-      row_grad<DT>(in.row, grad, V, __shfl_sync(~0u, y_l, i), shared_c.y, st, shared_c.x, s0 + tid, s0 + plan.per,
-                   THREADS);
-      continue;
-    }
-
-    // fp32: the exponentials, to the warp's base; bf16: the logits, whose exponentials are taken again (half the
-    // registers, so that more rows are on the SM at a time), to the row's base
-    const float f = DT == kF32 ? res.y * ex2(base - res.x) : res.y;
-    const float2 f2 = make_float2(f, f), minus_B = make_float2(-res.x, -res.x);
+    // fp32: the exponentials, to the warp's maximum; bf16: the logits, whose exponentials are taken again (half the
+    // registers, so that more rows are on the SM at a time), to the row's
+    const float f = DT == kF32 ? res.y * exp_diff(m, res.x) : res.y;
+    const float2 f2 = make_float2(f, f), minus_M = make_float2(-res.x, -res.x);
     if constexpr (DT == kBF16)  // unpacked again, not kept unpacked
 #pragma unroll
       for (int k = 0; k < K; ++k) asm volatile("" : "+r"(r[k].x), "+r"(r[k].y), "+r"(r[k].z), "+r"(r[k].w));
@@ -577,7 +536,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
 #pragma unroll
       for (int x = 0; x < N; x += 2) {
         float2 v = make_float2(g.v[x], g.v[x + 1]);
-        if constexpr (DT == kBF16) v = exp2_pair(v.x, v.y, minus_B);
+        if constexpr (DT == kBF16) v = exp_pair(v.x, v.y, minus_M);
         v = mul2(v, f2);
         g.v[x] = v.x;
         g.v[x + 1] = v.y;
@@ -744,11 +703,11 @@ __global__ void __launch_bounds__(kThreads, 6) preference_grad_kernel(const Matr
     if (q >= in.lo && q < in.lim) r[k] = ld_row(src + k * kThreads);
   }
   const float2 st = stats[t];
-  const bool natural = st.y < 0.0f, same = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
-  const float f = -c / fabsf(st.y);
-  const float2 minus_b = make_float2(-st.x, -st.x), f2 = make_float2(f, f);
+  const bool same = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
+  const float f = -c / st.y;
+  const float2 minus_m = make_float2(-st.x, -st.x), f2 = make_float2(f, f);
   uint4* dst = reinterpret_cast<uint4*>(grad - in.lead) + s0 + tid;
-  if (same && !natural) {
+  if (same) {
 #pragma unroll
     for (int k = 0; k < kGradSlots; ++k) {
       const int q = k * kThreads + tid;
@@ -756,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 6) preference_grad_kernel(const Matr
         Acc<DT> g = widen<DT>(r[k]);
 #pragma unroll
         for (int x = 0; x < N; x += 2) {
-          const float2 v = mul2(exp2_pair(g.v[x], g.v[x + 1], minus_b), f2);
+          const float2 v = mul2(exp_pair(g.v[x], g.v[x + 1], minus_m), f2);
           g.v[x] = v.x;
           g.v[x + 1] = v.y;
         }
@@ -764,18 +723,18 @@ __global__ void __launch_bounds__(kThreads, 6) preference_grad_kernel(const Matr
       }
     }
   }
-  // slots at the row's ends, and all of them in the rarer layouts and rows: by elements
+  // slots at the row's ends, and all of them where the gradient's rows start at another alignment: by elements
   const int end = (V + in.lead + N - 1) / N - s0;
 #pragma unroll 1
   for (int q = tid; q < kPiece && q < end; q += kThreads) {
-    if (same && !natural && q >= in.lo && q < in.lim) continue;
+    if (same && q >= in.lo && q < in.lim) continue;
     const int j = (s0 + q) * N - in.lead;
     float x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = j + i >= 0 && j + i < V ? to_float(row[j + i]) : -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float g = f * (natural ? exp_diff(x[i], st.x) : ex2(fmaf(x[i], kLog2e, -st.x)));
+      const float g = f * exp_diff(x[i], st.x);
       if (j + i >= 0 && j + i < V) from_float(grad + j + i, g);
     }
   }
