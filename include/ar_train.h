@@ -17,7 +17,9 @@
  * graph.  Kernels are launched with programmatic dependent launch, as the
  * all-reduce's are (ar.h, "Launch order"): stream order holds.
  * Results do not depend on timing: there are no floating-point atomics, and a
- * call repeated on the same device gives the same bits.
+ * call repeated on the same device gives the same bits.  (The one wait inside a
+ * kernel, of a cluster's blocks for one another, is bounded; a row whose wait ran
+ * out would give NaN.)
  *
  * Logits.  A matrix of `rows` tokens by `vocab` columns, AR_FLOAT32 or
  * AR_BFLOAT16; row t starts at logits + t * row_stride elements
@@ -144,9 +146,9 @@ ar_status_t ar_grad_norm(size_t ntensors, const void* const* grads, const size_t
 /*
  * Clipping by the global norm: norm as above, coef = min(1, max_norm /
  * (norm + eps)), outs[i] = grads[i] * coef rounded once to the tensor's type.
- *   outs     host array of device pointers; outs[i] may equal grads[i], any
- *            other overlap of an output with a gradient or another output is
- *            the caller's error (it is not checked).  NULL: in place for all
+ *   outs     host array of device pointers; outs[i] may equal grads[i], a part
+ *            of it is rejected; an overlap with another tensor or output is the
+ *            caller's error (it is not checked).  NULL: in place for all
  * With coef == 1 an output in place is left untouched.  An infinite norm
  * gives coef 0 and a NaN norm coef NaN, and the products follow (0 * infinity
  * is NaN).  max_norm and eps must be >= 0.
