@@ -29,8 +29,11 @@ class GradClipper:
 
     The list is checked and its addresses are laid out once; every call reads
     the gradients anew.  Calls of one clipper share a workspace of 32 KiB: they
-    may be on any stream but must not overlap on the GPU.
+    may be on any stream but must not overlap on the GPU.  A captured call needs
+    its clipper, like its gradients, for as long as it is replayed.
     """
+
+    NORMS = 128   # results handed out of one block; each is written by one call only
 
     def __init__(self, grads, out=None):
         what = "GradClipper"
@@ -77,6 +80,7 @@ class GradClipper:
             self._home = torch.cuda.current_stream().cuda_stream
             self._workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         self._at = self._workspace.data_ptr()
+        self._norms, self._next = None, self.NORMS
 
     def _begin(self, what: str, stream):
         """(stream handle, a new 0-dim norm): both belong to the call's stream."""
@@ -84,12 +88,16 @@ class GradClipper:
             raise ArError(AR_ERR_INVALID_ARG, f"{what}: gradients are on {self.device}, the current device is "
                                               f"cuda:{torch.cuda.current_device()}")
         handle = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else _stream_handle(stream)
-        if handle != self._home or stream is not None:
+        if handle != self._home:
             s = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
             self._workspace.record_stream(s)
             with torch.cuda.stream(s):
                 return handle, torch.empty((), dtype=torch.float32, device=self.device)
-        return handle, torch.empty((), dtype=torch.float32, device=self.device)
+        if self._next == self.NORMS:
+            self._norms = torch.empty(self.NORMS, dtype=torch.float32, device=self.device)
+            self._next = 0
+        self._next += 1
+        return handle, self._norms[self._next - 1]
 
     def norm(self, stream=None):
         """The global norm, a 0-dim float32 tensor."""

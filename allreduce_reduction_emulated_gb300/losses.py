@@ -17,8 +17,10 @@ logits        (tokens, vocab) float32 or bfloat16 CUDA tensor on the current
 targets       (tokens,) int64 or int32
 per-token     (tokens,) contiguous float32: weights, old_logprobs, ...
 grad          where the gradient goes: a tensor of the logits' shape and type, or
-              the logits themselves (in place); None allocates one with the logits'
-              row stride
+              the logits themselves (in place); None allocates one whose rows start
+              at the logits' alignments (for padded or odd layouts it may have a few
+              elements between its rows).  A gradient given at other alignments is
+              written element by element, which is slower
 stream        a torch stream or a cudaStream_t (default: the current stream)
 
 Nothing waits for the GPU and nothing is kept between calls.
@@ -88,8 +90,8 @@ def _indices(what: str, name: str, x, device: int, count: int):
 
 
 def _gradient(what: str, logits, grad, device: int, rows: int, vocab: int):
-    """(tensor for the gradient, its row stride); None makes one whose rows are
-    laid out like the logits', so that both start at the same alignments."""
+    """The tensor for the gradient; None makes one whose rows start at the logits'
+    alignments within 16 bytes (then both are read and written in whole vectors)."""
     if grad is None:
         return torch.empty_like(logits) if logits.is_contiguous() else _like_rows(logits, rows, vocab)
     if grad is not logits:
@@ -100,10 +102,13 @@ def _gradient(what: str, logits, grad, device: int, rows: int, vocab: int):
 
 
 def _like_rows(logits, rows: int, vocab: int):
-    """A new matrix with the logits' row stride (a padded one cut to `vocab`
-    columns), starting at the same alignment within 16 bytes."""
-    stride = logits.stride(0) if rows > 1 else vocab
-    lead = logits.data_ptr() % 16 // logits.element_size()
+    """A new matrix whose rows start at the logits' alignments: contiguous, or with
+    less than 16 bytes between the rows."""
+    size = logits.element_size()
+    lead = logits.data_ptr() % 16 // size
+    stride = vocab + ((logits.stride(0) - vocab) % (16 // size) if rows > 1 else 0)
+    if lead == 0 and stride == vocab:
+        return torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
     flat = torch.empty(lead + rows * stride, dtype=logits.dtype, device=logits.device)
     return flat.as_strided((rows, vocab), (stride, 1), lead)
 

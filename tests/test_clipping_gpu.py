@@ -179,6 +179,20 @@ def test_streams_repeats_and_graphs(dev):
     assert torch.equal(m, n) and all(torch.equal(a, b) for a, b in zip(outs, got))
 
 
+def test_every_call_has_its_own_norm(dev):
+    """More calls than one block of results: earlier results stay."""
+    g = make(dev, [5000], [torch.float32], 4)
+    c = GradClipper(g, out=[torch.empty_like(g[0])])
+    first = c.norm()
+    kept = []
+    for k in range(2 * GradClipper.NORMS + 3):
+        kept.append(c.norm())
+        g[0].mul_(1.01)
+    want = float(first)
+    for k, n in enumerate(kept):
+        assert abs(float(n) - want * 1.01 ** k) <= 1e-4 * want * 1.01 ** k
+
+
 def test_clips_again_what_it_clipped(dev):
     """In place, call after call with no host wait: the norm reaches the bound."""
     g = make(dev, [100_000, 33], BOTH, 2)

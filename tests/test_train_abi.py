@@ -148,6 +148,17 @@ def test_binding_checks_layouts(lib, monkeypatch):
     assert losses._gradient("x", x, x, 0, 4, 8) is x
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab,pad,shift", [(24, 0, 1), (24, 8, 0), (24, 5, 0), (25, 3, 2), (9, 40, 7), (1, 1, 0)])
+def test_a_new_gradient_has_the_logits_alignments(dtype, vocab, pad, shift):
+    whole = torch.zeros(6, vocab + pad + shift, dtype=dtype)
+    x = whole[:, shift:shift + vocab]
+    g = losses._like_rows(x, 6, vocab)
+    assert g.shape == x.shape and g.dtype == dtype and g.stride(1) == 1 and vocab <= g.stride(0) < vocab + 8
+    for t in range(6):
+        assert (g[t].data_ptr() - x[t].data_ptr()) % 16 == 0
+
+
 class CudaLike:
     """A stand-in for a CUDA tensor (a CPU tensor's memory)."""
 
