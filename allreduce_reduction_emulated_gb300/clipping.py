@@ -15,6 +15,7 @@ import torch
 from . import (AR_BFLOAT16, AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED, AR_FLOAT32, AR_SUCCESS, ArError, _stream_handle,
                library)
 
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 _DTYPES = {torch.float32: AR_FLOAT32, torch.bfloat16: AR_BFLOAT16}
 
 
@@ -84,9 +85,9 @@ class GradClipper:
 
     def _begin(self, what: str, stream):
         """(stream handle, a new 0-dim norm): both belong to the call's stream."""
-        if torch.cuda.current_device() != self._index:
+        if _current_device() != self._index:
             raise ArError(AR_ERR_INVALID_ARG, f"{what}: gradients are on {self.device}, the current device is "
-                                              f"cuda:{torch.cuda.current_device()}")
+                                              f"cuda:{_current_device()}")
         handle = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else _stream_handle(stream)
         if handle != self._home:
             s = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()

@@ -27,15 +27,13 @@ Nothing waits for the GPU and nothing is kept between calls.
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import AR_BFLOAT16, AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED, AR_FLOAT32, AR_SUCCESS, ArError, library
 
 _DTYPES = {torch.float32: AR_FLOAT32, torch.bfloat16: AR_BFLOAT16}
 _INDEX_BYTES = {torch.int64: 8, torch.int32: 4}
-_HERE = contextlib.nullcontext()
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _bad(what: str, why: str, status: int = AR_ERR_INVALID_ARG) -> ArError:
@@ -51,8 +49,8 @@ def _matrix(what: str, name: str, x):
     device = x.get_device()
     if device < 0:
         raise _bad(what, f"{name} is not in CUDA memory")
-    if device != torch.cuda.current_device():
-        raise _bad(what, f"{name} is on cuda:{device}, the current device is cuda:{torch.cuda.current_device()}")
+    if device != _current_device():
+        raise _bad(what, f"{name} is on cuda:{device}, the current device is cuda:{_current_device()}")
     rows, vocab = x.shape
     if rows and not vocab:
         raise _bad(what, f"{name} has no columns")
@@ -113,11 +111,21 @@ def _like_rows(logits, rows: int, vocab: int):
     return flat.as_strided((rows, vocab), (stride, 1), lead)
 
 
-def _on(device: int, stream):
-    """(the context in which outputs are allocated, the stream's handle).  What
-    is allocated for a stream has to come from that stream's memory pool."""
+def _outputs(what: str, logits, grad, device: int, rows: int, vocab: int, floats: int, stream):
+    """(gradient, float buffer, stream handle)"""
     if stream is None:
-        return _HERE, torch._C._cuda_getCurrentRawStream(device)
+        return (_gradient(what, logits, grad, device, rows, vocab),
+                torch.empty(floats, dtype=torch.float32, device=logits.device),
+                torch._C._cuda_getCurrentRawStream(device))
+    context, handle = _on(stream)
+    with context:
+        return (_gradient(what, logits, grad, device, rows, vocab),
+                torch.empty(floats, dtype=torch.float32, device=logits.device), handle)
+
+
+def _on(stream):
+    """(the context in which a given stream's outputs are allocated, its handle):
+    what is allocated for a stream has to come from that stream's memory pool."""
     if isinstance(stream, int):
         s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
         return torch.cuda.stream(s), stream
@@ -141,9 +149,14 @@ def token_logprobs(logits, targets, weights=None, out=None, stream=None):
     device, rows, vocab, stride = _matrix(what, "logits", logits)
     y, size = _indices(what, "targets", targets, device, rows)
     w = None if weights is None else _vector(what, "weights", weights, device, rows)
-    context, handle = _on(device, stream)
-    if out is None:
-        with context:
+    if stream is not None:
+        context, handle = _on(stream)
+        if out is None:
+            with context:
+                out = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    else:
+        handle = torch._C._cuda_getCurrentRawStream(device)
+        if out is None:
             out = torch.empty(rows, dtype=torch.float32, device=logits.device)
     to = _vector(what, "out", out, device, rows)
     _check(library().ar_token_logprobs(logits.data_ptr(), rows, vocab, stride, _DTYPES[logits.dtype], y, size, w,
@@ -190,10 +203,7 @@ def policy_loss(logits, targets, old_logprobs, advantages, ref_logprobs=None, we
     lib = library()
     bytes_ = lib.ar_policy_loss_workspace(rows)
     after = 4 + _whole(rows)                       # floats before the workspace: the statistics, logprobs
-    context, handle = _on(device, stream)
-    with context:
-        grad = _gradient(what, logits, grad, device, rows, vocab)
-        buffer = torch.empty(after + bytes_ // 4, dtype=torch.float32, device=logits.device)
+    grad, buffer, handle = _outputs(what, logits, grad, device, rows, vocab, after + bytes_ // 4, stream)
     at = buffer.data_ptr()
     _check(lib.ar_policy_loss(logits.data_ptr(), rows, vocab, stride, _DTYPES[logits.dtype], y, size, w, old, adv, ref,
                               clip_low, clip_high, kl_coef, scale, grad.data_ptr(),
@@ -247,10 +257,7 @@ def preference_loss(logits, targets, offsets, ref_logprobs=None, weights=None, b
     bytes_ = lib.ar_preference_loss_workspace(rows, pairs)
     first = 4 + _whole(pairs)                      # floats before logprobs: the loss, the margins
     after = first + _whole(rows)
-    context, handle = _on(device, stream)
-    with context:
-        grad = _gradient(what, logits, grad, device, rows, vocab)
-        buffer = torch.empty(after + bytes_ // 4, dtype=torch.float32, device=logits.device)
+    grad, buffer, handle = _outputs(what, logits, grad, device, rows, vocab, after + bytes_ // 4, stream)
     at = buffer.data_ptr()
     _check(lib.ar_preference_loss(logits.data_ptr(), rows, vocab, stride, _DTYPES[logits.dtype], y, size, w, off,
                                   off_size, pairs, ref, beta, label_smoothing, scale, grad.data_ptr(),

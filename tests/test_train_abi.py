@@ -124,7 +124,7 @@ class OnGpu(torch.Tensor):
 
 
 def test_binding_checks_layouts(lib, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(losses, "_current_device", lambda: 0)
     g = OnGpu.of
     x, y, v = g(torch.zeros(4, 8)), g(torch.zeros(4, dtype=torch.int64)), g(torch.zeros(4))
     off = g(torch.tensor([0, 2, 4]))
