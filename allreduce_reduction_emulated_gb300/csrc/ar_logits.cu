@@ -129,19 +129,23 @@ __device__ __forceinline__ uint4 no_logits(int dtype) {  // a slot of -infinity
   return make_uint4(v, v, v, v);
 }
 
-// A row's slice in one block, all the same in every thread: slots lo .. lim - 1
-// of the slice lie wholly in the row (lo is 1 where slot 0 begins before it), slot
-// `tail` (or none, -1) holds the row's last, `left` elements.
+// A row's slice in one block, all the same in every thread.  The row's slots are
+// counted from the 128-byte line in which it begins: a warp's 512 bytes then lie on four
+// lines, not on parts of five (policy losses, counted from the row's first 16 bytes: 2489 x
+// 50000 bf16 99 us, now 94; 1111 x 50001 fp32 79, now 75; rows of whole lines 639, now 644).
+// Slots lo .. lim - 1 of the slice lie wholly in the row; slot `head` (or none, -1) holds
+// its first elements behind others, slot `tail` (or none) its last `left` elements.
 template <int DT>
 struct Slice {
   static constexpr int N = Lanes<DT>::N;
   const typename ElemOf<DT>::T* row;
-  int lead, lo, lim, tail, left;
+  int lead, lo, lim, head, tail, left;
   __device__ __forceinline__ Slice(const typename ElemOf<DT>::T* r, int V, int s0, int per) : row(r) {
-    lead = (int)(((uintptr_t)r & 15) / sizeof(*r));
+    lead = (int)(((uintptr_t)r & 127) / sizeof(*r));
     const int full = (V + lead) / N - s0;
     left = (V + lead) % N;
-    lo = lead && s0 == 0;
+    head = s0 == 0 && lead % N ? lead / N : -1;
+    lo = s0 == 0 ? (lead + N - 1) / N : 0;
     lim = min(per, full);
     tail = left && full >= lo && full < per ? full : -1;
   }
@@ -155,8 +159,8 @@ struct Slice {
 // One pass with a running maximum, four slots per thread on the way while four are
 // worked on.  GROUP threads take a row: a warp (eight rows in a block) where there
 // are many rows, else the block; with few long rows, a cluster of C blocks.
-// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 154 us, 7.0 TB/s (reads alone are
-// faster than the copy); one row of 32768 3.0 us.
+// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 150 us, 7.2 TB/s (reads alone are
+// faster than the copy); one row of 32768 3.2 us.
 // The lanes' pairs (m, rest), each (1 + rest) e^m, as one; in every lane.
 __device__ __forceinline__ float2 warp_rest(float2 v) {
   const float M = warp_max(v.x);
@@ -217,10 +221,10 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
   };
   uint4 r[U], next[U] = {};
   load(0, r);
-  // the row's ends by elements: slot 0 where the row begins inside it, the last where it ends inside it
+  // the row's ends by elements
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    const int q = e == 0 ? (in.lo ? 0 : -1) : in.tail;
+    const int q = e == 0 ? in.head : in.tail;
     if (q >= 0 && q % GROUP == tid) {
       const int j = (s0 + q) * N - in.lead;
       float v[N], top = -INFINITY;
@@ -324,10 +328,10 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, co
 // block joins them and computes the token's loss, and one block barrier hands the
 // factors to the others, which write the gradient from their registers.
 //
-// Bound by HBM: 2 rows vocab es bytes.  8192 x 131072 bf16: 653 us, 6.58 TB/s; 4096 x 131072
-// fp32: 650 us, 6.61 TB/s; 4096 x 32768 bf16: 94 us, 5.73 TB/s.  Below that a row's own
-// chain (copies, sum, exchange, loss, stores: 3.7 us) shows: 2489 x 50001 100 us, 5.0 TB/s;
-// 300 x 70000 23 us, 3.7 TB/s.
+// Bound by HBM: 2 rows vocab es bytes.  8192 x 131072 bf16: 644 us, 6.67 TB/s; 4096 x 131072
+// fp32: 632 us, 6.80 TB/s; 4096 x 32768 bf16: 92 us, 5.83 TB/s.  Below that a row's own
+// chain (copies, sum, exchange, loss, stores: 3.7 us) shows: 2489 x 50001 99 us, 5.0 TB/s;
+// 300 x 70000 21 us, 4.0 TB/s.
 struct RowPlan {
   int C;        // blocks per cluster
   int per;      // slots per block: at most THREADS * K
@@ -381,21 +385,25 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
   const auto issue = [&](int i) {
     if (i < rows && (live >> i & 1)) {
       const Slice<DT> in(logits + i * a.stride, V, s0, plan.per);
-      // a slot that begins before the row also brings what lies there, but nothing from before the matrix
-      const bool before = in.lo && in.row - in.lead < a.logits;
+      // the head slot also brings what lies before the row, but nothing from before the matrix
+      const int head = in.lead / N;
+      const bool before = in.head >= 0 && in.row - in.lead % N < a.logits;
+      const int first = in.head >= 0 && !before ? head : in.lo;
       const char* src = reinterpret_cast<const char*>(in.row - in.lead) + (s0 + tid) * 16ll;
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (k * THREADS + tid < in.lim && (k > 0 || tid >= (int)before))
+        if (k * THREADS + tid < in.lim && (k > 0 || tid >= first))
           cp_async16(mine + k * THREADS * 16, src + k * THREADS * 16, 16);
       if (in.tail >= 0 && in.tail % THREADS == tid)
         cp_async16(mine + in.tail / THREADS * (THREADS * 16), src + in.tail / THREADS * (THREADS * 16),
                    in.left * (int)sizeof(E));
-      if (tid == 0 && before) {
-        E* to = reinterpret_cast<E*>(&next[0]);
-        for (int x = in.lead; x < N && x < in.lead + V; ++x) to[x] = in.row[x - in.lead];
-      } else if (tid == 0 && in.lo && in.lead + V < N) {  // the row begins and ends inside one slot
-        cp_async16(mine, src, (in.lead + V) * (int)sizeof(E));
+      if (in.head == tid) {
+        if (before) {
+          E* to = reinterpret_cast<E*>(&next[tid]);
+          for (int x = in.lead % N; x < N && x < in.lead % N + V; ++x) to[x] = in.row[x - in.lead % N];
+        } else if (in.lead % N + V < N) {  // the row begins and ends inside one slot
+          cp_async16(mine, src, (in.lead % N + V) * (int)sizeof(E));
+        }
       }
     }
     cp_async_commit();
@@ -440,24 +448,21 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       const Slice<DT> in(logits + i * a.stride, V, s0, plan.per);
 
       cp_async_wait<0>();
-      // -infinity into what the slots at the row's ends hold beside the row, and into the slot after them, which
-      // an earlier row of another alignment may have filled
-      if (in.lo && tid == 0) {
-        E* to = reinterpret_cast<E*>(&next[0]);
-        for (int x = 0; x < in.lead; ++x) from_float(to + x, -INFINITY);
+      // -infinity into what the slots at the row's ends hold beside the row, and into the slots before and after
+      // them, which an earlier row of another alignment may have filled
+      if (s0 == 0 && tid < in.lead / N) st_shared16(mine, no_logits(DT));
+      if (in.head == tid) {
+        E* to = reinterpret_cast<E*>(&next[tid]);
+        for (int x = 0; x < N; ++x)
+          if (x < in.lead % N || x >= in.lead % N + V) from_float(to + x, -INFINITY);
       }
-      const int end = (V + in.lead + N - 1) / N - s0;  // the slot after the row's last
       if (in.tail >= 0 && in.tail % THREADS == tid) {
         E* to = reinterpret_cast<E*>(&next[in.tail / THREADS * THREADS + tid]);
         for (int x = in.left; x < N; ++x) from_float(to + x, -INFINITY);
-      } else if (in.lo && V + in.lead < N && tid == 0) {
-        E* to = reinterpret_cast<E*>(&next[0]);
-        for (int x = V + in.lead; x < N; ++x) from_float(to + x, -INFINITY);
       }
-      if (end >= 0 && end < plan.per && s0 + end < plan.most && end % THREADS == tid) {
-        E* to = reinterpret_cast<E*>(&next[end / THREADS * THREADS + tid]);
-        for (int x = 0; x < N; ++x) from_float(to + x, -INFINITY);
-      }
+      const int end = max(0, (V + in.lead + N - 1) / N - s0);  // the slot after the row's last
+      const int after = end + ((tid - end) & (THREADS - 1));   // this thread's first one from there
+      if (after < min(plan.per, plan.most - s0)) st_shared16(mine + after / THREADS * (THREADS * 16), no_logits(DT));
     }
 
     // the slots as they are, kept until the gradient is written
@@ -519,7 +524,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     }
     ++done;
     // Where registers are shortest the slice is computed once more, not kept (4096 x 32768 bf16 94 -> 92 us, 2000 x
-    // 30000 fp32 92 -> 85; with 7 slots per thread it costs more than it frees, 2489 x 50001 bf16 101 -> 107).
+    // 30000 fp32 92 -> 85; with 7 slots per thread it costs more than it frees, 2489 x 50001 bf16 99 -> 105).
     int again = i;
     if constexpr (K == 8 && THREADS == 256) asm volatile("" : "+r"(again));
     const Slice<DT> in(logits + again * a.stride, V, s0, plan.per);
@@ -552,12 +557,12 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
           st_stream(reinterpret_cast<uint4*>(dst + k * THREADS * 16), narrow<DT>(values(k), 1.0f, false));
     }
     // slots at the row's ends, or all of them when the gradient's rows start at another alignment: by elements
-    const bool first = in.lo && tid == 0, last = in.tail >= 0 && in.tail % THREADS == tid;
+    const bool first = in.head == tid, last = in.tail >= 0 && in.tail % THREADS == tid;
     if (!same || first || last) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int q = k * THREADS + tid;
-        if (q < plan.per && (!same || (q == 0 && first) || (q == in.tail && last))) {
+        if (q < plan.per && (!same || (q == in.head && first) || (q == in.tail && last))) {
           const int j = (s0 + q) * N - in.lead;
           const Acc<DT> g = values(k);
 #pragma unroll
@@ -661,8 +666,8 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const PairParams p) {
 // before the first is used.  The rows go from the last to the first: what the
 // statistics' pass has read last is still in L2.
 // Bound by HBM: with the statistics' pass the logits are read twice, since a row's
-// factor needs its whole pair's log-probabilities: 6830 x 131072 bf16 773 us for the whole
-// loss, 6.95 TB/s of two reads and one write; 2489 x 50001 105 us.  2 / 4 / 8 slots: 120 / 114 /
+// factor needs its whole pair's log-probabilities: 6800 x 131072 bf16 768 us for the whole
+// loss, 6.96 TB/s of two reads and one write; 2400 x 50001 117 us.  2 / 4 / 8 slots: 120 / 114 /
 // 115 us (2400 x 50001).
 constexpr int kGradSlots = 4, kPiece = kThreads * kGradSlots;
 
@@ -750,13 +755,15 @@ inline unsigned grid_of(unsigned long long work) {
   return (unsigned)std::max(1ull, std::min<unsigned long long>(work, kMaxLossBlocks));
 }
 
-// Slots of a matrix's row at its worst alignment.
+// Slots of a matrix's row, from the line it begins in, at its worst alignment.
 template <int DT>
 unsigned long long row_slots(const LogitsCall& c, const void* matrix, size_t stride) {
   constexpr int N = Lanes<DT>::N;
-  const size_t es = sizeof(typename ElemOf<DT>::T);
-  const bool alike = c.rows == 1 || stride * es % 16 == 0;  // every row starts at the same alignment
-  const unsigned long long lead = alike ? ((uintptr_t)matrix & 15) / es : N - 1;
+  const size_t es = sizeof(typename ElemOf<DT>::T), at = ((uintptr_t)matrix & 127) / es;
+  // the rows' places in their lines: all the same, at a distance of whole slots, or any
+  const unsigned long long lead = c.rows == 1 || stride * es % 128 == 0 ? at
+                                  : stride * es % 16 == 0              ? 128 / es - N + at % N
+                                                                       : 128 / es - 1;
   return (c.vocab + lead + N - 1) / N;
 }
 
@@ -794,7 +801,7 @@ cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = cluster_config((unsigned)c.rows * C, kThreads, 0, C, c.stream, attr);
   return cudaLaunchKernelEx(&cfg, logprob_kernel<DT, kThreads>, Matrix<DT>(c),
-                            LogprobPlan{C, (int)((n + C - 1) / C)}, stats, factors);
+                            LogprobPlan{C, (int)(((n + C - 1) / C + 7) / 8 * 8)}, stats, factors);
 }
 
 // Rows per cluster, of 1 .. most.  A row takes a resident cluster 3.7 us by itself
@@ -856,7 +863,7 @@ cudaError_t launch_policy_row(const LogitsCall& c, const PolicyParams& p, unsign
   const auto kernel = policy_row_kernel<DT, THREADS, K, BLOCKS, CLUSTER>;
   RowPlan plan;
   plan.C = C;
-  plan.per = (int)((slots + C - 1) / C);
+  plan.per = (int)(((slots + C - 1) / C + 7) / 8 * 8);  // whole lines; still at most THREADS * K
   plan.zero = 0;
   plan.most = (int)slots;
   cudaError_t e = cudaSuccess;
