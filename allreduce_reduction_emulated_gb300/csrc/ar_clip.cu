@@ -42,20 +42,6 @@ constexpr unsigned int kRun = 16;
 // 112.  Above, nothing is gained and a hint of any kind costs 2% (9.7 GB: 2152 us
 // without, 2190 with), so the kernels come without them too.
 constexpr unsigned int kHintChunks = 16384, kKeptChunks = 1250;
-__device__ __forceinline__ uint64_t keep_policy(bool keep) {
-  uint64_t p;
-  if (keep) asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-  else asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-  return p;
-}
-template <bool HINTS>
-__device__ __forceinline__ uint4 ld_hint(const uint4* p, uint64_t policy) {
-  if constexpr (!HINTS) return ld_row(p);
-  uint4 r;
-  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p), "l"(policy));
-  return r;
-}
 
 struct Tensor {
   const void* grad;

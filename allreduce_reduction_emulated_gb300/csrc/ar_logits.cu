@@ -170,10 +170,18 @@ __device__ __forceinline__ float2 warp_rest(float2 v) {
 }
 
 struct LogprobPlan {
-  int C, per;  // blocks per row; slots per block
+  int C, per;              // blocks per row; slots per block
+  unsigned long long keep; // rows from here on stay in L2 (HINTS)
 };
 
-template <int DT, int GROUP>
+// Where the gradient follows and the matrix is not far larger than L2, the rows that
+// it begins with, the last kKeptBytes (the two halves of L2 may each hold a copy),
+// are to stay in L2 and the others to make room for them: the whole loss 55.3 ->
+// 51.7 us at 51 MB, 116.4 -> 113.6 at 240 MB, 187.5 -> 186.5 at 400 MB; nothing at 512 MB
+// and 1.8 GB.
+constexpr unsigned long long kKeptBytes = 40ull << 20, kHintBytes = 400ull << 20;
+
+template <int DT, int GROUP, bool HINTS>
 __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, const LogprobPlan plan, float2* stats,
                                                            float* factors) {
   constexpr int N = Lanes<DT>::N, U = 4, W = kThreads / 32;
@@ -198,16 +206,17 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
   const uint4* src = reinterpret_cast<const uint4*>(row - in.lead) + s0 + tid;
   const long long y = writer ? load_index(a.targets, a.target_bytes, t) : 0;
 
+  const uint64_t policy = HINTS ? keep_policy(t >= plan.keep) : 0;
   const auto load = [&](int at, uint4 (&r)[U]) {
     if (at + U * GROUP <= in.lim && at >= in.lo) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) r[u] = ld_row(src + at + u * GROUP);
+      for (int u = 0; u < U; ++u) r[u] = ld_hint<HINTS>(src + at + u * GROUP, policy);
     } else {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int q = at + u * GROUP + tid;
         r[u] = no_logits(DT);
-        if (q >= in.lo && q < in.lim) r[u] = ld_row(src + at + u * GROUP);
+        if (q >= in.lo && q < in.lim) r[u] = ld_hint<HINTS>(src + at + u * GROUP, policy);
       }
     }
   };
@@ -620,20 +629,25 @@ __device__ __forceinline__ unsigned long long offset_at(const PairParams& p, uns
 // factors.
 __global__ void __launch_bounds__(kThreads) pair_kernel(const PairParams p) {
   pdl_enter();
-  __shared__ float sh[2][kThreads / 32], side;
+  __shared__ float sh[kThreads / 32], side;
   for (unsigned long long i = blockIdx.x; i < p.pairs; i += gridDim.x) {
-    float R[2];
-    for (int k = 0; k < 2; ++k) {
-      const unsigned long long b = offset_at(p, 2 * i + k), e = offset_at(p, 2 * i + k + 1);
-      float v = 0.0f;
-      for (unsigned long long t = b + threadIdx.x; t < e; t += kThreads) {
-        const float w = p.weights ? p.weights[t] : 1.0f;
-        if (w != 0.0f) v += w * (p.ref_logprobs ? p.logprobs[t] - p.ref_logprobs[t] : p.logprobs[t]);
-      }
-      R[k] = block_sum<kThreads>(v, sh[k]);
+    // The two sequences in one signed sum, token against token: their log-probabilities cancel before they are large
+    // (two sums of some thousands each would round the difference at 1e-4).
+    const unsigned long long b0 = offset_at(p, 2 * i), b1 = offset_at(p, 2 * i + 1), b2 = offset_at(p, 2 * i + 2);
+    const unsigned long long n0 = b1 > b0 ? b1 - b0 : 0, n1 = b2 > b1 ? b2 - b1 : 0;
+    const auto term = [&](unsigned long long t) {
+      const float w = p.weights ? p.weights[t] : 1.0f;
+      if (w == 0.0f) return 0.0f;
+      return w * (p.ref_logprobs ? p.logprobs[t] - p.ref_logprobs[t] : p.logprobs[t]);
+    };
+    float v = 0.0f;
+    for (unsigned long long k = threadIdx.x; k < n0 || k < n1; k += kThreads) {
+      if (k < n0) v += term(b0 + k);
+      if (k < n1) v -= term(b1 + k);
     }
+    v = block_sum<kThreads>(v, sh);
     if (threadIdx.x == 0) {
-      const float z = p.beta * (R[0] - R[1]);
+      const float z = p.beta * v;
       // softplus(-z) = max(-z, 0) + log1p(e^-|z|)
       const float e = expf(-fabsf(z));
       const float sp = fmaxf(-z, 0.0f) + log1pf(e);
@@ -667,11 +681,11 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const PairParams p) {
 // statistics' pass has read last is still in L2.
 // Bound by HBM: with the statistics' pass the logits are read twice, since a row's
 // factor needs its whole pair's log-probabilities: 6800 x 131072 bf16 768 us for the whole
-// loss, 6.96 TB/s of two reads and one write; 2400 x 50001 117 us.  2 / 4 / 8 slots: 120 / 114 /
+// loss, 6.96 TB/s of two reads and one write; 2400 x 50001 114 us.  2 / 4 / 8 slots: 120 / 114 /
 // 115 us (2400 x 50001).
 constexpr int kGradSlots = 4, kPiece = kThreads * kGradSlots;
 
-template <int DT>
+template <int DT, bool HINTS>
 __global__ void __launch_bounds__(kThreads, 6) preference_grad_kernel(const Matrix<DT> a, const PairParams p,
                                                                       const float2* stats, unsigned pieces) {
   constexpr int N = Lanes<DT>::N;
@@ -701,11 +715,12 @@ __global__ void __launch_bounds__(kThreads, 6) preference_grad_kernel(const Matr
   }
   const Slice<DT> in(row, V, s0, kPiece);
   const uint4* src = reinterpret_cast<const uint4*>(row - in.lead) + s0 + tid;
+  const uint64_t once = HINTS ? keep_policy(false) : 0;
   uint4 r[kGradSlots];
 #pragma unroll
   for (int k = 0; k < kGradSlots; ++k) {
     const int q = k * kThreads + tid;
-    if (q >= in.lo && q < in.lim) r[k] = ld_row(src + k * kThreads);
+    if (q >= in.lo && q < in.lim) r[k] = ld_hint<HINTS>(src + k * kThreads, once);
   }
   const float2 st = stats[t];
   const bool same = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
@@ -786,22 +801,30 @@ inline cudaLaunchConfig_t cluster_config(unsigned grid, unsigned threads, int sm
 }
 
 template <int DT>
+bool small_for_l2(const LogitsCall& c) {
+  return c.rows * row_slots<DT>(c, c.logits, c.row_stride) * 16 <= kHintBytes;
+}
+
+template <int DT>
 cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
   const unsigned long long n = row_slots<DT>(c, c.logits, c.row_stride);
+  const bool hints = stats && small_for_l2<DT>(c);
+  const unsigned long long kept = kKeptBytes / (n * 16), keep = c.rows > kept ? c.rows - kept : 0;
   // A warp per row where that makes 16 warps for every SM (8192 x 9000 bf16: 23 us, a block per row 43; 4096 x 32768
   // 40 and 44; but 4096 x 131072 159 and 154, 1000 x 32768 23 and 12) or a row has no more for a warp to do.  Thousands of
   // warps leave no whole rows in L2, though: where the gradient follows, long rows take a block (preference 4 x 1024
   // x 131072: 789 us, with a warp per row 828).
   if (n <= 256 || (c.rows >= 16ull * c.sms && n <= (stats ? 2048 : 8192)))
-    return launch_kernel(logprob_kernel<DT, 32>, (unsigned)((c.rows + 7) / 8), kThreads, 0, c.stream, true,
-                         Matrix<DT>(c), LogprobPlan{1, (int)n}, stats, factors);
+    return launch_kernel(hints ? logprob_kernel<DT, 32, true> : logprob_kernel<DT, 32, false>,
+                         (unsigned)((c.rows + 7) / 8), kThreads, 0, c.stream, true, Matrix<DT>(c),
+                         LogprobPlan{1, (int)n, keep}, stats, factors);
   // a row over several blocks until there are two blocks for every SM, each with 1024 slots at least
   int C = 1;
   while (C < 8 && c.rows * C < 2ull * c.sms && n >= 2048ull * C) C *= 2;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = cluster_config((unsigned)c.rows * C, kThreads, 0, C, c.stream, attr);
-  return cudaLaunchKernelEx(&cfg, logprob_kernel<DT, kThreads>, Matrix<DT>(c),
-                            LogprobPlan{C, (int)(((n + C - 1) / C + 7) / 8 * 8)}, stats, factors);
+  return cudaLaunchKernelEx(&cfg, hints ? logprob_kernel<DT, kThreads, true> : logprob_kernel<DT, kThreads, false>,
+                            Matrix<DT>(c), LogprobPlan{C, (int)(((n + C - 1) / C + 7) / 8 * 8), keep}, stats, factors);
 }
 
 // Rows per cluster, of 1 .. most.  A row takes a resident cluster 3.7 us by itself
@@ -941,8 +964,9 @@ cudaError_t run_preference(const LogitsCall& c, const PairParams& p, float2* sta
   if (c.rows) e = run_logprobs<DT>(c, stats, p.factors);
   if (e == cudaSuccess && p.pairs) e = launch_kernel(pair_kernel, grid_of(p.pairs), kThreads, 0, c.stream, true, p);
   if (e == cudaSuccess)
-    e = launch_kernel(preference_grad_kernel<DT>, (unsigned)std::max(1ull, c.rows * pieces), kThreads, 0, c.stream,
-                      true, Matrix<DT>(c), p, (const float2*)stats, (unsigned)pieces);
+    e = launch_kernel(small_for_l2<DT>(c) ? preference_grad_kernel<DT, true> : preference_grad_kernel<DT, false>,
+                      (unsigned)std::max(1ull, c.rows * pieces), kThreads, 0, c.stream, true, Matrix<DT>(c), p,
+                      (const float2*)stats, (unsigned)pieces);
   return e;
 }
 

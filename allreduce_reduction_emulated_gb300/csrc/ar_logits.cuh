@@ -35,6 +35,23 @@ __device__ __forceinline__ uint4 ld_row(const uint4* p) {
   return r;
 }
 
+// A load whose lines L2 keeps for longest (keep) or drops first; where there is no
+// reason for either, ld_row.
+__device__ __forceinline__ uint64_t keep_policy(bool keep) {
+  uint64_t p;
+  if (keep) asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  else asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+template <bool HINTS>
+__device__ __forceinline__ uint4 ld_hint(const uint4* p, uint64_t policy) {
+  if constexpr (!HINTS) return ld_row(p);
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p), "l"(policy));
+  return r;
+}
+
 template <int DT> struct ElemOf;
 template <> struct ElemOf<kF32> { using T = float; };
 template <> struct ElemOf<kBF16> { using T = uint16_t; };

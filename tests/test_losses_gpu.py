@@ -291,6 +291,26 @@ def test_preference_targets_of_probability_zero(dev):
         assert bool(((r.grad.double() - want).abs() <= 1e-5 * want.abs() + 1e-12).all())
 
 
+@pytest.mark.parametrize("length", [1, 255, 600, 1025])
+def test_preference_of_equal_answers(dev, length):
+    """The same answer on both sides (rows alike in their lines), without a reference: every difference is exactly
+    0, and so is the margin, however long the answers are; the loss is log 2."""
+    logits, y, _, _, _, _ = inputs(dev, length, 1024, torch.float32, masked=0.0)
+    logits, y = logits.repeat(2, 1), y.repeat(2)
+    r = losses.preference_loss(logits, y, torch.tensor([0, length, 2 * length], device=dev), beta=0.5)
+    assert float(r.margins) == 0.0
+    tu.assert_close(r.loss, math.log(2.0), 2 ** -22)
+    assert torch.equal(r.grad[:length], -r.grad[length:])
+
+
+@pytest.mark.parametrize("rows,vocab", [(1500, 9001), (3000, 30000), (5200, 50001)])
+def test_preference_around_l2(dev, rows, vocab):
+    """Matrices of 27, 180 and 520 MB, around what L2 can keep for the gradient."""
+    logits, y, _, _, ref, w = inputs(dev, rows, vocab, torch.bfloat16)
+    n = rows // 6
+    check_preference(logits, y, torch.arange(0, rows + 1, n, device=dev)[:7], ref, w)
+
+
 # slots of 16 bytes at which the policy loss changes its shape (blocks, clusters, registers per thread)
 SHAPES = [512, 1024, 1536, 2048, 2560, 3584, 4096, 5120, 8192, 10240, 12288, 16384, 20480, 32768, 49152, 65536]
 
