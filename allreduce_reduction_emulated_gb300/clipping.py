@@ -16,7 +16,7 @@ from . import (AR_BFLOAT16, AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED, AR_FLOAT32, 
                library)
 
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
-_DTYPES = {torch.float32: AR_FLOAT32, torch.bfloat16: AR_BFLOAT16}
+_DTYPES = {torch.float32: (AR_FLOAT32, 4), torch.bfloat16: (AR_BFLOAT16, 2)}  # (code, bytes)
 
 
 class GradClipper:
@@ -45,36 +45,28 @@ class GradClipper:
         if len(self.out) != len(self.grads):
             raise ArError(AR_ERR_INVALID_ARG, f"{what}: {len(self.grads)} gradients, {len(self.out)} outputs")
         self.device = self.grads[0].device
-        spans = []
-        for name, tensors in (("grads", self.grads), ("out", self.out)):
-            if name == "out" and out is None:
-                continue
-            for i, (t, g) in enumerate(zip(tensors, self.grads)):
-                if t.dtype not in _DTYPES:
-                    raise ArError(AR_ERR_UNSUPPORTED, f"{what}: {name}[{i}] of {t.dtype}: float32 or bfloat16 needed")
-                if not t.is_cuda or not t.is_contiguous():
-                    raise ArError(AR_ERR_INVALID_ARG, f"{what}: {name}[{i}] is not a contiguous CUDA tensor")
-                if t.device != self.device:
-                    raise ArError(AR_ERR_INVALID_ARG, f"{what}: tensors on {self.device} and {t.device}; "
-                                                      "all must be on one GPU")
-                if t.dtype != g.dtype or t.numel() != g.numel():
-                    raise ArError(AR_ERR_INVALID_ARG, f"{what}: out[{i}] is {t.numel()} x {t.dtype}, the gradient is "
-                                                      f"{g.numel()} x {g.dtype}")
-                if name == "out" and t.data_ptr() == g.data_ptr():
-                    continue
-                if t.numel():
-                    spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), f"{name}[{i}]"))
+        self._index = self.device.index
+        ats, counts, dtypes = self._laid_out("grads", self.grads)
+        outs = ats
+        spans = [(at, at + n * size, "grads", i) for i, (at, n, (_, size)) in enumerate(zip(ats, counts, dtypes)) if n]
+        if out is not None:
+            outs, out_counts, out_dtypes = self._laid_out("out", self.out)
+            for i, (at, g, n, m, d, e) in enumerate(zip(outs, ats, out_counts, counts, out_dtypes, dtypes)):
+                if n != m or d is not e:
+                    raise ArError(AR_ERR_INVALID_ARG, f"{what}: out[{i}] is {n} x {self.out[i].dtype}, the gradient "
+                                                      f"is {m} x {self.grads[i].dtype}")
+                if n and at != g:
+                    spans.append((at, at + n * d[1], "out", i))
         spans.sort()
-        for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
+        for (_, end, a, i), (start, _, b, j) in zip(spans, spans[1:]):
             if start < end:
-                raise ArError(AR_ERR_INVALID_ARG, f"{what}: {a} and {b} share memory")
+                raise ArError(AR_ERR_INVALID_ARG, f"{what}: {a}[{i}] and {b}[{j}] share memory")
         n = len(self.grads)
         self._n = n
-        self._grads = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.grads])
-        self._outs = (ctypes.c_void_p * n)(*[t.data_ptr() for t in self.out])
-        self._counts = (ctypes.c_size_t * n)(*[t.numel() for t in self.grads])
-        self._dtypes = (ctypes.c_int * n)(*[_DTYPES[t.dtype] for t in self.grads])
-        self._index = self.device.index
+        self._grads = (ctypes.c_void_p * n)(*ats)
+        self._outs = (ctypes.c_void_p * n)(*outs)
+        self._counts = (ctypes.c_size_t * n)(*counts)
+        self._dtypes = (ctypes.c_int * n)(*[code for code, _ in dtypes])
         self._lib = library()
         self._bytes = self._lib.ar_grad_norm_workspace()
         with torch.cuda.device(self.device):
@@ -82,6 +74,24 @@ class GradClipper:
             self._workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         self._at = self._workspace.data_ptr()
         self._norms, self._next = None, self.NORMS
+
+    def _laid_out(self, name: str, tensors):
+        """(addresses, element counts, _DTYPES entries) of tensors the kernels can walk."""
+        what = "GradClipper"
+        ats, counts, dtypes = [], [], []
+        for i, t in enumerate(tensors):
+            kind = _DTYPES.get(t.dtype)
+            if kind is None:
+                raise ArError(AR_ERR_UNSUPPORTED, f"{what}: {name}[{i}] of {t.dtype}: float32 or bfloat16 needed")
+            if not t.is_cuda or not t.is_contiguous():
+                raise ArError(AR_ERR_INVALID_ARG, f"{what}: {name}[{i}] is not a contiguous CUDA tensor")
+            if t.device != self.device:
+                raise ArError(AR_ERR_INVALID_ARG, f"{what}: tensors on {self.device} and {t.device}; "
+                                                  "all must be on one GPU")
+            ats.append(t.data_ptr())
+            counts.append(t.numel())
+            dtypes.append(kind)
+        return ats, counts, dtypes
 
     def _begin(self, what: str, stream):
         """(stream handle, a new 0-dim norm): both belong to the call's stream."""

@@ -21,7 +21,10 @@ grad          where the gradient goes: a tensor of the logits' shape and type, o
               at the logits' alignments (for padded or odd layouts it may have a few
               elements between its rows).  A gradient given at other alignments is
               written element by element, which is slower
-stream        a torch stream or a cudaStream_t (default: the current stream)
+stream        a torch stream or a cudaStream_t (default: the current stream).  What is
+              allocated belongs to that stream; as with any kernel on a stream of
+              one's own, the caller orders it after whatever made the inputs and
+              keeps these until the stream is past the call
 
 Nothing waits for the GPU and nothing is kept between calls.
 """
@@ -66,6 +69,8 @@ def _matrix(what: str, name: str, x):
 
 def _vector(what: str, name: str, x, device: int, count: int) -> int:
     """Address of a per-token float32 vector."""
+    if not isinstance(x, torch.Tensor):
+        raise _bad(what, f"{name} must be a tensor, got {type(x).__name__}")
     if x.dtype != torch.float32:
         raise _bad(what, f"{name} of {x.dtype}: float32 needed", AR_ERR_UNSUPPORTED)
     if x.get_device() != device:
@@ -77,6 +82,8 @@ def _vector(what: str, name: str, x, device: int, count: int) -> int:
 
 def _indices(what: str, name: str, x, device: int, count: int):
     """(address, bytes per index) of a vector of indices."""
+    if not isinstance(x, torch.Tensor):
+        raise _bad(what, f"{name} must be a tensor, got {type(x).__name__}")
     size = _INDEX_BYTES.get(x.dtype)
     if size is None:
         raise _bad(what, f"{name} of {x.dtype}: int64 or int32 needed", AR_ERR_UNSUPPORTED)
@@ -246,7 +253,7 @@ def preference_loss(logits, targets, offsets, ref_logprobs=None, weights=None, b
     y, size = _indices(what, "targets", targets, device, rows)
     w = None if weights is None else _vector(what, "weights", weights, device, rows)
     ref = None if ref_logprobs is None else _vector(what, "ref_logprobs", ref_logprobs, device, rows)
-    n = offsets.numel()
+    n = offsets.numel() if isinstance(offsets, torch.Tensor) else 1
     if n % 2 == 0:
         raise _bad(what, f"offsets: 2 * pairs + 1 needed, got {n}")
     off, off_size = _indices(what, "offsets", offsets, device, n)

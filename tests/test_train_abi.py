@@ -148,6 +148,18 @@ def test_binding_checks_layouts(lib, monkeypatch):
     assert losses._gradient("x", x, x, 0, 4, 8) is x
 
 
+def test_binding_refuses_what_is_not_a_tensor(lib, monkeypatch):
+    monkeypatch.setattr(losses, "_current_device", lambda: 0)
+    g = OnGpu.of
+    x, y, v = g(torch.zeros(4, 8)), g(torch.zeros(4, dtype=torch.int64)), g(torch.zeros(4))
+    refused(lambda: losses.token_logprobs(x, None), "targets must be a tensor")
+    refused(lambda: losses.token_logprobs(x, [0, 1, 2, 3]), "targets must be a tensor")
+    refused(lambda: losses.policy_loss(x, y, None, v), "old_logprobs must be a tensor")
+    refused(lambda: losses.policy_loss(x, y, v, 1.0), "advantages must be a tensor")
+    refused(lambda: losses.policy_loss(x, y, v, v, weights=[1.0] * 4), "weights must be a tensor")
+    refused(lambda: losses.preference_loss(x, y, [0, 2, 4]), "offsets must be a tensor")
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("vocab,pad,shift", [(24, 0, 1), (24, 8, 0), (24, 5, 0), (25, 3, 2), (9, 40, 7), (1, 1, 0)])
 def test_a_new_gradient_has_the_logits_alignments(dtype, vocab, pad, shift):
