@@ -242,12 +242,9 @@ __device__ __forceinline__ void scale_chunk(const Tensor& t, unsigned int chunk,
         y.v[i + 1] = v.y;
       }
       E* to = out + c.element(q);
-      if (same) {
-        st_stream(reinterpret_cast<uint4*>(to), narrow<DT>(y, 1.0f, false));
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) from_float(to + i, y.v[i]);
-      }
+      const uint4 v = narrow<DT>(y, 1.0f, false);
+      if (same) st_stream(reinterpret_cast<uint4*>(to), v);
+      else store_apart(to, v, warp_within(q, c.lo, c.lim));
     }
   }
   c.partial_slots([&](long long j, const auto& x) {

@@ -564,14 +564,21 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       for (int k = 0; k < K; ++k)
         if (k * THREADS + tid < in.lim && (k > 0 || tid >= in.lo))
           st_stream(reinterpret_cast<uint4*>(dst + k * THREADS * 16), narrow<DT>(values(k), 1.0f, false));
+    } else {  // the gradient's rows start at another alignment (by words and halves: the registers of a shuffle slowed
+              // the other rows down, 4096 x 32768 bf16 91 -> 95 us)
+      E* dst = grad + ((s0 + tid) * N - in.lead);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (k * THREADS + tid < in.lim && (k > 0 || tid >= in.lo))
+          store_apart(dst + k * THREADS * N, narrow<DT>(values(k), 1.0f, false), false);
     }
-    // slots at the row's ends, or all of them when the gradient's rows start at another alignment: by elements
+    // slots at the row's ends, by elements
     const bool first = in.head == tid, last = in.tail >= 0 && in.tail % THREADS == tid;
-    if (!same || first || last) {
+    if (first || last) {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int q = k * THREADS + tid;
-        if (q < plan.per && (!same || (q == in.head && first) || (q == in.tail && last))) {
+        if ((q == in.head && first) || (q == in.tail && last)) {
           const int j = (s0 + q) * N - in.lead;
           const Acc<DT> g = values(k);
 #pragma unroll
@@ -726,28 +733,29 @@ __global__ void __launch_bounds__(kThreads, 6) preference_grad_kernel(const Matr
   const bool same = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
   const float f = -c / st.y;
   const float2 minus_m = make_float2(-st.x, -st.x), f2 = make_float2(f, f);
-  uint4* dst = reinterpret_cast<uint4*>(grad - in.lead) + s0 + tid;
-  if (same) {
+  E* dst = grad + ((long long)(s0 + tid) * N - in.lead);
 #pragma unroll
-    for (int k = 0; k < kGradSlots; ++k) {
-      const int q = k * kThreads + tid;
-      if (q >= in.lo && q < in.lim) {
-        Acc<DT> g = widen<DT>(r[k]);
+  for (int k = 0; k < kGradSlots; ++k) {
+    const int q = k * kThreads + tid;
+    if (q >= in.lo && q < in.lim) {
+      Acc<DT> g = widen<DT>(r[k]);
 #pragma unroll
-        for (int x = 0; x < N; x += 2) {
-          const float2 v = mul2(exp_pair(g.v[x], g.v[x + 1], minus_m), f2);
-          g.v[x] = v.x;
-          g.v[x + 1] = v.y;
-        }
-        st_stream(dst + k * kThreads, narrow<DT>(g, 1.0f, false));
+      for (int x = 0; x < N; x += 2) {
+        const float2 v = mul2(exp_pair(g.v[x], g.v[x + 1], minus_m), f2);
+        g.v[x] = v.x;
+        g.v[x + 1] = v.y;
       }
+      const uint4 v = narrow<DT>(g, 1.0f, false);
+      if (same) st_stream(reinterpret_cast<uint4*>(dst + k * kThreads * N), v);
+      else store_apart(dst + k * kThreads * N, v, warp_within(q, in.lo, in.lim));
     }
   }
-  // slots at the row's ends, and all of them where the gradient's rows start at another alignment: by elements
-  const int end = (V + in.lead + N - 1) / N - s0;
+  __syncwarp();  // the target's element follows, perhaps from another lane than its store
+  // slots at the row's ends, by elements
 #pragma unroll 1
-  for (int q = tid; q < kPiece && q < end; q += kThreads) {
-    if (same && q >= in.lo && q < in.lim) continue;
+  for (int e = 0; e < 2; ++e) {
+    const int q = e == 0 ? in.head : in.tail;
+    if (q < 0 || q % kThreads != tid) continue;
     const int j = (s0 + q) * N - in.lead;
     float x[N];
 #pragma unroll

@@ -20,7 +20,7 @@ grad          where the gradient goes: a tensor of the logits' shape and type, o
               the logits themselves (in place); None allocates one whose rows start
               at the logits' alignments (for padded or odd layouts it may have a few
               elements between its rows).  A gradient given at other alignments is
-              written element by element, which is slower
+              written in narrower stores, which takes longer
 stream        a torch stream or a cudaStream_t (default: the current stream).  What is
               allocated belongs to that stream; as with any kernel on a stream of
               one's own, the caller orders it after whatever made the inputs and
@@ -98,7 +98,9 @@ def _gradient(what: str, logits, grad, device: int, rows: int, vocab: int):
     """The tensor for the gradient; None makes one whose rows start at the logits'
     alignments within 16 bytes (then both are read and written in whole vectors)."""
     if grad is None:
-        return torch.empty_like(logits) if logits.is_contiguous() else _like_rows(logits, rows, vocab)
+        if logits.is_contiguous() and logits.data_ptr() % 16 == 0:
+            return torch.empty_like(logits)
+        return _like_rows(logits, rows, vocab)
     if grad is not logits:
         at, r, v, stride = _matrix(what, "grad", grad)
         if (at, r, v) != (device, rows, vocab) or grad.dtype != logits.dtype:

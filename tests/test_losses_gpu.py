@@ -311,6 +311,26 @@ def test_preference_around_l2(dev, rows, vocab):
     check_preference(logits, y, torch.arange(0, rows + 1, n, device=dev)[:7], ref, w)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [9, 1001, 9001, 40003])
+def test_gradients_at_other_alignments(dev, V, dtype):
+    """Gradients at every distance from the logits' alignment, targets at every place of
+    a slot and of a warp's stores: what is beside the rows stays."""
+    T = 24
+    logits, y, old, adv, ref, w = inputs(dev, T, V, dtype, seed=V)
+    w[:] = 1.0
+    y[:] = torch.arange(T, device=dev) * 33 % V
+    N = 16 // logits.element_size()
+    off = torch.tensor([0, 5, 11, 20, T], device=dev)
+    for shift in range(1, N):
+        room = torch.full((T, V + N), 9.0, dtype=dtype, device=dev)
+        check_preference(logits, y, off, ref, w, grad=room[:, shift:shift + V])
+        assert bool((room[:, :shift] == 9).all()) and bool((room[:, shift + V:] == 9).all())
+        room[:] = 9.0
+        check_policy(logits, y, old, adv, ref, w, grad=room[:, shift:shift + V])
+        assert bool((room[:, :shift] == 9).all()) and bool((room[:, shift + V:] == 9).all())
+
+
 # slots of 16 bytes at which the policy loss changes its shape (blocks, clusters, registers per thread)
 SHAPES = [512, 1024, 1536, 2048, 2560, 3584, 4096, 5120, 8192, 10240, 12288, 16384, 20480, 32768, 49152, 65536]
 
