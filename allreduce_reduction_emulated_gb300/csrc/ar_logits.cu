@@ -338,8 +338,8 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, co
 // factors to the others, which write the gradient from their registers.
 //
 // Bound by HBM: 2 rows vocab es bytes.  8192 x 131072 bf16: 644 us, 6.67 TB/s; 4096 x 131072
-// fp32: 632 us, 6.80 TB/s; 4096 x 32768 bf16: 92 us, 5.83 TB/s.  Below that a row's own
-// chain (copies, sum, exchange, loss, stores: 3.7 us) shows: 2489 x 50001 99 us, 5.0 TB/s;
+// fp32: 632 us, 6.80 TB/s; 4096 x 32768 bf16: 90 us, 5.97 TB/s.  Below that a row's own
+// chain (copies, sum, exchange, loss, stores: 3.7 us) shows: 2489 x 50001 97 us, 5.1 TB/s;
 // 300 x 70000 21 us, 4.0 TB/s.
 struct RowPlan {
   int C;        // blocks per cluster
@@ -839,9 +839,10 @@ cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
 // (2.0 in blocks of 128 threads: copies, sum, exchange, loss, stores); all resident
 // clusters' rows take 2 wave row_bytes / 6.8 TB/s together.
 // Where HBM is the longer by a fifth, the clusters' start-ups hide behind others'
-// transfers and small runs end evenly: one wave's share of the rows, at most 4, or 8
-// where two blocks fill an SM (us at 1 / 2 / 4 / 8 / 16 rows: 4096 x 32768 bf16 109 / 97 / 95 /
-// 99 / 101, 8192 x 131072 804 / 701 / 663 / 657 / 672).
+// transfers and small runs end evenly: one wave's share of the rows, at most 3, or 8
+// where two blocks fill an SM (us at 1 / 2 / 3 / 4 / 5 / 8 rows: 5000 x 30000 bf16 121 / 106 / 103 / 104 /
+// 106 / 113, 1500 x 30000 44 / 41 / 40 / 44 / 39 / 51, 1800 x 30000 50 / 45 / 42 / 46 / 50 / 50; 8192 x 131072
+// at 1 / 2 / 4 / 8 / 16: 804 / 701 / 663 / 657 / 672).
 // Where the row itself is, a wave takes its rows' time and a start-up of about one
 // row whether it is full or not: the least ceil(waves) (rows + 1) (300 x 70000 at 3 / 4 / 5 /
 // 6: 24.1 / 29.3 / 22.8 / 26.6; 700 x 100000 at 4 / 5 / 8 / 10: 59 / 57 / 69 / 55; 2489 x 50001 at
@@ -850,7 +851,7 @@ inline int rows_per_cluster(unsigned long long rows, int wave, double row_bytes,
   const double row_us = threads >= 256 ? 3.7 : 2.0, wave_us = 2.0 * wave * row_bytes / 6.8e6;
   int run = 1;
   if (wave_us > 1.2 * row_us) {
-    run = (int)std::max(1ull, std::min<unsigned long long>(two_blocks ? 8 : 4, (rows + wave / 2) / wave));
+    run = (int)std::max(1ull, std::min<unsigned long long>(two_blocks ? 8 : 3, (rows + wave / 2) / wave));
   } else {
     unsigned long long least = ~0ull;
     for (int k = 1; k <= (two_blocks ? 12 : 8); ++k) {
