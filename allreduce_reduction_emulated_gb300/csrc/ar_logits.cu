@@ -159,8 +159,8 @@ struct Slice {
 // One pass with a running maximum, four slots per thread on the way while four are
 // worked on.  GROUP threads take a row: a warp (eight rows in a block) where there
 // are many rows, else the block; with few long rows, a cluster of C blocks.
-// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 150 us, 7.2 TB/s (reads alone are
-// faster than the copy); one row of 32768 3.2 us.
+// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 152 us, 7.1 TB/s (reads alone are
+// faster than the copy); one row of 32768 3.1 us.
 // The lanes' pairs (m, rest), each (1 + rest) e^m, as one; in every lane.
 __device__ __forceinline__ float2 warp_rest(float2 v) {
   const float M = warp_max(v.x);
@@ -170,20 +170,19 @@ __device__ __forceinline__ float2 warp_rest(float2 v) {
 }
 
 struct LogprobPlan {
-  int C, per;              // blocks per row; slots per block
-  unsigned long long keep; // rows from here on stay in L2 (HINTS)
+  int C, per;  // blocks per row; slots per block
 };
 
-// Where the gradient follows and the matrix is not far larger than L2, the rows that
-// it begins with, the last kKeptBytes (the two halves of L2 may each hold a copy),
-// are to stay in L2 and the others to make room for them: the whole loss 55.3 ->
-// 51.7 us at 51 MB, 116.4 -> 113.6 at 240 MB, 187.5 -> 186.5 at 400 MB; nothing at 512 MB
-// and 1.8 GB.
+// Where the gradient follows and the matrix is not far larger than L2 (HINTS), the rows
+// that it begins with, `keep` and later, the last kKeptBytes (the two halves of L2 may
+// each hold a copy), are to stay in L2 and the others to make room for them: the whole
+// loss 55.3 -> 51.7 us at 51 MB, 116.4 -> 113.6 at 240 MB, 187.5 -> 186.5 at 400 MB; nothing
+// at 512 MB and 1.8 GB.
 constexpr unsigned long long kKeptBytes = 40ull << 20, kHintBytes = 400ull << 20;
 
 template <int DT, int GROUP, bool HINTS>
 __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, const LogprobPlan plan, float2* stats,
-                                                           float* factors) {
+                                                           float* factors, unsigned long long keep) {
   constexpr int N = Lanes<DT>::N, U = 4, W = kThreads / 32;
   using E = typename ElemOf<DT>::T;
   pdl_enter();
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
   const uint4* src = reinterpret_cast<const uint4*>(row - in.lead) + s0 + tid;
   const long long y = writer ? load_index(a.targets, a.target_bytes, t) : 0;
 
-  const uint64_t policy = HINTS ? keep_policy(t >= plan.keep) : 0;
+  const uint64_t policy = HINTS ? keep_policy(t >= keep) : 0;
   const auto load = [&](int at, uint4 (&r)[U]) {
     if (at + U * GROUP <= in.lim && at >= in.lo) {
 #pragma unroll
@@ -825,14 +824,14 @@ cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
   if (n <= 256 || (c.rows >= 16ull * c.sms && n <= (stats ? 2048 : 8192)))
     return launch_kernel(hints ? logprob_kernel<DT, 32, true> : logprob_kernel<DT, 32, false>,
                          (unsigned)((c.rows + 7) / 8), kThreads, 0, c.stream, true, Matrix<DT>(c),
-                         LogprobPlan{1, (int)n, keep}, stats, factors);
+                         LogprobPlan{1, (int)n}, stats, factors, keep);
   // a row over several blocks until there are two blocks for every SM, each with 1024 slots at least
   int C = 1;
   while (C < 8 && c.rows * C < 2ull * c.sms && n >= 2048ull * C) C *= 2;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = cluster_config((unsigned)c.rows * C, kThreads, 0, C, c.stream, attr);
   return cudaLaunchKernelEx(&cfg, hints ? logprob_kernel<DT, kThreads, true> : logprob_kernel<DT, kThreads, false>,
-                            Matrix<DT>(c), LogprobPlan{C, (int)(((n + C - 1) / C + 7) / 8 * 8), keep}, stats, factors);
+                            Matrix<DT>(c), LogprobPlan{C, (int)(((n + C - 1) / C + 7) / 8 * 8)}, stats, factors, keep);
 }
 
 // Rows per cluster, of 1 .. most.  A row takes a resident cluster 3.7 us by itself
