@@ -98,10 +98,13 @@ class GradClipper:
         if _current_device() != self._index:
             raise ArError(AR_ERR_INVALID_ARG, f"{what}: gradients are on {self.device}, the current device is "
                                               f"cuda:{_current_device()}")
-        handle = torch._C._cuda_getCurrentRawStream(self._index) if stream is None else _stream_handle(stream)
-        if handle != self._home:
+        current = torch._C._cuda_getCurrentRawStream(self._index)
+        handle = current if stream is None else _stream_handle(stream)
+        # The block of norms is memory of the home stream's pool, which is allocated from while home is current.
+        if handle != self._home or current != self._home:
             s = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
-            self._workspace.record_stream(s)
+            if handle != self._home:
+                self._workspace.record_stream(s)
             with torch.cuda.stream(s):
                 return handle, torch.empty((), dtype=torch.float32, device=self.device)
         if self._next == self.NORMS:
