@@ -16,6 +16,7 @@ from . import (AR_BFLOAT16, AR_ERR_INVALID_ARG, AR_ERR_UNSUPPORTED, AR_FLOAT32, 
                library)
 
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_capturing = torch.cuda.is_current_stream_capturing
 _DTYPES = {torch.float32: (AR_FLOAT32, 4), torch.bfloat16: (AR_BFLOAT16, 2)}  # (code, bytes)
 
 
@@ -74,6 +75,7 @@ class GradClipper:
             self._workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         self._at = self._workspace.data_ptr()
         self._norms, self._next = None, self.NORMS
+        self._captured = []
 
     def _laid_out(self, name: str, tensors):
         """(addresses, element counts, _DTYPES entries) of tensors the kernels can walk."""
@@ -100,13 +102,17 @@ class GradClipper:
                                               f"cuda:{_current_device()}")
         current = torch._C._cuda_getCurrentRawStream(self._index)
         handle = current if stream is None else _stream_handle(stream)
-        # The block of norms is memory of the home stream's pool, which is allocated from while home is current.
-        if handle != self._home or current != self._home:
+        # The block of norms is memory of the home stream's pool, which is allocated from while home is current.  A
+        # captured call has a norm to itself, which the clipper keeps: every replay writes it.
+        if handle != self._home or current != self._home or _capturing():
             s = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
             if handle != self._home:
                 self._workspace.record_stream(s)
             with torch.cuda.stream(s):
-                return handle, torch.empty((), dtype=torch.float32, device=self.device)
+                norm = torch.empty((), dtype=torch.float32, device=self.device)
+                if _capturing():
+                    self._captured.append(norm)
+                return handle, norm
         if self._next == self.NORMS:
             self._norms = torch.empty(self.NORMS, dtype=torch.float32, device=self.device)
             self._next = 0

@@ -46,3 +46,31 @@ def test_norms_are_from_the_pool_of_the_calls_stream(dev, current, call, given):
     for n in norms:
         assert abs(float(n) - 4000 ** 0.5) < 1e-4
         assert pool_of(n) == want.cuda_stream
+
+
+@pytest.mark.parametrize("how", ["current", "object", "handle"])
+def test_a_captured_call_keeps_its_norm(dev, how):
+    """A graph captured on the clipper's own stream writes its norm in every replay: no
+    other tensor may ever get that memory while the clipper is there."""
+    home = torch.cuda.Stream()
+    g = torch.full((1000,), 2.0, device=dev)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(home):
+        clipper = GradClipper([g])
+        clipper.norm()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=home):
+            norm = clipper.norm(stream={"current": None, "object": home, "handle": home.cuda_stream}[how])
+        graph.replay()
+        home.synchronize()
+        assert abs(float(norm) - 4000 ** 0.5) < 1e-4
+        at = norm.data_ptr()
+        del norm
+        for _ in range(GradClipper.NORMS + 2):        # a new block: the one before is given back
+            clipper.norm()
+        home.synchronize()
+        others = [torch.full((n,), -7.0, device=dev) for n in (128, 256, 1024) for _ in range(256)]
+        assert not [t for t in others if t.data_ptr() <= at < t.data_ptr() + 4 * t.numel()]
+        graph.replay()
+        home.synchronize()
+        assert all(bool((t == -7.0).all()) for t in others)
