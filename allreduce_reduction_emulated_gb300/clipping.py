@@ -9,6 +9,7 @@ Argument checks and marshalling only; the formulas are in include/ar_train.h.
 from __future__ import annotations
 
 import ctypes
+import threading
 
 import torch
 
@@ -31,7 +32,7 @@ class GradClipper:
 
     The list is checked and its addresses are laid out once; every call reads
     the gradients anew.  Calls of one clipper share a workspace of 32 KiB: they
-    may be on any stream but must not overlap on the GPU.  A captured call needs
+    may be on any stream and from any thread but must not overlap on the GPU.  A captured call needs
     its clipper, like its gradients, for as long as it is replayed.
     """
 
@@ -74,8 +75,10 @@ class GradClipper:
             self._home = torch.cuda.current_stream().cuda_stream
             self._workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
         self._at = self._workspace.data_ptr()
-        self._norms, self._next = None, self.NORMS
-        self._captured = []
+        self._norms, self._captured = [], []
+        # A call's kernels follow one another on the stream, whatever other threads call meanwhile: the library's
+        # functions run without the interpreter's lock.
+        self._lock = threading.Lock()
 
     def _laid_out(self, name: str, tensors):
         """(addresses, element counts, _DTYPES entries) of tensors the kernels can walk."""
@@ -113,17 +116,16 @@ class GradClipper:
                 if _capturing():
                     self._captured.append(norm)
                 return handle, norm
-        if self._next == self.NORMS:
-            self._norms = torch.empty(self.NORMS, dtype=torch.float32, device=self.device)
-            self._next = 0
-        self._next += 1
-        return handle, self._norms[self._next - 1]
+        if not self._norms:
+            self._norms.extend(torch.empty(self.NORMS, dtype=torch.float32, device=self.device).unbind())
+        return handle, self._norms.pop()
 
     def norm(self, stream=None):
         """The global norm, a 0-dim float32 tensor."""
-        handle, norm = self._begin("GradClipper.norm", stream)
-        st = self._lib.ar_grad_norm(self._n, self._grads, self._counts, self._dtypes, norm.data_ptr(),
-                                    self._at, self._bytes, handle)
+        with self._lock:
+            handle, norm = self._begin("GradClipper.norm", stream)
+            st = self._lib.ar_grad_norm(self._n, self._grads, self._counts, self._dtypes, norm.data_ptr(),
+                                        self._at, self._bytes, handle)
         if st != AR_SUCCESS:
             raise ArError(st, "GradClipper.norm")
         return norm
@@ -131,9 +133,10 @@ class GradClipper:
     def clip(self, max_norm: float, eps: float = 1e-6, stream=None):
         """Scales every gradient by min(1, max_norm / (norm + eps)) into `out`;
         returns the norm before clipping, a 0-dim float32 tensor."""
-        handle, norm = self._begin("GradClipper.clip", stream)
-        st = self._lib.ar_clip_grads(self._n, self._grads, self._outs, self._counts, self._dtypes, max_norm, eps,
-                                     norm.data_ptr(), self._at, self._bytes, handle)
+        with self._lock:
+            handle, norm = self._begin("GradClipper.clip", stream)
+            st = self._lib.ar_clip_grads(self._n, self._grads, self._outs, self._counts, self._dtypes, max_norm, eps,
+                                         norm.data_ptr(), self._at, self._bytes, handle)
         if st != AR_SUCCESS:
             raise ArError(st, "GradClipper.clip")
         return norm

@@ -1,5 +1,8 @@
 """Whose memory the norms of GradClipper are: the pool of the call's stream, one
 norm for one call, for as long as anything may write it."""
+import sys
+import threading
+
 import pytest
 import torch
 
@@ -74,3 +77,59 @@ def test_a_captured_call_keeps_its_norm(dev, how):
         graph.replay()
         home.synchronize()
         assert all(bool((t == -7.0).all()) for t in others)
+
+
+def test_threads_get_norms_of_their_own(dev):
+    """Calls from several threads on one stream, which runs them one after the other."""
+    clipper = GradClipper([torch.full((1000,), 2.0, device=dev)])
+    calls, threads = 5 * GradClipper.NORMS, 4
+    got = [[] for _ in range(threads)]
+    start = threading.Barrier(threads)
+
+    def work(mine):
+        start.wait()
+        for _ in range(calls):
+            mine.append(clipper.norm())
+
+    before = sys.getswitchinterval()
+    sys.setswitchinterval(1e-6)
+    try:
+        each = [threading.Thread(target=work, args=(mine,)) for mine in got]
+        for t in each:
+            t.start()
+        for t in each:
+            t.join()
+    finally:
+        sys.setswitchinterval(before)
+    torch.cuda.synchronize()
+    norms = [n for mine in got for n in mine]
+    assert len(norms) == calls * threads
+    assert len({n.data_ptr() for n in norms}) == len(norms)
+    assert all(abs(float(n) - 4000 ** 0.5) < 1e-4 for n in norms)
+
+
+def test_calls_from_threads_do_not_mix(dev):
+    """Clipping in place from several threads on one stream: each call takes the norm that the call
+    before it on the stream has left.  With bound and eps 1e4 a call makes n to n / (1 + n / 1e4), so
+    the reciprocals of the norms grow by 1e-4 from call to call.  The GPU is behind, so that launches wait."""
+    g = torch.full((8_000_000,), 8e6 ** -0.5, device=dev)
+    clipper = GradClipper([g])
+    calls, threads = 3000, 4
+    got = [[] for _ in range(threads)]
+    start = threading.Barrier(threads)
+
+    def work(mine):
+        start.wait()
+        for _ in range(calls):
+            mine.append(clipper.clip(1e4, eps=1e4))
+
+    each = [threading.Thread(target=work, args=(mine,)) for mine in got]
+    for t in each:
+        t.start()
+    for t in each:
+        t.join()
+    torch.cuda.synchronize()
+    inverse = sorted(1.0 / float(n) for mine in got for n in mine)
+    assert abs(inverse[0] - 1.0) < 1e-5
+    # a call's norm and coefficient each round a few times: 2e-6 of an inverse of at most 2.2
+    assert all(abs(b - a - 1e-4) < 1e-5 for a, b in zip(inverse, inverse[1:]))
