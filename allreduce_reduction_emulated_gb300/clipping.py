@@ -46,8 +46,7 @@ class GradClipper:
             raise ArError(AR_ERR_INVALID_ARG, f"{what}: no tensors")
         if len(self.out) != len(self.grads):
             raise ArError(AR_ERR_INVALID_ARG, f"{what}: {len(self.grads)} gradients, {len(self.out)} outputs")
-        self.device = self.grads[0].device
-        self._index = self.device.index
+        self.device = getattr(self.grads[0], "device", None)
         ats, counts, dtypes = self._laid_out("grads", self.grads)
         outs = ats
         spans = [(at, at + n * size, "grads", i) for i, (at, n, (_, size)) in enumerate(zip(ats, counts, dtypes)) if n]
@@ -64,7 +63,7 @@ class GradClipper:
             if start < end:
                 raise ArError(AR_ERR_INVALID_ARG, f"{what}: {a}[{i}] and {b}[{j}] share memory")
         n = len(self.grads)
-        self._n = n
+        self._n, self._index = n, self.device.index
         self._grads = (ctypes.c_void_p * n)(*ats)
         self._outs = (ctypes.c_void_p * n)(*outs)
         self._counts = (ctypes.c_size_t * n)(*counts)
@@ -85,6 +84,8 @@ class GradClipper:
         what = "GradClipper"
         ats, counts, dtypes = [], [], []
         for i, t in enumerate(tensors):
+            if not hasattr(t, "data_ptr"):
+                raise ArError(AR_ERR_INVALID_ARG, f"{what}: {name}[{i}] must be a tensor, got {type(t).__name__}")
             kind = _DTYPES.get(t.dtype)
             if kind is None:
                 raise ArError(AR_ERR_UNSUPPORTED, f"{what}: {name}[{i}] of {t.dtype}: float32 or bfloat16 needed")
