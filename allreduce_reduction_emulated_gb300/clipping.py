@@ -31,7 +31,9 @@ class GradClipper:
             (default: in place)
 
     The list is checked and its addresses are laid out once; every call reads
-    the gradients anew.  Calls of one clipper share a workspace of 32 KiB: they
+    the gradients anew.  The clipper keeps their memory: tensors that are made anew
+    (zero_grad(set_to_none=True)) or get another storage need a new clipper, which
+    goes best with gradients in flat buffers.  Calls of one clipper share a workspace of 32 KiB: they
     may be on any stream and from any thread but must not overlap on the GPU.  A captured call needs
     its clipper, like its gradients, for as long as it is replayed.
     """
@@ -64,6 +66,7 @@ class GradClipper:
                 raise ArError(AR_ERR_INVALID_ARG, f"{what}: {a}[{i}] and {b}[{j}] share memory")
         n = len(self.grads)
         self._n, self._index = n, self.device.index
+        self._memory = [t.untyped_storage() for t in (self.grads if out is None else self.grads + self.out)]
         self._grads = (ctypes.c_void_p * n)(*ats)
         self._outs = (ctypes.c_void_p * n)(*outs)
         self._counts = (ctypes.c_size_t * n)(*counts)

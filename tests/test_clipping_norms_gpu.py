@@ -133,3 +133,19 @@ def test_calls_from_threads_do_not_mix(dev):
     assert abs(inverse[0] - 1.0) < 1e-5
     # a call's norm and coefficient each round a few times: 2e-6 of an inverse of at most 2.2
     assert all(abs(b - a - 1e-4) < 1e-5 for a, b in zip(inverse, inverse[1:]))
+
+
+@pytest.mark.parametrize("which", ["grads", "out"])
+def test_memory_of_replaced_tensors_stays_the_clippers(dev, which):
+    """A tensor whose storage is replaced (t.data = ...): the clipper goes on with the memory that it was
+    given, which nothing else may get meanwhile."""
+    n = 1 << 20
+    g, o = torch.full((n,), 2.0, device=dev), torch.zeros(n, device=dev)
+    clipper = GradClipper([g], out=[o] if which == "out" else None)
+    t = o if which == "out" else g
+    at = t.data_ptr()
+    t.data = torch.zeros(8, device=dev)
+    others = [torch.full((n,), -7.0, device=dev) for _ in range(8)]
+    assert at not in [x.data_ptr() for x in others]
+    assert abs(float(clipper.clip(1.0)) - 2.0 * n ** 0.5) < 1e-2
+    assert all(bool((x == -7.0).all()) for x in others)
