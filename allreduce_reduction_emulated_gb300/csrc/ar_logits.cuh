@@ -342,8 +342,10 @@ __device__ __forceinline__ float policy_token(const PolicyParams& p, float old, 
     const float q = ref - lp;
     const float e = expm1f(q);  // e^q - 1 without cancellation: policies start at their reference
     const float kl = e - q;
-    term += p.kl_coef * kl;
-    d -= p.kl_coef * e;
+    if (p.kl_coef != 0.0f) {  // of a statistic alone nothing is added: it may be infinite
+      term += p.kl_coef * kl;
+      d -= p.kl_coef * e;
+    }
     sum.kl += w * kl;
   }
   sum.loss += w * term;

@@ -73,7 +73,8 @@ ar_status_t ar_token_logprobs(const void* logits, size_t rows, size_t vocab, siz
  *   grad[t, j] = scale w_t dterm_t ([j == y_t] - p[t, j]),  p = softmax of the row
  *
  *   old_logprobs, advantages   rows floats
- *   ref_logprobs  rows floats; NULL leaves the KL term out (kl_coef is then ignored)
+ *   ref_logprobs  rows floats; NULL leaves the KL term out (kl_coef is then ignored);
+ *                 with kl_coef == 0 it makes the statistic alone
  *   grad          rows by vocab, the logits' type, row stride grad_stride; may be
  *                 the logits themselves (same address and stride), any other
  *                 overlap with them is rejected
