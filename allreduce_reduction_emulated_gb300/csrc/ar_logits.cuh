@@ -68,7 +68,7 @@ __device__ __forceinline__ void from_float(uint16_t* p, float x) { *p = (uint16_
 // Element by element, at an even / odd distance, these took (2489 x 50001 bf16) 334 / 330 us,
 // now 111 / 175 (policy), 301 / 296, now 127 / 140 (preference); clipping 100M bf16 232 / 221, now
 // 93 / 108.  A whole slot put together by shuffles and stored as one took 140, 148 and 111.
-// fp32 (1111 x 50001): preference 125, now 105, but policy 86, now 106.
+// fp32 (1111 x 50001): preference 125, now 105; the policy loss stores its fp32 elements one by one.
 template <class E>
 __device__ __forceinline__ void store_apart(E* to, uint4 v, bool warp) {
   if (sizeof(E) == 4 || ((uintptr_t)to & 2) == 0) {
