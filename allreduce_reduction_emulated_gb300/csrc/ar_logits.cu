@@ -439,6 +439,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
 
   PolicySums sum;
   int done = 0;
+  uint32_t zero = 0;
   for (int i = 0; i < rows; ++i) {
     if (!(live >> i & 1)) {
       E* const grad = a.grad + (row0 + i) * a.grad_stride;
@@ -497,9 +498,9 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       s2[k & 1] = add2(s2[k & 1], part);
     }
     const float ws = warp_sum((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y));
-    // Once all pairs are there, gradients may overwrite the row (in place): not before this warp's targets' logits
-    // have arrived in their register.
-    const uint32_t zero = __float_as_uint(x_l) & plan.zero;
+    // Once all pairs are there, gradients may overwrite the row (in place): not before the targets' logits have arrived,
+    // in every lane, whichever lanes send.  So the addresses of the first pairs come from a vote on them.
+    if (done == 0) zero = __ballot_sync(~0u, __float_as_uint(x_l) & plan.zero);
     if constexpr (CLUSTER) {
       if (lane < C) st_async(pair_to + b * (kMaxCluster * W * 8) + zero, make_float2(m, ws), bars_to + 8 * b);
     } else {

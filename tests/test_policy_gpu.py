@@ -41,3 +41,21 @@ def test_kl_term_of_coefficient_zero_is_left_out(dev, V):
     r = losses.policy_loss(logits, y, old, adv, ref_logprobs=ref, kl_coef=0.0)
     assert torch.equal(r.loss, plain.loss) and torch.equal(r.grad, plain.grad)
     assert float(r.kl) == INF and math.isfinite(float(r.loss))
+
+
+@pytest.mark.parametrize("dtype", BOTH, ids=IDS)
+@pytest.mark.parametrize("T,V", [(3000, 3000), (2000, 9000), (1200, 50003), (300, 131072)])
+def test_in_place_behind_masked_rows(dev, T, V, dtype):
+    """In place where the first rows that a cluster works on are masked: the same bits as in a new gradient."""
+    g = torch.Generator(device=dev).manual_seed(V)
+    logits = (3 * torch.randn(T, V, device=dev, generator=g)).to(dtype)
+    y = torch.randint(0, V, (T,), device=dev, generator=g)
+    adv = torch.randn(T, device=dev, generator=g)
+    old = losses.token_logprobs(logits, y) + 0.1
+    for masked in (1, 2, 3, 5):
+        w = (torch.arange(T, device=dev) % (masked + 1) == masked).float()
+        first = losses.policy_loss(logits, y, old, adv, weights=w)
+        x = logits.clone()
+        again = losses.policy_loss(x, y, old, adv, weights=w, grad=x)
+        assert torch.equal(again.grad, first.grad) and torch.equal(again.stats, first.stats)
+        assert torch.equal(again.logprobs, first.logprobs)
