@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, co
 // a slice of the row in registers, K slots of 16 bytes per thread.  The slice of
 // the next row is on its way into shared memory (cp.async) while a row is worked
 // on; a thread reads only what it copied itself, so the copies need no barrier.
-// Each warp takes its maximum and its sum of exponentials, and sends the pair to
+// Each warp takes its maximum and its sum of exponentials, and sends the two to
 // every block of the cluster (st.async, counted by an mbarrier); one warp of each
 // block joins them and computes the token's loss, and one block barrier hands the
 // factors to the others, which write the gradient from their registers.
@@ -358,7 +358,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
   constexpr bool kEachWarp = !CLUSTER && W <= 4;  // every warp computes the token's loss for itself
   using E = typename ElemOf<DT>::T;
   extern __shared__ uint4 next[];                   // [K][THREADS]: the row that is on its way
-  // (maximum, sum) of every warp, by parity: a block may be one row ahead
+  // (maximum, rest) of every warp, by parity: a block may be one row ahead
   __shared__ float2 pairs[2][(CLUSTER ? kMaxCluster : 1) * W];
   __shared__ float4 result;
   __shared__ uint64_t bars[2];
@@ -497,14 +497,21 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       }
       s2[k & 1] = add2(s2[k & 1], part);
     }
-    const float ws = warp_sum((s2[0].x + s2[0].y) + (s2[1].x + s2[1].y));
+    // What is added to the maximum's 1 rounds, and for a near-certain token it is all that its log-probability is made
+    // of: each 1 is taken out before the others are added, and (m, rest) stands for (1 + rest) e^m from here on.
+    // (Compared and swapped, not fmaxf: a NaN has to stay.)
+    const float2 both = add2(s2[0], s2[1]);
+    const bool swap = both.y > both.x;
+    const float most = swap ? both.y : both.x, less = swap ? both.x : both.y;
+    const bool one = most >= 1.0f;                 // in the maximum's lane, and perhaps in others
+    const float rest = warp_sum((one ? most - 1.0f : most) + less) + (float)(__popc(__ballot_sync(~0u, one)) - 1);
     // Once all pairs are there, gradients may overwrite the row (in place): not before the targets' logits have arrived,
     // in every lane, whichever lanes send.  So the addresses of the first pairs come from a vote on them.
     if (done == 0) zero = __ballot_sync(~0u, __float_as_uint(x_l) & plan.zero);
     if constexpr (CLUSTER) {
-      if (lane < C) st_async(pair_to + b * (kMaxCluster * W * 8) + zero, make_float2(m, ws), bars_to + 8 * b);
+      if (lane < C) st_async(pair_to + b * (kMaxCluster * W * 8) + zero, make_float2(m, rest), bars_to + 8 * b);
     } else {
-      if (lane == 0) pairs[b][warp + zero] = make_float2(m, ws);
+      if (lane == 0) pairs[b][warp + zero] = make_float2(m, rest);
     }
     issue(i + 1);
 
@@ -512,18 +519,25 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     float4 res = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if constexpr (!CLUSTER) __syncthreads();
     if (kEachWarp || warp == 0) {
-      // the row's maximum M and sum S
+      // the row's maximum M and sum 1 + R
       const bool ok = !CLUSTER || mbar_wait(bars_at + 8 * b, done >> 1 & 1, kWaitLimit);
-      float M = -FLT_MAX, S = 0.0f;
+      float M = -FLT_MAX, R = 0.0f;
       for (int q = lane; q < C * W; q += 32) M = fmaxf(M, pairs[b][q].x);
       M = warp_max(M);
-      for (int q = lane; q < C * W; q += 32) S += pairs[b][q].y * exp_diff(pairs[b][q].x, M);
-      S = warp_sum(S);
-      if (!ok) S = __int_as_float(0x7fffffff);
-      const float lp = (__shfl_sync(~0u, x_l, i) - M) - logf(S);
+      int ones = -1;                               // pairs of the maximum, but for one
+      for (int q = lane; q - lane < C * W; q += 32) {
+        const float2 v = q < C * W ? pairs[b][q] : make_float2(-FLT_MAX, -1.0f);
+        R += v.x == M ? v.y : (1.0f + v.y) * exp_diff(v.x, M);
+        ones += __popc(__ballot_sync(~0u, v.x == M));
+      }
+      R = warp_sum(R) + (float)ones;
+      if (!ok) R = __int_as_float(0x7fffffff);
+      // log(1 + R): the logarithm of the rounded sum, and what its rounding took
+      const float S = 1.0f + R, inverse = 1.0f / S;
+      const float lp = (__shfl_sync(~0u, x_l, i) - M) - (logf(S) + __fdividef(R - (S - 1.0f), S));
       const float c = policy_token(p, __shfl_sync(~0u, old_l, i), __shfl_sync(~0u, adv_l, i),
                                    __shfl_sync(~0u, ref_l, i), __shfl_sync(~0u, w_l, i), lp, sum);
-      res = make_float4(M, -c / S, -c, lp);
+      res = make_float4(M, -c * inverse, -c, lp);
       if (rank == 0 && tid == 0) a.logprobs[row0 + i] = lp;
       if (!kEachWarp && lane == 0) result = res;
     }
@@ -533,9 +547,10 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     }
     ++done;
     // Where registers are shortest the slice is computed once more, not kept (4096 x 32768 bf16 94 -> 92 us, 2000 x
-    // 30000 fp32 92 -> 85; with 7 slots per thread it costs more than it frees, 2489 x 50001 bf16 99 -> 105).
+    // 30000 fp32 92 -> 85, 2000 x 26000 fp32 72.5 -> 70; with 7 slots of bf16 per thread it costs more than it frees,
+    // 2489 x 50001 99 -> 105).
     int again = i;
-    if constexpr (K == 8 && THREADS == 256) asm volatile("" : "+r"(again));
+    if constexpr (THREADS == 256 && (K == 8 || (K == 7 && DT == kF32))) asm volatile("" : "+r"(again));
     const Slice<DT> in(logits + again * a.stride, V, s0, plan.per);
     E* const grad = a.grad + (row0 + again) * a.grad_stride;
     // fp32: the exponentials, to the warp's maximum; bf16: the logits, whose exponentials are taken again (half the

@@ -59,3 +59,34 @@ def test_in_place_behind_masked_rows(dev, T, V, dtype):
         again = losses.policy_loss(x, y, old, adv, weights=w, grad=x)
         assert torch.equal(again.grad, first.grad) and torch.equal(again.stats, first.stats)
         assert torch.equal(again.logprobs, first.logprobs)
+
+
+@pytest.mark.parametrize("dtype", BOTH, ids=IDS)
+@pytest.mark.parametrize("low", [-14.0, -18.0, -24.0])
+@pytest.mark.parametrize("V", [5003, 9000, 20011, 50003, 131072, 262100])
+def test_near_certain_tokens(dev, V, low, dtype):
+    """One logit far above all others: lp = -log(1 + rest), the rest between 1e-7 and 0.3.  A thread
+    adds at most 32 of a row's terms (64 from 65536 columns on) to the maximum's 1 and may lose them (32 / V of
+    the rest); 1% of it covers that and what e^z rounds.  token_logprobs agrees, so that ratios of freshly scored tokens are 1, and the
+    target's gradient balances the other columns'."""
+    T = 13
+    g = torch.Generator(device=dev).manual_seed(V)
+    logits = (low + torch.rand(T, V, device=dev, generator=g)).to(dtype)
+    y = torch.arange(T, device=dev) * 389 % V
+    logits[torch.arange(T, device=dev), y] = 0.0
+    x = logits.double()
+    x[torch.arange(T, device=dev), y] = -INF
+    rest = x.exp().sum(1)
+    want = -torch.log1p(rest)
+    fresh = losses.token_logprobs(logits, y)
+    adv = torch.ones(T, device=dev)
+    r = losses.policy_loss(logits, y, fresh, adv, scale=-1.0)
+    assert bool(((r.logprobs.double() - want).abs() <= 0.01 * want.abs()).all())
+    assert bool(((fresh.double() - want).abs() <= 0.01 * want.abs()).all())
+    assert bool(((r.logprobs - fresh).double().abs() <= 0.01 * want.abs()).all())
+    # grad = r ([j = y] - p_j): 1 - p of the target, and the others' sum
+    p = rest / (1 + rest)
+    at = r.grad[torch.arange(T, device=dev), y].double()
+    assert bool(((at - p).abs() <= (0.01 + 2.0 ** -8) * p).all())
+    others = r.grad.double().sum(1) - at
+    assert bool(((others + p).abs() <= (0.01 + 2.0 ** -8) * p).all())
