@@ -356,6 +356,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS)
 policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, float4* partial) {
   constexpr int N = Lanes<DT>::N, W = THREADS / 32;
   constexpr bool kEachWarp = !CLUSTER && W <= 4;  // every warp computes the token's loss for itself
+  // A gradient at another alignment, in a loop as the aligned one has / by elements: bf16 2489 x 50001 175 / 328 us; fp32
+  // 8192 x 8000 (one block of 8 slots per thread) 95 / 99, other fp32, 1111 x 50001 105 / 89, 2000 x 60000 230 / 182,
+  // 16000 x 2000 56.5 / 52, and 4096 x 30000 204 / 213, where the loop's registers cost aligned rows more (2000 x 30000
+  // 80.4 / 78.2).
+  constexpr bool kWords = DT == kBF16 || (!CLUSTER && THREADS == 256 && K == 8);
   using E = typename ElemOf<DT>::T;
   extern __shared__ uint4 next[];                   // [K][THREADS]: the row that is on its way
   // (maximum, rest) of every warp, by parity: a block may be one row ahead
@@ -579,17 +584,16 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       for (int k = 0; k < K; ++k)
         if (k * THREADS + tid < in.lim && (k > 0 || tid >= in.lo))
           st_stream(reinterpret_cast<uint4*>(dst + k * THREADS * 16), narrow<DT>(values(k), 1.0f, false));
-    } else if constexpr (DT == kBF16) {  // the gradient's rows start at another alignment (by words and halves: the
-                                         // registers of a shuffle slowed the other rows down, 4096 x 32768 91 -> 95 us)
+    } else if constexpr (kWords) {  // the gradient's rows start at another alignment (by words and halves: the registers
+                                    // of a shuffle slowed the other rows down, 4096 x 32768 bf16 91 -> 95 us)
       E* dst = grad + ((s0 + tid) * N - in.lead);
 #pragma unroll
       for (int k = 0; k < K; ++k)
         if (k * THREADS + tid < in.lim && (k > 0 || tid >= in.lo))
           store_apart(dst + k * THREADS * N, narrow<DT>(values(k), 1.0f, false), false);
     }
-    // by elements: slots at the row's ends, and fp32 at another alignment (in a loop as above 1111 x 50001 took 105 us,
-    // not 89, 16000 x 2000 56, not 54; but 8192 x 8000 95, not 99)
-    const bool each = DT == kF32 && !same;
+    // by elements: slots at the row's ends, and all at another alignment but kWords
+    const bool each = !kWords && !same;
     const bool first = in.head == tid, last = in.tail >= 0 && in.tail % THREADS == tid;
     if (each || first || last) {
 #pragma unroll
