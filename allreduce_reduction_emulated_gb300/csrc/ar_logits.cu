@@ -11,6 +11,7 @@
 // Comments give times on one GB300 (152 SMs; a copy reaches 6.79 TB/s).
 #include <algorithm>
 #include <atomic>
+#include <climits>
 
 #include "ar_logits.cuh"
 #include "ar_train.h"
@@ -40,34 +41,21 @@ struct Matrix {
         target_bytes(c.target_bytes), weights(c.weights), logprobs(c.logprobs) {}
 };
 
-template <int DT>
-__device__ __forceinline__ MaxSum row_stats(const typename ElemOf<DT>::T* row, long long vocab, float2* sh) {
-  const Slots<DT> in(row, vocab);
-  MaxSum a;
-  const long long n = in.count();
-  for (long long s = threadIdx.x; s < n; s += kThreads) {
-    float x[Lanes<DT>::N];
-    in.load(s, x, -INFINITY);
-    a.add(x);
-  }
-  return block_join<kThreads>(a, sh);
-}
-
 // grad[j] = c * ([j == y] - p[j]).  The target's 1 - p is -expm1(log p).
 template <int DT>
 __device__ __forceinline__ void row_grad(const typename ElemOf<DT>::T* row, typename ElemOf<DT>::T* grad,
-                                         long long vocab, long long y, float lp, MaxSum st, float c) {
+                                         long long vocab, long long y, float lp, float m, float sum, float c) {
   constexpr int N = Lanes<DT>::N;
   const Slots<DT> in(row, vocab);
   const bool same = (((uintptr_t)row ^ (uintptr_t)grad) & 15) == 0;
-  const float f = -c / st.s;
+  const float f = -c / sum;
   const long long n = in.count();
   for (long long s = threadIdx.x; s < n; s += kThreads) {
     float x[N];
     in.load(s, x, -INFINITY);
     const long long j = in.first(s);
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = j + i == y ? -c * expm1f(lp) : f * exp_diff(x[i], st.m);
+    for (int i = 0; i < N; ++i) x[i] = j + i == y ? -c * expm1f(lp) : f * exp_diff(x[i], m);
     store_slot<DT>(in, grad, same, s, x);
   }
 }
@@ -151,16 +139,8 @@ struct Slice {
   }
 };
 
-// ----------------------------------------------------------- log-probabilities
+// -------------------------------------------------------------- one row's sum
 
-// Log-probability of every row's target; stats != NULL: {maximum, sum of e^(x -
-// maximum)} too, and 0 into factors[t], for the preference loss.
-//
-// One pass with a running maximum, four slots per thread on the way while four are
-// worked on.  GROUP threads take a row: a warp (eight rows in a block) where there
-// are many rows, else the block; with few long rows, a cluster of C blocks.
-// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 152 us, 7.1 TB/s (reads alone are
-// faster than the copy); one row of 32768 3.1 us.
 // The lanes' pairs (m, rest), each (1 + rest) e^m, as one; in every lane.
 __device__ __forceinline__ float2 warp_rest(float2 v) {
   const float M = warp_max(v.x);
@@ -169,43 +149,23 @@ __device__ __forceinline__ float2 warp_rest(float2 v) {
   return make_float2(M, warp_sum(part));
 }
 
-struct LogprobPlan {
-  int C, per;  // blocks per row; slots per block
-};
+// The same over a block of kThreads.  `sh` holds a pair per warp; the block must
+// synchronize before it is written again.
+__device__ __forceinline__ float2 block_rest(float2 v, float2* sh) {
+  const int lane = threadIdx.x & 31;
+  v = warp_rest(v);
+  if (lane == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_rest(lane < kThreads / 32 ? sh[lane] : make_float2(-FLT_MAX, -1.0f));
+}
 
-// Where the gradient follows and the matrix is not far larger than L2 (HINTS), the rows
-// that it begins with, `keep` and later, the last kKeptBytes (the two halves of L2 may
-// each hold a copy), are to stay in L2 and the others to make room for them: the whole
-// loss 55.3 -> 51.7 us at 51 MB, 116.4 -> 113.6 at 240 MB, 187.5 -> 186.5 at 400 MB; nothing
-// at 512 MB and 1.8 GB.
-constexpr unsigned long long kKeptBytes = 40ull << 20, kHintBytes = 400ull << 20;
-
+// One thread's share of a slice, by GROUP threads: the pair (m, rest) that stands for
+// (1 + rest) e^m.  One pass with a running maximum, four slots on the way while four are
+// worked on.
 template <int DT, int GROUP, bool HINTS>
-__global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, const LogprobPlan plan, float2* stats,
-                                                           float* factors, unsigned long long keep) {
-  constexpr int N = Lanes<DT>::N, U = 4, W = kThreads / 32;
-  using E = typename ElemOf<DT>::T;
-  pdl_enter();
-  __shared__ float2 sh[W], mine;
-  const int tid = threadIdx.x % GROUP, lane = threadIdx.x & 31;
-  const unsigned long long t = GROUP == kThreads ? blockIdx.x / plan.C
-                                                 : blockIdx.x * (unsigned long long)(kThreads / GROUP) +
-                                                       threadIdx.x / GROUP;
-  if (t >= a.rows) return;                         // whole warps; never with GROUP == kThreads
-  const int rank = GROUP == kThreads ? (int)cluster_rank() : 0;
-  const bool writer = rank == 0 && tid == 0;
-  if (writer && stats) factors[t] = 0.0f;
-  if (a.weights && a.weights[t] == 0.0f) {         // the same in all blocks of the cluster
-    if (writer) a.logprobs[t] = 0.0f;
-    return;
-  }
-  const int V = (int)a.vocab, s0 = rank * plan.per;
-  const E* row = a.logits + t * a.stride;
-  const Slice<DT> in(row, V, s0, plan.per);
-  const uint4* src = reinterpret_cast<const uint4*>(row - in.lead) + s0 + tid;
-  const long long y = writer ? load_index(a.targets, a.target_bytes, t) : 0;
-
-  const uint64_t policy = HINTS ? keep_policy(t >= keep) : 0;
+__device__ __forceinline__ float2 row_part(const Slice<DT>& in, int V, int s0, int tid, uint64_t policy) {
+  constexpr int N = Lanes<DT>::N, U = 4;
+  const uint4* src = reinterpret_cast<const uint4*>(in.row - in.lead) + s0 + tid;
   const auto load = [&](int at, uint4 (&r)[U]) {
     if (at + U * GROUP <= in.lim && at >= in.lo) {
 #pragma unroll
@@ -237,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
       const int j = (s0 + q) * N - in.lead;
       float v[N], top = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < N; ++x) v[x] = j + x >= 0 && j + x < V ? to_float(row[j + x]) : -INFINITY;
+      for (int x = 0; x < N; ++x) v[x] = j + x >= 0 && j + x < V ? to_float(in.row[j + x]) : -INFINITY;
 #pragma unroll
       for (int x = 0; x < N; ++x) top = fmaxf(top, v[x]);
       grow(top);
@@ -265,16 +225,62 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
     lost = add2(add, minus(add2(sum, minus(s2))));
     s2 = sum;
   }
-  // Joined: threads, warps, blocks, as pairs (m, rest) that stand for (1 + rest) e^m: for a near-certain token the sum
-  // is 1 and a little, and the little is its log-probability.
+  // for a near-certain token the sum is 1 and a little, and the little is its log-probability
   const bool swap = s2.y > s2.x;                   // not fmaxf: a NaN has to stay
   const float more = swap ? s2.y : s2.x, less = (swap ? s2.x : s2.y) + (lost.x + lost.y);
-  float2 v = make_float2(m, (more - 1.0f) + less);
-  v = warp_rest(v);
-  if constexpr (GROUP == kThreads) {
-    if (lane == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = warp_rest(lane < W ? sh[lane] : make_float2(-FLT_MAX, -1.0f));
+  return make_float2(m, (more - 1.0f) + less);
+}
+
+// ----------------------------------------------------------- log-probabilities
+
+// Log-probability of every row's target; stats != NULL: {maximum, sum of e^(x -
+// maximum)} too, and 0 into factors[t], for the preference loss.
+//
+// GROUP threads take a row: a warp (eight rows in a block) where there are many
+// rows, else the block; with few long rows, a cluster of C blocks.
+// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 152 us, 7.1 TB/s (reads alone are
+// faster than the copy); one row of 32768 3.1 us.
+struct LogprobPlan {
+  int C, per;  // blocks per row; slots per block
+};
+
+// Where the gradient follows and the matrix is not far larger than L2 (HINTS), the rows
+// that it begins with, `keep` and later, the last kKeptBytes (the two halves of L2 may
+// each hold a copy), are to stay in L2 and the others to make room for them: the whole
+// loss 55.3 -> 51.7 us at 51 MB, 116.4 -> 113.6 at 240 MB, 187.5 -> 186.5 at 400 MB; nothing
+// at 512 MB and 1.8 GB.
+constexpr unsigned long long kKeptBytes = 40ull << 20, kHintBytes = 400ull << 20;
+
+template <int DT, int GROUP, bool HINTS>
+__global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, const LogprobPlan plan, float2* stats,
+                                                           float* factors, unsigned long long keep) {
+  using E = typename ElemOf<DT>::T;
+  pdl_enter();
+  __shared__ float2 sh[kThreads / 32], mine;
+  const int tid = threadIdx.x % GROUP, lane = threadIdx.x & 31;
+  const unsigned long long t = GROUP == kThreads ? blockIdx.x / plan.C
+                                                 : blockIdx.x * (unsigned long long)(kThreads / GROUP) +
+                                                       threadIdx.x / GROUP;
+  if (t >= a.rows) return;                         // whole warps; never with GROUP == kThreads
+  const int rank = GROUP == kThreads ? (int)cluster_rank() : 0;
+  const bool writer = rank == 0 && tid == 0;
+  if (writer && stats) factors[t] = 0.0f;
+  if (a.weights && a.weights[t] == 0.0f) {         // the same in all blocks of the cluster
+    if (writer) a.logprobs[t] = 0.0f;
+    return;
+  }
+  const int V = (int)a.vocab, s0 = rank * plan.per;
+  const E* row = a.logits + t * a.stride;
+  const Slice<DT> in(row, V, s0, plan.per);
+  const long long y = writer ? load_index(a.targets, a.target_bytes, t) : 0;
+
+  const uint64_t policy = HINTS ? keep_policy(t >= keep) : 0;
+  // joined: threads, warps, blocks
+  float2 v = row_part<DT, GROUP, HINTS>(in, V, s0, tid, policy);
+  if constexpr (GROUP != kThreads) {
+    v = warp_rest(v);
+  } else {
+    v = block_rest(v, sh);
     if (plan.C > 1) {
       if (threadIdx.x == 0) mine = v;
       cluster_sync();
@@ -292,8 +298,9 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
 // --------------------------------------------------------------- policy loss
 
 // Rows too long to be held (above 65536 slots, 524,288 bf16 logits): a block per row,
-// which it reads twice, the second time from L2 (its whole range of sizes, before the
-// kernel below was there: 8192 x 131072 bf16 1200 us, 4096 x 32768 154 us).
+// which it reads twice.  1000 x 1048576 bf16 1395 us, 500 x 700000 497 us, 64 x 600001 322 us:
+// 0.44, 0.41 and 0.07 of one read and one write at the copy's rate (one block per SM and
+// second reads from HBM; few rows leave SMs idle).
 template <int DT>
 __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, const PolicyParams p, float4* partial) {
   pdl_enter();
@@ -310,16 +317,18 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, co
     }
     const typename ElemOf<DT>::T* row = a.logits + t * a.stride;
     const long long y = load_index(a.targets, a.target_bytes, t);
-    const MaxSum st = row_stats<DT>(row, (long long)a.vocab, sh);
+    const int V = (int)a.vocab;
+    const Slice<DT> in(row, V, 0, INT_MAX);
+    const float2 v = block_rest(row_part<DT, kThreads, false>(in, V, 0, threadIdx.x, 0), sh);
     if (threadIdx.x == 0) {
-      const float lp = target_logprob(row, (long long)a.vocab, y, st.m, st.s);
+      const float lp = y >= 0 && y < V ? (to_float(row[y]) - v.x) - log1pf(v.y) : __int_as_float(0x7fffffff);
       a.logprobs[t] = lp;
       sh_c[0] = policy_token(p, p.old_logprobs[t], p.advantages[t], p.ref_logprobs ? p.ref_logprobs[t] : 0.0f, w, lp,
                              sum);
       sh_c[1] = lp;
     }
     __syncthreads();  // also: the target's logit is read before an in-place gradient is written
-    row_grad<DT>(row, grad, (long long)a.vocab, y, sh_c[1], st, sh_c[0]);
+    row_grad<DT>(row, grad, V, y, sh_c[1], v.x, 1.0f + v.y, sh_c[0]);
     __syncthreads();
   }
   if (threadIdx.x == 0) partial[blockIdx.x] = make_float4(sum.loss, sum.kl, sum.clipped, sum.weight);

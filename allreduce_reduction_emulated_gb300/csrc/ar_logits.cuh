@@ -256,46 +256,10 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return r;
 }
 
-// ------------------------------------------------------------ statistics
+// ------------------------------------------------------------------ block sums
 
-// Running maximum m and sum s of e^(x - m).  m starts at the lowest finite
-// value, not at -infinity, so that x - m is never -infinity - -infinity.
-struct MaxSum {
-  float m = -FLT_MAX, s = 0.0f;
-  template <int N>
-  __device__ __forceinline__ void add(const float (&x)[N]) {
-    float mv = x[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) mv = fmaxf(mv, x[i]);
-    if (mv > m) {
-      s *= exp_diff(m, mv);
-      m = mv;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) s += exp_diff(x[i], m);
-  }
-  __device__ __forceinline__ void join(float m2, float s2) {
-    const float mm = fmaxf(m, m2);
-    s = s * exp_diff(m, mm) + s2 * exp_diff(m2, mm);
-    m = mm;
-  }
-};
-
-// Over a block of THREADS threads; every thread gets the result.  `sh` holds
-// THREADS / 32 pairs; the block must synchronize before it is written again.
-template <int THREADS>
-__device__ __forceinline__ MaxSum block_join(MaxSum a, float2* sh) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) a.join(__shfl_xor_sync(~0u, a.m, d), __shfl_xor_sync(~0u, a.s, d));
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = make_float2(a.m, a.s);
-  __syncthreads();
-  MaxSum r;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) r.join(sh[w].x, sh[w].y);
-  return r;
-}
-
-// Sum over a block; valid in every thread.  `sh` as above.
+// Sum over a block of THREADS threads; valid in every thread.  `sh` holds
+// THREADS / 32 values; the block must synchronize before it is written again.
 template <int THREADS, class T>
 __device__ __forceinline__ T block_sum(T v, T* sh) {
 #pragma unroll
@@ -309,13 +273,6 @@ __device__ __forceinline__ T block_sum(T v, T* sh) {
 }
 
 // ------------------------------------------------------------ per token
-
-// log-probability of the target; NaN for a target outside the row
-template <class E>
-__device__ __forceinline__ float target_logprob(const E* row, long long vocab, long long y, float m, float s) {
-  if (y < 0 || y >= vocab) return __int_as_float(0x7fffffff);
-  return (to_float(row[y]) - m) - logf(s);
-}
 
 struct PolicyParams {
   const float* old_logprobs;

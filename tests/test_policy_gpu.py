@@ -90,3 +90,26 @@ def test_near_certain_tokens(dev, V, low, dtype):
     assert bool(((at - p).abs() <= (0.01 + 2.0 ** -8) * p).all())
     others = r.grad.double().sum(1) - at
     assert bool(((others + p).abs() <= (0.01 + 2.0 ** -8) * p).all())
+
+
+@pytest.mark.parametrize("dtype", BOTH, ids=IDS)
+@pytest.mark.parametrize("V", [600001, (1 << 21) + 3, 1 << 24])
+def test_very_long_rows(dev, V, dtype):
+    """Rows that no cluster holds: flat ones, ones with a hundred equal maxima, near-certain tokens.  The bounds are
+    those of short rows: sums are carried over."""
+    T = 5
+    x = torch.full((T, V), -20.0, dtype=dtype, device=dev)
+    x[0] = 1.5
+    x[1, ::2] = -19.0
+    x[2, ::V // 100] = 0.0
+    x[3, 17], x[4, V - 1] = 8.0, 4.0
+    y = torch.tensor([3, 8, V // 100, 17, V - 1], device=dev)
+    w = torch.ones(T, device=dev)
+    want, p = tu.rows64(x, y)
+    fresh = losses.token_logprobs(x, y)
+    tu.assert_logprobs(fresh, want)
+    r = losses.policy_loss(x, y, fresh, w, scale=1.0)
+    tu.assert_logprobs(r.logprobs, want)
+    assert bool(((r.logprobs.double() - want)[3:].abs() <= 0.01 * want[3:].abs()).all())
+    assert bool(((r.logprobs - fresh).double()[3:].abs() <= 0.01 * want[3:].abs()).all())
+    tu.assert_grad(r.grad, y, tu.policy64(x, y, fresh, w, None, w)["c"], p, w.double(), extra=4e-6)
