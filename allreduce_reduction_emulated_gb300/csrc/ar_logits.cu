@@ -219,10 +219,10 @@ __device__ __forceinline__ float2 row_part(const Slice<DT>& in, int V, int s0, i
       r[u] = next[u];
     }
     // where the maximum is among the terms, every addition to its 1 rounds: four slots are added up first, and what
-    // that addition loses is carried over to the next
+    // that addition loses, of the larger or of the smaller, is carried over to the next
     const float2 add = add2(add2(add2(part[0], part[1]), add2(part[2], part[3])), lost);
-    const float2 sum = add2(s2, add);
-    lost = add2(add, minus(add2(sum, minus(s2))));
+    const float2 sum = add2(s2, add), had = add2(sum, minus(add));
+    lost = add2(add2(s2, minus(had)), add2(add, minus(add2(sum, minus(had)))));
     s2 = sum;
   }
   // for a near-certain token the sum is 1 and a little, and the little is its log-probability
