@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <cstdlib>
 
 #include "ar_logits.cuh"
 #include "ar_train.h"
@@ -355,10 +356,15 @@ struct RowPlan {
   int most;     // slots of a row at its worst alignment
   int run;      // rows per cluster, at most 32
   uint32_t zero;  // 0, which the compiler does not know
+  int late;     // for tests: the block of every cluster that gives its first wait up (-1: none)
 };
 
 constexpr int kMaxCluster = 16;
-constexpr uint32_t kWaitLimit = 1u << 20;  // polls; a wait that runs out gives NaN
+// Polls, together about a second.  A block whose wait for the cluster's pairs runs out waits for no others and uses its
+// barriers no more.  It goes on through its rows and sends its pairs, so that the other blocks end, each with one such
+// wait at most.  When all have ended, it waits as long again: what was sent to it has arrived, what they stored is in
+// place.  Then it makes all the cluster's rows NaN: a wrong one may be among the others.
+constexpr uint32_t kWaitPolls = 1u << 16;
 
 template <int DT, int THREADS, int K, int BLOCKS, bool CLUSTER>
 __global__ void __launch_bounds__(THREADS, BLOCKS)
@@ -452,8 +458,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
   if constexpr (CLUSTER) cluster_wait();  // every block's barriers are set up
 
   PolicySums sum;
-  int done = 0;
-  uint32_t zero = 0;
+  int done = 0;  // live rows; negative in warp 0 from where its wait for the cluster ran out
   for (int i = 0; i < rows; ++i) {
     if (!(live >> i & 1)) {
       E* const grad = a.grad + (row0 + i) * a.grad_stride;
@@ -466,7 +471,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
       continue;
     }
     const int b = done & 1;
-    if (CLUSTER && tid == 0) mbar_expect_tx(bars_at + 8 * b, C * W * 8);
+    if (CLUSTER && tid == 0 && done >= 0) mbar_expect_tx(bars_at + 8 * b, C * W * 8);
     {
       const Slice<DT> in(logits + i * a.stride, V, s0, plan.per);
 
@@ -521,6 +526,7 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     const float rest = warp_sum((one ? most - 1.0f : most) + less) + (float)(__popc(__ballot_sync(~0u, one)) - 1);
     // Once all pairs are there, gradients may overwrite the row (in place): not before the targets' logits have arrived,
     // in every lane, whichever lanes send.  So the addresses of the first pairs come from a vote on them.
+    uint32_t zero = 0;
     if (done == 0) zero = __ballot_sync(~0u, __float_as_uint(x_l) & plan.zero);
     if constexpr (CLUSTER) {
       if (lane < C) st_async(pair_to + b * (kMaxCluster * W * 8) + zero, make_float2(m, rest), bars_to + 8 * b);
@@ -534,7 +540,8 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     if constexpr (!CLUSTER) __syncthreads();
     if (kEachWarp || warp == 0) {
       // the row's maximum M and sum 1 + R
-      const bool ok = !CLUSTER || mbar_wait(bars_at + 8 * b, done >> 1 & 1, kWaitLimit);
+      if constexpr (CLUSTER)
+        if (done < 0 || !mbar_wait(bars_at + 8 * b, done >> 1 & 1, kWaitPolls) || rank == plan.late) done |= INT_MIN;
       float M = -FLT_MAX, R = 0.0f;
       for (int q = lane; q < C * W; q += 32) M = fmaxf(M, pairs[b][q].x);
       M = warp_max(M);
@@ -545,7 +552,6 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
         ones += __popc(__ballot_sync(~0u, v.x == M));
       }
       R = warp_sum(R) + (float)ones;
-      if (!ok) R = __int_as_float(0x7fffffff);
       // log(1 + R): the logarithm of the rounded sum, and what its rounding took
       const float S = 1.0f + R, inverse = 1.0f / S;
       const float lp = (__shfl_sync(~0u, x_l, i) - M) - (logf(S) + __fdividef(R - (S - 1.0f), S));
@@ -622,7 +628,21 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
     if (y >= 0 && yq >= 0 && yq < plan.per && yq % THREADS == tid) from_float(grad + y, res.z * expm1f(res.w));  // over its own store
   }
   if (rank == 0 && tid == 0) partial[cluster] = make_float4(sum.loss, sum.kl, sum.clipped, sum.weight);
-  if constexpr (CLUSTER) cluster_meet();   // no block leaves while another may still send to it
+  if constexpr (CLUSTER) {
+    cluster_meet();  // no block leaves while another may still send to it
+    if (done < 0) {
+      const float nan = __int_as_float(0x7fffffff);
+      for (uint32_t k = 0; k < kWaitPolls; ++k) __nanosleep(16000);
+      for (int i = 0; i < rows; ++i)
+        if (live >> i & 1) {
+          E* const grad = a.grad + (row0 + i) * a.grad_stride;
+#pragma unroll 1
+          for (int j = lane; j < V; j += 32) from_float(grad + j, nan);
+          if (lane == 0) a.logprobs[row0 + i] = nan;
+        }
+      if (lane == 0) partial[cluster] = make_float4(nan, nan, nan, nan);
+    }
+  }
 }
 
 // The blocks' sums in a fixed order.
@@ -918,6 +938,15 @@ int resident_clusters(const cudaLaunchConfig_t& cfg, int C, int sms) {
   return n;
 }
 
+// AR_LATE_BLOCK=<rank> (ar_train.h); read once.
+inline int late_block() {
+  static const int rank = [] {
+    const char* s = std::getenv("AR_LATE_BLOCK");
+    return s ? std::atoi(s) : -1;
+  }();
+  return rank;
+}
+
 template <int DT, int THREADS, int K, int BLOCKS, bool CLUSTER>
 cudaError_t launch_policy_row(const LogitsCall& c, const PolicyParams& p, unsigned long long slots, int C,
                               float4* partial, unsigned* sums) {
@@ -927,6 +956,7 @@ cudaError_t launch_policy_row(const LogitsCall& c, const PolicyParams& p, unsign
   plan.C = C;
   plan.per = (int)(((slots + C - 1) / C + 7) / 8 * 8);  // whole lines; still at most THREADS * K
   plan.zero = 0;
+  plan.late = late_block();
   plan.most = (int)slots;
   cudaError_t e = cudaSuccess;
   if (smem > 40 * 1024) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -18,8 +18,11 @@
  * all-reduce's are (ar.h, "Launch order"): stream order holds.
  * Results do not depend on timing: there are no floating-point atomics, and a
  * call repeated on the same device gives the same bits.  (The one wait inside a
- * kernel, of a cluster's blocks for one another, is bounded; a row whose wait ran
- * out would give NaN.)
+ * kernel, of a cluster's blocks for one another in the policy loss, is bounded to
+ * about a second.  Where one ran out, the cluster's rows, of which there are at most
+ * 32, would give NaN in gradient and log-probability, and so would the statistics.
+ * AR_LATE_BLOCK=<rank> in the environment of the process lets that block of
+ * every cluster give up its first wait: for tests.)
  *
  * Logits.  A matrix of `rows` tokens by `vocab` columns, AR_FLOAT32 or
  * AR_BFLOAT16; row t starts at logits + t * row_stride elements
