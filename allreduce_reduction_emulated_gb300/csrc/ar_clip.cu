@@ -172,16 +172,7 @@ struct Chunk {
 // thousands of squares each, and where these are alike the roundings all go one way:
 // the norm of 1.2G equal values was off by 1.4e-5.)
 struct Squares {
-  float sum = 0.0f, lost = 0.0f;
-  __device__ __forceinline__ void carry(float v) {
-    const float t = sum + v, b = t - sum;
-    lost += (sum - (t - b)) + (v - b);
-    sum = t;
-  }
-  __device__ __forceinline__ float value() const {
-    const float v = sum + lost;
-    return v == v ? v : sum;  // an infinite sum has lost infinity - infinity
-  }
+  Carried sum;
   template <int DT, bool HINTS>
   __device__ __forceinline__ void add(const Tensor& t, unsigned int chunk, uint64_t policy) {
     float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
@@ -200,7 +191,7 @@ struct Squares {
 #pragma unroll
       for (int i = 0; i < Lanes<DT>::N; ++i) acc[0].x = fmaf(x[i], x[i], acc[0].x);
     });
-    carry((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y));
+    sum.add((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y));
   }
 };
 
@@ -209,14 +200,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 square_sum_kernel(const __grid_constant__ Table<CAP> tab, float* partial) {
   pdl_enter();
   __shared__ float sh[kThreads / 32];
-  Squares sum;
+  Squares squares;
   const uint64_t keep = keep_policy(true), rest = keep_policy(false);
   for_chunks<false>(tab, [&](const Tensor& t, unsigned int c) {
     const uint64_t policy = tab.chunks - c <= tab.kept ? keep : rest;
-    if (t.dtype == kF32) sum.add<kF32, HINTS>(t, c, policy);
-    else sum.add<kBF16, HINTS>(t, c, policy);
+    if (t.dtype == kF32) squares.add<kF32, HINTS>(t, c, policy);
+    else squares.add<kBF16, HINTS>(t, c, policy);
   });
-  const float v = block_sum<kThreads>(sum.value(), sh);
+  const float v = block_sum<kThreads>(squares.sum.value(), sh);
   if (threadIdx.x == 0) partial[blockIdx.x] = v;
 }
 

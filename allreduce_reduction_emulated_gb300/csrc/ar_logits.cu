@@ -649,14 +649,20 @@ policy_row_kernel(const Matrix<DT> a, const PolicyParams p, const RowPlan plan, 
 __global__ void __launch_bounds__(kThreads) policy_sum_kernel(const float4* partial, int n, float scale, float* stats) {
   pdl_enter();
   __shared__ float sh[4][kThreads / 32];
-  float v[4] = {};
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const float4 q = partial[i];
-    v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
+  Carried v[4];
+  for (int i = threadIdx.x; i < n; i += 4 * kThreads) {
+    float4 q[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      q[u] = i + u * kThreads < n ? partial[i + u * kThreads] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    v[0].add((q[0].x + q[1].x) + (q[2].x + q[3].x));
+    v[1].add((q[0].y + q[1].y) + (q[2].y + q[3].y));
+    v[2].add((q[0].z + q[1].z) + (q[2].z + q[3].z));
+    v[3].add((q[0].w + q[1].w) + (q[2].w + q[3].w));
   }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float r = block_sum<kThreads>(v[k], sh[k]);
+    const float r = block_sum<kThreads>(v[k].value(), sh[k]);
     if (threadIdx.x == 0) stats[k] = scale * r;
   }
 }
@@ -697,12 +703,12 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const PairParams p) {
       if (w == 0.0f) return 0.0f;
       return w * (p.ref_logprobs ? p.logprobs[t] - p.ref_logprobs[t] : p.logprobs[t]);
     };
-    float v = 0.0f;
+    Carried sum;
     for (unsigned long long k = threadIdx.x; k < n0 || k < n1; k += kThreads) {
-      if (k < n0) v += term(b0 + k);
-      if (k < n1) v -= term(b1 + k);
+      if (k < n0) sum.add(term(b0 + k));
+      if (k < n1) sum.add(-term(b1 + k));
     }
-    v = block_sum<kThreads>(v, sh);
+    const float v = block_sum<kThreads>(sum.value(), sh);
     if (threadIdx.x == 0) {
       const float z = p.beta * v;
       // softplus(-z) = max(-z, 0) + log1p(e^-|z|)
@@ -750,9 +756,9 @@ __global__ void __launch_bounds__(kThreads, 6) preference_grad_kernel(const Matr
   pdl_enter();
   __shared__ float sh[kThreads / 32];
   if (blockIdx.x == 0) {
-    float v = 0.0f;
-    for (unsigned long long i = threadIdx.x; i < p.pairs; i += kThreads) v += p.pair_loss[i];
-    v = block_sum<kThreads>(v, sh);
+    Carried sum;
+    for (unsigned long long i = threadIdx.x; i < p.pairs; i += kThreads) sum.add(p.pair_loss[i]);
+    const float v = block_sum<kThreads>(sum.value(), sh);
     if (threadIdx.x == 0) *p.loss = p.scale * v;
   }
   const unsigned back = blockIdx.x / pieces;

@@ -258,6 +258,22 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 
 // ------------------------------------------------------------------ block sums
 
+// One thread's sum of many values: what an addition loses, of the larger or of the
+// smaller, is carried along.  (Where the values are alike the roundings of a plain sum all
+// go one way: 1500 additions 1.6e-5.)
+struct Carried {
+  float sum = 0.0f, lost = 0.0f;
+  __device__ __forceinline__ void add(float v) {
+    const float t = sum + v, b = t - sum;
+    lost += (sum - (t - b)) + (v - b);
+    sum = t;
+  }
+  __device__ __forceinline__ float value() const {
+    const float v = sum + lost;
+    return v == v ? v : sum;  // an infinite sum has lost infinity - infinity
+  }
+};
+
 // Sum over a block of THREADS threads; valid in every thread.  `sh` holds
 // THREADS / 32 values; the block must synchronize before it is written again.
 template <int THREADS, class T>

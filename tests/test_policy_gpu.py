@@ -113,3 +113,39 @@ def test_very_long_rows(dev, V, dtype):
     assert bool(((r.logprobs.double() - want)[3:].abs() <= 0.01 * want[3:].abs()).all())
     assert bool(((r.logprobs - fresh).double()[3:].abs() <= 0.01 * want[3:].abs()).all())
     tu.assert_grad(r.grad, y, tu.policy64(x, y, fresh, w, None, w)["c"], p, w.double(), extra=4e-6)
+
+
+def test_sums_of_many_rows(dev):
+    """Sums where every rounding goes the same way.  At most 32 rows are added up one after the other (16.5 2^-24 of
+    their sum), the clusters' sums are carried over in each thread and added in a tree (5 + 8 additions), the scale
+    rounds once: under 32 2^-24 = 2e-6."""
+    T = 3_000_001
+    x = torch.zeros(T, 8, device=dev)
+    y = torch.zeros(T, dtype=torch.int32, device=dev)
+    lp = losses.token_logprobs(x[:1], y[:1])[0]
+    old = lp.expand(T).contiguous()
+    adv = torch.ones(T, device=dev)
+    for w in (0.3, 0.7, 0.1, 0.45):
+        weights = torch.full((T,), w, device=dev)
+        r = losses.policy_loss(x, y, old, adv, weights=weights)
+        want = float(weights[0]) * T
+        assert abs(float(r.weight) - want) <= 2e-6 * want, (w, float(r.weight) / want - 1)
+        assert abs(float(r.loss) + want) <= 2.1e-6 * want, (w, float(r.loss) / want + 1)
+
+
+def test_preference_sums_of_many_pairs_and_tokens(dev):
+    """The loss over many pairs and a margin over a long sequence, every addition rounding the same way: carried over
+    in each thread, then a tree (13 additions): under 16 2^-24 = 1e-6."""
+    pairs = 400_000
+    x = torch.zeros(2 * pairs, 2, device=dev)
+    y = torch.zeros(2 * pairs, dtype=torch.int32, device=dev)
+    off = torch.arange(2 * pairs + 1, device=dev)
+    r = losses.preference_loss(x, y, off, scale=1.0)
+    want = pairs * math.log(2.0)
+    assert abs(float(r.loss) - want) <= 1.2e-6 * want, float(r.loss) / want - 1
+    for ref in (-0.3, -0.45, -1.1):
+        refs = torch.full((2 * pairs,), ref, device=dev)
+        off = torch.tensor([0, 2 * pairs, 2 * pairs], device=dev)
+        r = losses.preference_loss(x, y, off, refs, beta=1.0)
+        gain = float((r.logprobs[0] - refs[0]).double()) * 2 * pairs
+        assert abs(float(r.margins) - gain) <= 1e-6 * abs(gain), (ref, float(r.margins) / gain - 1)
