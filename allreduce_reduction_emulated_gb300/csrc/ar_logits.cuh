@@ -66,9 +66,9 @@ __device__ __forceinline__ void from_float(uint16_t* p, float x) { *p = (uint16_
 // warp stores consecutive slots (`warp`, the same in all lanes: an element may then be stored
 // by the lane before the one that holds it), else by halves at both ends.
 // Element by element, at an even / odd distance, these took (2489 x 50001 bf16) 334 / 330 us,
-// now 111 / 175 (policy), 301 / 296, now 127 / 140 (preference); clipping 100M bf16 232 / 221, now
-// 93 / 108.  A whole slot put together by shuffles and stored as one took 140, 148 and 111.
-// fp32 (1111 x 50001): preference 125, now 105; the policy loss stores its fp32 elements one by one.
+// now 110 / 174 (policy), 301 / 296, now 125 / 137 (preference); clipping 100M bf16 232 / 221, now
+// 94 / 108.  A whole slot put together by shuffles and stored as one took 140, 148 and 111.
+// fp32 (1111 x 50001): preference 125, now 103; the policy loss stores its fp32 elements one by one.
 template <class E>
 __device__ __forceinline__ void store_apart(E* to, uint4 v, bool warp) {
   if (sizeof(E) == 4 || ((uintptr_t)to & 2) == 0) {
@@ -106,7 +106,6 @@ struct Slots {
       : row(const_cast<E*>(p)), len(n), lead((int)(((uintptr_t)p & 15) / sizeof(E))) {}
   __device__ __forceinline__ long long count() const { return (len + lead + N - 1) / N; }
   __device__ __forceinline__ long long first(long long s) const { return s * N - lead; }
-  __device__ __forceinline__ bool whole(long long s) const { return first(s) >= 0 && first(s) + N <= len; }
 
   // slot s widened to fp32; elements outside the run read as `fill`
   __device__ __forceinline__ void load(long long s, float (&x)[N], float fill) const {
