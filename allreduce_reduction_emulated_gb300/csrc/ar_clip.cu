@@ -39,7 +39,8 @@ constexpr unsigned int kRun = 16;
 // L2 to keep the last kKeptChunks (40 MB; the two halves of L2 may each hold a copy)
 // and to drop the rest first, and the clipping kernel, which begins with the kept
 // ones, drops them as it goes: 160 MB read and written 38.5 -> 34.9 us, 480 MB 118 ->
-// 112.  Above, nothing is gained and a hint of any kind costs 2% (9.7 GB: 2152 us
+// 112.  (In place with coefficient 1 it reads nothing.  The next kernel's first pass over
+// 20 to 120 MB then takes up to 3 us longer than behind a plain sum, its second none.)  Above, nothing is gained and a hint of any kind costs 2% (9.7 GB: 2152 us
 // without, 2190 with), so the kernels come without them too.
 constexpr unsigned int kHintChunks = 16384, kKeptChunks = 1250;
 

@@ -239,8 +239,8 @@ __device__ __forceinline__ float2 row_part(const Slice<DT>& in, int V, int s0, i
 //
 // GROUP threads take a row: a warp (eight rows in a block) where there are many
 // rows, else the block; with few long rows, a cluster of C blocks.
-// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 152 us, 7.1 TB/s (reads alone are
-// faster than the copy); one row of 32768 3.1 us.
+// Bound by HBM: rows vocab es bytes; 4096 x 131072 bf16 154 us, 7.0 TB/s (reads alone are
+// faster than the copy); one row of 32768 2.5 us.
 struct LogprobPlan {
   int C, per;  // blocks per row; slots per block
 };
@@ -346,10 +346,10 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, co
 // block joins them and computes the token's loss, and one block barrier hands the
 // factors to the others, which write the gradient from their registers.
 //
-// Bound by HBM: 2 rows vocab es bytes.  8192 x 131072 bf16: 644 us, 6.67 TB/s; 4096 x 131072
-// fp32: 632 us, 6.80 TB/s; 4096 x 32768 bf16: 90 us, 5.97 TB/s.  Below that a row's own
-// chain (copies, sum, exchange, loss, stores: 3.7 us) shows: 2489 x 50001 97 us, 5.1 TB/s;
-// 300 x 70000 21 us, 4.0 TB/s.
+// Bound by HBM: 2 rows vocab es bytes.  8192 x 131072 bf16: 639 us, 6.72 TB/s; 4096 x 131072
+// fp32: 629 us, 6.82 TB/s; 4096 x 32768 bf16: 90 us, 5.94 TB/s.  Below that a row's own
+// chain (copies, sum, exchange, loss, stores: 3.7 us) shows: 2489 x 50001 95 us, 5.2 TB/s;
+// 300 x 70000 21 us, 4.1 TB/s.
 struct RowPlan {
   int C;        // blocks per cluster
   int per;      // slots per block: at most THREADS * K
@@ -743,8 +743,8 @@ __global__ void __launch_bounds__(kThreads) pair_kernel(const PairParams p) {
 // before the first is used.  The rows go from the last to the first: what the
 // statistics' pass has read last is still in L2.
 // Bound by HBM: with the statistics' pass the logits are read twice, since a row's
-// factor needs its whole pair's log-probabilities: 6800 x 131072 bf16 768 us for the whole
-// loss, 6.96 TB/s of two reads and one write; 2400 x 50001 114 us.  2 / 4 / 8 slots: 120 / 114 /
+// factor needs its whole pair's log-probabilities: 6800 x 131072 bf16 765 us for the whole
+// loss, 6.99 TB/s of two reads and one write; 2400 x 50001 114 us.  2 / 4 / 8 slots: 120 / 114 /
 // 115 us (2400 x 50001).
 constexpr int kGradSlots = 4, kPiece = kThreads * kGradSlots;
 
@@ -874,10 +874,10 @@ cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
   const unsigned long long n = row_slots<DT>(c, c.logits, c.row_stride);
   const bool hints = stats && small_for_l2<DT>(c);
   const unsigned long long kept = kKeptBytes / (n * 16), keep = c.rows > kept ? c.rows - kept : 0;
-  // A warp per row where that makes 16 warps for every SM (8192 x 9000 bf16: 23 us, a block per row 43; 4096 x 32768
-  // 40 and 44; but 4096 x 131072 159 and 154, 1000 x 32768 23 and 12) or a row has no more for a warp to do.  Thousands of
-  // warps leave no whole rows in L2, though: where the gradient follows, long rows take a block (preference 4 x 1024
-  // x 131072: 789 us, with a warp per row 828).
+  // A warp per row where that makes 16 warps for every SM (8192 x 9000 bf16: 27 us, a block per row 41; 4096 x 32768
+  // 46 and 46; but 4096 x 131072 163 and 155, 1000 x 32768 34 and 11) or a row has no more for a warp to do.  Thousands of
+  // warps leave no whole rows in L2, though: where the gradient follows, long rows take a block (preference 4096 x
+  // 131072: 465 us, with a warp per row 481).
   if (n <= 256 || (c.rows >= 16ull * c.sms && n <= (stats ? 2048 : 8192)))
     return launch_kernel(hints ? logprob_kernel<DT, 32, true> : logprob_kernel<DT, 32, false>,
                          (unsigned)((c.rows + 7) / 8), kThreads, 0, c.stream, true, Matrix<DT>(c),
@@ -896,13 +896,13 @@ cudaError_t run_logprobs(const LogitsCall& c, float2* stats, float* factors) {
 // clusters' rows take 2 wave row_bytes / 6.8 TB/s together.
 // Where HBM is the longer by a fifth, the clusters' start-ups hide behind others'
 // transfers and small runs end evenly: one wave's share of the rows, at most 3, or 8
-// where two blocks fill an SM (us at 1 / 2 / 3 / 4 / 5 / 8 rows: 5000 x 30000 bf16 121 / 106 / 103 / 104 /
-// 106 / 113, 1500 x 30000 44 / 41 / 40 / 44 / 39 / 51, 1800 x 30000 50 / 45 / 42 / 46 / 50 / 50; 8192 x 131072
-// at 1 / 2 / 4 / 8 / 16: 804 / 701 / 663 / 657 / 672).
+// where two blocks fill an SM (us at 1 / 2 / 3 / 4 / 5 / 8 rows: 5000 x 30000 bf16 121 / 106 / 102 / 103 /
+// 105 / 111, 1500 x 30000 43 / 39 / 37 / 41 / 37 / 48, 1800 x 30000 50 / 44 / 42 / 46 / 49 / 50; 8192 x 131072
+// at 1 / 2 / 4 / 8 / 16: 769 / 680 / 641 / 641 / 653).
 // Where the row itself is, a wave takes its rows' time and a start-up of about one
 // row whether it is full or not: the least ceil(waves) (rows + 1) (300 x 70000 at 3 / 4 / 5 /
-// 6: 24.1 / 29.3 / 22.8 / 26.6; 700 x 100000 at 4 / 5 / 8 / 10: 59 / 57 / 69 / 55; 2489 x 50001 at
-// 4 / 6 / 8: 102 / 101 / 108).  More only to bound the number of partial sums.
+// 6: 21.4 / 26.3 / 20.7 / 24.0; 700 x 100000 at 4 / 5 / 8 / 10: 58 / 55 / 67 / 52; 2489 x 50001 at
+// 2 / 3 / 4 / 6 / 8: 98 / 95 / 94 / 94 / 99).  More only to bound the number of partial sums.
 inline int rows_per_cluster(unsigned long long rows, int wave, double row_bytes, int threads, bool two_blocks) {
   const double row_us = threads >= 256 ? 3.7 : 2.0, wave_us = 2.0 * wave * row_bytes / 6.8e6;
   int run = 1;
