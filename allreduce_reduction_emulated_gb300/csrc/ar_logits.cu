@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(kThreads) logprob_kernel(const Matrix<DT> a, c
 
 // Rows too long to be held (above 65536 slots, 524,288 bf16 logits): a block per row,
 // which it reads twice.  1000 x 1048576 bf16 1395 us, 500 x 700000 497 us, 64 x 600001 322 us:
-// 0.44, 0.41 and 0.07 of one read and one write at the copy's rate (one block per SM and
-// second reads from HBM; few rows leave SMs idle).
+// 0.44, 0.41 and 0.07 of one read and one write at the copy's rate (the second read is from
+// HBM too, with one slot per thread on the way; few rows leave SMs idle).
 template <int DT>
 __global__ void __launch_bounds__(kThreads) policy_kernel(const Matrix<DT> a, const PolicyParams p, float4* partial) {
   pdl_enter();
