@@ -1,0 +1,378 @@
+// ar_experts.cu -- products of rows sorted by expert with their expert's weights, and
+// the gradient of the weights (ar_train.h), on the tensor-core product of ar_mma.cuh.
+//
+//   y[t, f] = sum_k W_e[f, k] x[t, k]      rows t of expert e
+//   dW_e[j, i] = sum_t b[t, j] a[t, i]     a, b: x and dy
+//
+// In both the 128 lanes of an accumulator are the side that is contiguous in the
+// output, so that a warp stores whole 64-byte (fp32: 128-byte) runs; and in the first the
+// rows of an expert are the columns, of which the matrix instructions take any multiple
+// of 16: an expert's ragged rest costs what its rows cost, not a whole tile.
+//
+// The offsets are read on the device, by every block: nothing waits for the host.
+#include <algorithm>
+
+#include "ar_mma.cuh"
+#include "ar_train.h"
+#include "ar_train_launch.h"
+
+namespace ar {
+
+namespace mma {
+
+cudaError_t make_map(CUtensorMap* map, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
+                     uint64_t y_stride, uint64_t z_stride) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<Encode>(f);
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  // A side of length one has no stride of its own; the map wants one that is whole all the same.
+  const cuuint64_t dims[3] = {nx, ny, nz};
+  const cuuint64_t y = ny > 1 ? y_stride * 2 : (nx * 2 + 15) / 16 * 16;
+  const cuuint64_t strides[2] = {y, nz > 1 ? z_stride * 2 : y};
+  const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
+  const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace mma
+
+namespace {
+
+using mma::Tile;
+
+// Row ranges of the experts, and what every block works out of them.
+struct Offsets {
+  const void* at;
+  int bytes, experts;
+  long long rows;
+  __device__ __forceinline__ int get(int i) const {
+    const long long v = bytes == 8 ? static_cast<const long long*>(at)[i] : (long long)static_cast<const int*>(at)[i];
+    return (int)(v < 0 ? 0 : v > rows ? rows : v);
+  }
+};
+
+// start[e]: first row of expert e, the largest offset so far (so that the ranges never
+// overlap, whatever the offsets hold); first[e]: tiles before it.
+struct Ranges {
+  int start[kMaxExperts + 1];
+  int first[kMaxExperts + 3];
+};
+
+// One warp; `count(rows)` is an expert's number of tiles.
+template <class Count>
+__device__ __forceinline__ void lay_out(const Offsets& o, Ranges& r, Count count) {
+  const int lane = threadIdx.x & 31;
+  int most = 0, tiles = 0;
+  for (int base = 0; base <= o.experts; base += 32) {
+    const int e = base + lane;
+    int a = e <= o.experts ? o.get(e) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(~0u, a, d);
+      if (lane >= d) a = max(a, v);
+    }
+    a = max(a, most);
+    // tiles of the expert before this offset
+    int before = __shfl_up_sync(~0u, a, 1);
+    if (lane == 0) before = most;
+    int n = e >= 1 && e <= o.experts ? count(a - before) : 0;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int v = __shfl_up_sync(~0u, n, d);
+      if (lane >= d) n += v;
+    }
+    if (e <= o.experts) {
+      r.start[e] = a;
+      r.first[e] = tiles + n;
+    }
+    most = __shfl_sync(~0u, a, 31);
+    tiles += __shfl_sync(~0u, n, 31);
+  }
+}
+
+// Last e in [0, n) with first[e] <= t.
+__device__ __forceinline__ int find(const int* first, int n, int t) {
+  int lo = 0;
+  for (int hi = n; hi - lo > 1;) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) { return (uint16_t)pack_bf16x2(v, 0.0f); }
+
+struct ForwardParams {
+  CUtensorMap weights, x;
+  Offsets offsets;
+  int out, in;             // W_e: out x in
+  bool w_depth;            // `in` is contiguous
+  void* y;
+  long long y_stride;
+  bool fp32, zero_rest;
+};
+
+template <int CG>
+struct Forward {
+  static constexpr bool kBf16 = true;
+  static constexpr int kWide = 128 * CG, kUnit = 16 * CG;  // most columns of a tile, and what they are a multiple of
+  using Params = ForwardParams;
+  struct Local {
+    Ranges r;
+  };
+  static __device__ __forceinline__ void begin(const Params& p, Local& l) {
+    if ((threadIdx.x >> 5) != 3) return;
+    const int f = (p.out + kRowsOfTile - 1) / kRowsOfTile;
+    const auto tiles = [&](int rows) { return (rows + kWide - 1) / kWide * f; };
+    lay_out(p.offsets, l.r, tiles);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      const int E = p.offsets.experts, n = l.r.first[E];
+      // the rows of no expert: in front, behind
+      const int front = p.zero_rest ? tiles(l.r.start[0]) : 0;
+      const int behind = p.zero_rest ? tiles((int)p.offsets.rows - l.r.start[E]) : 0;
+      l.r.first[E + 1] = n + front;
+      l.r.first[E + 2] = n + front + behind;
+    }
+  }
+  static constexpr int kRowsOfTile = mma::kRows * CG;
+  static __device__ __forceinline__ bool tile(const Params& p, const Local& l, int t, Tile& w) {
+    const int E = p.offsets.experts;
+    if (t >= l.r.first[E + 2]) return false;
+    const int e = find(l.r.first, E + 2, t), j = t - l.r.first[e];
+    const int begin = e < E ? l.r.start[e] : e == E ? 0 : l.r.start[E];
+    const int end = e < E ? l.r.start[e + 1] : e == E ? l.r.start[0] : (int)p.offsets.rows;
+    const int n = (end - begin + kWide - 1) / kWide;
+    const int width = ((end - begin + n - 1) / n + kUnit - 1) / kUnit * kUnit;
+    w.a = &p.weights;
+    w.b = &p.x;
+    w.a_row = j / n * kRowsOfTile;
+    w.b_row = begin + j % n * width;
+    w.a_z = e;
+    w.b_z = 0;
+    w.k = 0;
+    w.blocks = e < E ? (p.in + mma::kDepth - 1) / mma::kDepth : 0;
+    w.last = mma::kDepth;
+    // the tiles before may have taken all rows (rounding up to whole units)
+    const int left = end - w.b_row;
+    w.columns = left < width ? max(kUnit, (left + kUnit - 1) / kUnit * kUnit) : width;
+    w.a_depth = p.w_depth;
+    w.b_depth = true;
+    w.end = end;
+    return true;
+  }
+  struct Epilogue {
+    const Params& p;
+    long long at;   // of this lane in the tile's first row
+    int rows;       // that this tile stores
+    bool on;
+    __device__ __forceinline__ Epilogue(const Params& p, const Local&, int, const Tile& w, int row)
+        : p(p), at(w.b_row * p.y_stride + row), rows(min(w.columns, w.end - w.b_row)), on(row < p.out) {}
+    __device__ __forceinline__ void store(int c, const float (&v)[32]) const {
+      if (!on) return;
+      if (p.fp32) {
+        float* y = static_cast<float*>(p.y) + at + c * p.y_stride;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < rows) y[i * p.y_stride] = v[i];
+      } else {
+        uint16_t* y = static_cast<uint16_t*>(p.y) + at + c * p.y_stride;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < rows) y[i * p.y_stride] = bf16_bits(v[i]);
+      }
+    }
+  };
+};
+
+struct GradientParams {
+  CUtensorMap a, b;        // rows by ni, rows by nj
+  Offsets offsets;
+  int ni, nj;
+  void* dw;                // dW_e[j, i] at e * e_stride + j * j_stride + i
+  long long e_stride, j_stride;
+  bool fp32, add;
+};
+
+template <int CG>
+struct WeightGradient {
+  static constexpr bool kBf16 = true;
+  static constexpr int kWide = 128 * CG, kUnit = 16 * CG, kRowsOfTile = mma::kRows * CG;
+  using Params = GradientParams;
+  struct Local {
+    Ranges r;
+  };
+  static __device__ __forceinline__ void begin(const Params& p, Local& l) {
+    if ((threadIdx.x >> 5) == 3) lay_out(p.offsets, l.r, [](int) { return 0; });
+  }
+  static __device__ __forceinline__ bool tile(const Params& p, const Local& l, int t, Tile& w) {
+    const int fi = (p.ni + kRowsOfTile - 1) / kRowsOfTile, fj = (p.nj + kWide - 1) / kWide;
+    const int e = t / (fi * fj), rest = t % (fi * fj);
+    if (e >= p.offsets.experts) return false;
+    const int begin = l.r.start[e], n = l.r.start[e + 1] - begin;
+    w.a = &p.a;
+    w.b = &p.b;
+    w.a_row = rest % fi * kRowsOfTile;
+    w.b_row = rest / fi * kWide;
+    w.a_z = w.b_z = 0;
+    w.k = begin;
+    w.blocks = (n + mma::kDepth - 1) / mma::kDepth;
+    w.last = n - (w.blocks - 1) * mma::kDepth;
+    w.columns = min(kWide, (p.nj - w.b_row + kUnit - 1) / kUnit * kUnit);
+    w.a_depth = w.b_depth = false;
+    w.end = e;
+    return true;
+  }
+  struct Epilogue {
+    const Params& p;
+    long long at;
+    int columns;
+    bool on;
+    __device__ __forceinline__ Epilogue(const Params& p, const Local&, int, const Tile& w, int row)
+        : p(p), at(w.end * p.e_stride + w.b_row * p.j_stride + row), columns(min(w.columns, p.nj - w.b_row)),
+          on(row < p.ni && !(p.add && w.blocks == 0)) {}
+    __device__ __forceinline__ void store(int c, const float (&v)[32]) const {
+      if (!on) return;
+      if (p.fp32) {
+        float* d = static_cast<float*>(p.dw) + at + c * p.j_stride;
+        if (p.add) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < columns) d[i * p.j_stride] += v[i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < columns) d[i * p.j_stride] = v[i];
+        }
+      } else {
+        uint16_t* d = static_cast<uint16_t*>(p.dw) + at + c * p.j_stride;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < columns) {
+            const float old = p.add ? bf16_lo(d[i * p.j_stride]) : 0.0f;
+            d[i * p.j_stride] = bf16_bits(p.add ? old + v[i] : v[i]);
+          }
+      }
+    }
+  };
+};
+
+// ------------------------------------------------------------------ operands that TMA cannot read
+
+// nz x ny rows of nx bf16 each, at any alignment and strides, into rows of `pitch`
+// elements one behind the other.
+__global__ void __launch_bounds__(256) pack_kernel(const uint16_t* from, long long nx, long long ny, long long rows,
+                                                   long long y_stride, long long z_stride, uint16_t* to,
+                                                   long long pitch) {
+  pdl_enter();
+  const long long slots = pitch / 8;
+  for (long long v = blockIdx.x * 256ll + threadIdx.x; v < rows * slots; v += gridDim.x * 256ll) {
+    const long long r = v / slots, x = v % slots * 8;
+    const uint16_t* p = from + r / ny * z_stride + r % ny * y_stride + x;
+    uint16_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = x + i < nx ? p[i] : 0;
+    uint4 o;
+    o.x = e[0] | (uint32_t)e[1] << 16;
+    o.y = e[2] | (uint32_t)e[3] << 16;
+    o.z = e[4] | (uint32_t)e[5] << 16;
+    o.w = e[6] | (uint32_t)e[7] << 16;
+    *reinterpret_cast<uint4*>(to + r * pitch + x) = o;
+  }
+}
+
+constexpr size_t whole(size_t n) { return (n + 7) / 8 * 8; }
+
+// TMA wants addresses and strides of whole 16 bytes (strides that nothing follows do not count).
+bool direct(const ExpertMatrix& m) {
+  return ((uintptr_t)m.at & 15) == 0 && (m.ny <= 1 || m.y_stride % 8 == 0) && (m.nz <= 1 || m.z_stride % 8 == 0);
+}
+
+// The map of an operand; where it cannot be read as it is, of a copy in the workspace.
+cudaError_t operand(const ExpertMatrix& m, uint8_t*& workspace, int sms, cudaStream_t stream, CUtensorMap* map) {
+  if (!m.nx || !m.ny || !m.nz) return cudaSuccess;  // no tile reads it
+  if (direct(m)) return mma::make_map(map, true, m.at, m.nx, m.ny, m.nz, m.y_stride, m.z_stride);
+  const size_t pitch = whole(m.nx), rows = m.ny * m.nz;
+  uint16_t* to = reinterpret_cast<uint16_t*>(workspace);
+  workspace += expert_matrix_workspace(m);
+  const size_t blocks = std::min<size_t>((rows * (pitch / 8) + 255) / 256, (size_t)sms * 8);
+  const cudaError_t e =
+      launch_kernel(pack_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, true, static_cast<const uint16_t*>(m.at),
+                    (long long)m.nx, (long long)m.ny, (long long)rows, (long long)m.y_stride, (long long)m.z_stride, to,
+                    (long long)pitch);
+  if (e != cudaSuccess) return e;
+  return mma::make_map(map, true, to, m.nx, m.ny, m.nz, pitch, m.ny * pitch);
+}
+
+template <int CG>
+cudaError_t forward(const ExpertsCall& c, const ForwardParams& p) {
+  const long long f = ((long long)c.out + mma::kRows * CG - 1) / (mma::kRows * CG);
+  const long long groups = (long long)std::min<size_t>(c.experts, c.rows) + 2 + (long long)(c.rows / (128 * CG));
+  return mma::launch_product<CG, Forward<CG>>(p, f * groups, c.sms, c.stream);
+}
+
+template <int CG>
+cudaError_t weight_gradient(const ExpertsCall& c, const GradientParams& p) {
+  const long long w = 128 * CG;
+  const long long tiles = (p.ni + w - 1) / w * ((p.nj + w - 1) / w) * (long long)c.experts;
+  return mma::launch_product<CG, WeightGradient<CG>>(p, tiles, c.sms, c.stream);
+}
+
+}  // namespace
+
+size_t expert_matrix_workspace(const ExpertMatrix& m) {
+  return direct(m) ? 0 : (whole(m.nx) * m.ny * m.nz * 2 + 127) / 128 * 128;
+}
+
+cudaError_t launch_expert_product(const ExpertsCall& c) {
+  ForwardParams p = {};
+  uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+  cudaError_t e = operand(c.w, ws, c.sms, c.stream, &p.weights);
+  if (e == cudaSuccess) e = operand(c.x, ws, c.sms, c.stream, &p.x);
+  if (e != cudaSuccess) return e;
+  p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
+  p.out = (int)c.out;
+  p.in = (int)c.in;
+  p.w_depth = c.w_in_contiguous;
+  p.y = c.y;
+  p.y_stride = (long long)c.y_stride;
+  p.fp32 = c.dtype == AR_FLOAT32;
+  p.zero_rest = c.zero_rest;
+  const size_t pairs = ((c.out + 255) / 256) * std::max(std::min(c.experts, c.rows), c.rows / 256);
+  return pairs >= (size_t)c.sms ? forward<2>(c, p) : forward<1>(c, p);
+}
+
+cudaError_t launch_expert_weight_gradient(const ExpertsCall& c) {
+  GradientParams p = {};
+  uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+  // the contiguous side of dW is the lanes'
+  const bool lanes_in = c.w_in_contiguous;
+  cudaError_t e = operand(lanes_in ? c.x : c.dy, ws, c.sms, c.stream, &p.a);
+  if (e == cudaSuccess) e = operand(lanes_in ? c.dy : c.x, ws, c.sms, c.stream, &p.b);
+  if (e != cudaSuccess) return e;
+  p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
+  p.ni = (int)(lanes_in ? c.in : c.out);
+  p.nj = (int)(lanes_in ? c.out : c.in);
+  p.dw = c.y;
+  p.e_stride = (long long)c.w.z_stride;
+  p.j_stride = (long long)c.w.y_stride;
+  p.fp32 = c.dtype == AR_FLOAT32;
+  p.add = c.accumulate;
+  const size_t pairs = ((c.out + 255) / 256) * ((c.in + 255) / 256) * c.experts;
+  return pairs >= (size_t)c.sms ? weight_gradient<2>(c, p) : weight_gradient<1>(c, p);
+}
+
+}  // namespace ar

@@ -1,0 +1,425 @@
+// ar_mma.cuh -- the tensor-core product that the expert products (ar_experts.cu) and
+// the orthogonalisation (ar_orthogonal.cu) are made of: one persistent kernel whose
+// tiles, operands and epilogue come from a policy class.
+//
+//   D[i, j] = sum_k A[i, k] B[j, k]      A, B 16-bit (bf16 or fp16), D fp32 in tensor memory
+//
+// i runs over 128 lanes per block (256 per pair of blocks), j over up to 128 columns
+// per block of a pair (256 per pair; alone 128).  Either operand may lie with k or
+// with i / j next to each other in memory: the tensor cores read both.
+//
+// Roles of a block's 12 warps: warp 0 issues the TMA loads of a tile's 64-deep slices
+// into a ring of shared-memory stages, warp 1 issues the matrix instructions (of a pair
+// only the even block's), warps 4 to 11 read finished accumulators and hand them to the
+// policy's epilogue, in chunks of 32 columns.  There are two accumulators, so that
+// one tile's epilogue overlaps the next tile's products.
+//
+// Every wait is bounded (about a second).  A block that gives up tells its other warps;
+// what they have not computed by then becomes NaN in the output, copies and matrix
+// instructions on their way are let finish, tensor memory is freed and the block ends.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "ar_device.cuh"
+
+namespace ar {
+namespace mma {
+
+constexpr int kRows = 128;                 // i per block
+constexpr int kDepth = 64;                 // k per stage: 128 bytes, one swizzled row
+constexpr int kBoxBytes = 64 * kDepth * 2; // every TMA box is 64 x 64 elements
+constexpr int kStageBytes = 4 * kBoxBytes; // A: two boxes, B: up to two
+constexpr int kStages = 6;
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;
+constexpr uint32_t kPolls = 1u << 16;
+
+// ------------------------------------------------------------------ PTX
+
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+__device__ __forceinline__ void bar_init(uint32_t b, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(b), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(b) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(b), "r"(bytes) : "memory");
+}
+// Of a barrier anywhere in the cluster.
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t b) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
+}
+__device__ __forceinline__ void bar_expect_cluster(uint32_t b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(b), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(done)
+      : "r"(b), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// False where the phase did not end in time, or another warp of the block has given up.
+__device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity, volatile uint32_t* late) {
+  for (uint32_t n = 0; n < kPolls; ++n) {
+    if (bar_try(b, parity)) return true;
+    if (*late) return false;
+  }
+  *late = 1;
+  return false;
+}
+__device__ __forceinline__ uint32_t of_rank(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ bool elect() {
+  uint32_t one;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+  return one != 0;
+}
+
+// A box of `map` at (x, y, z) into shared memory; its bytes count on `bar`, which for
+// a pair may be the other block's.
+template <int CG>
+__device__ __forceinline__ void tma_load(uint32_t to, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns) {
+  if constexpr (CG == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+
+template <int CG>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+  else
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+// An arrival on `bar` (of a pair: on both blocks') once all matrix instructions issued so far are done.
+template <int CG>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// 32 columns of a warp's 32 lanes; a thread gets its lane's.
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ------------------------------------------------------------------ descriptors
+
+// Of an operand in shared memory, 128-byte swizzle, as its 64 x 64 boxes lie there
+// one behind the other: groups of eight 128-byte rows are 1024 bytes apart; where i
+// (or j) is contiguous, the next 64 of it are a box (8192 bytes) away.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t at, bool depth_contiguous) {
+  const uint64_t lead = depth_contiguous ? 1 : kBoxBytes >> 4;
+  return (uint64_t)((at & 0x3ffff) >> 4) | lead << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+// Sixteen further in k, in the descriptor's units of 16 bytes.
+__device__ __forceinline__ uint32_t depth_step(bool depth_contiguous) { return depth_contiguous ? 2 : 128; }
+
+// fp32 accumulators of 16-bit operands; columns: of both blocks of a pair.
+template <int CG>
+__device__ __forceinline__ uint32_t instruction(bool bf16, bool a_depth, bool b_depth, int columns) {
+  const uint32_t type = bf16 ? 1 : 0;
+  return 1u << 4 | type << 7 | type << 10 | (a_depth ? 0u : 1u) << 15 | (b_depth ? 0u : 1u) << 16 |
+         (uint32_t)(columns >> 3) << 17 | (uint32_t)(CG * kRows >> 4) << 24;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+// One tile of one product.
+struct Tile {
+  const CUtensorMap *a, *b;
+  int a_row, b_row;        // first i of the pair, first j
+  int a_z, b_z;            // third coordinate of either
+  int k, blocks;           // first k, number of 64-deep slices (0: the sum is 0)
+  int last;                // k of the last slice that count: from there on rows are made 0 (64: all count)
+  int columns;             // j of the tile, a multiple of 16 * CG, at most 128 * CG
+  bool a_depth, b_depth;   // k is the contiguous side
+  int end;                 // the policy's own
+};
+
+template <int CG>
+struct Shared {
+  alignas(1024) uint8_t stage[kStages][kStageBytes];
+  alignas(8) uint64_t full[kStages], empty[kStages], ready[2], drained[2], tail, done;
+  uint32_t tmem, late;
+};
+
+template <int CG, class Policy>
+constexpr int shared_bytes() {
+  return (int)sizeof(Shared<CG>) + (int)sizeof(typename Policy::Local) + 1024;
+}
+
+template <int CG, class Policy>
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ typename Policy::Params p) {
+  extern __shared__ uint8_t raw[];
+  auto& s = *reinterpret_cast<Shared<CG>*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
+  auto& local = *reinterpret_cast<typename Policy::Local*>(&s + 1);
+  constexpr uint32_t kColumns = 2 * 128 * CG;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+  const int first = blockIdx.x / CG, pairs = gridDim.x / CG;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      bar_init(saddr(&s.full[i]), CG);
+      bar_init(saddr(&s.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(saddr(&s.ready[i]), 1);
+      bar_init(saddr(&s.drained[i]), CG * kEpilogueWarps);
+    }
+    bar_init(saddr(&s.tail), 1);
+    bar_init(saddr(&s.done), 1);
+    s.late = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_enter();
+  // Tensor memory is taken behind the wait for the kernel before: a kernel that holds
+  // it has all it waits for.
+  if (warp == 2) tmem_alloc<CG>(saddr(&s.tmem), kColumns);
+  Policy::begin(p, local);
+  fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
+  volatile uint32_t* late = &s.late;
+
+  if (warp == 0) {
+    uint32_t slot = 0, phase = 0, tails = 0;
+    for (int t = first; !*late; t += pairs) {
+      Tile w;
+      if (!Policy::tile(p, local, t, w)) break;
+      const int boxes = (w.columns / CG + 63) / 64;
+      const uint32_t bytes = (2 + boxes) * kBoxBytes;
+      const int a0 = w.a_row + (int)rank * kRows, b0 = w.b_row + (int)rank * (w.columns / CG);
+      bool ok = true;
+      for (int i = 0; i < w.blocks; ++i) {
+        ok = bar_wait(saddr(&s.empty[slot]), phase ^ 1, late);
+        if (!ok) break;
+        const bool tail = w.last < kDepth && i == w.blocks - 1;
+        const uint32_t full = CG == 2 ? of_rank(saddr(&s.full[slot]), 0) : saddr(&s.full[slot]);
+        const uint32_t bar = tail ? saddr(&s.tail) : full;
+        const uint32_t at = saddr(s.stage[slot]);
+        const int k = w.k + i * kDepth;
+        __syncwarp();
+        if (lane == 0) {
+          if (tail || CG == 1) bar_expect(bar, bytes);
+          else bar_expect_cluster(bar, bytes);
+          for (int r = 0; r < 2; ++r)
+            tma_load<CG>(at + r * kBoxBytes, w.a, w.a_depth ? k : a0 + 64 * r, w.a_depth ? a0 + 64 * r : k, w.a_z, bar);
+          for (int r = 0; r < boxes; ++r)
+            tma_load<CG>(at + (2 + r) * kBoxBytes, w.b, w.b_depth ? k : b0 + 64 * r, w.b_depth ? b0 + 64 * r : k, w.b_z,
+                         bar);
+        }
+        __syncwarp();
+        if (tail) {
+          // Rows of the next expert, or of none, came along: both operands' become 0 (the
+          // other operand's could be infinite).  k is a box's outer side here: whole 128-byte rows.
+          ok = bar_wait(bar, tails++ & 1, late);
+          const int rows = kDepth - w.last;
+          for (int v = lane; v < (2 + boxes) * rows * 8; v += 32) {
+            const int box = v / (rows * 8), rest = v % (rows * 8);
+            *reinterpret_cast<uint4*>(s.stage[slot] + box * kBoxBytes + (w.last * 8 + rest) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (!ok) break;
+          if (lane == 0) {
+            if constexpr (CG == 2) bar_arrive_cluster(full);
+            else bar_arrive(full);
+          }
+        }
+        if (++slot == kStages) slot = 0, phase ^= 1;
+      }
+      if (!ok) break;
+    }
+  } else if (warp == 1 && rank == 0) {
+    const bool one = elect();  // one thread issues them all: a commit counts its own thread's
+    uint32_t slot = 0, phase = 0, n = 0;
+    for (int t = first; !*late; t += pairs) {
+      Tile w;
+      if (!Policy::tile(p, local, t, w)) break;
+      if (w.blocks == 0) continue;
+      const uint32_t buffer = n & 1, d = tmem + buffer * (kColumns / 2);
+      bool ok = bar_wait(saddr(&s.drained[buffer]), ((n >> 1) & 1) ^ 1, late);
+      ++n;
+      fence_after();
+      const uint32_t idesc = instruction<CG>(Policy::kBf16, w.a_depth, w.b_depth, w.columns);
+      const uint32_t a_step = depth_step(w.a_depth), b_step = depth_step(w.b_depth);
+      for (int i = 0; ok && i < w.blocks; ++i) {
+        ok = bar_wait(saddr(&s.full[slot]), phase, late);
+        if (!ok) break;
+        fence_after();
+        if (one) {
+          const uint32_t at = saddr(s.stage[slot]);
+          const uint64_t a = operand_desc(at, w.a_depth), b = operand_desc(at + 2 * kBoxBytes, w.b_depth);
+#pragma unroll
+          for (int k = 0; k < kDepth / 16; ++k) mma_f16<CG>(d, a + k * a_step, b + k * b_step, idesc, i + k > 0);
+          mma_commit<CG>(saddr(&s.empty[slot]));
+          if (i == w.blocks - 1) mma_commit<CG>(saddr(&s.ready[buffer]));
+        }
+        __syncwarp();
+        if (++slot == kStages) slot = 0, phase ^= 1;
+      }
+      if (!ok) break;
+    }
+    if (*late) {  // let what was issued finish
+      if (one) mma_commit<CG>(saddr(&s.done));
+      __syncwarp();
+      for (uint32_t i = 0; i < kPolls && !bar_try(saddr(&s.done), 0); ++i) {}
+    }
+  } else if (warp >= 4) {
+    const int e = warp - 4;
+    uint32_t n = 0;
+    bool ok = true;
+    for (int t = first;; t += pairs) {
+      Tile w;
+      if (!Policy::tile(p, local, t, w)) break;
+      const uint32_t buffer = n & 1, at = tmem + buffer * (kColumns / 2) + ((uint32_t)(e & 3) * 32 << 16);
+      if (w.blocks) {
+        ok = ok && bar_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
+        fence_after();
+      }
+      const int row = w.a_row + (int)rank * kRows + (e & 3) * 32 + lane;
+      typename Policy::Epilogue out(p, local, t, w, row);
+      for (int c = (e >> 2) * 32; c < w.columns; c += 32 * (kEpilogueWarps / 4)) {
+        float v[32];
+        if (w.blocks && ok) {
+          tmem_load(at + c, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = w.blocks ? __int_as_float(0x7fc00000) : 0.0f;
+        }
+        out.store(c, v);
+      }
+      if (w.blocks) {
+        ++n;
+        fence_before();
+        __syncwarp();
+        if (lane == 0 && ok) {
+          if constexpr (CG == 2) bar_arrive_cluster(of_rank(saddr(&s.drained[buffer]), 0));
+          else bar_arrive(saddr(&s.drained[buffer]));
+        }
+      }
+    }
+  }
+  __syncwarp();
+  if (*late) {
+    // Copies on their way into this block's memory take microseconds; 10 ms are theirs.
+    for (int i = 0; i < 10000; ++i) __nanosleep(1000);
+  }
+  fence_before();
+  __syncthreads();
+  if constexpr (CG == 2) cluster_sync();
+  if (warp == 2) {
+    fence_after();
+    tmem_free<CG>(tmem, kColumns);
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+// A 3-dimensional map over 16-bit elements with boxes of 64 x 64, 128-byte swizzle, zeros outside.
+// Strides in elements; addresses and strides are whole 16 bytes.
+cudaError_t make_map(CUtensorMap* map, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
+                     uint64_t y_stride, uint64_t z_stride);
+
+template <int CG, class Policy>
+cudaError_t launch_product(const typename Policy::Params& p, long long tiles, int sms, cudaStream_t stream) {
+  constexpr int bytes = shared_bytes<CG, Policy>();
+  static_assert(bytes <= 227 * 1024, "shared memory of a block");
+  const cudaError_t e =
+      cudaFuncSetAttribute(product_kernel<CG, Policy>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  const long long most = sms / CG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * CG));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, product_kernel<CG, Policy>, p);
+}
+
+}  // namespace mma
+}  // namespace ar

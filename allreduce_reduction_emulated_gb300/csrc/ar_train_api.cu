@@ -120,6 +120,41 @@ bool multiprocessors(int* sms) {
   return false;
 }
 
+// A matrix of 16-bit rows that a product reads: element alignment, rows at least as far apart as they are long.
+ar_status_t check_rows(const ar::ExpertMatrix& m) {
+  if (!m.nx || !m.ny || !m.nz) return AR_SUCCESS;
+  if (!aligned(m.at, 2) || (m.ny > 1 && m.y_stride < m.nx)) return AR_ERR_INVALID_ARG;
+  return span(m.ny, m.nx, m.ny > 1 ? m.y_stride : m.nx, 2) ? AR_SUCCESS : AR_ERR_INVALID_ARG;
+}
+
+// Sizes, offsets, the layout of the weights (or of their gradient) and the workspace of the expert products.
+// Fills in c.w and c.w_in_contiguous.
+ar_status_t check_experts(ar::ExpertsCall& c, const void* w, size_t es, size_t expert_stride, size_t out_stride,
+                          size_t in_stride) {
+  if (c.dtype == AR_INT32) return AR_ERR_UNSUPPORTED;
+  if (c.dtype != AR_FLOAT32 && c.dtype != AR_BFLOAT16) return AR_ERR_INVALID_ARG;
+  if (!index_bytes(c.offset_bytes)) return AR_ERR_INVALID_ARG;
+  if (c.rows > AR_MAX_TOKENS || c.experts > AR_MAX_EXPERTS || c.in > AR_MAX_FEATURES || c.out > AR_MAX_FEATURES)
+    return AR_ERR_UNSUPPORTED;
+  if (!aligned(c.offsets, (size_t)c.offset_bytes)) return AR_ERR_INVALID_ARG;
+  if (!c.experts || !c.in || !c.out) return AR_SUCCESS;
+  const size_t most = (size_t)1 << 40;
+  c.w_in_contiguous = in_stride == 1 && (out_stride >= c.in || c.out == 1);
+  if (!c.w_in_contiguous && !(out_stride == 1 && (in_stride >= c.out || c.in == 1))) return AR_ERR_INVALID_ARG;
+  size_t nx = c.in, ny = c.out, pitch = out_stride;
+  if (!c.w_in_contiguous) nx = c.out, ny = c.in, pitch = in_stride;
+  if (ny == 1) pitch = nx;
+  if (pitch > most || expert_stride > most || !aligned(w, es)) return AR_ERR_INVALID_ARG;
+  if (c.experts > 1 && expert_stride < (ny - 1) * pitch + nx) return AR_ERR_INVALID_ARG;
+  c.w = ar::ExpertMatrix{w, nx, ny, c.experts, pitch, expert_stride};
+  return AR_SUCCESS;
+}
+
+bool too_many_tiles(size_t a, size_t b, size_t n) {
+  const double tiles = ((double)a / 128 + 1) * ((double)b / 128 + (double)n);
+  return tiles > (double)(1 << 30);
+}
+
 }  // namespace
 
 extern "C" {
@@ -216,6 +251,68 @@ ar_status_t ar_clip_grads(size_t ntensors, const void* const* grads, void* const
   if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
   Range range("ar_clip_grads");
   return finish(ar::launch_clip_grads(c), "clip_grads", ntensors, 1);
+}
+
+size_t ar_expert_workspace(const void* at, size_t cols, size_t rows, size_t count, size_t row_stride,
+                           size_t matrix_stride) {
+  const size_t most = (size_t)1 << 40;
+  if (cols > AR_MAX_FEATURES || rows > AR_MAX_TOKENS || count > AR_MAX_EXPERTS || row_stride > most ||
+      matrix_stride > most)
+    return SIZE_MAX;
+  return ar::expert_matrix_workspace(ar::ExpertMatrix{at, cols, rows, count, row_stride, matrix_stride});
+}
+
+ar_status_t ar_expert_product(const void* x, size_t rows, size_t x_stride, const void* weights, size_t experts,
+                              size_t out, size_t in, size_t expert_stride, size_t out_stride, size_t in_stride,
+                              const void* offsets, int offset_bytes, void* y, size_t y_stride, ar_dtype_t y_dtype,
+                              int zero_rest, void* workspace, size_t workspace_bytes, void* stream) {
+  ar::ExpertsCall c = {};
+  c.rows = rows, c.experts = experts, c.in = in, c.out = out;
+  c.offsets = offsets, c.offset_bytes = offset_bytes;
+  c.x = ar::ExpertMatrix{x, in, rows, 1, rows > 1 ? x_stride : in, 0};
+  c.y = y, c.y_stride = rows > 1 ? y_stride : out, c.dtype = (int)y_dtype;
+  c.zero_rest = zero_rest != 0;
+  c.workspace = workspace, c.stream = static_cast<cudaStream_t>(stream);
+  ar_status_t st = check_experts(c, weights, 2, expert_stride, out_stride, in_stride);
+  if (st == AR_SUCCESS) st = check_rows(c.x);
+  if (st != AR_SUCCESS) return st;
+  if (too_many_tiles(out, rows, experts + 2)) return AR_ERR_UNSUPPORTED;
+  if (rows == 0 || out == 0) return AR_SUCCESS;
+  const size_t es = ar::elem_bytes(c.dtype);
+  const size_t there = c.y_stride < out ? 0 : span(rows, out, c.y_stride, es);
+  if (!aligned(y, es) || !there) return AR_ERR_INVALID_ARG;
+  if (in && overlap(x, span(rows, in, c.x.y_stride, 2), y, there)) return AR_ERR_INVALID_ARG;
+  const size_t need = ar::expert_matrix_workspace(c.x) + ar::expert_matrix_workspace(c.w);
+  if (workspace_bytes < need || (need && !aligned(workspace, 16))) return AR_ERR_INVALID_ARG;
+  if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
+  Range range("ar_expert_product");
+  return finish(ar::launch_expert_product(c), "expert_product", rows, out);
+}
+
+ar_status_t ar_expert_weight_gradient(const void* dy, size_t dy_stride, const void* x, size_t x_stride, size_t rows,
+                                      size_t experts, size_t out, size_t in, const void* offsets, int offset_bytes,
+                                      void* dw, size_t expert_stride, size_t out_stride, size_t in_stride,
+                                      ar_dtype_t dw_dtype, int accumulate, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  ar::ExpertsCall c = {};
+  c.rows = rows, c.experts = experts, c.in = in, c.out = out;
+  c.offsets = offsets, c.offset_bytes = offset_bytes;
+  c.x = ar::ExpertMatrix{x, in, rows, 1, rows > 1 ? x_stride : in, 0};
+  c.dy = ar::ExpertMatrix{dy, out, rows, 1, rows > 1 ? dy_stride : out, 0};
+  c.y = dw, c.dtype = (int)dw_dtype;
+  c.accumulate = accumulate != 0;
+  c.workspace = workspace, c.stream = static_cast<cudaStream_t>(stream);
+  ar_status_t st = check_experts(c, dw, ar::elem_bytes(c.dtype), expert_stride, out_stride, in_stride);
+  if (st == AR_SUCCESS) st = check_rows(c.x);
+  if (st == AR_SUCCESS) st = check_rows(c.dy);
+  if (st != AR_SUCCESS) return st;
+  if ((double)experts * ((double)in / 128 + 1) * ((double)out / 128 + 1) > (double)(1 << 30)) return AR_ERR_UNSUPPORTED;
+  if (experts == 0 || in == 0 || out == 0) return AR_SUCCESS;
+  const size_t need = ar::expert_matrix_workspace(c.x) + ar::expert_matrix_workspace(c.dy);
+  if (workspace_bytes < need || (need && !aligned(workspace, 16))) return AR_ERR_INVALID_ARG;
+  if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
+  Range range("ar_expert_weight_gradient");
+  return finish(ar::launch_expert_weight_gradient(c), "expert_weight_gradient", out, in);
 }
 
 }  // extern "C"

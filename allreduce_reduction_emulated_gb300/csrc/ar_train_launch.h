@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/ar.h"
+#include "../../include/ar_train.h"
 #include "ar_launch.h"
 
 namespace ar {
@@ -67,5 +68,34 @@ struct GradsCall {
 cudaError_t launch_grad_norm(const GradsCall& c);
 cudaError_t launch_clip_grads(const GradsCall& c);
 size_t grad_norm_workspace();
+
+// Rows of 16-bit elements: nz matrices of ny rows of nx elements (strides in elements).
+struct ExpertMatrix {
+  const void* at;
+  size_t nx, ny, nz, y_stride, z_stride;
+};
+
+constexpr int kMaxExperts = AR_MAX_EXPERTS;
+
+// One call of the expert products.
+struct ExpertsCall {
+  size_t rows, experts, in, out;
+  ExpertMatrix x, dy;              // rows by in, rows by out (dy: of the weight gradient)
+  ExpertMatrix w;                  // the weights, or the strides of their gradient: its contiguous side is nx
+  bool w_in_contiguous;
+  const void* offsets;
+  int offset_bytes;
+  void* y;                         // rows by out, or the weights' gradient
+  size_t y_stride;
+  int dtype;                       // of y: fp32 or bf16
+  bool zero_rest, accumulate;
+  void* workspace;
+  int sms;
+  cudaStream_t stream;
+};
+
+size_t expert_matrix_workspace(const ExpertMatrix& m);
+cudaError_t launch_expert_product(const ExpertsCall& c);
+cudaError_t launch_expert_weight_gradient(const ExpertsCall& c);
 
 }  // namespace ar

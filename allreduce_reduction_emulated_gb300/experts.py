@@ -1,0 +1,209 @@
+"""Products of rows sorted by expert with their expert's weights, and their
+gradients: the layers between the logits' gradient and the weights' gradients.
+
+    y = expert_product(x, weights, offsets)
+    dx, dw = expert_gradients(dy, x, weights, offsets)
+
+Argument checks and marshalling only: the formulas and the kernels' contract are in
+include/ar_train.h.  The functions build no autograd graph.
+
+x, dy         (rows, in) and (rows, out) bfloat16 CUDA tensors on the current device;
+              columns contiguous, rows at any stride
+weights       (experts, out, in) bfloat16; `in` or `out` contiguous, the other two at
+              any strides (a transposed view is fine)
+offsets       (experts + 1,) int64 or int32 on the GPU: expert e has rows
+              [offsets[e], offsets[e + 1]).  Nothing waits for their values
+stream        a torch stream or a cudaStream_t (default: the current stream).  What is
+              allocated belongs to that stream
+
+Rows of no expert (in front of offsets[0], behind offsets[-1]) are left as they are in
+a result that is given, and 0 in one that the call makes.  Operands whose address or
+strides are not whole 16 bytes are copied to a workspace first, which takes longer.
+Nothing waits for the GPU and nothing is kept between calls.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import AR_BFLOAT16, AR_ERR_UNSUPPORTED, AR_FLOAT32, library
+from .losses import _bad, _check, _current_device, _indices, _on
+
+_DTYPES = {torch.float32: AR_FLOAT32, torch.bfloat16: AR_BFLOAT16}
+
+
+def _rows(what: str, name: str, x, device: int | None = None, rows: int | None = None, dtypes=(torch.bfloat16,)):
+    """(device, rows, columns, row stride) of a matrix that the kernels can walk."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise _bad(what, f"{name} must be a 2-dimensional tensor (rows, columns)")
+    if x.dtype not in dtypes:
+        raise _bad(what, f"{name} of {x.dtype}: {' or '.join(str(d)[6:] for d in dtypes)} needed", AR_ERR_UNSUPPORTED)
+    at = x.get_device()
+    if at < 0:
+        raise _bad(what, f"{name} is not in CUDA memory")
+    if device is None:
+        if at != _current_device():
+            raise _bad(what, f"{name} is on cuda:{at}, the current device is cuda:{_current_device()}")
+    elif at != device:
+        raise _bad(what, f"{name} is on {x.device}, the other tensors are on cuda:{device}")
+    n, columns = x.shape
+    if rows is not None and n != rows:
+        raise _bad(what, f"{name} has {n} rows, {rows} needed")
+    stride, column = x.stride()
+    if column != 1 and columns > 1:
+        raise _bad(what, f"{name}: columns are not contiguous")
+    if n <= 1:
+        stride = columns
+    elif stride < columns:
+        raise _bad(what, f"{name}: rows overlap (stride {stride}, {columns} columns)")
+    return at, n, columns, stride
+
+
+def _weights(what: str, name: str, w, device: int, dtypes=(torch.bfloat16,)):
+    """(experts, out, in, expert stride, out stride, in stride)"""
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise _bad(what, f"{name} must be a 3-dimensional tensor (experts, out, in)")
+    if w.dtype not in dtypes:
+        raise _bad(what, f"{name} of {w.dtype}: {' or '.join(str(d)[6:] for d in dtypes)} needed", AR_ERR_UNSUPPORTED)
+    if w.get_device() != device:
+        raise _bad(what, f"{name} is on {w.device}, the other tensors are on cuda:{device}")
+    E, N, K = w.shape
+    e, n, k = w.stride()
+    # a side of length one has no stride of its own
+    if K == 1 and n == 1 and N > 1:
+        k = N
+    elif K == 1:
+        k = 1
+        n = max(n, 1) if N > 1 else 1
+    elif N == 1:
+        n = K if k == 1 else 1
+    if not ((k == 1 and n >= K) or (n == 1 and k >= N)) and w.numel():
+        raise _bad(what, f"{name}: `in` or `out` must be contiguous and rows must not overlap, got strides {w.stride()}")
+    whole = (N - 1) * n + (K - 1) * k + 1
+    if E > 1 and e < whole and w.numel():
+        raise _bad(what, f"{name}: experts overlap (stride {e}, a matrix spans {whole})")
+    return E, N, K, e, n, k
+
+
+def _space(lib, what: str, *matrices) -> int:
+    return sum(lib.ar_expert_workspace(*m) for m in matrices)
+
+
+def _stream_of(stream, device: int):
+    """(context, handle) of a call's stream."""
+    if stream is None:
+        return None, torch._C._cuda_getCurrentRawStream(device)
+    return _on(stream)
+
+
+def _made(context, make):
+    if context is None:
+        return make()
+    with context:
+        return make()
+
+
+def _contiguous(w_strides):
+    """(columns, rows, count, row stride, matrix stride) of the weights, contiguous side first."""
+    E, N, K, e, n, k = w_strides
+    return (K, N, E, n, e) if k == 1 else (N, K, E, k, e)
+
+
+def _product(what, lib, x, at_x, w, at_w, offsets, off_size, out, zero_rest, context, handle):
+    """y = the product into `out`; at_w: (experts, out, in, strides)."""
+    _, rows, K, x_stride = at_x
+    E, N, _, e, n, k = at_w
+    bytes_ = _space(lib, what, (x.data_ptr(), K, rows, 1, x_stride, 0), (w.data_ptr(), *_contiguous(at_w)))
+    space = _made(context, lambda: torch.empty(bytes_, dtype=torch.uint8, device=x.device)) if bytes_ else None
+    _check(lib.ar_expert_product(x.data_ptr(), rows, x_stride, w.data_ptr(), E, N, K, e, n, k, offsets, off_size,
+                                 out.data_ptr(), out.stride(0) if rows > 1 else N, _DTYPES[out.dtype], zero_rest,
+                                 None if space is None else space.data_ptr(), bytes_, handle), what)
+
+
+def expert_product(x, weights, offsets, out=None, dtype=None, stream=None):
+    """y[t] = weights[e] @ x[t] for the rows t of each expert e: (rows, out).
+
+    dtype   of a result that the call makes: bfloat16 (default) or float32
+    out     where the result goes: (rows, out), bfloat16 or float32, rows at any stride"""
+    what = "expert_product"
+    at_x = device, rows, K, _ = _rows(what, "x", x)
+    at_w = _weights(what, "weights", weights, device)
+    E, N = at_w[:2]
+    if at_w[2] != K:
+        raise _bad(what, f"x has {K} columns, the weights take {at_w[2]}")
+    off, size = _indices(what, "offsets", offsets, device, E + 1)
+    context, handle = _stream_of(stream, device)
+    fresh = out is None
+    if fresh:
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in _DTYPES:
+            raise _bad(what, f"dtype {dtype}: float32 or bfloat16 needed", AR_ERR_UNSUPPORTED)
+        out = _made(context, lambda: torch.empty((rows, N), dtype=dtype, device=x.device))
+    else:
+        if _rows(what, "out", out, device, rows, tuple(_DTYPES))[2] != N:
+            raise _bad(what, f"out has {out.shape[1]} columns, {N} needed")
+        if dtype is not None and out.dtype != dtype:
+            raise _bad(what, f"out is {out.dtype}, dtype is {dtype}")
+    _product(what, library(), x, at_x, weights, at_w, off, size, out, fresh, context, handle)
+    return out
+
+
+def expert_gradients(dy, x, weights, offsets, dx=None, dw=None, dw_dtype=None, accumulate: bool = False, need_dx=True,
+                     need_dw=True, stream=None):
+    """(dx, dw): the gradients of expert_product's x and weights from that of its result.
+
+    dx[t] = weights[e]^T dy[t];  dw[e] = sum over e's rows of dy[t] x[t]^T
+
+    dx, dw      where they go; None makes dx in bfloat16 and dw in dw_dtype (bfloat16
+                by default, or float32), laid out as the weights are.  A given dw may be a view
+                of a flat gradient buffer
+    accumulate  add to the dw that is given (an expert without rows keeps its own)
+    need_dx, need_dw   False leaves one out (None in its place)"""
+    what = "expert_gradients"
+    at_y = device, rows, N, dy_stride = _rows(what, "dy", dy)
+    at_x = _rows(what, "x", x, device, rows)
+    K, x_stride = at_x[2:]
+    at_w = _weights(what, "weights", weights, device)
+    E = at_w[0]
+    if at_w[1:3] != (N, K):
+        raise _bad(what, f"dy has {N} columns and x {K}, the weights are {tuple(at_w[1:3])}")
+    off, size = _indices(what, "offsets", offsets, device, E + 1)
+    if accumulate and (dw is None or not need_dw):
+        raise _bad(what, "accumulate needs a dw to add to")
+    context, handle = _stream_of(stream, device)
+    lib = library()
+    fresh = dx is None
+    if not need_dx:
+        dx = None
+    else:
+        if fresh:
+            dx = _made(context, lambda: torch.empty((rows, K), dtype=torch.bfloat16, device=x.device))
+        elif _rows(what, "dx", dx, device, rows, tuple(_DTYPES))[2] != K:
+            raise _bad(what, f"dx has {dx.shape[1]} columns, {K} needed")
+    at_dw = None
+    if not need_dw:
+        dw = None
+    elif dw is None:
+        dtype = torch.bfloat16 if dw_dtype is None else dw_dtype
+        if dtype not in _DTYPES:
+            raise _bad(what, f"dw_dtype {dtype}: float32 or bfloat16 needed", AR_ERR_UNSUPPORTED)
+        lanes = at_w[5] == 1
+        shape = (E, N, K) if lanes else (E, K, N)
+        dw = _made(context, lambda: torch.empty(shape, dtype=dtype, device=x.device))
+        dw = dw if lanes else dw.transpose(1, 2)
+        at_dw = _weights(what, "dw", dw, device, tuple(_DTYPES))
+    else:
+        at_dw = _weights(what, "dw", dw, device, tuple(_DTYPES))
+        if at_dw[:3] != (E, N, K):
+            raise _bad(what, f"dw is {tuple(dw.shape)}, the weights are {(E, N, K)}")
+        if dw_dtype is not None and dw.dtype != dw_dtype:
+            raise _bad(what, f"dw is {dw.dtype}, dw_dtype is {dw_dtype}")
+    if dx is not None:
+        E, N, K, e, n, k = at_w
+        _product(what, lib, dy, at_y, weights, (E, K, N, e, k, n), off, size, dx, fresh, context, handle)
+    if dw is not None:
+        bytes_ = _space(lib, what, (dy.data_ptr(), N, rows, 1, dy_stride, 0), (x.data_ptr(), K, rows, 1, x_stride, 0))
+        space = _made(context, lambda: torch.empty(bytes_, dtype=torch.uint8, device=x.device)) if bytes_ else None
+        _check(lib.ar_expert_weight_gradient(dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, rows, E, N, K, off, size,
+                                             dw.data_ptr(), *at_dw[3:], _DTYPES[dw.dtype], accumulate,
+                                             None if space is None else space.data_ptr(), bytes_, handle), what)
+    return dx, dw

@@ -6,6 +6,7 @@
  *   token under a policy, the clipped policy loss with a KL term and the
  *   preference loss over pairs of sequences, each with the gradient of the
  *   logits;
+ *   the products of expert layers and their gradients, between the two;
  *   after it, the global norm of the reduced gradients and clipping by it.
  *
  * Same conventions as ar.h: status codes, data types, plain device pointers
@@ -160,6 +161,66 @@ ar_status_t ar_grad_norm(size_t ntensors, const void* const* grads, const size_t
 ar_status_t ar_clip_grads(size_t ntensors, const void* const* grads, void* const* outs,
                           const size_t* counts, const ar_dtype_t* dtypes, float max_norm, float eps,
                           float* norm, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Products with the weights of each row's expert.  Rows are sorted by expert:
+ * expert e has rows [offsets[e], offsets[e + 1]) of x and y.
+ *
+ *   y[t, f] = sum_k W_e[f, k] x[t, k]
+ *
+ *   x         rows by `in`, AR_BFLOAT16; row t at x + t * x_stride elements
+ *             (x_stride >= in)
+ *   weights   experts matrices of `out` by `in`, AR_BFLOAT16; element (e, f, k) at
+ *             e * expert_stride + f * out_stride + k * in_stride elements.  One of
+ *             out_stride and in_stride is 1, the other at least the contiguous
+ *             side's length, and expert_stride at least a whole matrix
+ *   offsets   experts + 1 device indices of offset_bytes (4 or 8) bytes.  Values
+ *             outside [0, rows] are clamped, a smaller one than one before it
+ *             counts as that; an expert may have no rows
+ *   y         rows by `out`, y_dtype (AR_FLOAT32 or AR_BFLOAT16), row stride
+ *             y_stride; no part of the inputs.  Rows of no expert (in front of
+ *             offsets[0], behind offsets[experts]) are left as they are, or with
+ *             zero_rest != 0 made 0; rows of x outside the experts' are not read
+ *             into any result
+ *   workspace 16-byte aligned, at least the sum of ar_expert_workspace() of x and
+ *             of weights bytes: operands that are not 16-byte aligned, or whose
+ *             strides are not whole 16 bytes, are laid out there first.  NULL when
+ *             that is 0
+ * The same call gives the gradient of x: dx = ar_expert_product(dy, weights with
+ * `in` and `out` and their strides exchanged).  Sums are fp32, rounded once.
+ * rows == 0 or out == 0 is a no-op; in == 0 gives zeros for the experts' rows.
+ * Errors: AR_ERR_INVALID_ARG (NULL or misaligned pointer, strides, enum, workspace
+ * too small, overlap of y with x), AR_ERR_UNSUPPORTED (another data type, more than
+ * AR_MAX_TOKENS rows, AR_MAX_EXPERTS experts, AR_MAX_FEATURES columns or 2^30 tiles
+ * of 128 x 128), AR_ERR_CUDA.  Waits inside the kernel are bounded (about a second);
+ * what a block has not computed when one runs out is NaN.
+ */
+#define AR_MAX_EXPERTS 1024
+#define AR_MAX_FEATURES ((size_t)1 << 24)
+
+/* Workspace of an operand of `count` matrices of `rows` rows of `cols` contiguous
+ * bf16 elements, with the rows and the matrices at these strides (elements). */
+size_t ar_expert_workspace(const void* at, size_t cols, size_t rows, size_t count, size_t row_stride,
+                           size_t matrix_stride);
+ar_status_t ar_expert_product(const void* x, size_t rows, size_t x_stride, const void* weights, size_t experts,
+                              size_t out, size_t in, size_t expert_stride, size_t out_stride, size_t in_stride,
+                              const void* offsets, int offset_bytes, void* y, size_t y_stride, ar_dtype_t y_dtype,
+                              int zero_rest, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of the weights: dW_e[f, k] = sum over expert e's rows of dy[t, f] x[t, k],
+ * 0 for an expert without rows; with accumulate != 0 added to what dW holds.
+ *   dy        rows by `out`, x rows by `in`, AR_BFLOAT16
+ *   dw        dw_dtype (AR_FLOAT32 or AR_BFLOAT16), laid out by its three strides as
+ *             the weights are
+ *   workspace the sum of ar_expert_workspace() of dy and of x
+ * Everything else as for ar_expert_product.
+ */
+ar_status_t ar_expert_weight_gradient(const void* dy, size_t dy_stride, const void* x, size_t x_stride, size_t rows,
+                                      size_t experts, size_t out, size_t in, const void* offsets, int offset_bytes,
+                                      void* dw, size_t expert_stride, size_t out_stride, size_t in_stride,
+                                      ar_dtype_t dw_dtype, int accumulate, void* workspace, size_t workspace_bytes,
+                                      void* stream);
 
 #ifdef __cplusplus
 }
