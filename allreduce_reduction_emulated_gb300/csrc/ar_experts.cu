@@ -20,8 +20,8 @@ namespace ar {
 
 namespace mma {
 
-cudaError_t make_map(CUtensorMap* map, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
-                     uint64_t y_stride, uint64_t z_stride) {
+cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
+                     uint64_t y_stride, uint64_t z_stride, bool depth, uint32_t box_rows) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -34,12 +34,15 @@ cudaError_t make_map(CUtensorMap* map, bool bf16, const void* base, uint64_t nx,
     return reinterpret_cast<Encode>(f);
   }();
   if (!encode) return cudaErrorNotSupported;
+  *kind = depth ? kDepthRows : nx % 64 == 0 ? kWideRows : kNarrowRows;
   // A side of length one has no stride of its own; the map wants one that is whole all the same.
-  const cuuint64_t dims[3] = {nx, ny, nz};
   const cuuint64_t y = ny > 1 ? y_stride * 2 : (nx * 2 + 15) / 16 * 16;
-  const cuuint64_t strides[2] = {y, nz > 1 ? z_stride * 2 : y};
-  const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
-  const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+  const cuuint64_t z = nz > 1 ? z_stride * 2 : y;
+  const bool wide = *kind == kWideRows;
+  const cuuint64_t dims[4] = {wide ? 64 : nx, ny, wide ? nx / 64 : nz, wide ? nz : 1};
+  const cuuint64_t strides[3] = {y, wide ? 128 : z, z};
+  const cuuint32_t box[4] = {64, depth ? box_rows : 64, wide ? 2u : 1u, 1}, step[4] = {1, 1, 1, 1};
+  const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -115,14 +118,83 @@ __device__ __forceinline__ int find(const int* first, int n, int t) {
 
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return (uint16_t)pack_bf16x2(v, 0.0f); }
 
+// Stores a warp's chunks of 32 lanes by 32 columns: column c of a tile is `stride` elements behind column
+// c - 1, a lane next to its neighbour.
+struct Store {
+  void* to;             // of the tile's first column, the warp's first lane
+  long long stride;
+  int lanes, columns;   // that are stored: of the warp (may be negative), of the tile
+  bool fp32, add, vectors;
+  uint32_t staging;
+
+  __device__ __forceinline__ void chunk(uint32_t at, int c, mma::Source source) const {
+    const int lane = threadIdx.x & 31;
+    float v[32];
+    if (fp32 || add || source != mma::kSums) {
+      // a lane's 32 columns: a warp stores whole 128-byte runs of fp32
+      if (source == mma::kSums) {
+        mma::tmem_rows(at, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = source == mma::kZeros ? 0.0f : __int_as_float(0x7fc00000);
+      }
+      if (lane >= lanes) return;
+      if (fp32) {
+        float* y = static_cast<float*>(to) + lane + c * stride;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < columns) y[i * stride] = add ? y[i * stride] + v[i] : v[i];
+      } else {
+        uint16_t* y = static_cast<uint16_t*>(to) + lane + c * stride;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < columns) y[i * stride] = bf16_bits(add ? bf16_lo(y[i * stride]) + v[i] : v[i]);
+      }
+      return;
+    }
+    // bf16: 8 x 8 matrices are transposed on their way through shared memory, 64 bytes a column.  A
+    // column's four 16-byte parts are exchanged by (column / 2) % 4: neither side has bank conflicts.
+    mma::tmem_fragments(at, v);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int column = 8 * q + (lane & 7), part = lane >> 3;
+      mma::store_transposed(staging + column * 64 + ((part ^ (column >> 1 & 3)) << 4), pack_bf16x2(v[4 * q], v[4 * q + 1]),
+                            pack_bf16x2(v[4 * q + 2], v[4 * q + 3]), pack_bf16x2(v[16 + 4 * q], v[16 + 4 * q + 1]),
+                            pack_bf16x2(v[16 + 4 * q + 2], v[16 + 4 * q + 3]));
+    }
+    __syncwarp();
+    uint16_t* y = static_cast<uint16_t*>(to) + c * stride;
+    const int part = lane & 3;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int column = 8 * q + (lane >> 2);
+      uint4 o;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                   : "r"(staging + column * 64 + ((part ^ (column >> 1 & 3)) << 4)));
+      if (c + column >= columns) continue;
+      uint16_t* d = y + column * stride + part * 8;
+      if (vectors && part * 8 + 8 <= lanes) {
+        *reinterpret_cast<uint4*>(d) = o;
+      } else {
+        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (part * 8 + i < lanes) d[i] = (uint16_t)(w[i / 2] >> (i % 2 * 16));
+      }
+    }
+    __syncwarp();
+  }
+};
+
 struct ForwardParams {
-  CUtensorMap weights, x;
+  CUtensorMap weights, x, x_few;  // x_few: boxes of 32 rows
+  mma::Kind w_kind;
   Offsets offsets;
   int out, in;             // W_e: out x in
-  bool w_depth;            // `in` is contiguous
   void* y;
   long long y_stride;
-  bool fp32, zero_rest;
+  bool fp32, vectors, zero_rest;
 };
 
 template <int CG>
@@ -158,7 +230,6 @@ struct Forward {
     const int n = (end - begin + kWide - 1) / kWide;
     const int width = ((end - begin + n - 1) / n + kUnit - 1) / kUnit * kUnit;
     w.a = &p.weights;
-    w.b = &p.x;
     w.a_row = j / n * kRowsOfTile;
     w.b_row = begin + j % n * width;
     w.a_z = e;
@@ -169,48 +240,35 @@ struct Forward {
     // the tiles before may have taken all rows (rounding up to whole units)
     const int left = end - w.b_row;
     w.columns = left < width ? max(kUnit, (left + kUnit - 1) / kUnit * kUnit) : width;
-    w.a_depth = p.w_depth;
-    w.b_depth = true;
+    w.a_kind = p.w_kind;
+    w.b_kind = mma::kDepthRows;
+    const bool few = w.columns <= 32 * CG;
+    w.b = few ? &p.x_few : &p.x;
+    w.b_bytes = few ? mma::kBoxBytes / 2 : 2 * mma::kBoxBytes;
     w.end = end;
     return true;
   }
-  struct Epilogue {
-    const Params& p;
-    long long at;   // of this lane in the tile's first row
-    int rows;       // that this tile stores
-    bool on;
-    __device__ __forceinline__ Epilogue(const Params& p, const Local&, int, const Tile& w, int row)
-        : p(p), at(w.b_row * p.y_stride + row), rows(min(w.columns, w.end - w.b_row)), on(row < p.out) {}
-    __device__ __forceinline__ void store(int c, const float (&v)[32]) const {
-      if (!on) return;
-      if (p.fp32) {
-        float* y = static_cast<float*>(p.y) + at + c * p.y_stride;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < rows) y[i * p.y_stride] = v[i];
-      } else {
-        uint16_t* y = static_cast<uint16_t*>(p.y) + at + c * p.y_stride;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < rows) y[i * p.y_stride] = bf16_bits(v[i]);
-      }
-    }
+  struct Epilogue : Store {
+    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, uint32_t staging)
+        : Store{static_cast<uint8_t*>(p.y) + (w.b_row * p.y_stride + row) * (p.fp32 ? 4 : 2), p.y_stride, p.out - row,
+                min(w.columns, w.end - w.b_row), p.fp32, false, p.vectors, staging} {}
   };
 };
 
 struct GradientParams {
   CUtensorMap a, b;        // rows by ni, rows by nj
+  mma::Kind a_kind, b_kind;
   Offsets offsets;
   int ni, nj;
   void* dw;                // dW_e[j, i] at e * e_stride + j * j_stride + i
   long long e_stride, j_stride;
-  bool fp32, add;
+  bool fp32, add, vectors;
 };
 
 template <int CG>
 struct WeightGradient {
   static constexpr bool kBf16 = true;
-  static constexpr int kWide = 128 * CG, kUnit = 16 * CG, kRowsOfTile = mma::kRows * CG;
+  static constexpr int kWide = 128 * CG, kUnit = 64 * CG, kRowsOfTile = mma::kRows * CG;
   using Params = GradientParams;
   struct Local {
     Ranges r;
@@ -232,41 +290,17 @@ struct WeightGradient {
     w.blocks = (n + mma::kDepth - 1) / mma::kDepth;
     w.last = n - (w.blocks - 1) * mma::kDepth;
     w.columns = min(kWide, (p.nj - w.b_row + kUnit - 1) / kUnit * kUnit);
-    w.a_depth = w.b_depth = false;
+    w.a_kind = p.a_kind;
+    w.b_kind = p.b_kind;
+    w.b_bytes = p.b_kind == mma::kNarrowRows && w.columns <= 64 * CG ? mma::kBoxBytes : 2 * mma::kBoxBytes;
     w.end = e;
     return true;
   }
-  struct Epilogue {
-    const Params& p;
-    long long at;
-    int columns;
-    bool on;
-    __device__ __forceinline__ Epilogue(const Params& p, const Local&, int, const Tile& w, int row)
-        : p(p), at(w.end * p.e_stride + w.b_row * p.j_stride + row), columns(min(w.columns, p.nj - w.b_row)),
-          on(row < p.ni && !(p.add && w.blocks == 0)) {}
-    __device__ __forceinline__ void store(int c, const float (&v)[32]) const {
-      if (!on) return;
-      if (p.fp32) {
-        float* d = static_cast<float*>(p.dw) + at + c * p.j_stride;
-        if (p.add) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < columns) d[i * p.j_stride] += v[i];
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < columns) d[i * p.j_stride] = v[i];
-        }
-      } else {
-        uint16_t* d = static_cast<uint16_t*>(p.dw) + at + c * p.j_stride;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < columns) {
-            const float old = p.add ? bf16_lo(d[i * p.j_stride]) : 0.0f;
-            d[i * p.j_stride] = bf16_bits(p.add ? old + v[i] : v[i]);
-          }
-      }
-    }
+  struct Epilogue : Store {
+    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, uint32_t staging)
+        : Store{static_cast<uint8_t*>(p.dw) + (w.end * p.e_stride + w.b_row * p.j_stride + row) * (p.fp32 ? 4 : 2),
+                p.j_stride, p.add && w.blocks == 0 ? 0 : p.ni - row, min(w.columns, p.nj - w.b_row), p.fp32, p.add,
+                p.vectors, staging} {}
   };
 };
 
@@ -302,19 +336,29 @@ bool direct(const ExpertMatrix& m) {
 }
 
 // The map of an operand; where it cannot be read as it is, of a copy in the workspace.
-cudaError_t operand(const ExpertMatrix& m, uint8_t*& workspace, int sms, cudaStream_t stream, CUtensorMap* map) {
+cudaError_t operand(ExpertMatrix m, bool depth, uint8_t*& workspace, int sms, cudaStream_t stream, CUtensorMap* map,
+                    mma::Kind* kind, CUtensorMap* few = nullptr) {
   if (!m.nx || !m.ny || !m.nz) return cudaSuccess;  // no tile reads it
-  if (direct(m)) return mma::make_map(map, true, m.at, m.nx, m.ny, m.nz, m.y_stride, m.z_stride);
-  const size_t pitch = whole(m.nx), rows = m.ny * m.nz;
-  uint16_t* to = reinterpret_cast<uint16_t*>(workspace);
-  workspace += expert_matrix_workspace(m);
-  const size_t blocks = std::min<size_t>((rows * (pitch / 8) + 255) / 256, (size_t)sms * 8);
-  const cudaError_t e =
-      launch_kernel(pack_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, true, static_cast<const uint16_t*>(m.at),
-                    (long long)m.nx, (long long)m.ny, (long long)rows, (long long)m.y_stride, (long long)m.z_stride, to,
-                    (long long)pitch);
-  if (e != cudaSuccess) return e;
-  return mma::make_map(map, true, to, m.nx, m.ny, m.nz, pitch, m.ny * pitch);
+  if (!direct(m)) {
+    const size_t pitch = whole(m.nx), rows = m.ny * m.nz;
+    uint16_t* to = reinterpret_cast<uint16_t*>(workspace);
+    workspace += expert_matrix_workspace(m);
+    const size_t blocks = std::min<size_t>((rows * (pitch / 8) + 255) / 256, (size_t)sms * 8);
+    const cudaError_t e =
+        launch_kernel(pack_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, true, static_cast<const uint16_t*>(m.at),
+                      (long long)m.nx, (long long)m.ny, (long long)rows, (long long)m.y_stride, (long long)m.z_stride, to,
+                      (long long)pitch);
+    if (e != cudaSuccess) return e;
+    m = ExpertMatrix{to, m.nx, m.ny, m.nz, pitch, m.ny * pitch};
+  }
+  const cudaError_t e = mma::make_map(map, kind, true, m.at, m.nx, m.ny, m.nz, m.y_stride, m.z_stride, depth, 128);
+  if (e != cudaSuccess || !few) return e;
+  return mma::make_map(few, kind, true, m.at, m.nx, m.ny, m.nz, m.y_stride, m.z_stride, depth, 32);
+}
+
+// Whether rows of results can be stored 16 bytes at a time.
+bool vectors(const void* at, size_t stride, size_t matrix_stride = 0) {
+  return ((uintptr_t)at & 15) == 0 && stride % 8 == 0 && matrix_stride % 8 == 0;
 }
 
 template <int CG>
@@ -340,16 +384,17 @@ size_t expert_matrix_workspace(const ExpertMatrix& m) {
 cudaError_t launch_expert_product(const ExpertsCall& c) {
   ForwardParams p = {};
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
-  cudaError_t e = operand(c.w, ws, c.sms, c.stream, &p.weights);
-  if (e == cudaSuccess) e = operand(c.x, ws, c.sms, c.stream, &p.x);
+  mma::Kind kind;
+  cudaError_t e = operand(c.w, c.w_in_contiguous, ws, c.sms, c.stream, &p.weights, &p.w_kind);
+  if (e == cudaSuccess) e = operand(c.x, true, ws, c.sms, c.stream, &p.x, &kind, &p.x_few);
   if (e != cudaSuccess) return e;
   p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
   p.out = (int)c.out;
   p.in = (int)c.in;
-  p.w_depth = c.w_in_contiguous;
   p.y = c.y;
   p.y_stride = (long long)c.y_stride;
   p.fp32 = c.dtype == AR_FLOAT32;
+  p.vectors = vectors(c.y, c.y_stride);
   p.zero_rest = c.zero_rest;
   const size_t pairs = ((c.out + 255) / 256) * std::max(std::min(c.experts, c.rows), c.rows / 256);
   return pairs >= (size_t)c.sms ? forward<2>(c, p) : forward<1>(c, p);
@@ -360,8 +405,8 @@ cudaError_t launch_expert_weight_gradient(const ExpertsCall& c) {
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   // the contiguous side of dW is the lanes'
   const bool lanes_in = c.w_in_contiguous;
-  cudaError_t e = operand(lanes_in ? c.x : c.dy, ws, c.sms, c.stream, &p.a);
-  if (e == cudaSuccess) e = operand(lanes_in ? c.dy : c.x, ws, c.sms, c.stream, &p.b);
+  cudaError_t e = operand(lanes_in ? c.x : c.dy, false, ws, c.sms, c.stream, &p.a, &p.a_kind);
+  if (e == cudaSuccess) e = operand(lanes_in ? c.dy : c.x, false, ws, c.sms, c.stream, &p.b, &p.b_kind);
   if (e != cudaSuccess) return e;
   p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
   p.ni = (int)(lanes_in ? c.in : c.out);
@@ -371,6 +416,7 @@ cudaError_t launch_expert_weight_gradient(const ExpertsCall& c) {
   p.j_stride = (long long)c.w.y_stride;
   p.fp32 = c.dtype == AR_FLOAT32;
   p.add = c.accumulate;
+  p.vectors = vectors(c.y, c.w.y_stride, c.w.z_stride);
   const size_t pairs = ((c.out + 255) / 256) * ((c.in + 255) / 256) * c.experts;
   return pairs >= (size_t)c.sms ? weight_gradient<2>(c, p) : weight_gradient<1>(c, p);
 }

@@ -31,12 +31,13 @@ namespace mma {
 
 constexpr int kRows = 128;                 // i per block
 constexpr int kDepth = 64;                 // k per stage: 128 bytes, one swizzled row
-constexpr int kBoxBytes = 64 * kDepth * 2; // every TMA box is 64 x 64 elements
-constexpr int kStageBytes = 4 * kBoxBytes; // A: two boxes, B: up to two
+constexpr int kBoxBytes = 64 * kDepth * 2; // 64 x 64 elements, 128-byte rows
+constexpr int kStageBytes = 4 * kBoxBytes; // A: two of them, B: up to two
 constexpr int kStages = 6;
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr uint32_t kPolls = 1u << 16;
+constexpr int kStaging = 2048;             // bytes of each epilogue warp: 32 x 32 16-bit results
 
 // ------------------------------------------------------------------ PTX
 
@@ -55,17 +56,18 @@ __device__ __forceinline__ void bar_expect(uint32_t b, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t b) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
 }
+// Relaxed: what it announces is counted by the barrier itself.  With release semantics, and waits that acquire
+// at the cluster's scope, every slice took 0.3 us more (4864 x 2048 x 8192: 235 us against 107).
 __device__ __forceinline__ void bar_expect_cluster(uint32_t b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(b), "r"(bytes)
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(b), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-      : "=r"(done)
-      : "r"(b), "r"(parity)
-      : "memory");
+  asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+               : "=r"(done)
+               : "r"(b), "r"(parity)
+               : "memory");
   return done != 0;
 }
 // False where the phase did not end in time, or another warp of the block has given up.
@@ -96,19 +98,19 @@ __device__ __forceinline__ bool elect() {
   return one != 0;
 }
 
-// A box of `map` at (x, y, z) into shared memory; its bytes count on `bar`, which for
+// A box of `map` at (x, y, z, u) into shared memory; its bytes count on `bar`, which for
 // a pair may be the other block's.
 template <int CG>
-__device__ __forceinline__ void tma_load(uint32_t to, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void tma_load(uint32_t to, const CUtensorMap* map, int x, int y, int z, int u, uint32_t bar) {
   if constexpr (CG == 2)
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
         : "memory");
 }
 
@@ -158,21 +160,39 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
 // 32 columns of a warp's 32 lanes; a thread gets its lane's.
-__device__ __forceinline__ void tmem_load(uint32_t at, float (&v)[32]) {
+__device__ __forceinline__ void tmem_rows(uint32_t at, float (&v)[32]) {
   uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(at));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(at));
+  tmem_wait();
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// The same 32 x 32 values as the fragments of 8 x 8 matrices that stmatrix takes: v[16 h + 4 q + i] is
+// row 16 h + lane / 4 + 8 (i / 2), column 8 q + 2 (lane % 4) + i % 2.
+__device__ __forceinline__ void tmem_fragments(uint32_t at, float (&v)[32]) {
+  uint32_t r[32];
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(at));
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(at + (16u << 16)));
+  tmem_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// Four 8 x 8 matrices of 16-bit values, columns as rows: lane l gives the address of column l % 8 of matrix l / 8.
+__device__ __forceinline__ void store_transposed(uint32_t to, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
 }
 
 // ------------------------------------------------------------------ descriptors
@@ -198,24 +218,50 @@ __device__ __forceinline__ uint32_t instruction(bool bf16, bool a_depth, bool b_
 
 // ------------------------------------------------------------------ the kernel
 
+// How an operand lies in memory, which says what its map and its boxes are like.
+enum Kind : int {
+  kDepthRows,   // k contiguous: a box is 64 k of up to 128 rows
+  kWideRows,    // i (or j) contiguous, a multiple of 64 of them: a box is 2 x 64 i of 64 k
+  kNarrowRows,  // i contiguous, any number of them: 64 i of 64 k, two loads
+};
+
 // One tile of one product.
 struct Tile {
   const CUtensorMap *a, *b;
+  Kind a_kind, b_kind;
   int a_row, b_row;        // first i of the pair, first j
-  int a_z, b_z;            // third coordinate of either
+  int a_z, b_z;            // which matrix of the map
   int k, blocks;           // first k, number of 64-deep slices (0: the sum is 0)
-  int last;                // k of the last slice that count: from there on rows are made 0 (64: all count)
-  int columns;             // j of the tile, a multiple of 16 * CG, at most 128 * CG
-  bool a_depth, b_depth;   // k is the contiguous side
+  int last;                // rows of the last slice that count: the others are made 0 (64: all count)
+  int columns;             // j of the tile, a multiple of 16 * CG (kWideRows: 64 * CG), at most 128 * CG
+  int b_bytes;             // of B's box(es) per block and slice
   int end;                 // the policy's own
 };
+
+// What a chunk of a tile's epilogue is made of.
+enum Source : int { kZeros, kSums, kLate };
 
 template <int CG>
 struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
+  alignas(128) uint8_t staging[kEpilogueWarps][kStaging];
   alignas(8) uint64_t full[kStages], empty[kStages], ready[2], drained[2], tail, done;
   uint32_t tmem, late;
 };
+
+// A slice of an operand: `bytes` of it, from its row `row` and from k on.
+template <int CG>
+__device__ __forceinline__ void load_rows(uint32_t to, const CUtensorMap* map, Kind kind, int row, int k, int z, int bytes,
+                                          uint32_t bar) {
+  if (kind == kDepthRows) {
+    tma_load<CG>(to, map, k, row, z, 0, bar);
+  } else if (kind == kWideRows) {
+    tma_load<CG>(to, map, 0, k, row >> 6, z, bar);
+  } else {
+    tma_load<CG>(to, map, row, k, z, 0, bar);
+    if (bytes > kBoxBytes) tma_load<CG>(to + kBoxBytes, map, row + 64, k, z, 0, bar);
+  }
+}
 
 template <int CG, class Policy>
 constexpr int shared_bytes() {
@@ -262,8 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int t = first; !*late; t += pairs) {
       Tile w;
       if (!Policy::tile(p, local, t, w)) break;
-      const int boxes = (w.columns / CG + 63) / 64;
-      const uint32_t bytes = (2 + boxes) * kBoxBytes;
+      const uint32_t bytes = 2 * kBoxBytes + w.b_bytes;
       const int a0 = w.a_row + (int)rank * kRows, b0 = w.b_row + (int)rank * (w.columns / CG);
       bool ok = true;
       for (int i = 0; i < w.blocks; ++i) {
@@ -274,15 +319,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const uint32_t bar = tail ? saddr(&s.tail) : full;
         const uint32_t at = saddr(s.stage[slot]);
         const int k = w.k + i * kDepth;
-        __syncwarp();
         if (lane == 0) {
           if (tail || CG == 1) bar_expect(bar, bytes);
           else bar_expect_cluster(bar, bytes);
-          for (int r = 0; r < 2; ++r)
-            tma_load<CG>(at + r * kBoxBytes, w.a, w.a_depth ? k : a0 + 64 * r, w.a_depth ? a0 + 64 * r : k, w.a_z, bar);
-          for (int r = 0; r < boxes; ++r)
-            tma_load<CG>(at + (2 + r) * kBoxBytes, w.b, w.b_depth ? k : b0 + 64 * r, w.b_depth ? b0 + 64 * r : k, w.b_z,
-                         bar);
+          load_rows<CG>(at, w.a, w.a_kind, a0, k, w.a_z, 2 * kBoxBytes, bar);
+          load_rows<CG>(at + 2 * kBoxBytes, w.b, w.b_kind, b0, k, w.b_z, w.b_bytes, bar);
         }
         __syncwarp();
         if (tail) {
@@ -290,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           // other operand's could be infinite).  k is a box's outer side here: whole 128-byte rows.
           ok = bar_wait(bar, tails++ & 1, late);
           const int rows = kDepth - w.last;
-          for (int v = lane; v < (2 + boxes) * rows * 8; v += 32) {
+          for (int v = lane; v < (int)bytes / kBoxBytes * rows * 8; v += 32) {
             const int box = v / (rows * 8), rest = v % (rows * 8);
             *reinterpret_cast<uint4*>(s.stage[slot] + box * kBoxBytes + (w.last * 8 + rest) * 16) = make_uint4(0, 0, 0, 0);
           }
@@ -317,15 +358,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       bool ok = bar_wait(saddr(&s.drained[buffer]), ((n >> 1) & 1) ^ 1, late);
       ++n;
       fence_after();
-      const uint32_t idesc = instruction<CG>(Policy::kBf16, w.a_depth, w.b_depth, w.columns);
-      const uint32_t a_step = depth_step(w.a_depth), b_step = depth_step(w.b_depth);
+      const uint32_t idesc = instruction<CG>(Policy::kBf16, w.a_kind == kDepthRows, w.b_kind == kDepthRows, w.columns);
+      const uint32_t a_step = depth_step(w.a_kind == kDepthRows), b_step = depth_step(w.b_kind == kDepthRows);
       for (int i = 0; ok && i < w.blocks; ++i) {
         ok = bar_wait(saddr(&s.full[slot]), phase, late);
         if (!ok) break;
         fence_after();
         if (one) {
           const uint32_t at = saddr(s.stage[slot]);
-          const uint64_t a = operand_desc(at, w.a_depth), b = operand_desc(at + 2 * kBoxBytes, w.b_depth);
+          const uint64_t a = operand_desc(at, w.a_kind == kDepthRows),
+                         b = operand_desc(at + 2 * kBoxBytes, w.b_kind == kDepthRows);
 #pragma unroll
           for (int k = 0; k < kDepth / 16; ++k) mma_f16<CG>(d, a + k * a_step, b + k * b_step, idesc, i + k > 0);
           mma_commit<CG>(saddr(&s.empty[slot]));
@@ -353,18 +395,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         ok = ok && bar_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
         fence_after();
       }
-      const int row = w.a_row + (int)rank * kRows + (e & 3) * 32 + lane;
-      typename Policy::Epilogue out(p, local, t, w, row);
-      for (int c = (e >> 2) * 32; c < w.columns; c += 32 * (kEpilogueWarps / 4)) {
-        float v[32];
-        if (w.blocks && ok) {
-          tmem_load(at + c, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = w.blocks ? __int_as_float(0x7fc00000) : 0.0f;
-        }
-        out.store(c, v);
-      }
+      const int row = w.a_row + (int)rank * kRows + (e & 3) * 32;
+      typename Policy::Epilogue out(p, local, w, row, saddr(s.staging[e]));
+      for (int c = (e >> 2) * 32; c < w.columns; c += 32 * (kEpilogueWarps / 4))
+        out.chunk(at + c, c, !w.blocks ? kZeros : ok ? kSums : kLate);
       if (w.blocks) {
         ++n;
         fence_before();
@@ -392,10 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 
 // ------------------------------------------------------------------ host
 
-// A 3-dimensional map over 16-bit elements with boxes of 64 x 64, 128-byte swizzle, zeros outside.
-// Strides in elements; addresses and strides are whole 16 bytes.
-cudaError_t make_map(CUtensorMap* map, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
-                     uint64_t y_stride, uint64_t z_stride);
+// The map of `nz` matrices of `ny` rows of `nx` contiguous 16-bit elements; 128-byte swizzle, zeros outside.
+// Strides in elements; addresses and strides are whole 16 bytes.  depth: nx is k, and a box has `box` rows; else nx
+// is i (or j).  Returns how it is to be loaded.
+cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
+                     uint64_t y_stride, uint64_t z_stride, bool depth, uint32_t box);
 
 template <int CG, class Policy>
 cudaError_t launch_product(const typename Policy::Params& p, long long tiles, int sms, cudaStream_t stream) {
