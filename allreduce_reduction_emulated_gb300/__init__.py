@@ -102,11 +102,13 @@ def library() -> ctypes.CDLL:
                 L.ar_expert_product.argtypes = [vp, sz, sz, vp, sz, sz, sz, sz, sz, sz, vp, i, vp, sz, i, i, vp, sz, vp]
                 L.ar_expert_weight_gradient.argtypes = [vp, sz, vp, sz, sz, sz, sz, sz, vp, i, vp, sz, sz, sz, i, i, vp,
                                                         sz, vp]
+                L.ar_orthogonalize.argtypes = [sz, vp, vp, vp, vp, vp, vp, vp, vp, f, i, i, vp, f, vp, sz, vp]
                 for fn in (L.ar_token_logprobs, L.ar_policy_loss, L.ar_preference_loss, L.ar_grad_norm,
-                           L.ar_clip_grads, L.ar_expert_product, L.ar_expert_weight_gradient):
+                           L.ar_clip_grads, L.ar_expert_product, L.ar_expert_weight_gradient, L.ar_orthogonalize):
                     fn.restype = i
                 for fn, args in ((L.ar_policy_loss_workspace, [sz]), (L.ar_preference_loss_workspace, [sz, sz]),
-                                 (L.ar_grad_norm_workspace, []), (L.ar_expert_workspace, [vp, sz, sz, sz, sz, sz])):
+                                 (L.ar_grad_norm_workspace, []), (L.ar_expert_workspace, [vp, sz, sz, sz, sz, sz]),
+                                 (L.ar_orthogonalize_workspace, [sz, vp, vp, vp, i])):
                     fn.argtypes, fn.restype = args, sz
                 _lib = L
     return _lib

@@ -152,37 +152,14 @@ struct Store {
       }
       return;
     }
-    // bf16: 8 x 8 matrices are transposed on their way through shared memory, 64 bytes a column.  A
-    // column's four 16-byte parts are exchanged by (column / 2) % 4: neither side has bank conflicts.
+    // bf16: 8 x 8 matrices are transposed on their way through shared memory, 64 bytes a column
     mma::tmem_fragments(at, v);
+    uint32_t w[16];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int column = 8 * q + (lane & 7), part = lane >> 3;
-      mma::store_transposed(staging + column * 64 + ((part ^ (column >> 1 & 3)) << 4), pack_bf16x2(v[4 * q], v[4 * q + 1]),
-                            pack_bf16x2(v[4 * q + 2], v[4 * q + 3]), pack_bf16x2(v[16 + 4 * q], v[16 + 4 * q + 1]),
-                            pack_bf16x2(v[16 + 4 * q + 2], v[16 + 4 * q + 3]));
-    }
+    for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+    mma::stage_columns(staging, w);
     __syncwarp();
-    uint16_t* y = static_cast<uint16_t*>(to) + c * stride;
-    const int part = lane & 3;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int column = 8 * q + (lane >> 2);
-      uint4 o;
-      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
-                   : "r"(staging + column * 64 + ((part ^ (column >> 1 & 3)) << 4)));
-      if (c + column >= columns) continue;
-      uint16_t* d = y + column * stride + part * 8;
-      if (vectors && part * 8 + 8 <= lanes) {
-        *reinterpret_cast<uint4*>(d) = o;
-      } else {
-        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (part * 8 + i < lanes) d[i] = (uint16_t)(w[i / 2] >> (i % 2 * 16));
-      }
-    }
+    mma::put_columns(staging, static_cast<uint16_t*>(to) + c * stride, stride, lanes, columns - c, vectors);
     __syncwarp();
   }
 };

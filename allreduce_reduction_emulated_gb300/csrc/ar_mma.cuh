@@ -195,6 +195,45 @@ __device__ __forceinline__ void store_transposed(uint32_t to, uint32_t a, uint32
                : "memory");
 }
 
+// ------------------------------------------------------------------ a warp's 32 x 32 results
+
+// In a warp's staging memory 32 columns of 32 16-bit rows lie 64 bytes each; their 16-byte parts are
+// exchanged by (column / 2) % 4, so that neither side has bank conflicts.
+__device__ __forceinline__ uint32_t staged(uint32_t staging, int column, int part) {
+  return staging + column * 64 + ((part ^ (column >> 1 & 3)) << 4);
+}
+// The fragments of tmem_fragments, packed in pairs of columns: w[8 h + 2 q + i].
+__device__ __forceinline__ void stage_columns(uint32_t staging, const uint32_t (&w)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    store_transposed(staged(staging, 8 * q + (lane & 7), lane >> 3), w[2 * q], w[2 * q + 1], w[8 + 2 * q],
+                     w[8 + 2 * q + 1]);
+}
+// The staged columns to memory, `stride` elements apart; `rows` of each, `columns` of them.
+__device__ __forceinline__ void put_columns(uint32_t staging, uint16_t* to, long long stride, int rows, int columns,
+                                            bool vectors) {
+  const int lane = threadIdx.x & 31, part = lane & 3;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int column = 8 * q + (lane >> 2);
+    uint4 o;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
+                 : "r"(staged(staging, column, part)));
+    if (column >= columns) continue;
+    uint16_t* d = to + column * stride + part * 8;
+    if (vectors && part * 8 + 8 <= rows) {
+      *reinterpret_cast<uint4*>(d) = o;
+    } else {
+      const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (part * 8 + i < rows) d[i] = (uint16_t)(w[i / 2] >> (i % 2 * 16));
+    }
+  }
+}
+
 // ------------------------------------------------------------------ descriptors
 
 // Of an operand in shared memory, 128-byte swizzle, as its 64 x 64 boxes lie there

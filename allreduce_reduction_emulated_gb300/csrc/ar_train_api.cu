@@ -45,6 +45,7 @@ bool aligned(const void* p, size_t n) { return p && ((uintptr_t)p & (n - 1)) == 
 bool aligned_or_null(const void* p, size_t n) { return !p || aligned(p, n); }
 bool index_bytes(int n) { return n == 4 || n == 8; }
 bool nan(float x) { return !(x == x); }
+bool finite(float x) { return x - x == 0.0f; }
 
 ar_status_t finish(cudaError_t e, const char* what, size_t a, size_t b) {
   if (debug()) std::fprintf(stderr, "[ar] %s %zu x %zu status=%s\n", what, a, b, cudaGetErrorString(e));
@@ -313,6 +314,46 @@ ar_status_t ar_expert_weight_gradient(const void* dy, size_t dy_stride, const vo
   if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
   Range range("ar_expert_weight_gradient");
   return finish(ar::launch_expert_weight_gradient(c), "expert_weight_gradient", out, in);
+}
+
+size_t ar_orthogonalize_workspace(size_t nstacks, const size_t* counts, const size_t* rows, const size_t* cols,
+                                  int steps) {
+  if (nstacks && (!counts || !rows || !cols)) return SIZE_MAX;
+  for (size_t i = 0; i < nstacks; ++i)
+    if (counts[i] > AR_MAX_MATRICES || rows[i] > AR_MAX_SIDE || cols[i] > AR_MAX_SIDE) return SIZE_MAX;
+  if (steps < 1 || steps > AR_MAX_ORTHOGONAL_STEPS) return SIZE_MAX;
+  ar::OrthogonalCall c = {};
+  c.nstacks = nstacks, c.counts = counts, c.rows = rows, c.cols = cols, c.steps = steps;
+  return ar::orthogonal_workspace(c);
+}
+
+ar_status_t ar_orthogonalize(size_t nstacks, const void* const* grads, float* const* momentum, void* const* outs,
+                             const size_t* counts, const size_t* rows, const size_t* cols, const ar_dtype_t* dtypes,
+                             const float* scales, float beta, int nesterov, int steps, const float* coefficients,
+                             float eps, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!coefficients || steps < 1 || steps > AR_MAX_ORTHOGONAL_STEPS) return AR_ERR_INVALID_ARG;
+  if (!finite(beta) || !finite(eps) || eps < 0.0f) return AR_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i)
+    if (!finite(coefficients[i])) return AR_ERR_INVALID_ARG;
+  if (nstacks && (!grads || !outs || !counts || !rows || !cols || !dtypes)) return AR_ERR_INVALID_ARG;
+  for (size_t i = 0; i < nstacks; ++i) {
+    if (dtypes[i] == AR_INT32) return AR_ERR_UNSUPPORTED;
+    if (dtypes[i] != AR_FLOAT32 && dtypes[i] != AR_BFLOAT16) return AR_ERR_INVALID_ARG;
+    if (counts[i] > AR_MAX_MATRICES || rows[i] > AR_MAX_SIDE || cols[i] > AR_MAX_SIDE) return AR_ERR_UNSUPPORTED;
+    if (scales && !finite(scales[i])) return AR_ERR_INVALID_ARG;
+    if (!counts[i] || !rows[i] || !cols[i]) continue;
+    if (!aligned(grads[i], ar::elem_bytes(dtypes[i])) || !aligned(outs[i], 2)) return AR_ERR_INVALID_ARG;
+    if (momentum && !aligned(momentum[i], 4)) return AR_ERR_INVALID_ARG;
+  }
+  ar::OrthogonalCall c = {nstacks, grads, momentum, outs, counts, rows, cols, dtypes, scales, beta, nesterov != 0,
+                          steps, coefficients[0], coefficients[1], coefficients[2], eps, workspace, 0,
+                          static_cast<cudaStream_t>(stream)};
+  if (!ar::orthogonal_bounded(c)) return AR_ERR_INVALID_ARG;
+  const size_t need = ar::orthogonal_workspace(c);
+  if (workspace_bytes < need || (need && !aligned(workspace, 16))) return AR_ERR_INVALID_ARG;
+  if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
+  Range range("ar_orthogonalize");
+  return finish(ar::launch_orthogonal(c), "orthogonalize", nstacks, (size_t)steps);
 }
 
 }  // extern "C"

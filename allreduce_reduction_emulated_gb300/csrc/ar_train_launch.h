@@ -94,6 +94,28 @@ struct ExpertsCall {
   cudaStream_t stream;
 };
 
+// One call of the orthogonalisation (host arrays, read during the call).
+struct OrthogonalCall {
+  size_t nstacks;
+  const void* const* grads;
+  float* const* momentum;          // NULL: none
+  void* const* outs;
+  const size_t *counts, *rows, *cols;
+  const ar_dtype_t* dtypes;        // of the gradients: fp32 or bf16
+  const float* scales;             // NULL: 1
+  float beta;
+  bool nesterov;
+  int steps;
+  float a, b, c, eps;
+  void* workspace;
+  int sms;
+  cudaStream_t stream;
+};
+
+size_t orthogonal_workspace(const OrthogonalCall& c);
+bool orthogonal_bounded(const OrthogonalCall& c);
+cudaError_t launch_orthogonal(const OrthogonalCall& c);
+
 size_t expert_matrix_workspace(const ExpertMatrix& m);
 cudaError_t launch_expert_product(const ExpertsCall& c);
 cudaError_t launch_expert_weight_gradient(const ExpertsCall& c);

@@ -7,7 +7,8 @@
  *   preference loss over pairs of sequences, each with the gradient of the
  *   logits;
  *   the products of expert layers and their gradients, between the two;
- *   after it, the global norm of the reduced gradients and clipping by it.
+ *   after it, the global norm of the reduced gradients, clipping by it, and
+ *   updates of matrices orthogonalised by Newton-Schulz products.
  *
  * Same conventions as ar.h: status codes, data types, plain device pointers
  * owned by the caller, one cudaStream_t per call (NULL = legacy default
@@ -221,6 +222,45 @@ ar_status_t ar_expert_weight_gradient(const void* dy, size_t dy_stride, const vo
                                       void* dw, size_t expert_stride, size_t out_stride, size_t in_stride,
                                       ar_dtype_t dw_dtype, int accumulate, void* workspace, size_t workspace_bytes,
                                       void* stream);
+
+/*
+ * Orthogonalised updates.  Stack i holds counts[i] matrices of rows[i] by cols[i],
+ * contiguous, one behind the other.  For each matrix g:
+ *
+ *   m   <- beta m + g;  u = g + beta m with nesterov != 0, else m   (no momentum: u = g)
+ *   X    = u / (|u| + eps)                                          (|u|: Frobenius norm)
+ *   steps times, with (a, b, c) = coefficients:
+ *          A = X X^T,  X <- a X + (b A + c A^2) X    (rows <= cols; else A = X^T X, from the right)
+ *   out  = scale X
+ *
+ *   grads     host array of device pointers, AR_FLOAT32 or AR_BFLOAT16 by dtypes
+ *   momentum  host array of device pointers, fp32, updated; NULL: no momentum
+ *   outs      host array of device pointers, bf16.  outs[i] may be grads[i] where that is bf16; any
+ *             other overlap of the tensors is the caller's error
+ *   scales    host array of a factor for each stack, NULL: 1
+ *   steps     1 to AR_MAX_ORTHOGONAL_STEPS
+ *   workspace at least ar_orthogonalize_workspace() bytes, 16-byte aligned; its contents on
+ *             entry do not matter
+ * Momentum, norms and all sums are fp32; X, A and b A + c A^2 are held between the products in fp16 times
+ * powers of two that follow from bounds of the singular values; the result is rounded once to bf16.
+ * A matrix of zeros gives zeros; one whose norm is not finite (a square above the fp32 range makes
+ * it infinite) gives NaN.  Empty stacks are left out.  Pointers need element alignment only.
+ * The host arrays are read during the call only.  Errors: AR_ERR_INVALID_ARG (NULL or misaligned pointer, enum,
+ * steps, a parameter that is not finite, eps < 0, coefficients under which the singular values of a matrix of
+ * norm 1 exceed 10^6, workspace too small), AR_ERR_UNSUPPORTED (AR_INT32, a side above AR_MAX_SIDE, more than
+ * AR_MAX_MATRICES matrices in a stack), AR_ERR_CUDA.  Waits inside the kernels are bounded (about a second);
+ * what a block has not computed when one runs out is NaN.
+ */
+#define AR_MAX_ORTHOGONAL_STEPS 16
+#define AR_MAX_SIDE ((size_t)1 << 16)
+#define AR_MAX_MATRICES ((size_t)1 << 12)
+
+size_t ar_orthogonalize_workspace(size_t nstacks, const size_t* counts, const size_t* rows, const size_t* cols,
+                                  int steps);
+ar_status_t ar_orthogonalize(size_t nstacks, const void* const* grads, float* const* momentum, void* const* outs,
+                             const size_t* counts, const size_t* rows, const size_t* cols, const ar_dtype_t* dtypes,
+                             const float* scales, float beta, int nesterov, int steps, const float* coefficients,
+                             float eps, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
