@@ -37,6 +37,7 @@ constexpr int kStages = 6;
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr uint32_t kPolls = 1u << 16;
+constexpr int kChunkStep = 32 * (kEpilogueWarps / 4);  // from one chunk of a warp to its next
 constexpr int kStaging = 2048;             // bytes of each epilogue warp: 32 x 32 16-bit results
 
 // ------------------------------------------------------------------ PTX
@@ -257,6 +258,14 @@ __device__ __forceinline__ uint32_t instruction(bool bf16, bool a_depth, bool b_
 
 // ------------------------------------------------------------------ the kernel
 
+// What a policy without dependencies between its tiles has for them.
+struct Independent {
+  template <class Params>
+  static __device__ __forceinline__ bool wait(const Params&, const struct Tile&, volatile uint32_t*) { return true; }
+  template <class Params>
+  static __device__ __forceinline__ void done(const Params&, const struct Tile&) {}
+};
+
 // How an operand lies in memory, which says what its map and its boxes are like.
 enum Kind : int {
   kDepthRows,   // k contiguous: a box is 64 k of up to 128 rows
@@ -274,7 +283,7 @@ struct Tile {
   int last;                // rows of the last slice that count: the others are made 0 (64: all count)
   int columns;             // j of the tile, a multiple of 16 * CG (kWideRows: 64 * CG), at most 128 * CG
   int b_bytes;             // of B's box(es) per block and slice
-  int end;                 // the policy's own
+  int end, shape, stage, step;  // the policy's own
 };
 
 // What a chunk of a tile's epilogue is made of.
@@ -347,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int t = first; !*late; t += pairs) {
       Tile w;
       if (!Policy::tile(p, local, t, w)) break;
+      if (w.blocks && !Policy::wait(p, w, late)) break;
       const uint32_t bytes = 2 * kBoxBytes + w.b_bytes;
       const int a0 = w.a_row + (int)rank * kRows, b0 = w.b_row + (int)rank * (w.columns / CG);
       bool ok = true;
@@ -430,13 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       Tile w;
       if (!Policy::tile(p, local, t, w)) break;
       const uint32_t buffer = n & 1, at = tmem + buffer * (kColumns / 2) + ((uint32_t)(e & 3) * 32 << 16);
+      const int row = w.a_row + (int)rank * kRows + (e & 3) * 32;
+      ok = ok && Policy::wait(p, w, late);
+      typename Policy::Epilogue out(p, local, w, row, (e >> 2) * 32, saddr(s.staging[e]));
       if (w.blocks) {
         ok = ok && bar_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
         fence_after();
       }
-      const int row = w.a_row + (int)rank * kRows + (e & 3) * 32;
-      typename Policy::Epilogue out(p, local, w, row, saddr(s.staging[e]));
-      for (int c = (e >> 2) * 32; c < w.columns; c += 32 * (kEpilogueWarps / 4))
+      for (int c = (e >> 2) * 32; c < w.columns; c += kChunkStep)
         out.chunk(at + c, c, !w.blocks ? kZeros : ok ? kSums : kLate);
       if (w.blocks) {
         ++n;
@@ -447,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           else bar_arrive(saddr(&s.drained[buffer]));
         }
       }
+      Policy::done(p, w);
     }
   }
   __syncwarp();
@@ -471,8 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
                      uint64_t y_stride, uint64_t z_stride, bool depth, uint32_t box);
 
+// `together`: the blocks wait for one another, so all of them have to be on the GPU at once.
 template <int CG, class Policy>
-cudaError_t launch_product(const typename Policy::Params& p, long long tiles, int sms, cudaStream_t stream) {
+cudaError_t launch_product(const typename Policy::Params& p, long long tiles, int sms, cudaStream_t stream,
+                           bool together = false) {
   constexpr int bytes = shared_bytes<CG, Policy>();
   static_assert(bytes <= 227 * 1024, "shared memory of a block");
   const cudaError_t e =
@@ -485,8 +499,13 @@ cudaError_t launch_product(const typename Policy::Params& p, long long tiles, in
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  if (together) {
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  }
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = CG;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;

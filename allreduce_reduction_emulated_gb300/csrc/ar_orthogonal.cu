@@ -4,8 +4,8 @@
 //   u = g + beta m (or m, or g);  X = u / (|u| + eps)
 //   `steps` times:  A = X X^T (of a tall matrix X^T X),  B = b A + c A^2,  X <- a X + B X
 //
-// Two passes over the gradients (momentum and sums of squares; the scaled 16-bit copy), then three products a
-// step, each one launch over all matrices of all shapes.  A and B are symmetric: only their blocks on one
+// Two passes over the gradients (momentum and sums of squares; the scaled 16-bit copy), then one launch for all
+// products of all steps and shapes.  A and B are symmetric: only their blocks on one
 // side of the diagonal are computed, and stored to both.
 //
 // Between products X, A and B are held in fp16, not in bf16: its 11 bits keep the result within
@@ -60,6 +60,7 @@ struct PrepareParams {
   float* partial;            // one per chunk
   float* coefs;              // kCoefs per matrix and step
   void** outs;               // one per matrix
+  unsigned int* done;        // one per matrix: made 0
 };
 
 constexpr int kThreads = 256, kSlotsPerThread = 8;
@@ -208,6 +209,7 @@ __global__ void __launch_bounds__(kThreads) halve_kernel(const __grid_constant__
   if (at.chunk == 0) {
     if (threadIdx.x < p.steps)
       coefficients(p, norm, s.scale, threadIdx.x, p.coefs + ((size_t)matrix * p.steps + threadIdx.x) * kCoefs);
+    if (threadIdx.x == 0) p.done[matrix] = 0;
     if (threadIdx.x == 0) p.outs[matrix] = static_cast<uint16_t*>(s.out) + (size_t)at.matrix * s.rows * s.cols;
   }
   const float power = power_for(norm);
@@ -224,25 +226,25 @@ __global__ void __launch_bounds__(kThreads) halve_kernel(const __grid_constant__
 
 enum Stage : int { kGram, kSquare, kApply };
 
+// The matrices of one shape in the product kernel.  A stage's result has nj rows of ni.
 struct Shape {
-  CUtensorMap a, b;
-  mma::Kind a_kind, b_kind;
-  int ni, nj, k;                 // lanes' side, columns' side, depth
+  CUtensorMap gram[2], apply[2], a, b;   // of X in either place for either product; of A; of B
+  mma::Kind gram_kind, apply_kind;
+  int rows, cols, side;
+  int x_pitch, a_pitch;          // multiples of 64; what is stored behind a row's end is read by nothing
   int count, matrix;             // matrices, and the number of the first
-  int first, tiles;              // first tile, tiles of a matrix
-  const __half* old;             // what is added to: nj rows of `pitch`
-  __half* to;                    // nj rows of `pitch` (of the last step: `outs`, contiguous)
-  int pitch;                     // a multiple of 64; what is stored behind a row's end is read by nothing
-  long long matrix_stride;       // of old and to
+  int first[3], tiles[3];        // of each stage: first tile in it, tiles of a matrix
+  __half *x[2], *to_a, *to_b;
   bool vectors;                  // the results' rows are whole 16 bytes
 };
 
-struct StepParams {
+struct StepsParams {
   Shape shape[kMaxShapes];
-  int shapes, tiles;
-  const float* coefs;            // of this step, `coef_stride` apart
-  int coef_stride;
-  void* const* outs;             // last step: where the results go
+  int shapes, steps;
+  int stage_tiles[3];
+  const float* coefs;            // kCoefs per matrix and step
+  void* const* outs;             // where the results of the last step go
+  unsigned int* done;            // per matrix: epilogue warps that have stored their part of a tile
 };
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -250,94 +252,169 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int STAGE, int CG>
-struct Product {
+// All tiles of all steps in one launch: those of the first product of all matrices, of the second, of the
+// third, then the next step's.  A tile waits until all tiles of its matrix before it are stored, which
+// with several matrices they mostly are: nobody waits for the last tile of a launch, and a step of a small
+// matrix costs three times the way through the chip, not three launches (8.4 us each).
+template <int CG>
+struct Steps {
   static constexpr bool kBf16 = false;
   static constexpr int kSide = 128 * CG;
-  using Params = StepParams;
+  static constexpr unsigned int kParts = CG * mma::kEpilogueWarps;  // of a tile
+  using Params = StepsParams;
   struct Local {};
   static __device__ __forceinline__ void begin(const Params&, Local&) {}
   static __device__ __forceinline__ bool tile(const Params& p, const Local&, int t, Tile& w) {
-    if (t >= p.tiles) return false;
+    const int per_step = p.stage_tiles[0] + p.stage_tiles[1] + p.stage_tiles[2];
+    const int step = t / per_step;
+    if (step >= p.steps) return false;
+    t -= step * per_step;
+    int stage = 0;
+    while (t >= p.stage_tiles[stage]) t -= p.stage_tiles[stage++];
     int q = 0;
-    while (q + 1 < p.shapes && p.shape[q + 1].first <= t) ++q;
+    while (q + 1 < p.shapes && p.shape[q + 1].first[stage] <= t) ++q;
     const Shape& s = p.shape[q];
-    const int z = (t - s.first) / s.tiles;
-    int j = (t - s.first) % s.tiles, i;
-    if (STAGE == kApply) {
-      const int fi = (s.ni + kSide - 1) / kSide;
+    const int z = (t - s.first[stage]) / s.tiles[stage];
+    int j = (t - s.first[stage]) - z * s.tiles[stage], i;
+    const bool wide = s.rows <= s.cols;
+    int nj = s.side;
+    if (stage == kApply) {
+      const int fi = (s.cols + kSide - 1) / kSide;
       i = j % fi;
       j = j / fi;
+      nj = s.rows;
+      // lanes are the columns of X: D[i, j] = sum_k X[k, i] B[j, k] of a wide one, sum_k B[i, k] X[j, k] of a tall one
+      w.a = wide ? &s.apply[step & 1] : &s.b;
+      w.b = wide ? &s.b : &s.apply[step & 1];
+      w.a_kind = wide ? s.apply_kind : mma::kDepthRows;
+      w.b_kind = wide ? mma::kDepthRows : s.apply_kind;
     } else {  // on and above the diagonal: block column j has j + 1 of them
       int c = (int)((sqrtf(8.0f * j + 1.0f) - 1.0f) * 0.5f);
       while ((c + 1) * (c + 2) / 2 <= j) ++c;
       while (c * (c + 1) / 2 > j) --c;
       i = j - c * (c + 1) / 2;
       j = c;
+      w.a = w.b = stage == kGram ? &s.gram[step & 1] : &s.a;
+      w.a_kind = w.b_kind = stage == kGram ? s.gram_kind : mma::kDepthRows;
     }
-    w.a = &s.a;
-    w.b = &s.b;
-    w.a_kind = s.a_kind;
-    w.b_kind = s.b_kind;
     w.a_row = i * kSide;
     w.b_row = j * kSide;
     w.a_z = w.b_z = z;
     w.k = 0;
-    w.blocks = (s.k + mma::kDepth - 1) / mma::kDepth;
+    w.blocks = ((stage == kGram ? max(s.rows, s.cols) : s.side) + mma::kDepth - 1) / mma::kDepth;
     w.last = mma::kDepth;
-    const int unit = (s.b_kind == mma::kDepthRows ? 16 : 64) * CG;
-    w.columns = min(kSide, (s.nj - w.b_row + unit - 1) / unit * unit);
+    const int unit = (w.b_kind == mma::kDepthRows ? 16 : 64) * CG;
+    w.columns = min(kSide, (nj - w.b_row + unit - 1) / unit * unit);
     w.b_bytes = 2 * mma::kBoxBytes;
-    w.end = q << 20 | z;
+    w.shape = q;
+    w.stage = stage;
+    w.step = step;
     return true;
   }
+
+  // The tiles of this matrix before this stage, in all their parts.
+  static __device__ __forceinline__ bool wait(const Params& p, const Tile& w, volatile uint32_t* late) {
+    const Shape& s = p.shape[w.shape];
+    unsigned int before = (s.tiles[0] + s.tiles[1] + s.tiles[2]) * w.step;
+    for (int i = 0; i < w.stage; ++i) before += s.tiles[i];
+    before *= kParts;
+    if (before == 0) return true;
+    const unsigned int* at = p.done + s.matrix + w.a_z;
+    bool ok = false;
+    for (uint32_t n = 0; n < 16 * mma::kPolls; ++n) {
+      unsigned int v;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+      ok = v >= before;
+      if (ok || *late) break;
+    }
+    if (!ok) *late = 1;
+    // what was stored there is read by TMA too
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    return __all_sync(~0u, ok);
+  }
+  static __device__ __forceinline__ void done(const Params& p, const Tile& w) {
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      __threadfence();
+      atomicAdd(p.done + p.shape[w.shape].matrix + w.a_z, 1u);
+    }
+  }
+
   struct Epilogue {
-    const Shape& s;
     float x, y;                  // of the old value, of the sum
-    const __half* old;           // of the tile's first column, the warp's first lane
+    const __half* old;           // of the tile's first column, the warp's first lane; NULL: none
     uint16_t *to, *mirror;
-    long long stride;
+    long long stride, old_stride, mirror_stride;
     int lanes, columns, pads, pad_columns;  // of the sides, and with what lies behind a row's end
-    bool last;
+    bool last, vectors;
     uint32_t staging;
-    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, uint32_t staging)
-        : s(p.shape[w.end >> 20]), staging(staging) {
-      const int z = w.end & 0xfffff;
-      const float* f = p.coefs + (long long)(s.matrix + z) * p.coef_stride;
-      x = STAGE == kGram ? 0.0f : STAGE == kSquare ? f[1] : f[3];
-      y = STAGE == kGram ? f[0] : STAGE == kSquare ? f[2] : f[4];
-      last = STAGE == kApply && p.outs;
-      const long long at = z * s.matrix_stride;
-      old = STAGE == kGram ? nullptr : s.old + at + (long long)w.b_row * s.pitch + row;
-      stride = last ? s.ni : s.pitch;
-      to = (last ? static_cast<uint16_t*>(p.outs[s.matrix + z]) : reinterpret_cast<uint16_t*>(s.to) + at) +
-           w.b_row * stride + row;
+    uint4 next[4];               // the old values of the next chunk, loaded ahead
+
+    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int c, uint32_t staging)
+        : staging(staging) {
+      const Shape& s = p.shape[w.shape];
+      const int z = w.a_z, matrix = s.matrix + z;
+      const float* f = p.coefs + ((long long)matrix * p.steps + w.step) * kCoefs;
+      const int ni = w.stage == kApply ? s.cols : s.side, nj = w.stage == kApply ? s.rows : s.side;
+      const int pitch = w.stage == kApply ? s.x_pitch : s.a_pitch;
+      const long long at = (long long)z * nj * pitch, here = at + (long long)w.b_row * pitch + row;
+      last = w.stage == kApply && w.step + 1 == p.steps;
+      vectors = true;
+      stride = old_stride = mirror_stride = pitch;
+      mirror = nullptr;
+      if (w.stage == kGram) {
+        x = 0.0f, y = f[0];
+        old = nullptr;
+        to = reinterpret_cast<uint16_t*>(s.to_a) + here;
+      } else if (w.stage == kSquare) {
+        x = f[1], y = f[2];
+        old = s.to_a + here;
+        to = reinterpret_cast<uint16_t*>(s.to_b) + here;
+      } else {
+        x = f[3], y = f[4];
+        old = s.x[w.step & 1] + here;
+        to = reinterpret_cast<uint16_t*>(s.x[(w.step + 1) & 1]) + here;
+        if (last) {
+          stride = ni;
+          to = static_cast<uint16_t*>(p.outs[matrix]) + (long long)w.b_row * ni + row;
+          vectors = s.vectors;
+        }
+      }
       // a block off the diagonal is stored a second time, lanes as rows
-      mirror = STAGE != kApply && w.a_row != w.b_row
-                   ? reinterpret_cast<uint16_t*>(s.to) + at + (long long)row * s.pitch + w.b_row
-                   : nullptr;
-      lanes = s.ni - row;
-      pads = s.pitch - row;
-      columns = min(w.columns, s.nj - w.b_row);
-      pad_columns = s.pitch - w.b_row;
+      if (w.stage != kApply && w.a_row != w.b_row)
+        mirror = reinterpret_cast<uint16_t*>(w.stage == kGram ? s.to_a : s.to_b) + at + (long long)row * pitch + w.b_row;
+      lanes = ni - row;
+      pads = pitch - row;
+      columns = min(w.columns, nj - w.b_row);
+      pad_columns = pitch - w.b_row;
+      load_next(c);
     }
 
-    __device__ __forceinline__ void chunk(uint32_t at, int c, mma::Source source) const {
+    __device__ __forceinline__ void load_next(int c) {
+      if (!old) return;
+      const int lane = threadIdx.x & 31, part = lane & 3;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int column = c + 8 * q + (lane >> 2);
+        next[q] = make_uint4(0, 0, 0, 0);
+        if (column < columns && part * 8 < pads)
+          next[q] = __ldcg(reinterpret_cast<const uint4*>(old + column * old_stride + part * 8));
+      }
+    }
+
+    __device__ __forceinline__ void chunk(uint32_t at, int c, mma::Source source) {
       const int lane = threadIdx.x & 31;
       uint32_t o[16] = {};
-      if (STAGE != kGram) {
+      if (old) {
         // the old values' columns into the staging memory, and out again as fragments
         const int part = lane & 3;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int column = 8 * q + (lane >> 2);
-          uint4 r = make_uint4(0, 0, 0, 0);
-          if (c + column < columns && part * 8 < pads)
-            r = *reinterpret_cast<const uint4*>(old + (long long)(c + column) * s.pitch + part * 8);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mma::staged(staging, column, part)), "r"(r.x),
-                       "r"(r.y), "r"(r.z), "r"(r.w)
+        for (int q = 0; q < 4; ++q)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           mma::staged(staging, 8 * q + (lane >> 2), part)),
+                       "r"(next[q].x), "r"(next[q].y), "r"(next[q].z), "r"(next[q].w)
                        : "memory");
-        }
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -346,6 +423,7 @@ struct Product {
                        : "r"(mma::staged(staging, 8 * q + (lane & 7), lane >> 3))
                        : "memory");
         __syncwarp();
+        load_next(c + mma::kChunkStep);
       }
       float v[32];
       if (source == mma::kSums) {
@@ -357,61 +435,72 @@ struct Product {
       uint32_t w[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
         float lo = y * v[2 * i], hi = y * v[2 * i + 1];
-        if (STAGE != kGram) {
-          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
-          lo += x * b.x;
-          hi += x * b.y;
-        }
+        if (old) lo += x * b.x, hi += x * b.y;
         w[i] = last ? pack_bf16x2(lo, hi) : half2_bits(lo, hi);
       }
       mma::stage_columns(staging, w);
       __syncwarp();
-      mma::put_columns(staging, to + c * stride, stride, last ? lanes : pads, columns - c, !last || s.vectors);
+      mma::put_columns(staging, to + c * stride, stride, last ? lanes : pads, columns - c, vectors);
       __syncwarp();
-      if (STAGE != kApply && mirror) {
-        // as rows: a lane group's fragments are whole 16 bytes of a row
+      if (mirror) {
+        // as rows: the four matrices of rows 8 h and on are its columns 0, 8, 16 and 24
 #pragma unroll
-        for (int h = 0; h < 4; ++h)  // rows 8 h ..; the four matrices are its columns 0, 8, 16, 24
+        for (int h = 0; h < 4; ++h)
           asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
                            mma::staged(staging, 8 * h + (lane & 7), lane >> 3)),
                        "r"(w[8 * (h / 2) + h % 2]), "r"(w[8 * (h / 2) + 2 + h % 2]), "r"(w[8 * (h / 2) + 4 + h % 2]),
                        "r"(w[8 * (h / 2) + 6 + h % 2])
                        : "memory");
         __syncwarp();
-        mma::put_columns(staging, mirror + c, s.pitch, pad_columns - c, lanes, true);
+        mma::put_columns(staging, mirror + c, mirror_stride, pad_columns - c, lanes, true);
         __syncwarp();
       }
     }
   };
 };
 
-// Tiles of all shapes at this side of a tile; with `set`, noted in them.
-template <int STAGE>
-long long count_tiles(StepParams& p, int side, bool set) {
-  long long total = 0;
-  for (int q = 0; q < p.shapes; ++q) {
-    Shape& s = p.shape[q];
-    const long long fi = (s.ni + side - 1) / side, fj = (s.nj + side - 1) / side;
-    const long long one = STAGE == kApply ? fi * fj : fj * (fj + 1) / 2;
-    if (set) s.tiles = (int)one, s.first = (int)std::min<long long>(total, 1 << 30);
-    total += one * s.count;
+// Tiles of all shapes at this side of a tile, and an estimate of the time in units of a 64-deep slice of a
+// pair's tile: a stage takes at least one tile's way, and 5 slices' time go into its epilogue.
+double count_tiles(StepsParams& p, int side, int workers, double slice) {
+  double time = 0.0;
+  for (int stage = 0; stage < 3; ++stage) {
+    long long total = 0;
+    double work = 0.0, longest = 0.0;
+    for (int q = 0; q < p.shapes; ++q) {
+      Shape& s = p.shape[q];
+      const auto blocks = [&](long long n) { return (n + side - 1) / side; };
+      const long long fs = blocks(s.side);
+      const long long one = stage == kApply ? blocks(s.rows) * blocks(s.cols) : fs * (fs + 1) / 2;
+      s.tiles[stage] = (int)one;
+      s.first[stage] = (int)std::min<long long>(total, 1 << 30);
+      total += one * s.count;
+      const double tile = slice * ((stage == kGram ? std::max(s.rows, s.cols) : s.side) / 64.0) + 5.0;
+      work += tile * one * s.count;
+      longest = std::max(longest, tile);
+    }
+    p.stage_tiles[stage] = (int)std::min<long long>(total, 1 << 30);
+    time += std::max(work / workers, longest);
   }
-  return total;
+  return time;
 }
 
-template <int STAGE>
-cudaError_t launch_stage(StepParams& p, int sms, cudaStream_t stream) {
-  // Pairs of blocks (256 x 256) unless they leave most of the GPU idle: a block alone takes 128 x 128, a quarter,
-  // at about half the rate per multiprocessor.
-  const long long in_pairs = count_tiles<STAGE>(p, 256, false), alone = count_tiles<STAGE>(p, 128, false);
-  const long long pairs = std::max(1, sms / 2);
-  const bool pair = (in_pairs + pairs - 1) / pairs <= (alone + sms - 1) / sms;
-  const long long tiles = count_tiles<STAGE>(p, pair ? 256 : 128, true);
-  if (tiles > 1 << 30) return cudaErrorInvalidValue;
-  p.tiles = (int)tiles;
-  return pair ? mma::launch_product<2, Product<STAGE, 2>>(p, tiles, sms, stream)
-              : mma::launch_product<1, Product<STAGE, 1>>(p, tiles, sms, stream);
+cudaError_t launch_steps(StepsParams& p, int sms, cudaStream_t stream) {
+  // Pairs of blocks (256 x 256) or blocks alone (128 x 128, a quarter, at about 0.6 of a pair's slice).
+  const int pairs = std::max(1, sms / 2);
+  const double pair = count_tiles(p, 256, pairs, 1.0), alone = count_tiles(p, 128, sms, 0.6);
+  const bool in_pairs = pair <= alone;
+  if (in_pairs) count_tiles(p, 256, pairs, 1.0);
+  long long tiles = 0;
+  int most = 0;
+  for (int stage = 0; stage < 3; ++stage) {
+    tiles += p.stage_tiles[stage];
+    most = std::max(most, p.stage_tiles[stage]);
+  }
+  if (tiles * p.steps > 1 << 30) return cudaErrorInvalidValue;
+  return in_pairs ? mma::launch_product<2, Steps<2>>(p, most, sms, stream, true)
+                  : mma::launch_product<1, Steps<1>>(p, most, sms, stream, true);
 }
 
 // ------------------------------------------------------------------ one group of stacks
@@ -435,6 +524,7 @@ struct Group {
   size_t matrices, chunks, bytes;
   float *partial, *coefs;
   void** outs;
+  unsigned int* done;
 };
 
 size_t chunks_of(size_t rows, size_t cols) { return (rows * up(cols, 8) / 8 + kChunk - 1) / kChunk; }
@@ -478,6 +568,7 @@ void gather(const OrthogonalCall& c, size_t first, uint8_t* base, Group& g) {
   g.partial = reinterpret_cast<float*>(take(g.chunks * 4));
   g.coefs = reinterpret_cast<float*>(take(g.matrices * c.steps * kCoefs * 4));
   g.outs = reinterpret_cast<void**>(take(g.matrices * 8));
+  g.done = reinterpret_cast<unsigned int*>(take(g.matrices * 4));
   g.bytes = at;
 }
 
@@ -507,7 +598,7 @@ cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const flo
   p.beta = c.beta, p.nesterov = c.nesterov, p.eps = c.eps;
   p.a = c.a, p.b = c.b, p.c = c.c, p.growth = growth, p.steps = c.steps;
   std::memcpy(p.cap, cap, sizeof p.cap);
-  p.partial = g.partial, p.coefs = g.coefs, p.outs = g.outs;
+  p.partial = g.partial, p.coefs = g.coefs, p.outs = g.outs, p.done = g.done;
   size_t used[kMaxShapes] = {}, chunk = 0;
   for (size_t i = first; i < g.end; ++i) {
     const short k = g.of[i - first];
@@ -533,58 +624,35 @@ cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const flo
   if (p.stacks == 0) return cudaSuccess;
   cudaError_t e = launch_kernel(norm_sum_kernel, dim3((unsigned)chunk), dim3(kThreads), 0, c.stream, true, p);
   if (e == cudaSuccess) e = launch_kernel(halve_kernel, dim3((unsigned)chunk), dim3(kThreads), 0, c.stream, true, p);
-  // The maps of the three products, those that read X for either of its two places.
-  StepParams step[3][2];
-  for (int j = 0; j < 2; ++j)
-    for (int k = 0; e == cudaSuccess && k < g.classes; ++k) {
-      const Class& l = g.cls[k];
-      const bool wide = l.rows <= l.cols;
-      const size_t side = std::min(l.rows, l.cols), px = up(l.cols, 64), pa = up(side, 64);
-      const auto map = [&](CUtensorMap* to, mma::Kind* kind, const __half* at, size_t rows, size_t cols, size_t pitch,
-                           bool depth) {
-        // as i or j the padded row is read: what lies behind its end becomes lanes or columns that nothing uses
-        if (e == cudaSuccess)
-          e = mma::make_map(to, kind, false, at, depth ? cols : pitch, rows, l.count, pitch, rows * pitch, depth, 128);
-      };
-      Shape s = {};
-      s.count = (int)l.count;
-      s.matrix = (int)l.matrix;
-      s.vectors = l.vectors;
-      s.ni = s.nj = (int)side;
-      s.pitch = (int)pa;
-      s.matrix_stride = (long long)(side * pa);
-      Shape& gram = step[kGram][j].shape[k] = s;
-      gram.k = (int)std::max(l.rows, l.cols);
-      gram.to = l.a;
-      map(&gram.a, &gram.a_kind, l.x[j], l.rows, l.cols, px, wide);
-      gram.b = gram.a, gram.b_kind = gram.a_kind;
-      Shape& square = step[kSquare][j].shape[k] = s;
-      square.k = (int)side;
-      square.old = l.a, square.to = l.b;
-      map(&square.a, &square.a_kind, l.a, side, side, pa, true);
-      square.b = square.a, square.b_kind = square.a_kind;
-      // lanes are the columns of X: of a wide one D[i, j] = sum_k X[k, i] B[j, k], of a tall one sum_k B[i, k] X[j, k]
-      Shape& apply = step[kApply][j].shape[k] = s;
-      apply.ni = (int)l.cols, apply.nj = (int)l.rows, apply.k = (int)side;
-      apply.pitch = (int)px;
-      apply.matrix_stride = (long long)(l.rows * px);
-      apply.old = l.x[j], apply.to = l.x[1 - j];
-      map(wide ? &apply.a : &apply.b, wide ? &apply.a_kind : &apply.b_kind, l.x[j], l.rows, l.cols, px, !wide);
-      map(wide ? &apply.b : &apply.a, wide ? &apply.b_kind : &apply.a_kind, l.b, side, side, pa, true);
+  StepsParams q;
+  for (int k = 0; e == cudaSuccess && k < g.classes; ++k) {
+    const Class& l = g.cls[k];
+    Shape& s = q.shape[k];
+    const bool wide = l.rows <= l.cols;
+    const size_t side = std::min(l.rows, l.cols), px = up(l.cols, 64), pa = up(side, 64);
+    s.rows = (int)l.rows, s.cols = (int)l.cols, s.side = (int)side;
+    s.x_pitch = (int)px, s.a_pitch = (int)pa;
+    s.count = (int)l.count, s.matrix = (int)l.matrix;
+    s.to_a = l.a, s.to_b = l.b;
+    s.vectors = l.vectors;
+    mma::Kind depth;
+    const auto map = [&](CUtensorMap* to, mma::Kind* kind, const __half* at, size_t rows, size_t cols, size_t pitch,
+                         bool depth) {
+      // as i or j the padded row is read: what lies behind its end becomes lanes or columns that nothing uses
+      if (e == cudaSuccess)
+        e = mma::make_map(to, kind, false, at, depth ? cols : pitch, rows, l.count, pitch, rows * pitch, depth, 128);
+    };
+    for (int j = 0; j < 2; ++j) {
+      s.x[j] = l.x[j];
+      map(&s.gram[j], &s.gram_kind, l.x[j], l.rows, l.cols, px, wide);
+      map(&s.apply[j], &s.apply_kind, l.x[j], l.rows, l.cols, px, !wide);
     }
-  for (int k = 0; e == cudaSuccess && k < c.steps; ++k) {
-    for (int i = 0; i < 3; ++i) {
-      StepParams& q = step[i][k & 1];
-      q.shapes = g.classes;
-      q.coefs = g.coefs + k * kCoefs;
-      q.coef_stride = c.steps * kCoefs;
-      q.outs = k + 1 == c.steps ? g.outs : nullptr;
-    }
-    e = launch_stage<kGram>(step[kGram][k & 1], c.sms, c.stream);
-    if (e == cudaSuccess) e = launch_stage<kSquare>(step[kSquare][k & 1], c.sms, c.stream);
-    if (e == cudaSuccess) e = launch_stage<kApply>(step[kApply][k & 1], c.sms, c.stream);
+    map(&s.a, &depth, l.a, side, side, pa, true);
+    map(&s.b, &depth, l.b, side, side, pa, true);
   }
-  return e;
+  q.shapes = g.classes, q.steps = c.steps;
+  q.coefs = g.coefs, q.outs = g.outs, q.done = g.done;
+  return e == cudaSuccess ? launch_steps(q, c.sms, c.stream) : e;
 }
 
 }  // namespace
