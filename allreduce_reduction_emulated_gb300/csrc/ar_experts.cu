@@ -11,6 +11,7 @@
 //
 // The offsets are read on the device, by every block: nothing waits for the host.
 #include <algorithm>
+#include <cmath>
 
 #include "ar_mma.cuh"
 #include "ar_train.h"
@@ -175,8 +176,8 @@ struct ForwardParams {
 };
 
 template <int CG>
-struct Forward : mma::Independent {
-  static constexpr bool kBf16 = true;
+struct Forward {
+  static constexpr bool kBf16 = true, kOrdered = false;
   static constexpr int kWide = 128 * CG, kUnit = 16 * CG;  // most columns of a tile, and what they are a multiple of
   using Params = ForwardParams;
   struct Local {
@@ -243,8 +244,8 @@ struct GradientParams {
 };
 
 template <int CG>
-struct WeightGradient : mma::Independent {
-  static constexpr bool kBf16 = true;
+struct WeightGradient {
+  static constexpr bool kBf16 = true, kOrdered = false;
   static constexpr int kWide = 128 * CG, kUnit = 64 * CG, kRowsOfTile = mma::kRows * CG;
   using Params = GradientParams;
   struct Local {
@@ -373,8 +374,11 @@ cudaError_t launch_expert_product(const ExpertsCall& c) {
   p.fp32 = c.dtype == AR_FLOAT32;
   p.vectors = vectors(c.y, c.y_stride);
   p.zero_rest = c.zero_rest;
-  const size_t pairs = ((c.out + 255) / 256) * std::max(std::min(c.experts, c.rows), c.rows / 256);
-  return pairs >= (size_t)c.sms ? forward<2>(c, p) : forward<1>(c, p);
+  // the offsets are on the device: as if all experts had the same number of rows
+  const double some = (double)std::max<size_t>(1, std::min(c.experts, c.rows));
+  const auto tiles = [&](double side) { return std::ceil(c.out / side) * some * std::ceil(c.rows / some / side); };
+  return mma::better_in_pairs(tiles(256), tiles(128), std::ceil(c.in / 64.0), c.sms) ? forward<2>(c, p)
+                                                                                      : forward<1>(c, p);
 }
 
 cudaError_t launch_expert_weight_gradient(const ExpertsCall& c) {
@@ -394,8 +398,10 @@ cudaError_t launch_expert_weight_gradient(const ExpertsCall& c) {
   p.fp32 = c.dtype == AR_FLOAT32;
   p.add = c.accumulate;
   p.vectors = vectors(c.y, c.w.y_stride, c.w.z_stride);
-  const size_t pairs = ((c.out + 255) / 256) * ((c.in + 255) / 256) * c.experts;
-  return pairs >= (size_t)c.sms ? weight_gradient<2>(c, p) : weight_gradient<1>(c, p);
+  const auto tiles = [&](double side) { return std::ceil(c.out / side) * std::ceil(c.in / side) * c.experts; };
+  const double slices = std::ceil((double)c.rows / c.experts / 64.0);
+  return mma::better_in_pairs(tiles(256), tiles(128), slices, c.sms) ? weight_gradient<2>(c, p)
+                                                                      : weight_gradient<1>(c, p);
 }
 
 }  // namespace ar

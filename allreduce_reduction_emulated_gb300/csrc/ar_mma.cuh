@@ -215,19 +215,25 @@ __device__ __forceinline__ void stage_columns(uint32_t staging, const uint32_t (
 __device__ __forceinline__ void put_columns(uint32_t staging, uint16_t* to, long long stride, int rows, int columns,
                                             bool vectors) {
   const int lane = threadIdx.x & 31, part = lane & 3;
+  uint4 o[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int column = 8 * q + (lane >> 2);
-    uint4 o;
+  for (int q = 0; q < 4; ++q)
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w)
-                 : "r"(staged(staging, column, part)));
-    if (column >= columns) continue;
-    uint16_t* d = to + column * stride + part * 8;
+                 : "=r"(o[q].x), "=r"(o[q].y), "=r"(o[q].z), "=r"(o[q].w)
+                 : "r"(staged(staging, 8 * q + (lane >> 2), part)));
+  uint16_t* d = to + (lane >> 2) * stride + part * 8;
+  if (vectors && rows >= 32 && columns >= 32) {  // of the whole warp: no branches between the stores
+#pragma unroll
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(d + q * (8 * stride)) = o[q];
+    return;
+  }
+  for (int q = 0; q < 4; ++q, d += 8 * stride) {
+    if (8 * q + (lane >> 2) >= columns) break;
+    const uint4 v = q == 0 ? o[0] : q == 1 ? o[1] : q == 2 ? o[2] : o[3];
     if (vectors && part * 8 + 8 <= rows) {
-      *reinterpret_cast<uint4*>(d) = o;
+      *reinterpret_cast<uint4*>(d) = v;
     } else {
-      const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (part * 8 + i < rows) d[i] = (uint16_t)(w[i / 2] >> (i % 2 * 16));
@@ -258,14 +264,6 @@ __device__ __forceinline__ uint32_t instruction(bool bf16, bool a_depth, bool b_
 
 // ------------------------------------------------------------------ the kernel
 
-// What a policy without dependencies between its tiles has for them.
-struct Independent {
-  template <class Params>
-  static __device__ __forceinline__ bool wait(const Params&, const struct Tile&, volatile uint32_t*) { return true; }
-  template <class Params>
-  static __device__ __forceinline__ void done(const Params&, const struct Tile&) {}
-};
-
 // How an operand lies in memory, which says what its map and its boxes are like.
 enum Kind : int {
   kDepthRows,   // k contiguous: a box is 64 k of up to 128 rows
@@ -294,22 +292,44 @@ struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
   alignas(128) uint8_t staging[kEpilogueWarps][kStaging];
   alignas(8) uint64_t full[kStages], empty[kStages], ready[2], drained[2], tail, done;
-  uint32_t tmem, late;
+  uint32_t tmem, late, go;
 };
 
-// A slice of an operand: `bytes` of it, from its row `row` and from k on.
-template <int CG>
-__device__ __forceinline__ void load_rows(uint32_t to, const CUtensorMap* map, Kind kind, int row, int k, int z, int bytes,
-                                          uint32_t bar) {
-  if (kind == kDepthRows) {
-    tma_load<CG>(to, map, k, row, z, 0, bar);
-  } else if (kind == kWideRows) {
-    tma_load<CG>(to, map, 0, k, row >> 6, z, bar);
-  } else {
-    tma_load<CG>(to, map, row, k, z, 0, bar);
-    if (bytes > kBoxBytes) tma_load<CG>(to + kBoxBytes, map, row + 64, k, z, 0, bar);
+// Until the producer has let the n-th tile of this block go.
+__device__ __forceinline__ bool go_wait(uint32_t at, uint32_t n, volatile uint32_t* late) {
+  for (uint32_t i = 0; i < 1024 * kPolls; ++i) {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    if ((int)(v - n) >= 0) return true;
+    if (*late) return false;
+    __nanosleep(20);
   }
+  *late = 1;
+  return false;
 }
+
+// Where the next slice of an operand is, and how far the one behind it.
+struct Boxes {
+  const CUtensorMap* map;
+  int x, y, z, u, dx, dy;
+  bool two;                // a second box, 64 rows further
+  __device__ __forceinline__ Boxes(const CUtensorMap* map, Kind kind, int row, int k, int matrix, int bytes)
+      : map(map), two(kind == kNarrowRows && bytes > kBoxBytes) {
+    x = kind == kDepthRows ? k : kind == kWideRows ? 0 : row;
+    y = kind == kDepthRows ? row : k;
+    z = kind == kWideRows ? row >> 6 : matrix;
+    u = kind == kWideRows ? matrix : 0;
+    dx = kind == kDepthRows ? kDepth : 0;
+    dy = kDepth - dx;
+  }
+  template <int CG>
+  __device__ __forceinline__ void load(uint32_t to, uint32_t bar) {
+    tma_load<CG>(to, map, x, y, z, u, bar);
+    if (two) tma_load<CG>(to + kBoxBytes, map, x + 64, y, z, u, bar);
+    x += dx;
+    y += dy;
+  }
+};
 
 template <int CG, class Policy>
 constexpr int shared_bytes() {
@@ -336,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     bar_init(saddr(&s.tail), 1);
     bar_init(saddr(&s.done), 1);
-    s.late = 0;
+    s.late = s.go = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_enter();
@@ -352,49 +372,68 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   volatile uint32_t* late = &s.late;
 
   if (warp == 0) {
-    uint32_t slot = 0, phase = 0, tails = 0;
+    const bool one = elect();
+    const uint32_t empty = saddr(&s.empty[0]), stages = saddr(s.stage[0]);
+    const uint32_t full = CG == 2 ? of_rank(saddr(&s.full[0]), 0) : saddr(&s.full[0]);
+    uint32_t slot = 0, phase = 0, tails = 0, released = 0;
     for (int t = first; !*late; t += pairs) {
       Tile w;
       if (!Policy::tile(p, local, t, w)) break;
-      if (w.blocks && !Policy::wait(p, w, late)) break;
+      if constexpr (Policy::kOrdered) {
+        if (!Policy::wait(p, w, late)) break;
+        if (lane == 0) asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(saddr(&s.go)), "r"(++released) : "memory");
+      }
       const uint32_t bytes = 2 * kBoxBytes + w.b_bytes;
-      const int a0 = w.a_row + (int)rank * kRows, b0 = w.b_row + (int)rank * (w.columns / CG);
+      Boxes a(w.a, w.a_kind, w.a_row + (int)rank * kRows, w.k, w.a_z, 2 * kBoxBytes);
+      Boxes b(w.b, w.b_kind, w.b_row + (int)rank * (w.columns / CG), w.k, w.b_z, w.b_bytes);
+      // One thread issues all whole slices.
+      const bool tail = w.last < kDepth;
+      const int whole = w.blocks - (tail ? 1 : 0);
       bool ok = true;
-      for (int i = 0; i < w.blocks; ++i) {
-        ok = bar_wait(saddr(&s.empty[slot]), phase ^ 1, late);
-        if (!ok) break;
-        const bool tail = w.last < kDepth && i == w.blocks - 1;
-        const uint32_t full = CG == 2 ? of_rank(saddr(&s.full[slot]), 0) : saddr(&s.full[slot]);
-        const uint32_t bar = tail ? saddr(&s.tail) : full;
-        const uint32_t at = saddr(s.stage[slot]);
-        const int k = w.k + i * kDepth;
-        if (lane == 0) {
-          if (tail || CG == 1) bar_expect(bar, bytes);
-          else bar_expect_cluster(bar, bytes);
-          load_rows<CG>(at, w.a, w.a_kind, a0, k, w.a_z, 2 * kBoxBytes, bar);
-          load_rows<CG>(at + 2 * kBoxBytes, w.b, w.b_kind, b0, k, w.b_z, w.b_bytes, bar);
+      if (one) {
+        for (int i = 0; i < whole; ++i) {
+          ok = bar_wait(empty + 8 * slot, phase ^ 1, late);
+          if (!ok) break;
+          if constexpr (CG == 2) bar_expect_cluster(full + 8 * slot, bytes);
+          else bar_expect(full + 8 * slot, bytes);
+          const uint32_t at = stages + slot * kStageBytes;
+          a.load<CG>(at, full + 8 * slot);
+          b.load<CG>(at + 2 * kBoxBytes, full + 8 * slot);
+          if (++slot == kStages) slot = 0, phase ^= 1;
+        }
+      }
+      __syncwarp();
+      if (!__all_sync(~0u, ok)) break;
+      if (!one) {  // the others keep count
+        const uint32_t n = slot + whole;
+        phase ^= n / kStages & 1;
+        slot = n % kStages;
+      }
+      if (tail) {
+        // Rows of the next expert, or of none, come along: both operands' become 0 (the other
+        // operand's could be infinite).  k is a box's outer side here: whole 128-byte rows.
+        ok = bar_wait(empty + 8 * slot, phase ^ 1, late);
+        if (ok && one) {
+          bar_expect(saddr(&s.tail), bytes);
+          a.load<CG>(stages + slot * kStageBytes, saddr(&s.tail));
+          b.load<CG>(stages + slot * kStageBytes + 2 * kBoxBytes, saddr(&s.tail));
         }
         __syncwarp();
-        if (tail) {
-          // Rows of the next expert, or of none, came along: both operands' become 0 (the
-          // other operand's could be infinite).  k is a box's outer side here: whole 128-byte rows.
-          ok = bar_wait(bar, tails++ & 1, late);
-          const int rows = kDepth - w.last;
-          for (int v = lane; v < (int)bytes / kBoxBytes * rows * 8; v += 32) {
-            const int box = v / (rows * 8), rest = v % (rows * 8);
-            *reinterpret_cast<uint4*>(s.stage[slot] + box * kBoxBytes + (w.last * 8 + rest) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (!ok) break;
-          if (lane == 0) {
-            if constexpr (CG == 2) bar_arrive_cluster(full);
-            else bar_arrive(full);
-          }
+        ok = ok && bar_wait(saddr(&s.tail), tails++ & 1, late);
+        if (!__all_sync(~0u, ok)) break;
+        const int rows = kDepth - w.last;
+        for (int v = lane; v < (int)bytes / kBoxBytes * rows * 8; v += 32) {
+          const int box = v / (rows * 8), rest = v % (rows * 8);
+          *reinterpret_cast<uint4*>(s.stage[slot] + box * kBoxBytes + (w.last * 8 + rest) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (one) {
+          if constexpr (CG == 2) bar_arrive_cluster(full + 8 * slot);
+          else bar_arrive(full + 8 * slot);
         }
         if (++slot == kStages) slot = 0, phase ^= 1;
       }
-      if (!ok) break;
     }
   } else if (warp == 1 && rank == 0) {
     const bool one = elect();  // one thread issues them all: a commit counts its own thread's
@@ -434,14 +473,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
   } else if (warp >= 4) {
     const int e = warp - 4;
-    uint32_t n = 0;
+    uint32_t n = 0, tiles = 0;
     bool ok = true;
     for (int t = first;; t += pairs) {
       Tile w;
       if (!Policy::tile(p, local, t, w)) break;
       const uint32_t buffer = n & 1, at = tmem + buffer * (kColumns / 2) + ((uint32_t)(e & 3) * 32 << 16);
       const int row = w.a_row + (int)rank * kRows + (e & 3) * 32;
-      ok = ok && Policy::wait(p, w, late);
+      if constexpr (Policy::kOrdered) ok = ok && go_wait(saddr(&s.go), ++tiles, late);
       typename Policy::Epilogue out(p, local, w, row, (e >> 2) * 32, saddr(s.staging[e]));
       if (w.blocks) {
         ok = ok && bar_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
@@ -458,7 +497,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           else bar_arrive(saddr(&s.drained[buffer]));
         }
       }
-      Policy::done(p, w);
+      if constexpr (Policy::kOrdered) {
+        // all parts of this block are stored: one thread says so for all
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
+        if (e == 0 && lane == 0) Policy::done(p, w);
+      }
     }
   }
   __syncwarp();
@@ -482,6 +526,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 // is i (or j).  Returns how it is to be loaded.
 cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
                      uint64_t y_stride, uint64_t z_stride, bool depth, uint32_t box);
+
+// Whether `in_pairs` tiles of pairs of blocks (256 x 256) take less time than `alone` tiles of blocks (128 x
+// 128, a quarter of the work): both in whole waves over the multiprocessors, a slice at 0.27 us (the matrix
+// instructions) against 0.20 (its loads), and what a tile takes besides.
+inline bool better_in_pairs(double in_pairs, double alone, double slices, int sms) {
+  const double pairs = sms / 2 > 0 ? sms / 2 : 1;
+  const auto whole = [](double n) { return (double)(long long)(n + 0.999999); };
+  return whole(in_pairs / pairs) * (0.27 * slices + 3.0) <= whole(alone / sms) * (0.20 * slices + 2.0);
+}
 
 // `together`: the blocks wait for one another, so all of them have to be on the GPU at once.
 template <int CG, class Policy>

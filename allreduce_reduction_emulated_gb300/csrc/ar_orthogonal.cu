@@ -244,7 +244,7 @@ struct StepsParams {
   int stage_tiles[3];
   const float* coefs;            // kCoefs per matrix and step
   void* const* outs;             // where the results of the last step go
-  unsigned int* done;            // per matrix: epilogue warps that have stored their part of a tile
+  unsigned int* done;            // per matrix: blocks that have stored their part of a tile
 };
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
@@ -258,9 +258,8 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 // matrix costs three times the way through the chip, not three launches (8.4 us each).
 template <int CG>
 struct Steps {
-  static constexpr bool kBf16 = false;
+  static constexpr bool kBf16 = false, kOrdered = true;
   static constexpr int kSide = 128 * CG;
-  static constexpr unsigned int kParts = CG * mma::kEpilogueWarps;  // of a tile
   using Params = StepsParams;
   struct Local {};
   static __device__ __forceinline__ void begin(const Params&, Local&) {}
@@ -279,9 +278,10 @@ struct Steps {
     const bool wide = s.rows <= s.cols;
     int nj = s.side;
     if (stage == kApply) {
-      const int fi = (s.cols + kSide - 1) / kSide;
-      i = j % fi;
-      j = j / fi;
+      // the shorter side first: what is on the GPU at once covers all of it, and X is read once
+      const int fi = (s.cols + kSide - 1) / kSide, fj = (s.rows + kSide - 1) / kSide;
+      i = wide ? j / fj : j % fi;
+      j = wide ? j % fj : j / fi;
       nj = s.rows;
       // lanes are the columns of X: D[i, j] = sum_k X[k, i] B[j, k] of a wide one, sum_k B[i, k] X[j, k] of a tall one
       w.a = wide ? &s.apply[step & 1] : &s.b;
@@ -312,16 +312,16 @@ struct Steps {
     return true;
   }
 
-  // The tiles of this matrix before this stage, in all their parts.
+  // The tiles of this matrix before this stage, each in CG parts.
   static __device__ __forceinline__ bool wait(const Params& p, const Tile& w, volatile uint32_t* late) {
     const Shape& s = p.shape[w.shape];
     unsigned int before = (s.tiles[0] + s.tiles[1] + s.tiles[2]) * w.step;
     for (int i = 0; i < w.stage; ++i) before += s.tiles[i];
-    before *= kParts;
+    before *= CG;
     if (before == 0) return true;
     const unsigned int* at = p.done + s.matrix + w.a_z;
     bool ok = false;
-    for (uint32_t n = 0; n < 16 * mma::kPolls; ++n) {
+    for (uint32_t n = 0; n < 16 * mma::kPolls; ++n) {  // about 0.7 us each
       unsigned int v;
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
       ok = v >= before;
@@ -333,19 +333,15 @@ struct Steps {
     return __all_sync(~0u, ok);
   }
   static __device__ __forceinline__ void done(const Params& p, const Tile& w) {
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-      __threadfence();
-      atomicAdd(p.done + p.shape[w.shape].matrix + w.a_z, 1u);
-    }
+    __threadfence();
+    atomicAdd(p.done + p.shape[w.shape].matrix + w.a_z, 1u);
   }
 
   struct Epilogue {
     float x, y;                  // of the old value, of the sum
     const __half* old;           // of the tile's first column, the warp's first lane; NULL: none
     uint16_t *to, *mirror;
-    long long stride, old_stride, mirror_stride;
+    long long stride, stride_in;   // of the results' columns; of the old values' and the mirrored rows
     int lanes, columns, pads, pad_columns;  // of the sides, and with what lies behind a row's end
     bool last, vectors;
     uint32_t staging;
@@ -361,7 +357,7 @@ struct Steps {
       const long long at = (long long)z * nj * pitch, here = at + (long long)w.b_row * pitch + row;
       last = w.stage == kApply && w.step + 1 == p.steps;
       vectors = true;
-      stride = old_stride = mirror_stride = pitch;
+      stride = stride_in = pitch;
       mirror = nullptr;
       if (w.stage == kGram) {
         x = 0.0f, y = f[0];
@@ -393,13 +389,13 @@ struct Steps {
 
     __device__ __forceinline__ void load_next(int c) {
       if (!old) return;
-      const int lane = threadIdx.x & 31, part = lane & 3;
+      const int lane = threadIdx.x & 31, part = lane & 3, column = c + (lane >> 2);
+      const __half* from = old + column * stride_in + part * 8;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int column = c + 8 * q + (lane >> 2);
         next[q] = make_uint4(0, 0, 0, 0);
-        if (column < columns && part * 8 < pads)
-          next[q] = __ldcg(reinterpret_cast<const uint4*>(old + column * old_stride + part * 8));
+        if (column + 8 * q < columns && part * 8 < pads)
+          next[q] = __ldcg(reinterpret_cast<const uint4*>(from + q * (8 * stride_in)));
       }
     }
 
@@ -454,7 +450,7 @@ struct Steps {
                        "r"(w[8 * (h / 2) + 6 + h % 2])
                        : "memory");
         __syncwarp();
-        mma::put_columns(staging, mirror + c, mirror_stride, pad_columns - c, lanes, true);
+        mma::put_columns(staging, mirror + c, stride_in, pad_columns - c, lanes, true);
         __syncwarp();
       }
     }
@@ -487,9 +483,9 @@ double count_tiles(StepsParams& p, int side, int workers, double slice) {
 }
 
 cudaError_t launch_steps(StepsParams& p, int sms, cudaStream_t stream) {
-  // Pairs of blocks (256 x 256) or blocks alone (128 x 128, a quarter, at about 0.6 of a pair's slice).
+  // Pairs of blocks (256 x 256) or blocks alone: 128 x 128, a quarter, whose slices take 0.75 as long.
   const int pairs = std::max(1, sms / 2);
-  const double pair = count_tiles(p, 256, pairs, 1.0), alone = count_tiles(p, 128, sms, 0.6);
+  const double pair = count_tiles(p, 256, pairs, 1.0), alone = count_tiles(p, 128, sms, 0.75);
   const bool in_pairs = pair <= alone;
   if (in_pairs) count_tiles(p, 256, pairs, 1.0);
   long long tiles = 0;
@@ -579,14 +575,26 @@ bool bounds(const OrthogonalCall& c, float* cap, float* growth) {
   double most = 1.0, grow = 1e-30;
   for (int k = 0; k <= c.steps; ++k) {
     cap[k] = (float)most;
+    if (!(cap[k] < 1e6f)) return false;
+    // over [0, most], of f(s) = a + b s^2 + c s^4 and of s f(s): at the end, and where a derivative is 0
     double next = 1e-30;
-    for (int i = 0; i <= 4096; ++i) {
-      const double s = most * i / 4096, f = std::fabs(a + s * s * (b + s * s * q));
-      next = std::max(next, s * f);
+    const auto at = [&](double t) {  // t = s^2
+      if (!(t >= 0.0 && t <= most * most)) return;
+      const double f = std::fabs(a + t * (b + t * q));
+      next = std::max(next, std::sqrt(t) * f);
       grow = std::max(grow, f);
+    };
+    at(0.0);
+    at(most * most);
+    if (q != 0.0) at(-b / (2.0 * q));
+    const double root = 9.0 * b * b - 20.0 * a * q;
+    if (q != 0.0 && root >= 0.0) {
+      at((-3.0 * b + std::sqrt(root)) / (10.0 * q));
+      at((-3.0 * b - std::sqrt(root)) / (10.0 * q));
+    } else if (q == 0.0 && b != 0.0) {
+      at(-a / (3.0 * b));
     }
     most = 1.01 * next;
-    if (!(cap[k] < 1e6f)) return false;
   }
   *growth = (float)(1.01 * grow);
   return *growth < 1e12f;
