@@ -84,39 +84,36 @@ def _weights(what: str, name: str, w, device: int, dtypes=(torch.bfloat16,)):
     return E, N, K, e, n, k
 
 
-def _space(lib, what: str, *matrices) -> int:
-    return sum(lib.ar_expert_workspace(*m) for m in matrices)
+def _space(lib, device, *operands) -> tuple:
+    """(tensor or None, address, bytes) of the workspace of (address, columns, rows, count, row stride, matrix
+    stride) operands; none where all of them are aligned, which needs no call to know."""
+    bits = 0
+    for at, _, _, _, row, matrix in operands:
+        bits |= at | row << 1 | matrix << 1
+    if not bits & 15:
+        return None, None, 0
+    n = sum(lib.ar_expert_workspace(*o) for o in operands)
+    if not n:
+        return None, None, 0
+    t = torch.empty(n, dtype=torch.uint8, device=device)
+    return t, t.data_ptr(), n
 
 
-def _stream_of(stream, device: int):
-    """(context, handle) of a call's stream."""
-    if stream is None:
-        return None, torch._C._cuda_getCurrentRawStream(device)
-    return _on(stream)
-
-
-def _made(context, make):
-    if context is None:
-        return make()
-    with context:
-        return make()
-
-
-def _contiguous(w_strides):
-    """(columns, rows, count, row stride, matrix stride) of the weights, contiguous side first."""
-    E, N, K, e, n, k = w_strides
-    return (K, N, E, n, e) if k == 1 else (N, K, E, k, e)
-
-
-def _product(what, lib, x, at_x, w, at_w, offsets, off_size, out, zero_rest, context, handle):
+def _product(what, lib, x, at_x, w, at_w, offsets, off_size, out, zero_rest, handle):
     """y = the product into `out`; at_w: (experts, out, in, strides)."""
     _, rows, K, x_stride = at_x
     E, N, _, e, n, k = at_w
-    bytes_ = _space(lib, what, (x.data_ptr(), K, rows, 1, x_stride, 0), (w.data_ptr(), *_contiguous(at_w)))
-    space = _made(context, lambda: torch.empty(bytes_, dtype=torch.uint8, device=x.device)) if bytes_ else None
-    _check(lib.ar_expert_product(x.data_ptr(), rows, x_stride, w.data_ptr(), E, N, K, e, n, k, offsets, off_size,
-                                 out.data_ptr(), out.stride(0) if rows > 1 else N, _DTYPES[out.dtype], zero_rest,
-                                 None if space is None else space.data_ptr(), bytes_, handle), what)
+    x_at, w_at = x.data_ptr(), w.data_ptr()
+    by_weights = (w_at, K, N, E, n, e) if k == 1 else (w_at, N, K, E, k, e)
+    space, at, bytes_ = _space(lib, x.device, (x_at, K, rows, 1, x_stride, 0), by_weights)
+    _check(lib.ar_expert_product(x_at, rows, x_stride, w_at, E, N, K, e, n, k, offsets, off_size, out.data_ptr(),
+                                 out.stride(0) if rows > 1 else N, _DTYPES[out.dtype], zero_rest, at, bytes_, handle),
+           what)
+
+
+def _of(x, shape, dtype):
+    """A new tensor beside x."""
+    return torch.empty(shape, dtype=dtype, device=x.device)
 
 
 def expert_product(x, weights, offsets, out=None, dtype=None, stream=None):
@@ -131,19 +128,26 @@ def expert_product(x, weights, offsets, out=None, dtype=None, stream=None):
     if at_w[2] != K:
         raise _bad(what, f"x has {K} columns, the weights take {at_w[2]}")
     off, size = _indices(what, "offsets", offsets, device, E + 1)
-    context, handle = _stream_of(stream, device)
-    fresh = out is None
-    if fresh:
-        dtype = torch.bfloat16 if dtype is None else dtype
-        if dtype not in _DTYPES:
+    if out is None:
+        if dtype is not None and dtype not in _DTYPES:
             raise _bad(what, f"dtype {dtype}: float32 or bfloat16 needed", AR_ERR_UNSUPPORTED)
-        out = _made(context, lambda: torch.empty((rows, N), dtype=dtype, device=x.device))
     else:
         if _rows(what, "out", out, device, rows, tuple(_DTYPES))[2] != N:
             raise _bad(what, f"out has {out.shape[1]} columns, {N} needed")
         if dtype is not None and out.dtype != dtype:
             raise _bad(what, f"out is {out.dtype}, dtype is {dtype}")
-    _product(what, library(), x, at_x, weights, at_w, off, size, out, fresh, context, handle)
+    if stream is not None:
+        context, handle = _on(stream)
+        with context:
+            return _into(what, x, at_x, weights, at_w, off, size, out, dtype, handle)
+    return _into(what, x, at_x, weights, at_w, off, size, out, dtype, torch._C._cuda_getCurrentRawStream(device))
+
+
+def _into(what, x, at_x, weights, at_w, off, size, out, dtype, handle):
+    fresh = out is None
+    if fresh:
+        out = _of(x, (at_x[1], at_w[1]), torch.bfloat16 if dtype is None else dtype)
+    _product(what, library(), x, at_x, weights, at_w, off, size, out, fresh, handle)
     return out
 
 
@@ -169,41 +173,50 @@ def expert_gradients(dy, x, weights, offsets, dx=None, dw=None, dw_dtype=None, a
     off, size = _indices(what, "offsets", offsets, device, E + 1)
     if accumulate and (dw is None or not need_dw):
         raise _bad(what, "accumulate needs a dw to add to")
-    context, handle = _stream_of(stream, device)
-    lib = library()
-    fresh = dx is None
-    if not need_dx:
-        dx = None
-    else:
-        if fresh:
-            dx = _made(context, lambda: torch.empty((rows, K), dtype=torch.bfloat16, device=x.device))
-        elif _rows(what, "dx", dx, device, rows, tuple(_DTYPES))[2] != K:
-            raise _bad(what, f"dx has {dx.shape[1]} columns, {K} needed")
+    if dx is not None and need_dx and _rows(what, "dx", dx, device, rows, tuple(_DTYPES))[2] != K:
+        raise _bad(what, f"dx has {dx.shape[1]} columns, {K} needed")
     at_dw = None
-    if not need_dw:
-        dw = None
-    elif dw is None:
-        dtype = torch.bfloat16 if dw_dtype is None else dw_dtype
-        if dtype not in _DTYPES:
-            raise _bad(what, f"dw_dtype {dtype}: float32 or bfloat16 needed", AR_ERR_UNSUPPORTED)
-        lanes = at_w[5] == 1
-        shape = (E, N, K) if lanes else (E, K, N)
-        dw = _made(context, lambda: torch.empty(shape, dtype=dtype, device=x.device))
-        dw = dw if lanes else dw.transpose(1, 2)
-        at_dw = _weights(what, "dw", dw, device, tuple(_DTYPES))
-    else:
+    if dw is not None and need_dw:
         at_dw = _weights(what, "dw", dw, device, tuple(_DTYPES))
         if at_dw[:3] != (E, N, K):
             raise _bad(what, f"dw is {tuple(dw.shape)}, the weights are {(E, N, K)}")
         if dw_dtype is not None and dw.dtype != dw_dtype:
             raise _bad(what, f"dw is {dw.dtype}, dw_dtype is {dw_dtype}")
-    if dx is not None:
-        E, N, K, e, n, k = at_w
-        _product(what, lib, dy, at_y, weights, (E, K, N, e, k, n), off, size, dx, fresh, context, handle)
-    if dw is not None:
-        bytes_ = _space(lib, what, (dy.data_ptr(), N, rows, 1, dy_stride, 0), (x.data_ptr(), K, rows, 1, x_stride, 0))
-        space = _made(context, lambda: torch.empty(bytes_, dtype=torch.uint8, device=x.device)) if bytes_ else None
-        _check(lib.ar_expert_weight_gradient(dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, rows, E, N, K, off, size,
-                                             dw.data_ptr(), *at_dw[3:], _DTYPES[dw.dtype], accumulate,
-                                             None if space is None else space.data_ptr(), bytes_, handle), what)
+    elif dw_dtype is not None and dw_dtype not in _DTYPES:
+        raise _bad(what, f"dw_dtype {dw_dtype}: float32 or bfloat16 needed", AR_ERR_UNSUPPORTED)
+    if not need_dx:
+        dx = None
+    if not need_dw:
+        dw = None
+    if stream is not None:
+        context, handle = _on(stream)
+        with context:
+            return _both(what, dy, at_y, x, at_x, weights, at_w, off, size, dx, dw, at_dw, dw_dtype, accumulate, need_dx,
+                         need_dw, handle)
+    return _both(what, dy, at_y, x, at_x, weights, at_w, off, size, dx, dw, at_dw, dw_dtype, accumulate, need_dx, need_dw,
+                 torch._C._cuda_getCurrentRawStream(device))
+
+
+def _both(what, dy, at_y, x, at_x, weights, at_w, off, size, dx, dw, at_dw, dw_dtype, accumulate, need_dx, need_dw,
+          handle):
+    lib = library()
+    E, N, K, e, n, k = at_w
+    _, rows, _, dy_stride = at_y
+    x_stride = at_x[3]
+    if need_dx:
+        fresh = dx is None
+        if fresh:
+            dx = _of(x, (rows, K), torch.bfloat16)
+        _product(what, lib, dy, at_y, weights, (E, K, N, e, k, n), off, size, dx, fresh, handle)
+    if need_dw:
+        if dw is None:
+            dtype = torch.bfloat16 if dw_dtype is None else dw_dtype
+            if k == 1:
+                dw, at_dw = _of(x, (E, N, K), dtype), (E, N, K, N * K, K, 1)
+            else:
+                dw, at_dw = _of(x, (E, K, N), dtype).transpose(1, 2), (E, N, K, N * K, 1, N)
+        dy_at, x_at = dy.data_ptr(), x.data_ptr()
+        space, at, bytes_ = _space(lib, x.device, (dy_at, N, rows, 1, dy_stride, 0), (x_at, K, rows, 1, x_stride, 0))
+        _check(lib.ar_expert_weight_gradient(dy_at, dy_stride, x_at, x_stride, rows, E, N, K, off, size, dw.data_ptr(),
+                                             *at_dw[3:], _DTYPES[dw.dtype], accumulate, at, bytes_, handle), what)
     return dx, dw
