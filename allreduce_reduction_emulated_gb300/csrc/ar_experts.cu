@@ -42,7 +42,7 @@ cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, 
   const bool wide = *kind == kWideRows;
   const cuuint64_t dims[4] = {wide ? 64 : nx, ny, wide ? nx / 64 : nz, wide ? nz : 1};
   const cuuint64_t strides[3] = {y, wide ? 128 : z, z};
-  const cuuint32_t box[4] = {64, depth ? box_rows : 64, wide ? 2u : 1u, 1}, step[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, depth ? box_rows : 64, wide ? box_rows / 64 : 1, 1}, step[4] = {1, 1, 1, 1};
   const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

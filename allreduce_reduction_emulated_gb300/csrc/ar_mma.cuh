@@ -245,9 +245,9 @@ __device__ __forceinline__ void put_columns(uint32_t staging, uint16_t* to, long
 
 // Of an operand in shared memory, 128-byte swizzle, as its 64 x 64 boxes lie there
 // one behind the other: groups of eight 128-byte rows are 1024 bytes apart; where i
-// (or j) is contiguous, the next 64 of it are a box (8192 bytes) away.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t at, bool depth_contiguous) {
-  const uint64_t lead = depth_contiguous ? 1 : kBoxBytes >> 4;
+// (or j) is contiguous, the next 64 of it are a box (8192 bytes, or `box`) away.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t at, bool depth_contiguous, int box = kBoxBytes) {
+  const uint64_t lead = depth_contiguous ? 1 : box >> 4;
   return (uint64_t)((at & 0x3ffff) >> 4) | lead << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
          (uint64_t)2 << 61;
 }
@@ -267,7 +267,7 @@ __device__ __forceinline__ uint32_t instruction(bool bf16, bool a_depth, bool b_
 // How an operand lies in memory, which says what its map and its boxes are like.
 enum Kind : int {
   kDepthRows,   // k contiguous: a box is 64 k of up to 128 rows
-  kWideRows,    // i (or j) contiguous, a multiple of 64 of them: a box is 2 x 64 i of 64 k
+  kWideRows,    // i (or j) contiguous, a multiple of 64 of them: a box is one or two times 64 i of 64 k
   kNarrowRows,  // i contiguous, any number of them: 64 i of 64 k, two loads
 };
 
@@ -522,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 // ------------------------------------------------------------------ host
 
 // The map of `nz` matrices of `ny` rows of `nx` contiguous 16-bit elements; 128-byte swizzle, zeros outside.
-// Strides in elements; addresses and strides are whole 16 bytes.  depth: nx is k, and a box has `box` rows; else nx
-// is i (or j).  Returns how it is to be loaded.
+// Strides in elements; addresses and strides are whole 16 bytes.  depth: nx is k; else nx is i (or j).  A box has
+// `box` i (64 or 128; of kNarrowRows always 64).  Returns how it is to be loaded.
 cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
                      uint64_t y_stride, uint64_t z_stride, bool depth, uint32_t box);
 

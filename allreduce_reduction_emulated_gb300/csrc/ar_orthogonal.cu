@@ -46,6 +46,7 @@ struct Stack {
   unsigned int first;     // chunk of its first matrix
   unsigned int matrix;    // number of its first matrix
   bool bf16, vectors;     // vectors: rows of the gradient are whole 16 bytes
+  bool out_vectors;       // and of the result
   float scale;
 };
 
@@ -67,15 +68,16 @@ constexpr int kThreads = 256, kSlotsPerThread = 8;
 constexpr unsigned int kChunk = kThreads * kSlotsPerThread;  // slots
 
 // Sum over the block, in a fixed order; every thread gets it.
+template <int THREADS = kThreads>
 __device__ __forceinline__ float block_sum(float v) {
-  __shared__ float part[kThreads / 32];
+  __shared__ float part[THREADS / 32];
 #pragma unroll
   for (int d = 16; d; d /= 2) v += __shfl_xor_sync(~0u, v, d);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) s += part[i];
+  for (int i = 0; i < THREADS / 32; ++i) s += part[i];
   return s;
 }
 
@@ -118,17 +120,14 @@ __device__ __forceinline__ Place place(const PrepareParams& p) {
   return Place{&s, k / s.chunks, k % s.chunks};
 }
 
-// One chunk of one matrix: the update u of every slot to `use`.  With MOMENTUM, the new momentum is
-// written where WRITE, else it is there already.
+// Slots [begin, end) of one matrix, `threads` at a time: the update u of each to `use`.  With momentum, the new one
+// is written where WRITE, else it is there already.
 template <bool WRITE, class F>
-__device__ __forceinline__ void walk(const PrepareParams& p, const Place& at, F use) {
-  const Stack& s = *at.s;
-  const size_t base = (size_t)at.matrix * s.rows * s.cols;
-  const unsigned int total = s.rows * s.slots;
+__device__ __forceinline__ void walk(const PrepareParams& p, const Stack& s, unsigned int matrix, unsigned int begin,
+                                     unsigned int end, unsigned int threads, F use) {
+  const size_t base = (size_t)matrix * s.rows * s.cols;
 #pragma unroll 2
-  for (int i = 0; i < kSlotsPerThread; ++i) {
-    const unsigned int slot = at.chunk * kChunk + i * kThreads + threadIdx.x;
-    if (slot >= total) break;
+  for (unsigned int slot = begin + threadIdx.x; slot < end; slot += threads) {
     const unsigned int row = slot / s.slots, col = (slot - row * s.slots) * 8;
     const int left = (int)(s.cols - col);
     const size_t e = base + (size_t)row * s.cols + col;
@@ -158,11 +157,18 @@ __device__ __forceinline__ void walk(const PrepareParams& p, const Place& at, F 
   }
 }
 
+// One chunk of one matrix.
+template <bool WRITE, class F>
+__device__ __forceinline__ void walk_chunk(const PrepareParams& p, const Place& at, F use) {
+  const unsigned int begin = at.chunk * kChunk, total = at.s->rows * at.s->slots;
+  walk<WRITE>(p, *at.s, at.matrix, begin, min(begin + kChunk, total), kThreads, use);
+}
+
 __global__ void __launch_bounds__(kThreads) norm_sum_kernel(const __grid_constant__ PrepareParams p) {
   pdl_enter();
   const Place at = place(p);
   float sum = 0.0f;
-  walk<true>(p, at, [&](unsigned, unsigned, int, const float (&u)[8]) {
+  walk_chunk<true>(p, at, [&](unsigned, unsigned, int, const float (&u)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) sum += u[j] * u[j];
   });
@@ -214,12 +220,224 @@ __global__ void __launch_bounds__(kThreads) halve_kernel(const __grid_constant__
   }
   const float power = power_for(norm);
   __half* x = s.x + (size_t)at.matrix * s.rows * s.pitch;
-  walk<false>(p, at, [&](unsigned row, unsigned col, int, const float (&u)[8]) {
+  walk_chunk<false>(p, at, [&](unsigned row, unsigned col, int, const float (&u)[8]) {
     __half2 h[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(u[2 * j] * power, u[2 * j + 1] * power);
     *reinterpret_cast<uint4*>(x + (size_t)row * s.pitch + col) = *reinterpret_cast<const uint4*>(h);
   });
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ------------------------------------------------------------------ small matrices, whole in one block
+
+// Up to 128 by 512 a matrix stays in one block's shared memory through all steps, and so do A and B: what
+// a step costs is the matrix instructions' way and three turns through the registers (about 3 us), where the
+// tiles of the launch below go through L2 and wait for one another (14 us).
+//
+// X lies as boxes of 128 rows (the short side) by 64 columns, 128-byte swizzle.  The first product reads
+// it with the columns as k, the third with the rows as k: the tensor cores take the same bytes both ways.
+// A and B are symmetric boxes of 128 x 64 each, two behind one another.
+constexpr int kSmallSide = 128, kSmallLong = 512, kSmallThreads = 512;
+constexpr int kBox = kSmallSide * 128;  // bytes
+constexpr int kSquareBytes = 2 * kBox;
+
+struct SmallShared {
+  uint64_t done;
+  uint32_t tmem, late;
+  float coefs[kMaxSteps * kCoefs];
+};
+
+constexpr int small_bytes(int boxes) { return 1024 + 2 * kSquareBytes + boxes * kBox + (int)sizeof(SmallShared); }
+
+// Address of 16 bytes: row, 8 columns from `col` on.
+__device__ __forceinline__ uint32_t swizzled(uint32_t base, int row, int col) {
+  return base + (col >> 6) * kBox + row * 128 + (((col >> 3 & 7) ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void put16(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 get16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+// Eight columns of x old + y sum, rounded to fp16 (or bf16).
+__device__ __forceinline__ uint4 combine8(float x, uint4 old, float y, const float* v, bool bf16) {
+  const uint32_t o[4] = {old.x, old.y, old.z, old.w};
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
+    const float lo = x * b.x + y * v[2 * i], hi = x * b.y + y * v[2 * i + 1];
+    w[i] = bf16 ? pack_bf16x2(lo, hi) : half2_bits(lo, hi);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int COLUMNS>  // of tensor memory: at least 128, at least the long side
+__global__ void __launch_bounds__(kSmallThreads, COLUMNS == 128 ? 2 : 1) small_kernel(const __grid_constant__ PrepareParams p) {
+  extern __shared__ uint8_t raw[];
+  const uint32_t base = (mma::saddr(raw) + 1023) & ~1023u;
+  const uint32_t sa = base, sb = base + kSquareBytes, sx = base + 2 * kSquareBytes;
+  constexpr int kBoxes = COLUMNS / 64;
+  auto& s = *reinterpret_cast<SmallShared*>(raw + (sx + kBoxes * kBox - mma::saddr(raw)));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mma::bar_init(mma::saddr(&s.done), 1);
+    s.late = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_enter();
+  if (warp == 0) mma::tmem_alloc<1>(mma::saddr(&s.tmem), COLUMNS);
+  const Place at = place(p);  // a chunk is a whole matrix here
+  const Stack& k = *at.s;
+  const unsigned int matrix = at.matrix;
+  const bool wide = k.rows <= k.cols;
+  const int side = wide ? k.rows : k.cols, length = wide ? k.cols : k.rows;
+  const int boxes = (length + 63) / 64;
+  const unsigned int total = k.rows * k.slots;
+
+  float sum = 0.0f;
+  walk<true>(p, k, matrix, 0, total, kSmallThreads, [&](unsigned, unsigned, int, const float (&u)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += u[j] * u[j];
+  });
+  const float norm = sqrtf(block_sum<kSmallThreads>(sum));
+  if (threadIdx.x < p.steps) coefficients(p, norm, k.scale, threadIdx.x, s.coefs + threadIdx.x * kCoefs);
+  const float power = power_for(norm);
+  // zeros behind the matrix' sides
+  for (int v = threadIdx.x; v < boxes * (kBox / 16); v += kSmallThreads) put16(sx + v * 16, make_uint4(0, 0, 0, 0));
+  __syncthreads();
+  walk<false>(p, k, matrix, 0, total, kSmallThreads, [&](unsigned row, unsigned col, int left, const float (&u)[8]) {
+    __half h[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = __float2half_rn(u[j] * power);
+    if (wide) {  // u is 0 behind the row's end
+      put16(swizzled(sx, row, col), *reinterpret_cast<const uint4*>(h));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < left)
+          asm volatile("st.shared.u16 [%0], %1;" ::"r"(swizzled(sx, col + j, row) + (row & 7) * 2),
+                       "h"(__half_as_ushort(h[j]))
+                       : "memory");
+    }
+  });
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  mma::fence_before();
+  __syncthreads();
+  mma::fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
+  volatile uint32_t* late = &s.late;
+  uint32_t phase = 0;
+  const int row = (warp & 3) * 32 + lane, group = warp >> 2;   // of four groups of columns
+  const uint32_t mine = tmem + ((uint32_t)(warp & 3) * 32 << 16);
+  const bool one = mma::elect();
+  bool ok = true;
+  const auto wait = [&] {  // for the matrix instructions
+    ok = mma::bar_wait(mma::saddr(&s.done), phase, late) && ok;
+    phase ^= 1;
+    mma::fence_after();
+  };
+  const auto hand_over = [&] {  // what the threads have stored, to the matrix instructions
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    mma::fence_before();
+    __syncthreads();
+    mma::fence_after();
+  };
+  const auto sums = [&](int col, float (&v)[32]) {
+    if (ok) {
+      mma::tmem_rows(mine + col, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = __int_as_float(0x7fc00000);
+    }
+  };
+  const uint32_t square = mma::instruction<1>(false, true, true, kSmallSide);
+  for (int step = 0; step < p.steps; ++step) {
+    const float* f = s.coefs + step * kCoefs;
+    const bool last = step + 1 == p.steps;
+    if (warp == 0 && one) {
+      for (int b = 0; b < boxes; ++b)
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t d = mma::operand_desc(sx + b * kBox, true) + i * mma::depth_step(true);
+          mma::mma_f16<1>(tmem, d, d, square, b + i > 0);
+        }
+      mma::mma_commit<1>(mma::saddr(&s.done));
+    }
+    __syncwarp();
+    wait();
+    float v[32];
+    uint4 a[4];
+    sums(group * 32, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = combine8(0.0f, make_uint4(0, 0, 0, 0), f[0], v + 8 * i, false);
+      put16(swizzled(sa, row, group * 32 + 8 * i), a[i]);
+    }
+    hand_over();
+    if (warp == 0 && one) {
+      for (int b = 0; b < 2; ++b)
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t d = mma::operand_desc(sa + b * kBox, true) + i * mma::depth_step(true);
+          mma::mma_f16<1>(tmem, d, d, square, b + i > 0);
+        }
+      mma::mma_commit<1>(mma::saddr(&s.done));
+    }
+    __syncwarp();
+    wait();
+    sums(group * 32, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put16(swizzled(sb, row, group * 32 + 8 * i), combine8(f[1], a[i], f[2], v + 8 * i, false));
+    hand_over();
+    if (warp == 0 && one) {
+      // X with its columns contiguous: the next 64 of them are a box away
+      for (int n = 0; n < boxes * 64; n += 256) {
+        const int columns = min(256, boxes * 64 - n);
+        const uint32_t idesc = mma::instruction<1>(false, true, false, columns);
+        for (int i = 0; i < kSmallSide / 16; ++i) {
+          const uint64_t l = mma::operand_desc(sb + (i >> 2) * kBox, true) + (i & 3) * mma::depth_step(true);
+          const uint64_t r = mma::operand_desc(sx + (n >> 6) * kBox, false, kBox) + i * mma::depth_step(false);
+          mma::mma_f16<1>(tmem + n, l, r, idesc, i > 0);
+        }
+      }
+      mma::mma_commit<1>(mma::saddr(&s.done));
+    }
+    __syncwarp();
+    wait();
+    for (int col = group * 32; col < boxes * 64; col += 128) {
+      sums(col, v);
+      uint16_t* out = static_cast<uint16_t*>(k.out) + (size_t)matrix * k.rows * k.cols;
+      if (wide) out += (size_t)row * length + col;
+      else out += (size_t)col * side + row;
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x = swizzled(sx, row, col + 8 * i);
+        const uint4 r = combine8(f[3], get16(x), f[4], v + 8 * i, last);
+        if (!last) put16(x, r);
+        else if (wide && k.out_vectors && row < side && col + 8 * i + 8 <= length) *reinterpret_cast<uint4*>(out + 8 * i) = r;
+        w[4 * i] = r.x, w[4 * i + 1] = r.y, w[4 * i + 2] = r.z, w[4 * i + 3] = r.w;
+      }
+      if (last && row < side && !(wide && k.out_vectors)) {
+        const size_t stride = wide ? 1 : side;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (col + i < length) out[i * stride] = (uint16_t)(w[i / 2] >> (i % 2 * 16));
+      }
+    }
+    hand_over();
+  }
+  if (__syncthreads_or(*late != 0)) {  // what the matrix instructions still do takes microseconds; 10 ms are theirs
+    for (int i = 0; i < 10000; ++i) __nanosleep(1000);
+    __syncthreads();
+  }
+  if (warp == 0) mma::tmem_free<1>(tmem, COLUMNS);
 }
 
 // ------------------------------------------------------------------ the products
@@ -228,7 +446,7 @@ enum Stage : int { kGram, kSquare, kApply };
 
 // The matrices of one shape in the product kernel.  A stage's result has nj rows of ni.
 struct Shape {
-  CUtensorMap gram[2], apply[2], a, b;   // of X in either place for either product; of A; of B
+  CUtensorMap gram[2][2], apply[2], a[2], b;   // of X in either place, as either operand; of A, as either; of B
   mma::Kind gram_kind, apply_kind;
   int rows, cols, side;
   int x_pitch, a_pitch;          // multiples of 64; what is stored behind a row's end is read by nothing
@@ -241,16 +459,11 @@ struct Shape {
 struct StepsParams {
   Shape shape[kMaxShapes];
   int shapes, steps;
-  int stage_tiles[3];
+  int stage_tiles[3], width;     // columns of a tile
   const float* coefs;            // kCoefs per matrix and step
   void* const* outs;             // where the results of the last step go
   unsigned int* done;            // per matrix: blocks that have stored their part of a tile
 };
-
-__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // All tiles of all steps in one launch: those of the first product of all matrices, of the second, of the
 // third, then the next step's.  A tile waits until all tiles of its matrix before it are stored, which
@@ -279,7 +492,7 @@ struct Steps {
     int nj = s.side;
     if (stage == kApply) {
       // the shorter side first: what is on the GPU at once covers all of it, and X is read once
-      const int fi = (s.cols + kSide - 1) / kSide, fj = (s.rows + kSide - 1) / kSide;
+      const int fi = (s.cols + kSide - 1) / kSide, fj = (s.rows + p.width - 1) / p.width;
       i = wide ? j / fj : j % fi;
       j = wide ? j % fj : j / fi;
       nj = s.rows;
@@ -288,24 +501,34 @@ struct Steps {
       w.b = wide ? &s.b : &s.apply[step & 1];
       w.a_kind = wide ? s.apply_kind : mma::kDepthRows;
       w.b_kind = wide ? mma::kDepthRows : s.apply_kind;
-    } else {  // on and above the diagonal: block column j has j + 1 of them
+    } else if (p.width == kSide) {  // on and above the diagonal: column j of blocks has j + 1 of them
       int c = (int)((sqrtf(8.0f * j + 1.0f) - 1.0f) * 0.5f);
       while ((c + 1) * (c + 2) / 2 <= j) ++c;
       while (c * (c + 1) / 2 > j) --c;
       i = j - c * (c + 1) / 2;
       j = c;
-      w.a = w.b = stage == kGram ? &s.gram[step & 1] : &s.a;
+    } else {  // columns 2 c and 2 c + 1 of half blocks have c + 1 each
+      int c = (int)((sqrtf(4.0f * j + 1.0f) - 1.0f) * 0.5f);
+      while ((c + 1) * (c + 2) <= j) ++c;
+      while (c * (c + 1) > j) --c;
+      const int rest = j - c * (c + 1);
+      i = rest % (c + 1);
+      j = 2 * c + rest / (c + 1);
+    }
+    if (stage != kApply) {
+      w.a = stage == kGram ? &s.gram[step & 1][0] : &s.a[0];
+      w.b = stage == kGram ? &s.gram[step & 1][1] : &s.a[1];
       w.a_kind = w.b_kind = stage == kGram ? s.gram_kind : mma::kDepthRows;
     }
     w.a_row = i * kSide;
-    w.b_row = j * kSide;
+    w.b_row = j * p.width;
     w.a_z = w.b_z = z;
     w.k = 0;
     w.blocks = ((stage == kGram ? max(s.rows, s.cols) : s.side) + mma::kDepth - 1) / mma::kDepth;
     w.last = mma::kDepth;
     const int unit = (w.b_kind == mma::kDepthRows ? 16 : 64) * CG;
-    w.columns = min(kSide, (nj - w.b_row + unit - 1) / unit * unit);
-    w.b_bytes = 2 * mma::kBoxBytes;
+    w.columns = min(p.width, (nj - w.b_row + unit - 1) / unit * unit);
+    w.b_bytes = p.width / CG * 128;
     w.shape = q;
     w.stage = stage;
     w.step = step;
@@ -377,8 +600,8 @@ struct Steps {
           vectors = s.vectors;
         }
       }
-      // a block off the diagonal is stored a second time, lanes as rows
-      if (w.stage != kApply && w.a_row != w.b_row)
+      // a block above the diagonal is stored a second time, lanes as rows
+      if (w.stage != kApply && w.b_row >= w.a_row + kSide)
         mirror = reinterpret_cast<uint16_t*>(w.stage == kGram ? s.to_a : s.to_b) + at + (long long)row * pitch + w.b_row;
       lanes = ni - row;
       pads = pitch - row;
@@ -457,49 +680,95 @@ struct Steps {
   };
 };
 
-// Tiles of all shapes at this side of a tile, and an estimate of the time in units of a 64-deep slice of a
-// pair's tile: a stage takes at least one tile's way, and 5 slices' time go into its epilogue.
-double count_tiles(StepsParams& p, int side, int workers, double slice) {
+// How the products are cut: blocks alone or in pairs, columns of a tile.
+struct Cut {
+  int pair, width;
+};
+// A tile's slice and its epilogue, in us: the loads of 16 KiB of A and 8 or 16 of B a block bound a slice but of the
+// whole pair's tile, which the matrix instructions do.
+constexpr Cut kCuts[4] = {{2, 256}, {2, 128}, {1, 128}, {1, 64}};
+constexpr double kSlice[4] = {0.30, 0.17, 0.18, 0.14}, kEnd[4] = {1.5, 0.8, 0.8, 0.4};
+constexpr double kTurn = 3.0;  // of a stage, from its last tile's sums to the next stage's first
+
+long long stage_tiles(int stage, long long rows, long long cols, const Cut& cut) {
+  const auto over = [](long long n, long long d) { return (n + d - 1) / d; };
+  const long long side = 128 * cut.pair;
+  if (stage == kApply) return over(cols, side) * over(rows, cut.width);
+  const long long fj = over(std::min(rows, cols), cut.width), q = fj / 2;
+  return cut.width == side ? fj * (fj + 1) / 2 : q * (q + 1) + (fj & 1 ? q + 1 : 0);
+}
+
+// Time of a step of `n` shapes: a stage takes its tiles' time over all multiprocessors, but at least a tile's.
+struct Sizes {
+  long long rows, cols, count;
+};
+double step_time(const Sizes* sizes, int n, int cut, int sms) {
   double time = 0.0;
   for (int stage = 0; stage < 3; ++stage) {
-    long long total = 0;
     double work = 0.0, longest = 0.0;
-    for (int q = 0; q < p.shapes; ++q) {
-      Shape& s = p.shape[q];
-      const auto blocks = [&](long long n) { return (n + side - 1) / side; };
-      const long long fs = blocks(s.side);
-      const long long one = stage == kApply ? blocks(s.rows) * blocks(s.cols) : fs * (fs + 1) / 2;
-      s.tiles[stage] = (int)one;
-      s.first[stage] = (int)std::min<long long>(total, 1 << 30);
-      total += one * s.count;
-      const double tile = slice * ((stage == kGram ? std::max(s.rows, s.cols) : s.side) / 64.0) + 5.0;
-      work += tile * one * s.count;
+    for (int q = 0; q < n; ++q) {
+      const Sizes& s = sizes[q];
+      const long long depth = stage == kGram ? std::max(s.rows, s.cols) : std::min(s.rows, s.cols);
+      const double tile = kSlice[cut] * ((depth + 63) / 64) + kEnd[cut];
+      work += tile * (double)(stage_tiles(stage, s.rows, s.cols, kCuts[cut]) * s.count);
       longest = std::max(longest, tile);
     }
-    p.stage_tiles[stage] = (int)std::min<long long>(total, 1 << 30);
-    time += std::max(work / workers, longest);
+    time += std::max(work / std::max(1, sms / kCuts[cut].pair), longest) + kTurn;
   }
   return time;
 }
-
-cudaError_t launch_steps(StepsParams& p, int sms, cudaStream_t stream) {
-  // Pairs of blocks (256 x 256) or blocks alone: 128 x 128, a quarter, whose slices take 0.75 as long.
-  const int pairs = std::max(1, sms / 2);
-  const double pair = count_tiles(p, 256, pairs, 1.0), alone = count_tiles(p, 128, sms, 0.75);
-  const bool in_pairs = pair <= alone;
-  if (in_pairs) count_tiles(p, 256, pairs, 1.0);
-  long long tiles = 0;
-  int most = 0;
-  for (int stage = 0; stage < 3; ++stage) {
-    tiles += p.stage_tiles[stage];
-    most = std::max(most, p.stage_tiles[stage]);
-  }
-  if (tiles * p.steps > 1 << 30) return cudaErrorInvalidValue;
-  return in_pairs ? mma::launch_product<2, Steps<2>>(p, most, sms, stream, true)
-                  : mma::launch_product<1, Steps<1>>(p, most, sms, stream, true);
+int best_cut(const Sizes* sizes, int n, int sms) {
+  int best = 0;
+  for (int i = 1; i < 4; ++i)
+    if (step_time(sizes, n, i, sms) < step_time(sizes, n, best, sms)) best = i;
+  return best;
 }
 
 // ------------------------------------------------------------------ one group of stacks
+
+// Tensor-memory columns of the kernel that takes matrices of this shape whole; 0: they go in tiles.
+int whole_columns(size_t rows, size_t cols) {
+  const size_t side = std::min(rows, cols), length = std::max(rows, cols);
+  return side > kSmallSide || length > kSmallLong ? 0 : length <= 128 ? 128 : length <= 256 ? 256 : 512;
+}
+
+// The small matrices go whole where that is faster.  Alone they nearly always do; beside others, whose tiles
+// leave room for theirs, it is the time of a launch more.  Times in us, measured: 128 x 128 24, 128 x 512
+// 50, in tiles 256 x 256 75.
+bool take_whole(const OrthogonalCall& c) {
+  double alone = 0.0;
+  Sizes rest[kMaxShapes], all[kMaxShapes];
+  int nr = 0, na = 0;
+  double whole[3] = {}, longest[3] = {};
+  for (size_t i = 0; i < c.nstacks; ++i) {
+    if (!c.counts[i] || !c.rows[i] || !c.cols[i]) continue;
+    const Sizes s = {(long long)c.rows[i], (long long)c.cols[i], (long long)c.counts[i]};
+    const auto put = [&](Sizes* to, int& n) {  // shapes beyond kMaxShapes count as the last
+      for (int q = 0; q < n; ++q)
+        if ((to[q].rows == s.rows && to[q].cols == s.cols) || q == kMaxShapes - 1) {
+          to[q].count += s.count;
+          return;
+        }
+      to[n++] = s;
+    };
+    put(all, na);
+    const int columns = whole_columns(c.rows[i], c.cols[i]);
+    if (!columns) {
+      put(rest, nr);
+      continue;
+    }
+    const int k = columns == 512 ? 2 : columns == 256 ? 1 : 0;
+    const double length = (double)std::max(c.rows[i], c.cols[i]);
+    whole[k] += (double)c.counts[i];
+    longest[k] = std::max(longest[k], 6.0 + 0.035 * length + c.steps * (2.2 + 0.008 * length));
+  }
+  for (int k = 0; k < 3; ++k) alone += longest[k] * std::ceil(whole[k] / (c.sms * (k == 0 ? 2 : 1)));
+  const double start = 10.0;
+  const auto tiles = [&](const Sizes* s, int n) {
+    return n ? start + c.steps * step_time(s, n, best_cut(s, n, c.sms), c.sms) : 0.0;
+  };
+  return alone + tiles(rest, nr) <= tiles(all, na);
+}
 
 // The matrices of one shape, and where they lie in the workspace.
 struct Class {
@@ -516,7 +785,7 @@ struct Group {
   size_t end;
   int classes;
   Class cls[kMaxShapes];
-  short of[kMaxStacks];          // class of each stack, -1: empty
+  short of[kMaxStacks];          // class of each stack, -1: empty, or taken whole
   size_t matrices, chunks, bytes;
   float *partial, *coefs;
   void** outs;
@@ -525,13 +794,14 @@ struct Group {
 
 size_t chunks_of(size_t rows, size_t cols) { return (rows * up(cols, 8) / 8 + kChunk - 1) / kChunk; }
 
-void gather(const OrthogonalCall& c, size_t first, uint8_t* base, Group& g) {
+// `whole`: without the small matrices.
+void gather(const OrthogonalCall& c, size_t first, bool whole, uint8_t* base, Group& g) {
   g.classes = 0;
   g.matrices = g.chunks = 0;
   size_t i = first;
   for (; i < c.nstacks && i - first < kMaxStacks; ++i) {
     short k = -1;
-    if (c.counts[i] && c.rows[i] && c.cols[i]) {
+    if (c.counts[i] && c.rows[i] && c.cols[i] && !(whole && whole_columns(c.rows[i], c.cols[i]))) {
       for (k = 0; k < g.classes && !(g.cls[k].rows == c.rows[i] && g.cls[k].cols == c.cols[i]); ++k) {}
       if (k == g.classes) {
         if (g.classes == kMaxShapes) break;
@@ -600,32 +870,69 @@ bool bounds(const OrthogonalCall& c, float* cap, float* growth) {
   return *growth < 1e12f;
 }
 
-cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const float* cap, float growth) {
-  PrepareParams p;
+// What the kernels that read gradients have in common; no stacks yet.
+void start(const OrthogonalCall& c, const float* cap, float growth, PrepareParams& p) {
   p.stacks = 0;
   p.beta = c.beta, p.nesterov = c.nesterov, p.eps = c.eps;
   p.a = c.a, p.b = c.b, p.c = c.c, p.growth = growth, p.steps = c.steps;
   std::memcpy(p.cap, cap, sizeof p.cap);
+  p.partial = p.coefs = nullptr, p.outs = nullptr, p.done = nullptr;
+}
+
+Stack& add(const OrthogonalCall& c, size_t i, size_t chunk, size_t chunks, PrepareParams& p) {
+  float* m = c.momentum ? c.momentum[i] : nullptr;
+  Stack& s = p.stack[p.stacks++];
+  s.grad = c.grads[i], s.momentum = m, s.out = c.outs[i], s.x = nullptr;
+  s.rows = (unsigned)c.rows[i], s.cols = (unsigned)c.cols[i], s.pitch = (unsigned)up(c.cols[i], 64);
+  s.slots = (unsigned)(up(c.cols[i], 8) / 8);
+  s.chunks = (unsigned)chunks, s.first = (unsigned)chunk, s.matrix = 0;
+  s.bf16 = c.dtypes[i] == AR_BFLOAT16;
+  s.vectors = c.cols[i] % 8 == 0 && ((uintptr_t)c.grads[i] & 15) == 0 && ((uintptr_t)m & 15) == 0;
+  s.out_vectors = c.cols[i] % 8 == 0 && ((uintptr_t)c.outs[i] & 15) == 0;
+  s.scale = c.scales ? c.scales[i] : 1.0f;
+  return s;
+}
+
+// The stacks of small matrices, kMaxStacks at a time.
+template <int COLUMNS>
+cudaError_t run_whole(const OrthogonalCall& c, const float* cap, float growth) {
+  constexpr int bytes = small_bytes(COLUMNS / 64);
+  PrepareParams p;
+  start(c, cap, growth, p);
+  size_t matrices = 0;
+  const auto launch = [&]() -> cudaError_t {
+    if (p.stacks == 0) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(small_kernel<COLUMNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess)
+      e = launch_kernel(small_kernel<COLUMNS>, dim3((unsigned)matrices), dim3(kSmallThreads), bytes, c.stream, true, p);
+    p.stacks = 0;
+    matrices = 0;
+    return e;
+  };
+  for (size_t i = 0; i < c.nstacks; ++i) {
+    if (!c.counts[i] || !c.rows[i] || !c.cols[i] || whole_columns(c.rows[i], c.cols[i]) != COLUMNS) continue;
+    add(c, i, matrices, 1, p);
+    matrices += c.counts[i];
+    if (p.stacks == kMaxStacks) {
+      const cudaError_t e = launch();
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return launch();
+}
+
+cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const float* cap, float growth) {
+  PrepareParams p;
+  start(c, cap, growth, p);
   p.partial = g.partial, p.coefs = g.coefs, p.outs = g.outs, p.done = g.done;
   size_t used[kMaxShapes] = {}, chunk = 0;
   for (size_t i = first; i < g.end; ++i) {
     const short k = g.of[i - first];
     if (k < 0) continue;
     const Class& l = g.cls[k];
-    const size_t pitch = up(l.cols, 64);
-    const bool bf16 = c.dtypes[i] == AR_BFLOAT16;
-    float* m = c.momentum ? c.momentum[i] : nullptr;
-    Stack& s = p.stack[p.stacks++];
-    s.grad = c.grads[i], s.momentum = m, s.out = c.outs[i];
-    s.x = l.x[0] + used[k] * l.rows * pitch;
-    s.rows = (unsigned)l.rows, s.cols = (unsigned)l.cols, s.pitch = (unsigned)pitch;
-    s.slots = (unsigned)(up(l.cols, 8) / 8);
-    s.chunks = (unsigned)chunks_of(l.rows, l.cols);
-    s.first = (unsigned)chunk;
+    Stack& s = add(c, i, chunk, chunks_of(l.rows, l.cols), p);
+    s.x = l.x[0] + used[k] * l.rows * s.pitch;
     s.matrix = l.matrix + (unsigned)used[k];
-    s.bf16 = bf16;
-    s.vectors = l.cols % 8 == 0 && ((uintptr_t)c.grads[i] & 15) == 0 && ((uintptr_t)m & 15) == 0;
-    s.scale = c.scales ? c.scales[i] : 1.0f;
     used[k] += c.counts[i];
     chunk += c.counts[i] * s.chunks;
   }
@@ -633,6 +940,12 @@ cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const flo
   cudaError_t e = launch_kernel(norm_sum_kernel, dim3((unsigned)chunk), dim3(kThreads), 0, c.stream, true, p);
   if (e == cudaSuccess) e = launch_kernel(halve_kernel, dim3((unsigned)chunk), dim3(kThreads), 0, c.stream, true, p);
   StepsParams q;
+  Sizes sizes[kMaxShapes];
+  for (int k = 0; k < g.classes; ++k)
+    sizes[k] = Sizes{(long long)g.cls[k].rows, (long long)g.cls[k].cols, (long long)g.cls[k].count};
+  const Cut cut = kCuts[best_cut(sizes, g.classes, c.sms)];
+  const uint32_t half = (uint32_t)(cut.width / cut.pair);  // j of a block
+  long long total[3] = {};
   for (int k = 0; e == cudaSuccess && k < g.classes; ++k) {
     const Class& l = g.cls[k];
     Shape& s = q.shape[k];
@@ -645,33 +958,49 @@ cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const flo
     s.vectors = l.vectors;
     mma::Kind depth;
     const auto map = [&](CUtensorMap* to, mma::Kind* kind, const __half* at, size_t rows, size_t cols, size_t pitch,
-                         bool depth) {
+                         bool depth, uint32_t box) {
       // as i or j the padded row is read: what lies behind its end becomes lanes or columns that nothing uses
       if (e == cudaSuccess)
-        e = mma::make_map(to, kind, false, at, depth ? cols : pitch, rows, l.count, pitch, rows * pitch, depth, 128);
+        e = mma::make_map(to, kind, false, at, depth ? cols : pitch, rows, l.count, pitch, rows * pitch, depth, box);
     };
     for (int j = 0; j < 2; ++j) {
       s.x[j] = l.x[j];
-      map(&s.gram[j], &s.gram_kind, l.x[j], l.rows, l.cols, px, wide);
-      map(&s.apply[j], &s.apply_kind, l.x[j], l.rows, l.cols, px, !wide);
+      map(&s.gram[j][0], &s.gram_kind, l.x[j], l.rows, l.cols, px, wide, 128);
+      map(&s.gram[j][1], &s.gram_kind, l.x[j], l.rows, l.cols, px, wide, half);
+      map(&s.apply[j], &s.apply_kind, l.x[j], l.rows, l.cols, px, !wide, wide ? 128 : half);
     }
-    map(&s.a, &depth, l.a, side, side, pa, true);
-    map(&s.b, &depth, l.b, side, side, pa, true);
+    map(&s.a[0], &depth, l.a, side, side, pa, true, 128);
+    map(&s.a[1], &depth, l.a, side, side, pa, true, half);
+    map(&s.b, &depth, l.b, side, side, pa, true, wide ? half : 128);
+    for (int stage = 0; stage < 3; ++stage) {
+      const long long one = stage_tiles(stage, sizes[k].rows, sizes[k].cols, cut);
+      if (total[stage] + one * sizes[k].count > 1 << 24) return cudaErrorInvalidValue;
+      s.first[stage] = (int)total[stage];
+      s.tiles[stage] = (int)one;
+      total[stage] += one * sizes[k].count;
+    }
   }
+  for (int stage = 0; stage < 3; ++stage) q.stage_tiles[stage] = (int)total[stage];
+  q.width = cut.width;
   q.shapes = g.classes, q.steps = c.steps;
   q.coefs = g.coefs, q.outs = g.outs, q.done = g.done;
-  return e == cudaSuccess ? launch_steps(q, c.sms, c.stream) : e;
+  if (e != cudaSuccess) return e;
+  const long long most = std::max(total[0], std::max(total[1], total[2]));
+  return cut.pair == 2 ? mma::launch_product<2, Steps<2>>(q, most, c.sms, c.stream, true)
+                       : mma::launch_product<1, Steps<1>>(q, most, c.sms, c.stream, true);
 }
 
 }  // namespace
 
 size_t orthogonal_workspace(const OrthogonalCall& c) {
+  // the groups depend on whether the small matrices are taken whole, and that on the device
   size_t most = 0;
   Group g;
-  for (size_t i = 0; i < c.nstacks; i = g.end) {
-    gather(c, i, nullptr, g);
-    most = std::max(most, g.bytes);
-  }
+  for (const bool whole : {false, true})
+    for (size_t i = 0; i < c.nstacks; i = g.end) {
+      gather(c, i, whole, nullptr, g);
+      most = std::max(most, g.bytes);
+    }
   return most;
 }
 
@@ -683,11 +1012,19 @@ bool orthogonal_bounded(const OrthogonalCall& c) {
 cudaError_t launch_orthogonal(const OrthogonalCall& c) {
   float cap[kMaxSteps + 1] = {}, growth;
   if (!bounds(c, cap, &growth)) return cudaErrorInvalidValue;
+  const bool whole = take_whole(c);
+  cudaError_t e = cudaSuccess;
+  if (whole) {
+    e = run_whole<512>(c, cap, growth);
+    if (e == cudaSuccess) e = run_whole<256>(c, cap, growth);
+    if (e == cudaSuccess) e = run_whole<128>(c, cap, growth);
+    if (e != cudaSuccess) return e;
+  }
   Group g;
   for (size_t i = 0; i < c.nstacks; i = g.end) {
-    gather(c, i, static_cast<uint8_t*>(c.workspace), g);
+    gather(c, i, whole, static_cast<uint8_t*>(c.workspace), g);
     if (g.chunks > 1u << 30 || g.matrices > 1u << 20) return cudaErrorInvalidValue;
-    const cudaError_t e = run(c, g, i, cap, growth);
+    e = run(c, g, i, cap, growth);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
