@@ -227,7 +227,7 @@ struct Forward {
     return true;
   }
   struct Epilogue : Store {
-    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, uint32_t staging)
+    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, uint32_t staging, const float*)
         : Store{static_cast<uint8_t*>(p.y) + (w.b_row * p.y_stride + row) * (p.fp32 ? 4 : 2), p.y_stride, p.out - row,
                 min(w.columns, w.end - w.b_row), p.fp32, false, p.vectors, staging} {}
   };
@@ -275,7 +275,7 @@ struct WeightGradient {
     return true;
   }
   struct Epilogue : Store {
-    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, uint32_t staging)
+    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, uint32_t staging, const float*)
         : Store{static_cast<uint8_t*>(p.dw) + (w.end * p.e_stride + w.b_row * p.j_stride + row) * (p.fp32 ? 4 : 2),
                 p.j_stride, p.add && w.blocks == 0 ? 0 : p.ni - row, min(w.columns, p.nj - w.b_row), p.fp32, p.add,
                 p.vectors, staging} {}

@@ -34,6 +34,7 @@ constexpr int kDepth = 64;                 // k per stage: 128 bytes, one swizzl
 constexpr int kBoxBytes = 64 * kDepth * 2; // 64 x 64 elements, 128-byte rows
 constexpr int kStageBytes = 4 * kBoxBytes; // A: two of them, B: up to two
 constexpr int kStages = 6;
+constexpr int kAhead = 16;
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr uint32_t kPolls = 1u << 16;
@@ -293,6 +294,7 @@ struct Shared {
   alignas(128) uint8_t staging[kEpilogueWarps][kStaging];
   alignas(8) uint64_t full[kStages], empty[kStages], ready[2], drained[2], tail, done;
   uint32_t tmem, late, go;
+  float factors[kAhead][2];      // of the tiles that the producer has let go
 };
 
 // Until the producer has let the n-th tile of this block go.
@@ -381,7 +383,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (!Policy::tile(p, local, t, w)) break;
       if constexpr (Policy::kOrdered) {
         if (!Policy::wait(p, w, late)) break;
-        if (lane == 0) asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(saddr(&s.go)), "r"(++released) : "memory");
+        // The epilogue's factors come along: its warps find them in shared memory.  The stages and accumulators
+        // let the producer be at most kStages + 2 tiles ahead.
+        if (lane < 2) s.factors[released % kAhead][lane] = Policy::factor(p, w, lane);
+        __syncwarp();
+        ++released;
+        if (lane == 0) asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(saddr(&s.go)), "r"(released) : "memory");
       }
       const uint32_t bytes = 2 * kBoxBytes + w.b_bytes;
       Boxes a(w.a, w.a_kind, w.a_row + (int)rank * kRows, w.k, w.a_z, 2 * kBoxBytes);
@@ -481,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const uint32_t buffer = n & 1, at = tmem + buffer * (kColumns / 2) + ((uint32_t)(e & 3) * 32 << 16);
       const int row = w.a_row + (int)rank * kRows + (e & 3) * 32;
       if constexpr (Policy::kOrdered) ok = ok && go_wait(saddr(&s.go), ++tiles, late);
-      typename Policy::Epilogue out(p, local, w, row, (e >> 2) * 32, saddr(s.staging[e]));
+      typename Policy::Epilogue out(p, local, w, row, (e >> 2) * 32, saddr(s.staging[e]), s.factors[(tiles - 1) % kAhead]);
       if (w.blocks) {
         ok = ok && bar_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
         fence_after();

@@ -58,14 +58,16 @@ struct PrepareParams {
   float eps, a, b, c, growth;
   float cap[kMaxSteps + 1];  // bounds of the singular values before each step
   int steps;
+  unsigned int chunk;        // slots of a chunk
   float* partial;            // one per chunk
   float* coefs;              // kCoefs per matrix and step
   void** outs;               // one per matrix
   unsigned int* done;        // one per matrix: made 0
 };
 
-constexpr int kThreads = 256, kSlotsPerThread = 8;
-constexpr unsigned int kChunk = kThreads * kSlotsPerThread;  // slots
+// A chunk is what one block takes: up to 2048 slots, fewer where that would leave multiprocessors idle.
+constexpr int kThreads = 256;
+constexpr unsigned int kMostChunk = 2048;
 
 // Sum over the block, in a fixed order; every thread gets it.
 template <int THREADS = kThreads>
@@ -108,15 +110,15 @@ struct Place {
   unsigned int matrix, chunk;  // of the stack, of the matrix
 };
 
-__device__ __forceinline__ Place place(const PrepareParams& p) {
+__device__ __forceinline__ Place place(const PrepareParams& p, unsigned int block) {
   int lo = 0;
   for (int hi = p.stacks; hi - lo > 1;) {
     const int mid = (lo + hi) >> 1;
-    if (p.stack[mid].first <= blockIdx.x) lo = mid;
+    if (p.stack[mid].first <= block) lo = mid;
     else hi = mid;
   }
   const Stack& s = p.stack[lo];
-  const unsigned int k = blockIdx.x - s.first;
+  const unsigned int k = block - s.first;
   return Place{&s, k / s.chunks, k % s.chunks};
 }
 
@@ -126,7 +128,7 @@ template <bool WRITE, class F>
 __device__ __forceinline__ void walk(const PrepareParams& p, const Stack& s, unsigned int matrix, unsigned int begin,
                                      unsigned int end, unsigned int threads, F use) {
   const size_t base = (size_t)matrix * s.rows * s.cols;
-#pragma unroll 2
+#pragma unroll 4
   for (unsigned int slot = begin + threadIdx.x; slot < end; slot += threads) {
     const unsigned int row = slot / s.slots, col = (slot - row * s.slots) * 8;
     const int left = (int)(s.cols - col);
@@ -160,13 +162,13 @@ __device__ __forceinline__ void walk(const PrepareParams& p, const Stack& s, uns
 // One chunk of one matrix.
 template <bool WRITE, class F>
 __device__ __forceinline__ void walk_chunk(const PrepareParams& p, const Place& at, F use) {
-  const unsigned int begin = at.chunk * kChunk, total = at.s->rows * at.s->slots;
-  walk<WRITE>(p, *at.s, at.matrix, begin, min(begin + kChunk, total), kThreads, use);
+  const unsigned int begin = at.chunk * p.chunk, total = at.s->rows * at.s->slots;
+  walk<WRITE>(p, *at.s, at.matrix, begin, min(begin + p.chunk, total), kThreads, use);
 }
 
 __global__ void __launch_bounds__(kThreads) norm_sum_kernel(const __grid_constant__ PrepareParams p) {
   pdl_enter();
-  const Place at = place(p);
+  const Place at = place(p, blockIdx.x);
   float sum = 0.0f;
   walk_chunk<true>(p, at, [&](unsigned, unsigned, int, const float (&u)[8]) {
 #pragma unroll
@@ -205,9 +207,11 @@ __device__ __forceinline__ void coefficients(const PrepareParams& p, float norm,
 
 __global__ void __launch_bounds__(kThreads) halve_kernel(const __grid_constant__ PrepareParams p) {
   pdl_enter();
-  const Place at = place(p);
+  // from the last chunk to the first: it begins with what the kernel before has left in L2
+  const unsigned int block = gridDim.x - 1 - blockIdx.x;
+  const Place at = place(p, block);
   const Stack& s = *at.s;
-  const float* partial = p.partial + (blockIdx.x - at.chunk);
+  const float* partial = p.partial + (block - at.chunk);
   float sum = 0.0f;
   for (unsigned int i = threadIdx.x; i < s.chunks; i += kThreads) sum += partial[i];
   const float norm = sqrtf(block_sum(sum));
@@ -294,7 +298,7 @@ __global__ void __launch_bounds__(kSmallThreads, COLUMNS == 128 ? 2 : 1) small_k
   }
   pdl_enter();
   if (warp == 0) mma::tmem_alloc<1>(mma::saddr(&s.tmem), COLUMNS);
-  const Place at = place(p);  // a chunk is a whole matrix here
+  const Place at = place(p, blockIdx.x);  // a chunk is a whole matrix here
   const Stack& k = *at.s;
   const unsigned int matrix = at.matrix;
   const bool wide = k.rows <= k.cols;
@@ -560,6 +564,12 @@ struct Steps {
     atomicAdd(p.done + p.shape[w.shape].matrix + w.a_z, 1u);
   }
 
+  // Of the old value (0) and of the sum (1) in the epilogue.
+  static __device__ __forceinline__ float factor(const Params& p, const Tile& w, int which) {
+    const float* f = p.coefs + ((long long)(p.shape[w.shape].matrix + w.a_z) * p.steps + w.step) * kCoefs;
+    return which ? __ldcg(f + (w.stage == kGram ? 0 : 2 * w.stage)) : w.stage == kGram ? 0.0f : __ldcg(f + 2 * w.stage - 1);
+  }
+
   struct Epilogue {
     float x, y;                  // of the old value, of the sum
     const __half* old;           // of the tile's first column, the warp's first lane; NULL: none
@@ -570,11 +580,11 @@ struct Steps {
     uint32_t staging;
     uint4 next[4];               // the old values of the next chunk, loaded ahead
 
-    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int c, uint32_t staging)
-        : staging(staging) {
+    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int c, uint32_t staging,
+                                        const float* factors)
+        : x(factors[0]), y(factors[1]), staging(staging) {
       const Shape& s = p.shape[w.shape];
       const int z = w.a_z, matrix = s.matrix + z;
-      const float* f = p.coefs + ((long long)matrix * p.steps + w.step) * kCoefs;
       const int ni = w.stage == kApply ? s.cols : s.side, nj = w.stage == kApply ? s.rows : s.side;
       const int pitch = w.stage == kApply ? s.x_pitch : s.a_pitch;
       const long long at = (long long)z * nj * pitch, here = at + (long long)w.b_row * pitch + row;
@@ -583,15 +593,12 @@ struct Steps {
       stride = stride_in = pitch;
       mirror = nullptr;
       if (w.stage == kGram) {
-        x = 0.0f, y = f[0];
         old = nullptr;
         to = reinterpret_cast<uint16_t*>(s.to_a) + here;
       } else if (w.stage == kSquare) {
-        x = f[1], y = f[2];
         old = s.to_a + here;
         to = reinterpret_cast<uint16_t*>(s.to_b) + here;
       } else {
-        x = f[3], y = f[4];
         old = s.x[w.step & 1] + here;
         to = reinterpret_cast<uint16_t*>(s.x[(w.step + 1) & 1]) + here;
         if (last) {
@@ -787,17 +794,23 @@ struct Group {
   Class cls[kMaxShapes];
   short of[kMaxStacks];          // class of each stack, -1: empty, or taken whole
   size_t matrices, chunks, bytes;
+  unsigned int chunk;            // slots
   float *partial, *coefs;
   void** outs;
   unsigned int* done;
 };
 
-size_t chunks_of(size_t rows, size_t cols) { return (rows * up(cols, 8) / 8 + kChunk - 1) / kChunk; }
+size_t slots_of(size_t rows, size_t cols) { return rows * (up(cols, 8) / 8); }
+// Slots of a chunk for so many in all: about 1200 blocks, whole rounds of a block's threads.
+unsigned int chunk_for(size_t slots) {
+  return (unsigned int)std::min<size_t>(kMostChunk, std::max<size_t>(kThreads, slots / 1200 / kThreads * kThreads));
+}
 
 // `whole`: without the small matrices.
 void gather(const OrthogonalCall& c, size_t first, bool whole, uint8_t* base, Group& g) {
   g.classes = 0;
   g.matrices = g.chunks = 0;
+  size_t slots = 0;
   size_t i = first;
   for (; i < c.nstacks && i - first < kMaxStacks; ++i) {
     short k = -1;
@@ -810,11 +823,14 @@ void gather(const OrthogonalCall& c, size_t first, bool whole, uint8_t* base, Gr
       g.cls[k].count += c.counts[i];
       g.cls[k].vectors &= c.cols[i] % 8 == 0 && (c.outs == nullptr || ((uintptr_t)c.outs[i] & 15) == 0);
       g.matrices += c.counts[i];
-      g.chunks += c.counts[i] * chunks_of(c.rows[i], c.cols[i]);
+      slots += c.counts[i] * slots_of(c.rows[i], c.cols[i]);
     }
     g.of[i - first] = k;
   }
   g.end = i;
+  g.chunk = chunk_for(slots);
+  for (i = first; i < g.end; ++i)
+    if (g.of[i - first] >= 0) g.chunks += c.counts[i] * ((slots_of(c.rows[i], c.cols[i]) + g.chunk - 1) / g.chunk);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
     uint8_t* p = base + at;
@@ -876,6 +892,7 @@ void start(const OrthogonalCall& c, const float* cap, float growth, PrepareParam
   p.beta = c.beta, p.nesterov = c.nesterov, p.eps = c.eps;
   p.a = c.a, p.b = c.b, p.c = c.c, p.growth = growth, p.steps = c.steps;
   std::memcpy(p.cap, cap, sizeof p.cap);
+  p.chunk = 0;
   p.partial = p.coefs = nullptr, p.outs = nullptr, p.done = nullptr;
 }
 
@@ -924,13 +941,14 @@ cudaError_t run_whole(const OrthogonalCall& c, const float* cap, float growth) {
 cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const float* cap, float growth) {
   PrepareParams p;
   start(c, cap, growth, p);
+  p.chunk = g.chunk;
   p.partial = g.partial, p.coefs = g.coefs, p.outs = g.outs, p.done = g.done;
   size_t used[kMaxShapes] = {}, chunk = 0;
   for (size_t i = first; i < g.end; ++i) {
     const short k = g.of[i - first];
     if (k < 0) continue;
     const Class& l = g.cls[k];
-    Stack& s = add(c, i, chunk, chunks_of(l.rows, l.cols), p);
+    Stack& s = add(c, i, chunk, (slots_of(l.rows, l.cols) + g.chunk - 1) / g.chunk, p);
     s.x = l.x[0] + used[k] * l.rows * s.pitch;
     s.matrix = l.matrix + (unsigned)used[k];
     used[k] += c.counts[i];
