@@ -34,7 +34,7 @@ constexpr int kDepth = 64;                 // k per stage: 128 bytes, one swizzl
 constexpr int kBoxBytes = 64 * kDepth * 2; // 64 x 64 elements, 128-byte rows
 constexpr int kStageBytes = 4 * kBoxBytes; // A: two of them, B: up to two
 constexpr int kStages = 6;
-constexpr int kAhead = 16;
+constexpr int kAhead = 8;                  // tiles worked out ahead
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr uint32_t kPolls = 1u << 16;
@@ -293,22 +293,12 @@ struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
   alignas(128) uint8_t staging[kEpilogueWarps][kStaging];
   alignas(8) uint64_t full[kStages], empty[kStages], ready[2], drained[2], tail, done;
-  uint32_t tmem, late, go;
-  float factors[kAhead][2];      // of the tiles that the producer has let go
+  // Tiles that the producer has worked out, with their epilogue's factors (columns 0: there are no more).
+  uint64_t filled[kAhead], taken[kAhead];
+  Tile tiles[kAhead];
+  float factors[kAhead][2];
+  uint32_t tmem, late;
 };
-
-// Until the producer has let the n-th tile of this block go.
-__device__ __forceinline__ bool go_wait(uint32_t at, uint32_t n, volatile uint32_t* late) {
-  for (uint32_t i = 0; i < 1024 * kPolls; ++i) {
-    uint32_t v;
-    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    if ((int)(v - n) >= 0) return true;
-    if (*late) return false;
-    __nanosleep(20);
-  }
-  *late = 1;
-  return false;
-}
 
 // Where the next slice of an operand is, and how far the one behind it.
 struct Boxes {
@@ -358,7 +348,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     bar_init(saddr(&s.tail), 1);
     bar_init(saddr(&s.done), 1);
-    s.late = s.go = 0;
+    for (int i = 0; i < kAhead; ++i) {
+      bar_init(saddr(&s.filled[i]), 1);
+      bar_init(saddr(&s.taken[i]), kEpilogueWarps + (rank == 0 ? 1 : 0));
+    }
+    s.late = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_enter();
@@ -377,19 +371,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const bool one = elect();
     const uint32_t empty = saddr(&s.empty[0]), stages = saddr(s.stage[0]);
     const uint32_t full = CG == 2 ? of_rank(saddr(&s.full[0]), 0) : saddr(&s.full[0]);
-    uint32_t slot = 0, phase = 0, tails = 0, released = 0;
-    for (int t = first; !*late; t += pairs) {
+    uint32_t slot = 0, phase = 0, tails = 0;
+    for (uint32_t t = 0;; ++t) {
       Tile w;
-      if (!Policy::tile(p, local, t, w)) break;
-      if constexpr (Policy::kOrdered) {
-        if (!Policy::wait(p, w, late)) break;
-        // The epilogue's factors come along: its warps find them in shared memory.  The stages and accumulators
-        // let the producer be at most kStages + 2 tiles ahead.
-        if (lane < 2) s.factors[released % kAhead][lane] = Policy::factor(p, w, lane);
-        __syncwarp();
-        ++released;
-        if (lane == 0) asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(saddr(&s.go)), "r"(released) : "memory");
-      }
+      const bool more = Policy::tile(p, local, first + (int)t * pairs, w);
+      const uint32_t at = t % kAhead;
+      if (!bar_wait(saddr(&s.taken[at]), (t / kAhead & 1) ^ 1, late)) break;
+      if constexpr (Policy::kOrdered)
+        if (more && !Policy::wait(p, w, late)) break;
+      if (!more) w.columns = 0;
+      if (lane == 0) s.tiles[at] = w;
+      if constexpr (Policy::kOrdered)
+        if (more && lane < 2) s.factors[at][lane] = Policy::factor(p, w, lane);
+      __syncwarp();
+      if (lane == 0) bar_arrive(saddr(&s.filled[at]));
+      if (!more) break;
       const uint32_t bytes = 2 * kBoxBytes + w.b_bytes;
       Boxes a(w.a, w.a_kind, w.a_row + (int)rank * kRows, w.k, w.a_z, 2 * kBoxBytes);
       Boxes b(w.b, w.b_kind, w.b_row + (int)rank * (w.columns / CG), w.k, w.b_z, w.b_bytes);
@@ -445,9 +441,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   } else if (warp == 1 && rank == 0) {
     const bool one = elect();  // one thread issues them all: a commit counts its own thread's
     uint32_t slot = 0, phase = 0, n = 0;
-    for (int t = first; !*late; t += pairs) {
-      Tile w;
-      if (!Policy::tile(p, local, t, w)) break;
+    for (uint32_t t = 0;; ++t) {
+      const uint32_t place = t % kAhead;
+      if (!bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) break;
+      const Tile w = s.tiles[place];
+      __syncwarp();
+      if (lane == 0) bar_arrive(saddr(&s.taken[place]));
+      if (w.columns == 0) break;
       if (w.blocks == 0) continue;
       const uint32_t buffer = n & 1, d = tmem + buffer * (kColumns / 2);
       bool ok = bar_wait(saddr(&s.drained[buffer]), ((n >> 1) & 1) ^ 1, late);
@@ -480,15 +480,26 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
   } else if (warp >= 4) {
     const int e = warp - 4;
-    uint32_t n = 0, tiles = 0;
+    uint32_t n = 0;
     bool ok = true;
-    for (int t = first;; t += pairs) {
+    for (uint32_t t = 0;; ++t) {
+      const uint32_t place = t % kAhead;
       Tile w;
-      if (!Policy::tile(p, local, t, w)) break;
+      float factors[2] = {0.0f, 0.0f};
+      ok = ok && bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late);
+      ok = __all_sync(~0u, ok);
+      if (ok) {
+        w = s.tiles[place];
+        if constexpr (Policy::kOrdered) factors[0] = s.factors[place][0], factors[1] = s.factors[place][1];
+        __syncwarp();
+        if (lane == 0) bar_arrive(saddr(&s.taken[place]));
+        if (w.columns == 0) break;
+      } else if (!Policy::tile(p, local, first + (int)t * pairs, w)) {
+        break;
+      }
       const uint32_t buffer = n & 1, at = tmem + buffer * (kColumns / 2) + ((uint32_t)(e & 3) * 32 << 16);
       const int row = w.a_row + (int)rank * kRows + (e & 3) * 32;
-      if constexpr (Policy::kOrdered) ok = ok && go_wait(saddr(&s.go), ++tiles, late);
-      typename Policy::Epilogue out(p, local, w, row, (e >> 2) * 32, saddr(s.staging[e]), s.factors[(tiles - 1) % kAhead]);
+      typename Policy::Epilogue out(p, local, w, row, (e >> 2) * 32, saddr(s.staging[e]), factors);
       if (w.blocks) {
         ok = ok && bar_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
         fence_after();

@@ -2,7 +2,7 @@
 // tensor-core product of ar_mma.cuh.
 //
 //   u = g + beta m (or m, or g);  X = u / (|u| + eps)
-//   `steps` times:  A = X X^T (of a tall matrix X^T X),  B = b A + c A^2,  X <- a X + B X
+//   `steps` times:  A = X X^T (of a tall matrix X^T X),  B = a I + b A + c A^2,  X <- B X
 //
 // Two passes over the gradients (momentum and sums of squares; the scaled 16-bit copy), then one launch for all
 // products of all steps and shapes.  A and B are symmetric: only their blocks on one
@@ -13,7 +13,9 @@
 // tensor cores are as fast.  fp16's range is met by powers of two: all singular values of
 // X have a bound that follows from the coefficients, so that every element's has, and each
 // matrix is held times the power of two that brings the bound to 2^13.  Sums are fp32, and
-// b A and a X are added in fp32 from the 16-bit values before the one rounding.
+// a I + b A is added in fp32 before B's one rounding.  (With a I in B the last product needs no
+// X but its operand; B's diagonal is rounded once more than with a X added apart, and the result is no
+// less exact: 1.3e-3 instead of 1.4e-3 before the last rounding.)
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -186,7 +188,7 @@ __device__ __forceinline__ float power_for(float bound) {
 }
 
 // What the epilogues multiply with.  With X = r X', A = A' / sa, B = B' / sb (primed: as held):
-//   A' = sa r^2 X' X'^T;  B' = sb b / sa A' + sb c / sa^2 A' A';  X_next' = s a r X' + s r / sb B' X'
+//   A' = sa r^2 X' X'^T;  B' = sb a I + sb b / sa A' + sb c / sa^2 A' A';  X_next' = s r / sb B' X'
 __device__ __forceinline__ void coefficients(const PrepareParams& p, float norm, float scale, int step, float* to) {
   const float part = norm == 0.0f ? 0.0f : norm / (norm + p.eps);  // of the first X; below 1 where eps counts
   const auto bound = [&](int k) {
@@ -196,12 +198,12 @@ __device__ __forceinline__ void coefficients(const PrepareParams& p, float norm,
   };
   const float now = bound(step), sq = now * now;
   const float r = norm == 0.0f ? 1.0f : step == 0 ? 1.0f / (norm + p.eps) / power_for(norm) : 1.0f / power_for(now);
-  const float sa = power_for(sq), sb = power_for(fabsf(p.b) * sq + fabsf(p.c) * sq * sq);
+  const float sa = power_for(sq), sb = power_for(fabsf(p.a) + fabsf(p.b) * sq + fabsf(p.c) * sq * sq);
   const float s = step + 1 == p.steps ? scale : power_for(bound(step + 1));
   to[0] = sa * r * r;
   to[1] = sb / sa * p.b;
   to[2] = sb / sa * p.c / sa;
-  to[3] = s * r * p.a;
+  to[3] = sb * p.a;
   to[4] = s * r / sb;
 }
 
@@ -264,11 +266,6 @@ __device__ __forceinline__ uint32_t swizzled(uint32_t base, int row, int col) {
 }
 __device__ __forceinline__ void put16(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint4 get16(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
 }
 // Eight columns of x old + y sum, rounded to fp16 (or bf16).
 __device__ __forceinline__ uint4 combine8(float x, uint4 old, float y, const float* v, bool bf16) {
@@ -397,7 +394,9 @@ __global__ void __launch_bounds__(kSmallThreads, COLUMNS == 128 ? 2 : 1) small_k
     wait();
     sums(group * 32, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) put16(swizzled(sb, row, group * 32 + 8 * i), combine8(f[1], a[i], f[2], v + 8 * i, false));
+    for (int i = 0; i < 32; ++i) v[i] = f[2] * v[i] + (group * 32 + i == row ? f[3] : 0.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put16(swizzled(sb, row, group * 32 + 8 * i), combine8(f[1], a[i], 1.0f, v + 8 * i, false));
     hand_over();
     if (warp == 0 && one) {
       // X with its columns contiguous: the next 64 of them are a box away
@@ -423,7 +422,7 @@ __global__ void __launch_bounds__(kSmallThreads, COLUMNS == 128 ? 2 : 1) small_k
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t x = swizzled(sx, row, col + 8 * i);
-        const uint4 r = combine8(f[3], get16(x), f[4], v + 8 * i, last);
+        const uint4 r = combine8(0.0f, make_uint4(0, 0, 0, 0), f[4], v + 8 * i, last);
         if (!last) put16(x, r);
         else if (wide && k.out_vectors && row < side && col + 8 * i + 8 <= length) *reinterpret_cast<uint4*>(out + 8 * i) = r;
         w[4 * i] = r.x, w[4 * i + 1] = r.y, w[4 * i + 2] = r.z, w[4 * i + 3] = r.w;
@@ -564,15 +563,17 @@ struct Steps {
     atomicAdd(p.done + p.shape[w.shape].matrix + w.a_z, 1u);
   }
 
-  // Of the old value (0) and of the sum (1) in the epilogue.
+  // Of the sum (0) and, of the second product, of A (1) in the epilogue.
   static __device__ __forceinline__ float factor(const Params& p, const Tile& w, int which) {
     const float* f = p.coefs + ((long long)(p.shape[w.shape].matrix + w.a_z) * p.steps + w.step) * kCoefs;
-    return which ? __ldcg(f + (w.stage == kGram ? 0 : 2 * w.stage)) : w.stage == kGram ? 0.0f : __ldcg(f + 2 * w.stage - 1);
+    if (which == 0) return __ldcg(f + 2 * w.stage);
+    return w.stage == kSquare ? __ldcg(f + 1) : 0.0f;
   }
 
   struct Epilogue {
-    float x, y;                  // of the old value, of the sum
-    const __half* old;           // of the tile's first column, the warp's first lane; NULL: none
+    float x, y, diagonal;        // of A, of the sum; what is added where row and column are the same
+    int row, column;             // of the warp's first lane, of the tile
+    const __half* old;           // A, of the tile's first column, the warp's first lane; NULL: none
     uint16_t *to, *mirror;
     long long stride, stride_in;   // of the results' columns; of the old values' and the mirrored rows
     int lanes, columns, pads, pad_columns;  // of the sides, and with what lies behind a row's end
@@ -582,7 +583,7 @@ struct Steps {
 
     __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int c, uint32_t staging,
                                         const float* factors)
-        : x(factors[0]), y(factors[1]), staging(staging) {
+        : x(factors[1]), y(factors[0]), diagonal(0.0f), row(row), column(w.b_row), staging(staging) {
       const Shape& s = p.shape[w.shape];
       const int z = w.a_z, matrix = s.matrix + z;
       const int ni = w.stage == kApply ? s.cols : s.side, nj = w.stage == kApply ? s.rows : s.side;
@@ -598,8 +599,10 @@ struct Steps {
       } else if (w.stage == kSquare) {
         old = s.to_a + here;
         to = reinterpret_cast<uint16_t*>(s.to_b) + here;
+        if (w.b_row < w.a_row + kSide)
+          diagonal = __ldcg(p.coefs + ((long long)matrix * p.steps + w.step) * kCoefs + 3);
       } else {
-        old = s.x[w.step & 1] + here;
+        old = nullptr;
         to = reinterpret_cast<uint16_t*>(s.x[(w.step + 1) & 1]) + here;
         if (last) {
           stride = ni;
@@ -664,6 +667,11 @@ struct Steps {
         const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
         float lo = y * v[2 * i], hi = y * v[2 * i + 1];
         if (old) lo += x * b.x, hi += x * b.y;
+        if (diagonal != 0.0f) {
+          const int off = row + (lane >> 2) + 8 * (i & 1) + 16 * (i >> 3) - (column + c + 8 * (i >> 1 & 3) + 2 * (lane & 3));
+          if (off == 0) lo += diagonal;
+          if (off == 1) hi += diagonal;
+        }
         w[i] = last ? pack_bf16x2(lo, hi) : half2_bits(lo, hi);
       }
       mma::stage_columns(staging, w);
