@@ -21,11 +21,13 @@ namespace ar {
 
 namespace mma {
 
-cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
-                     uint64_t y_stride, uint64_t z_stride, bool depth, uint32_t box_rows) {
-  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+namespace {
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                            const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encoder() {
   static const Encode encode = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -34,6 +36,14 @@ cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, 
       f = nullptr;
     return reinterpret_cast<Encode>(f);
   }();
+  return encode;
+}
+
+}  // namespace
+
+cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
+                     uint64_t y_stride, uint64_t z_stride, bool depth, uint32_t box_rows) {
+  const Encode encode = encoder();
   if (!encode) return cudaErrorNotSupported;
   *kind = depth ? kDepthRows : nx % 64 == 0 ? kWideRows : kNarrowRows;
   // A side of length one has no stride of its own; the map wants one that is whole all the same.
@@ -46,6 +56,20 @@ cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, 
   const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
                             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_store_map(CUtensorMap* map, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
+                           uint64_t y_stride, uint64_t z_stride) {
+  const Encode encode = encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const cuuint64_t y = ny > 1 ? y_stride * 2 : (nx * 2 + 15) / 16 * 16;
+  const cuuint64_t dims[3] = {nx, ny, nz}, strides[2] = {y, nz > 1 ? z_stride * 2 : y};
+  const cuuint32_t box[3] = {32, 32, 1}, step[3] = {1, 1, 1};
+  const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -126,7 +150,9 @@ struct Store {
   long long stride;
   int lanes, columns;   // that are stored: of the warp (may be negative), of the tile
   bool fp32, add, vectors;
-  uint32_t staging;
+  const CUtensorMap* map;   // bf16 at whole 16 bytes: of the results, in boxes of 32 x 32
+  int x, y, z;              // in it
+  mma::Staging& staging;
 
   __device__ __forceinline__ void chunk(uint32_t at, int c, mma::Source source) const {
     const int lane = threadIdx.x & 31;
@@ -158,15 +184,20 @@ struct Store {
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-    mma::stage_columns(staging, w);
-    __syncwarp();
-    mma::put_columns(staging, static_cast<uint16_t*>(to) + c * stride, stride, lanes, columns - c, vectors);
-    __syncwarp();
+    const uint32_t area = staging.next();
+    mma::stage_columns(area, w);
+    if (vectors && c + 32 <= columns) {  // whole chunks by TMA; the map ends where a row of results does
+      staging.store(area, map, x, y + c, z, lanes > 0);
+    } else {
+      __syncwarp();
+      mma::put_columns(area, static_cast<uint16_t*>(to) + c * stride, stride, lanes, columns - c, vectors);
+      staging.release();
+    }
   }
 };
 
 struct ForwardParams {
-  CUtensorMap weights, x, x_few;  // x_few: boxes of 32 rows
+  CUtensorMap weights, x, x_few, y_map;  // x_few: boxes of 32 rows
   mma::Kind w_kind;
   Offsets offsets;
   int out, in;             // W_e: out x in
@@ -178,6 +209,7 @@ struct ForwardParams {
 template <int CG>
 struct Forward {
   static constexpr bool kBf16 = true, kOrdered = false;
+  static constexpr int kStages = 5;
   static constexpr int kWide = 128 * CG, kUnit = 16 * CG;  // most columns of a tile, and what they are a multiple of
   using Params = ForwardParams;
   struct Local {
@@ -227,14 +259,15 @@ struct Forward {
     return true;
   }
   struct Epilogue : Store {
-    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, uint32_t staging, const float*)
+    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, mma::Staging& staging,
+                                        const float*)
         : Store{static_cast<uint8_t*>(p.y) + (w.b_row * p.y_stride + row) * (p.fp32 ? 4 : 2), p.y_stride, p.out - row,
-                min(w.columns, w.end - w.b_row), p.fp32, false, p.vectors, staging} {}
+                min(w.columns, w.end - w.b_row), p.fp32, false, p.vectors, &p.y_map, row, w.b_row, 0, staging} {}
   };
 };
 
 struct GradientParams {
-  CUtensorMap a, b;        // rows by ni, rows by nj
+  CUtensorMap a, b, dw_map;  // rows by ni, rows by nj; dW
   mma::Kind a_kind, b_kind;
   Offsets offsets;
   int ni, nj;
@@ -246,6 +279,7 @@ struct GradientParams {
 template <int CG>
 struct WeightGradient {
   static constexpr bool kBf16 = true, kOrdered = false;
+  static constexpr int kStages = 5;
   static constexpr int kWide = 128 * CG, kUnit = 64 * CG, kRowsOfTile = mma::kRows * CG;
   using Params = GradientParams;
   struct Local {
@@ -275,10 +309,11 @@ struct WeightGradient {
     return true;
   }
   struct Epilogue : Store {
-    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, uint32_t staging, const float*)
+    __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, mma::Staging& staging,
+                                        const float*)
         : Store{static_cast<uint8_t*>(p.dw) + (w.end * p.e_stride + w.b_row * p.j_stride + row) * (p.fp32 ? 4 : 2),
                 p.j_stride, p.add && w.blocks == 0 ? 0 : p.ni - row, min(w.columns, p.nj - w.b_row), p.fp32, p.add,
-                p.vectors, staging} {}
+                p.vectors, &p.dw_map, row, w.b_row, w.end, staging} {}
   };
 };
 
@@ -373,6 +408,10 @@ cudaError_t launch_expert_product(const ExpertsCall& c) {
   p.y_stride = (long long)c.y_stride;
   p.fp32 = c.dtype == AR_FLOAT32;
   p.vectors = vectors(c.y, c.y_stride);
+  if (p.vectors && !p.fp32) {
+    e = mma::make_store_map(&p.y_map, true, c.y, c.out, c.rows, 1, c.y_stride, 0);
+    if (e != cudaSuccess) return e;
+  }
   p.zero_rest = c.zero_rest;
   // the offsets are on the device: as if all experts had the same number of rows
   const double some = (double)std::max<size_t>(1, std::min(c.experts, c.rows));
@@ -398,6 +437,10 @@ cudaError_t launch_expert_weight_gradient(const ExpertsCall& c) {
   p.fp32 = c.dtype == AR_FLOAT32;
   p.add = c.accumulate;
   p.vectors = vectors(c.y, c.w.y_stride, c.w.z_stride);
+  if (p.vectors && !p.fp32) {
+    e = mma::make_store_map(&p.dw_map, true, c.y, p.ni, p.nj, c.experts, c.w.y_stride, c.w.z_stride);
+    if (e != cudaSuccess) return e;
+  }
   const auto tiles = [&](double side) { return std::ceil(c.out / side) * std::ceil(c.in / side) * c.experts; };
   const double slices = std::ceil((double)c.rows / c.experts / 64.0);
   return mma::better_in_pairs(tiles(256), tiles(128), slices, c.sms) ? weight_gradient<2>(c, p)

@@ -33,13 +33,12 @@ constexpr int kRows = 128;                 // i per block
 constexpr int kDepth = 64;                 // k per stage: 128 bytes, one swizzled row
 constexpr int kBoxBytes = 64 * kDepth * 2; // 64 x 64 elements, 128-byte rows
 constexpr int kStageBytes = 4 * kBoxBytes; // A: two of them, B: up to two
-constexpr int kStages = 6;
 constexpr int kAhead = 8;                  // tiles worked out ahead
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr uint32_t kPolls = 1u << 16;
 constexpr int kChunkStep = 32 * (kEpilogueWarps / 4);  // from one chunk of a warp to its next
-constexpr int kStaging = 2048;             // bytes of each epilogue warp: 32 x 32 16-bit results
+constexpr int kStaging = 2048;             // 32 x 32 16-bit results; each epilogue warp has two of them
 
 // ------------------------------------------------------------------ PTX
 
@@ -115,6 +114,19 @@ __device__ __forceinline__ void tma_load(uint32_t to, const CUtensorMap* map, in
         "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
         : "memory");
 }
+
+// 32 x 32 16-bit values from shared memory to (x, y, z) of `map`; what lies outside the map is not stored.
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t from, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(from)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -212,6 +224,32 @@ __device__ __forceinline__ void stage_columns(uint32_t staging, const uint32_t (
     store_transposed(staged(staging, 8 * q + (lane & 7), lane >> 3), w[2 * q], w[2 * q + 1], w[8 + 2 * q],
                      w[8 + 2 * q + 1]);
 }
+// An epilogue warp's two staging areas in turn.  Every use ends in a commit, of stores or of nothing, so
+// that "all but the last" are those from the area that comes next.
+struct Staging {
+  uint32_t base;
+  uint32_t used = 0;
+  __device__ __forceinline__ explicit Staging(uint32_t base) : base(base) {}
+  __device__ __forceinline__ uint32_t next() {
+    if ((threadIdx.x & 31) == 0) bulk_wait_read<1>();
+    __syncwarp();
+    return base + (used++ & 1) * kStaging;
+  }
+  // What the warp has staged at `from` to (x, y, z) of map, where that is inside.
+  __device__ __forceinline__ void store(uint32_t from, const CUtensorMap* map, int x, int y, int z, bool inside) const {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      if (inside) tma_store(map, from, x, y, z);
+      bulk_commit();
+    }
+  }
+  __device__ __forceinline__ void release() const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bulk_commit();
+  }
+};
+
 // The staged columns to memory, `stride` elements apart; `rows` of each, `columns` of them.
 __device__ __forceinline__ void put_columns(uint32_t staging, uint16_t* to, long long stride, int rows, int columns,
                                             bool vectors) {
@@ -288,13 +326,13 @@ struct Tile {
 // What a chunk of a tile's epilogue is made of.
 enum Source : int { kZeros, kSums, kLate };
 
-template <int CG>
+template <int kStages>
 struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
-  alignas(128) uint8_t staging[kEpilogueWarps][kStaging];
+  alignas(1024) uint8_t staging[kEpilogueWarps][2 * kStaging];
   alignas(8) uint64_t full[kStages], empty[kStages], ready[2], drained[2], tail, done;
   // Tiles that the producer has worked out, with their epilogue's factors (columns 0: there are no more).
-  uint64_t filled[kAhead], taken[kAhead];
+  uint64_t filled[kAhead], taken[kAhead], stored[kAhead];
   Tile tiles[kAhead];
   float factors[kAhead][2];
   uint32_t tmem, late;
@@ -325,13 +363,14 @@ struct Boxes {
 
 template <int CG, class Policy>
 constexpr int shared_bytes() {
-  return (int)sizeof(Shared<CG>) + (int)sizeof(typename Policy::Local) + 1024;
+  return (int)sizeof(Shared<Policy::kStages>) + (int)sizeof(typename Policy::Local) + 1024;
 }
 
 template <int CG, class Policy>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ typename Policy::Params p) {
   extern __shared__ uint8_t raw[];
-  auto& s = *reinterpret_cast<Shared<CG>*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
+  constexpr int kStages = Policy::kStages;
+  auto& s = *reinterpret_cast<Shared<kStages>*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
   auto& local = *reinterpret_cast<typename Policy::Local*>(&s + 1);
   constexpr uint32_t kColumns = 2 * 128 * CG;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -350,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     bar_init(saddr(&s.done), 1);
     for (int i = 0; i < kAhead; ++i) {
       bar_init(saddr(&s.filled[i]), 1);
-      bar_init(saddr(&s.taken[i]), kEpilogueWarps + (rank == 0 ? 1 : 0));
+      bar_init(saddr(&s.taken[i]), kEpilogueWarps + (rank == 0 ? 1 : 0) + (Policy::kOrdered ? 1 : 0));
+      bar_init(saddr(&s.stored[i]), kEpilogueWarps);
     }
     s.late = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -482,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int e = warp - 4;
     uint32_t n = 0;
     bool ok = true;
+    Staging staging(saddr(s.staging[e]));
     for (uint32_t t = 0;; ++t) {
       const uint32_t place = t % kAhead;
       Tile w;
@@ -499,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       }
       const uint32_t buffer = n & 1, at = tmem + buffer * (kColumns / 2) + ((uint32_t)(e & 3) * 32 << 16);
       const int row = w.a_row + (int)rank * kRows + (e & 3) * 32;
-      typename Policy::Epilogue out(p, local, w, row, (e >> 2) * 32, saddr(s.staging[e]), factors);
+      typename Policy::Epilogue out(p, local, w, row, (e >> 2) * 32, staging, factors);
       if (w.blocks) {
         ok = ok && bar_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
         fence_after();
@@ -515,11 +556,29 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           else bar_arrive(saddr(&s.drained[buffer]));
         }
       }
-      if constexpr (Policy::kOrdered) {
-        // all parts of this block are stored: one thread says so for all
-        asm volatile("fence.proxy.async.global;" ::: "memory");
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpilogueWarps) : "memory");
-        if (e == 0 && lane == 0) Policy::done(p, w);
+      if constexpr (Policy::kOrdered) {  // warp 3 says so once all warps have stored their parts
+        if (lane == 0) bulk_wait();
+        __syncwarp();
+        if (lane == 0) bar_arrive(saddr(&s.stored[place]));
+      }
+    }
+    if (lane == 0) bulk_wait();
+  } else if (warp == 3) {
+    if constexpr (Policy::kOrdered) {
+      for (uint32_t t = 0;; ++t) {
+        const uint32_t place = t % kAhead;
+        Tile w;
+        if (bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) {
+          w = s.tiles[place];
+          __syncwarp();
+          if (lane == 0) bar_arrive(saddr(&s.taken[place]));
+          if (w.columns == 0) break;
+        } else if (!Policy::tile(p, local, first + (int)t * pairs, w)) {
+          break;
+        }
+        // in a block that has given up too: its NaN are to be there before others read on
+        for (uint32_t i = 0; i < 2 * kPolls && !bar_try(saddr(&s.stored[place]), t / kAhead & 1); ++i) {}
+        if (lane == 0) Policy::done(p, w);
       }
     }
   }
@@ -544,6 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 // `box` i (64 or 128; of kNarrowRows always 64).  Returns how it is to be loaded.
 cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
                      uint64_t y_stride, uint64_t z_stride, bool depth, uint32_t box);
+
+// The same for results stored in boxes of 32 x 32, 64-byte swizzle (as staged() lays them out).
+cudaError_t make_store_map(CUtensorMap* map, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
+                           uint64_t y_stride, uint64_t z_stride);
 
 // Whether `in_pairs` tiles of pairs of blocks (256 x 256) take less time than `alone` tiles of blocks (128 x
 // 128, a quarter of the work): both in whole waves over the multiprocessors, a slice at 0.27 us (the matrix
