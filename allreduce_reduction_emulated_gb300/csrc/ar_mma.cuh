@@ -8,10 +8,11 @@
 // per block of a pair (256 per pair; alone 128).  Either operand may lie with k or
 // with i / j next to each other in memory: the tensor cores read both.
 //
-// Roles of a block's 12 warps: warp 0 issues the TMA loads of a tile's 64-deep slices
-// into a ring of shared-memory stages, warp 1 issues the matrix instructions (of a pair
-// only the even block's), warps 4 to 11 read finished accumulators and hand them to the
-// policy's epilogue, in chunks of 32 columns.  There are two accumulators, so that
+// Roles of a block's 12 warps: warp 2 works out the tiles, warp 0 issues the TMA loads of a
+// tile's 64-deep slices into a ring of shared-memory stages, warp 1 issues the matrix
+// instructions (of a pair only the even block's), warps 4 to 11 read finished accumulators and
+// hand them to the policy's epilogue, in chunks of 32 columns; warp 3 tells of stored tiles where
+// others wait for them.  There are two accumulators, so that
 // one tile's epilogue overlaps the next tile's products.
 //
 // Every wait is bounded (about a second).  A block that gives up tells its other warps;
@@ -331,7 +332,7 @@ struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
   alignas(1024) uint8_t staging[kEpilogueWarps][2 * kStaging];
   alignas(8) uint64_t full[kStages], empty[kStages], ready[2], drained[2], tail, done;
-  // Tiles that the producer has worked out, with their epilogue's factors (columns 0: there are no more).
+  // Tiles that have been worked out, with their epilogue's factors (columns 0: there are no more).
   uint64_t filled[kAhead], taken[kAhead], stored[kAhead];
   Tile tiles[kAhead];
   float factors[kAhead][2];
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     bar_init(saddr(&s.done), 1);
     for (int i = 0; i < kAhead; ++i) {
       bar_init(saddr(&s.filled[i]), 1);
-      bar_init(saddr(&s.taken[i]), kEpilogueWarps + (rank == 0 ? 1 : 0) + (Policy::kOrdered ? 1 : 0));
+      bar_init(saddr(&s.taken[i]), kEpilogueWarps + 1 + (rank == 0 ? 1 : 0) + (Policy::kOrdered ? 1 : 0));
       bar_init(saddr(&s.stored[i]), kEpilogueWarps);
     }
     s.late = 0;
@@ -407,25 +408,38 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s.tmem);
   volatile uint32_t* late = &s.late;
 
-  if (warp == 0) {
+  if (warp == 2) {
+    // Works the tiles out for all others, and waits for what they depend on, up to kAhead tiles early: in the loading
+    // warp this took 2 us of every tile.
+    for (uint32_t t = 0;; ++t) {
+      Tile w;
+      const bool more = Policy::tile(p, local, first + (int)t * pairs, w);
+      const uint32_t place = t % kAhead;
+      if (!bar_wait(saddr(&s.taken[place]), (t / kAhead & 1) ^ 1, late)) break;
+      if constexpr (Policy::kOrdered) {
+        if (more && !Policy::wait(p, w, late)) break;
+        if (more && lane < 2) s.factors[place][lane] = Policy::factor(p, w, lane);
+      }
+      if (!more) w.columns = 0;
+      if (lane == 0) s.tiles[place] = w;
+      __syncwarp();
+      if (lane == 0) bar_arrive(saddr(&s.filled[place]));
+      if (!more) break;
+    }
+  } else if (warp == 0) {
     const bool one = elect();
     const uint32_t empty = saddr(&s.empty[0]), stages = saddr(s.stage[0]);
     const uint32_t full = CG == 2 ? of_rank(saddr(&s.full[0]), 0) : saddr(&s.full[0]);
     uint32_t slot = 0, phase = 0, tails = 0;
     for (uint32_t t = 0;; ++t) {
-      Tile w;
-      const bool more = Policy::tile(p, local, first + (int)t * pairs, w);
-      const uint32_t at = t % kAhead;
-      if (!bar_wait(saddr(&s.taken[at]), (t / kAhead & 1) ^ 1, late)) break;
-      if constexpr (Policy::kOrdered)
-        if (more && !Policy::wait(p, w, late)) break;
-      if (!more) w.columns = 0;
-      if (lane == 0) s.tiles[at] = w;
-      if constexpr (Policy::kOrdered)
-        if (more && lane < 2) s.factors[at][lane] = Policy::factor(p, w, lane);
+      const uint32_t place = t % kAhead;
+      if (!bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) break;
+      const Tile w = s.tiles[place];
       __syncwarp();
-      if (lane == 0) bar_arrive(saddr(&s.filled[at]));
-      if (!more) break;
+      if (lane == 0) bar_arrive(saddr(&s.taken[place]));
+      if (w.columns == 0) break;
+      // what other blocks have stored is read by TMA from here on
+      if constexpr (Policy::kOrdered) asm volatile("fence.proxy.async.global;" ::: "memory");
       const uint32_t bytes = 2 * kBoxBytes + w.b_bytes;
       Boxes a(w.a, w.a_kind, w.a_row + (int)rank * kRows, w.k, w.a_z, 2 * kBoxBytes);
       Boxes b(w.b, w.b_kind, w.b_row + (int)rank * (w.columns / CG), w.k, w.b_z, w.b_bytes);

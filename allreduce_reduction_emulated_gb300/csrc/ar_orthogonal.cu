@@ -556,8 +556,6 @@ struct Steps {
       if (ok || *late) break;
     }
     if (!ok) *late = 1;
-    // what was stored there is read by TMA too
-    asm volatile("fence.proxy.async.global;" ::: "memory");
     return __all_sync(~0u, ok);
   }
   static __device__ __forceinline__ void done(const Params& p, const Tile& w) {
