@@ -209,7 +209,7 @@ struct ForwardParams {
 template <int CG>
 struct Forward {
   static constexpr bool kBf16 = true, kOrdered = false;
-  static constexpr int kStages = 5;
+  static constexpr int kStages = 5, kAreas = 2;
   static constexpr int kWide = 128 * CG, kUnit = 16 * CG;  // most columns of a tile, and what they are a multiple of
   using Params = ForwardParams;
   struct Local {
@@ -279,7 +279,7 @@ struct GradientParams {
 template <int CG>
 struct WeightGradient {
   static constexpr bool kBf16 = true, kOrdered = false;
-  static constexpr int kStages = 5;
+  static constexpr int kStages = 5, kAreas = 2;
   static constexpr int kWide = 128 * CG, kUnit = 64 * CG, kRowsOfTile = mma::kRows * CG;
   using Params = GradientParams;
   struct Local {

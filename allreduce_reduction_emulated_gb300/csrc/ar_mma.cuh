@@ -39,7 +39,7 @@ constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr uint32_t kPolls = 1u << 16;
 constexpr int kChunkStep = 32 * (kEpilogueWarps / 4);  // from one chunk of a warp to its next
-constexpr int kStaging = 2048;             // 32 x 32 16-bit results; each epilogue warp has two of them
+constexpr int kStaging = 2048;             // 32 x 32 16-bit results
 
 // ------------------------------------------------------------------ PTX
 
@@ -57,6 +57,11 @@ __device__ __forceinline__ void bar_expect(uint32_t b, uint32_t bytes) {
 // Of a barrier anywhere in the cluster.
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t b) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
+}
+// Relaxed: for what is no longer in use, not for what was written.  Releasing at the cluster's scope waits for
+// the warp's stores on their way to memory, 2 us of every tile.
+__device__ __forceinline__ void bar_free_cluster(uint32_t b) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(b) : "memory");
 }
 // Relaxed: what it announces is counted by the barrier itself.  With release semantics, and waits that acquire
 // at the cluster's scope, every slice took 0.3 us more (4864 x 2048 x 8192: 235 us against 107).
@@ -327,10 +332,10 @@ struct Tile {
 // What a chunk of a tile's epilogue is made of.
 enum Source : int { kZeros, kSums, kLate };
 
-template <int kStages>
+template <int kStages, int kAreas>
 struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
-  alignas(1024) uint8_t staging[kEpilogueWarps][2 * kStaging];
+  alignas(1024) uint8_t staging[kEpilogueWarps][kAreas * kStaging];
   alignas(8) uint64_t full[kStages], empty[kStages], ready[2], drained[2], tail, done;
   // Tiles that have been worked out, with their epilogue's factors (columns 0: there are no more).
   uint64_t filled[kAhead], taken[kAhead], stored[kAhead];
@@ -364,14 +369,14 @@ struct Boxes {
 
 template <int CG, class Policy>
 constexpr int shared_bytes() {
-  return (int)sizeof(Shared<Policy::kStages>) + (int)sizeof(typename Policy::Local) + 1024;
+  return (int)sizeof(Shared<Policy::kStages, Policy::kAreas>) + (int)sizeof(typename Policy::Local) + 1024;
 }
 
 template <int CG, class Policy>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ typename Policy::Params p) {
   extern __shared__ uint8_t raw[];
   constexpr int kStages = Policy::kStages;
-  auto& s = *reinterpret_cast<Shared<kStages>*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
+  auto& s = *reinterpret_cast<Shared<kStages, Policy::kAreas>*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
   auto& local = *reinterpret_cast<typename Policy::Local*>(&s + 1);
   constexpr uint32_t kColumns = 2 * 128 * CG;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -418,6 +423,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (!bar_wait(saddr(&s.taken[place]), (t / kAhead & 1) ^ 1, late)) break;
       if constexpr (Policy::kOrdered) {
         if (more && !Policy::wait(p, w, late)) break;
+        // what other blocks have stored is read by TMA from here on (in the loading warp the fence holds the loads up)
+        asm volatile("fence.proxy.async.global;" ::: "memory");
         if (more && lane < 2) s.factors[place][lane] = Policy::factor(p, w, lane);
       }
       if (!more) w.columns = 0;
@@ -438,8 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       __syncwarp();
       if (lane == 0) bar_arrive(saddr(&s.taken[place]));
       if (w.columns == 0) break;
-      // what other blocks have stored is read by TMA from here on
-      if constexpr (Policy::kOrdered) asm volatile("fence.proxy.async.global;" ::: "memory");
       const uint32_t bytes = 2 * kBoxBytes + w.b_bytes;
       Boxes a(w.a, w.a_kind, w.a_row + (int)rank * kRows, w.k, w.a_z, 2 * kBoxBytes);
       Boxes b(w.b, w.b_kind, w.b_row + (int)rank * (w.columns / CG), w.k, w.b_z, w.b_bytes);
@@ -566,12 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         fence_before();
         __syncwarp();
         if (lane == 0 && ok) {
-          if constexpr (CG == 2) bar_arrive_cluster(of_rank(saddr(&s.drained[buffer]), 0));
+          if constexpr (CG == 2) bar_free_cluster(of_rank(saddr(&s.drained[buffer]), 0));
           else bar_arrive(saddr(&s.drained[buffer]));
         }
       }
       if constexpr (Policy::kOrdered) {  // warp 3 says so once all warps have stored their parts
-        if (lane == 0) bulk_wait();
         __syncwarp();
         if (lane == 0) bar_arrive(saddr(&s.stored[place]));
       }
@@ -592,6 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         // in a block that has given up too: its NaN are to be there before others read on
         for (uint32_t i = 0; i < 2 * kPolls && !bar_try(saddr(&s.stored[place]), t / kAhead & 1); ++i) {}
+        // the fence covers what the epilogue's warps stored before they arrived
         if (lane == 0) Policy::done(p, w);
       }
     }

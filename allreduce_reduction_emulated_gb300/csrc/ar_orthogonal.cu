@@ -450,13 +450,12 @@ enum Stage : int { kGram, kSquare, kApply };
 // The matrices of one shape in the product kernel.  A stage's result has nj rows of ni.
 struct Shape {
   CUtensorMap gram[2][2], apply[2], a[2], b;   // of X in either place, as either operand; of A, as either; of B
-  CUtensorMap to_x[2], to_a, to_b;             // as results
   mma::Kind gram_kind, apply_kind;
   int rows, cols, side;
-  int a_pitch;                   // of A's rows: a multiple of 64, what lies behind a row's end counts nowhere
+  int x_pitch, a_pitch;          // multiples of 64; what lies behind a row's end counts nowhere
   int count, matrix;             // matrices, and the number of the first
   int first[3], tiles[3];        // of each stage: first tile in it, tiles of a matrix
-  const __half* old;             // A
+  __half *x[2], *to_a, *to_b;
   bool vectors;                  // the results' rows are whole 16 bytes
 };
 
@@ -476,7 +475,7 @@ struct StepsParams {
 template <int CG>
 struct Steps {
   static constexpr bool kBf16 = false, kOrdered = true;
-  static constexpr int kStages = 5;
+  static constexpr int kStages = 6, kAreas = 1;
   static constexpr int kSide = 128 * CG;
   using Params = StepsParams;
   struct Local {};
@@ -574,42 +573,46 @@ struct Steps {
     float x, y, diagonal;        // of A, of the sum; what is added where row and column are the same
     int row, column;             // of the warp's first lane, of the tile
     const __half* old;           // A, of the tile's first column, the warp's first lane; NULL: none
-    uint16_t* out;               // of the last step: the result, likewise
-    const CUtensorMap* to;       // of the others, and where in it
-    int z;
-    long long stride, stride_in;   // of the result's columns; of A's
-    int lanes, columns, pads;    // of the sides, and with what lies behind a row's end
-    bool mirror, vectors;
-    mma::Staging& staging;
+    uint16_t *to, *mirror;       // likewise; a block above the diagonal is stored a second time, lanes as rows
+    long long stride, stride_in; // of the results' columns; of A's, and of the mirrored rows
+    int lanes, columns, pads, pad_columns;  // of the sides, and with what lies behind a row's end
+    bool last, vectors;
+    uint32_t staging;
     uint4 next[4];               // the old values of the next chunk, loaded ahead
 
     __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int c,
-                                        mma::Staging& staging, const float* factors)
-        : x(factors[1]), y(factors[0]), diagonal(0.0f), row(row), column(w.b_row), staging(staging) {
+                                        mma::Staging& area, const float* factors)
+        : x(factors[1]), y(factors[0]), diagonal(0.0f), row(row), column(w.b_row), staging(area.base) {
       const Shape& s = p.shape[w.shape];
-      const int matrix = s.matrix + w.a_z;
+      const int z = w.a_z, matrix = s.matrix + z;
       const int ni = w.stage == kApply ? s.cols : s.side, nj = w.stage == kApply ? s.rows : s.side;
-      z = w.a_z;
+      const int pitch = w.stage == kApply ? s.x_pitch : s.a_pitch;
+      const long long at = (long long)z * nj * pitch, here = at + (long long)w.b_row * pitch + row;
+      last = w.stage == kApply && w.step + 1 == p.steps;
+      vectors = true;
+      stride = stride_in = pitch;
       old = nullptr;
-      out = nullptr;
-      stride = ni, stride_in = s.a_pitch;
-      if (w.stage == kGram) {
-        to = &s.to_a;
-      } else if (w.stage == kSquare) {
-        old = s.old + ((long long)z * nj + w.b_row) * s.a_pitch + row;
-        to = &s.to_b;
-        if (w.b_row < w.a_row + kSide)
-          diagonal = __ldcg(p.coefs + ((long long)matrix * p.steps + w.step) * kCoefs + 3);
+      mirror = nullptr;
+      if (w.stage == kApply) {
+        to = reinterpret_cast<uint16_t*>(s.x[(w.step + 1) & 1]) + here;
+        if (last) {
+          stride = ni;
+          to = static_cast<uint16_t*>(p.outs[matrix]) + (long long)w.b_row * ni + row;
+          vectors = s.vectors;
+        }
       } else {
-        to = &s.to_x[(w.step + 1) & 1];
-        if (w.step + 1 == p.steps) out = static_cast<uint16_t*>(p.outs[matrix]) + (long long)w.b_row * ni + row;
+        uint16_t* result = reinterpret_cast<uint16_t*>(w.stage == kGram ? s.to_a : s.to_b);
+        to = result + here;
+        if (w.b_row >= w.a_row + kSide) mirror = result + at + (long long)row * pitch + w.b_row;
+        if (w.stage == kSquare) {
+          old = s.to_a + here;
+          if (!mirror) diagonal = __ldcg(p.coefs + ((long long)matrix * p.steps + w.step) * kCoefs + 3);
+        }
       }
-      // a block above the diagonal is stored a second time, lanes as rows
-      mirror = w.stage != kApply && w.b_row >= w.a_row + kSide;
-      vectors = s.vectors;
       lanes = ni - row;
-      pads = s.a_pitch - row;
+      pads = pitch - row;
       columns = min(w.columns, nj - w.b_row);
+      pad_columns = pitch - w.b_row;
       load_next(c);
     }
 
@@ -630,11 +633,11 @@ struct Steps {
       uint32_t o[16] = {};
       if (old) {
         // A's columns into the staging memory, and out again as fragments
-        const uint32_t area = staging.next();
         const int part = lane & 3;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(mma::staged(area, 8 * q + (lane >> 2), part)),
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           mma::staged(staging, 8 * q + (lane >> 2), part)),
                        "r"(next[q].x), "r"(next[q].y), "r"(next[q].z), "r"(next[q].w)
                        : "memory");
         __syncwarp();
@@ -642,9 +645,9 @@ struct Steps {
         for (int q = 0; q < 4; ++q)
           asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                        : "=r"(o[2 * q]), "=r"(o[2 * q + 1]), "=r"(o[8 + 2 * q]), "=r"(o[8 + 2 * q + 1])
-                       : "r"(mma::staged(area, 8 * q + (lane & 7), lane >> 3))
+                       : "r"(mma::staged(staging, 8 * q + (lane & 7), lane >> 3))
                        : "memory");
-        staging.release();
+        __syncwarp();
         load_next(c + mma::kChunkStep);
       }
       float v[32];
@@ -665,29 +668,24 @@ struct Steps {
           if (off == 0) lo += diagonal;
           if (off == 1) hi += diagonal;
         }
-        w[i] = out ? pack_bf16x2(lo, hi) : half2_bits(lo, hi);
+        w[i] = last ? pack_bf16x2(lo, hi) : half2_bits(lo, hi);
       }
-      const uint32_t area = staging.next();
-      mma::stage_columns(area, w);
-      const bool inside = lanes > 0 && c < columns;
-      if (out) {
-        __syncwarp();
-        mma::put_columns(area, out + c * stride, stride, lanes, columns - c, vectors);
-        staging.release();
-      } else {
-        staging.store(area, to, row, column + c, z, inside);
-      }
+      mma::stage_columns(staging, w);
+      __syncwarp();
+      mma::put_columns(staging, to + c * stride, stride, last ? lanes : pads, columns - c, vectors);
+      __syncwarp();
       if (mirror) {
         // as rows: the four matrices of rows 8 h and on are its columns 0, 8, 16 and 24
-        const uint32_t turned = staging.next();
 #pragma unroll
         for (int h = 0; h < 4; ++h)
           asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
-                           mma::staged(turned, 8 * h + (lane & 7), lane >> 3)),
+                           mma::staged(staging, 8 * h + (lane & 7), lane >> 3)),
                        "r"(w[8 * (h / 2) + h % 2]), "r"(w[8 * (h / 2) + 2 + h % 2]), "r"(w[8 * (h / 2) + 4 + h % 2]),
                        "r"(w[8 * (h / 2) + 6 + h % 2])
                        : "memory");
-        staging.store(turned, to, column + c, row, z, inside);
+        __syncwarp();
+        mma::put_columns(staging, mirror + c, stride_in, pad_columns - c, lanes, true);
+        __syncwarp();
       }
     }
   };
@@ -976,9 +974,9 @@ cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const flo
     const bool wide = l.rows <= l.cols;
     const size_t side = std::min(l.rows, l.cols), px = up(l.cols, 64), pa = up(side, 64);
     s.rows = (int)l.rows, s.cols = (int)l.cols, s.side = (int)side;
-    s.a_pitch = (int)pa;
+    s.x_pitch = (int)px, s.a_pitch = (int)pa;
     s.count = (int)l.count, s.matrix = (int)l.matrix;
-    s.old = l.a;
+    s.to_a = l.a, s.to_b = l.b;
     s.vectors = l.vectors;
     mma::Kind depth;
     const auto map = [&](CUtensorMap* to, mma::Kind* kind, const __half* at, size_t rows, size_t cols, size_t pitch,
@@ -988,14 +986,11 @@ cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const flo
         e = mma::make_map(to, kind, false, at, depth ? cols : pitch, rows, l.count, pitch, rows * pitch, depth, box);
     };
     for (int j = 0; j < 2; ++j) {
-      if (e == cudaSuccess)
-        e = mma::make_store_map(&s.to_x[j], false, l.x[j], l.cols, l.rows, l.count, px, l.rows * px);
+      s.x[j] = l.x[j];
       map(&s.gram[j][0], &s.gram_kind, l.x[j], l.rows, l.cols, px, wide, 128);
       map(&s.gram[j][1], &s.gram_kind, l.x[j], l.rows, l.cols, px, wide, half);
       map(&s.apply[j], &s.apply_kind, l.x[j], l.rows, l.cols, px, !wide, wide ? 128 : half);
     }
-    if (e == cudaSuccess) e = mma::make_store_map(&s.to_a, false, l.a, side, side, l.count, pa, side * pa);
-    if (e == cudaSuccess) e = mma::make_store_map(&s.to_b, false, l.b, side, side, l.count, pa, side * pa);
     map(&s.a[0], &depth, l.a, side, side, pa, true, 128);
     map(&s.a[1], &depth, l.a, side, side, pa, true, half);
     map(&s.b, &depth, l.b, side, side, pa, true, wide ? half : 128);
