@@ -60,17 +60,17 @@ cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_store_map(CUtensorMap* map, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
+cudaError_t make_store_map(CUtensorMap* map, bool fp32, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
                            uint64_t y_stride, uint64_t z_stride) {
   const Encode encode = encoder();
   if (!encode) return cudaErrorNotSupported;
-  const cuuint64_t y = ny > 1 ? y_stride * 2 : (nx * 2 + 15) / 16 * 16;
-  const cuuint64_t dims[3] = {nx, ny, nz}, strides[2] = {y, nz > 1 ? z_stride * 2 : y};
+  const cuuint64_t size = fp32 ? 4 : 2, y = ny > 1 ? y_stride * size : (nx * size + 15) / 16 * 16;
+  const cuuint64_t dims[3] = {nx, ny, nz}, strides[2] = {y, nz > 1 ? z_stride * size : y};
   const cuuint32_t box[3] = {32, 32, 1}, step[3] = {1, 1, 1};
-  const CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+  const CUresult r = encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                             const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                            fp32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -150,33 +150,52 @@ struct Store {
   long long stride;
   int lanes, columns;   // that are stored: of the warp (may be negative), of the tile
   bool fp32, add, vectors;
-  const CUtensorMap* map;   // bf16 at whole 16 bytes: of the results, in boxes of 32 x 32
+  const CUtensorMap* map;   // at whole 16 bytes: of the results, in boxes of 32 x 32
   int x, y, z;              // in it
   mma::Staging& staging;
 
-  __device__ __forceinline__ void chunk(uint32_t at, int c, mma::Source source) const {
+  // A lane's 32 columns as they are: a warp stores whole 128-byte runs of fp32.
+  __device__ __forceinline__ void put(int c, const float (&v)[32]) const {
     const int lane = threadIdx.x & 31;
+    if (fp32 && vectors && !add && c + 32 <= columns) {
+      // whole chunks by TMA: 32 stores to shared memory, a column's 128 bytes each, and one to memory
+      const uint32_t area = staging.next() + lane * 4;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) asm volatile("st.shared.f32 [%0], %1;" ::"r"(area + i * 128), "f"(v[i]) : "memory");
+      staging.store(area - lane * 4, map, x, y + c, z, lanes > 0);
+      return;
+    }
+    if (lane >= lanes) return;
+    if (fp32) {
+      float* y = static_cast<float*>(to) + lane + c * stride;
+      if (add) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          if (c + i < columns) y[i * stride] += v[i];
+          if (i % 8 == 7) asm volatile("" ::: "memory");  // eight old values at a time: registers
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < columns) y[i * stride] = v[i];
+      }
+    } else {
+      uint16_t* y = static_cast<uint16_t*>(to) + lane + c * stride;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (c + i < columns) y[i * stride] = bf16_bits(add ? bf16_lo(y[i * stride]) + v[i] : v[i]);
+    }
+  }
+  __device__ __forceinline__ void chunk(uint32_t at, int c, mma::Source source) const {
     float v[32];
-    if (fp32 || add || source != mma::kSums) {
-      // a lane's 32 columns: a warp stores whole 128-byte runs of fp32
+    if (add || source != mma::kSums) {
       if (source == mma::kSums) {
         mma::tmem_rows(at, v);
       } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = source == mma::kZeros ? 0.0f : __int_as_float(0x7fc00000);
       }
-      if (lane >= lanes) return;
-      if (fp32) {
-        float* y = static_cast<float*>(to) + lane + c * stride;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < columns) y[i * stride] = add ? y[i * stride] + v[i] : v[i];
-      } else {
-        uint16_t* y = static_cast<uint16_t*>(to) + lane + c * stride;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < columns) y[i * stride] = bf16_bits(add ? bf16_lo(y[i * stride]) + v[i] : v[i]);
-      }
+      put(c, v);
       return;
     }
     // bf16: 8 x 8 matrices are transposed on their way through shared memory, 64 bytes a column
@@ -203,14 +222,16 @@ struct ForwardParams {
   int out, in;             // W_e: out x in
   void* y;
   long long y_stride;
-  bool fp32, vectors, zero_rest;
+  bool vectors, zero_rest;
 };
 
-template <int CG>
+// FP32: of the results, whose sums over a long k are taken in runs, in tiles of half the columns.
+template <int CG, bool FP32>
 struct Forward {
   static constexpr bool kBf16 = true, kOrdered = false;
-  static constexpr int kStages = 5, kAreas = 2;
-  static constexpr int kWide = 128 * CG, kUnit = 16 * CG;  // most columns of a tile, and what they are a multiple of
+  static constexpr int kStages = !FP32 ? 5 : CG == 2 ? 6 : 4, kAreas = 2, kArea = FP32 ? 4096 : 2048, kRun = FP32 ? 8 : 0;
+  static constexpr int kBytesB = (FP32 ? 128 / CG : 128) * 128;
+  static constexpr int kWide = FP32 ? 128 : 128 * CG, kUnit = 16 * CG;  // most columns of a tile, and what they are a multiple of
   using Params = ForwardParams;
   struct Local {
     Ranges r;
@@ -254,15 +275,15 @@ struct Forward {
     w.b_kind = mma::kDepthRows;
     const bool few = w.columns <= 32 * CG;
     w.b = few ? &p.x_few : &p.x;
-    w.b_bytes = few ? mma::kBoxBytes / 2 : 2 * mma::kBoxBytes;
+    w.b_bytes = few ? mma::kBoxBytes / 2 : kWide / CG * 128;
     w.end = end;
     return true;
   }
   struct Epilogue : Store {
     __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, mma::Staging& staging,
                                         const float*)
-        : Store{static_cast<uint8_t*>(p.y) + (w.b_row * p.y_stride + row) * (p.fp32 ? 4 : 2), p.y_stride, p.out - row,
-                min(w.columns, w.end - w.b_row), p.fp32, false, p.vectors, &p.y_map, row, w.b_row, 0, staging} {}
+        : Store{static_cast<uint8_t*>(p.y) + (w.b_row * p.y_stride + row) * (FP32 ? 4 : 2), p.y_stride, p.out - row,
+                min(w.columns, w.end - w.b_row), FP32, false, p.vectors, &p.y_map, row, w.b_row, 0, staging} {}
   };
 };
 
@@ -273,14 +294,15 @@ struct GradientParams {
   int ni, nj;
   void* dw;                // dW_e[j, i] at e * e_stride + j * j_stride + i
   long long e_stride, j_stride;
-  bool fp32, add, vectors;
+  bool add, vectors;
 };
 
-template <int CG>
+template <int CG, bool FP32>
 struct WeightGradient {
   static constexpr bool kBf16 = true, kOrdered = false;
-  static constexpr int kStages = 5, kAreas = 2;
-  static constexpr int kWide = 128 * CG, kUnit = 64 * CG, kRowsOfTile = mma::kRows * CG;
+  static constexpr int kStages = !FP32 ? 5 : CG == 2 ? 6 : 4, kAreas = 2, kArea = FP32 ? 4096 : 2048, kRun = FP32 ? 8 : 0;
+  static constexpr int kBytesB = (FP32 ? 128 / CG : 128) * 128;
+  static constexpr int kWide = FP32 ? 128 : 128 * CG, kUnit = 64 * CG, kRowsOfTile = mma::kRows * CG;
   using Params = GradientParams;
   struct Local {
     Ranges r;
@@ -304,15 +326,15 @@ struct WeightGradient {
     w.columns = min(kWide, (p.nj - w.b_row + kUnit - 1) / kUnit * kUnit);
     w.a_kind = p.a_kind;
     w.b_kind = p.b_kind;
-    w.b_bytes = p.b_kind == mma::kNarrowRows && w.columns <= 64 * CG ? mma::kBoxBytes : 2 * mma::kBoxBytes;
+    w.b_bytes = p.b_kind == mma::kNarrowRows && w.columns <= 64 * CG ? mma::kBoxBytes : kWide / CG * 128;
     w.end = e;
     return true;
   }
   struct Epilogue : Store {
     __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, mma::Staging& staging,
                                         const float*)
-        : Store{static_cast<uint8_t*>(p.dw) + (w.end * p.e_stride + w.b_row * p.j_stride + row) * (p.fp32 ? 4 : 2),
-                p.j_stride, p.add && w.blocks == 0 ? 0 : p.ni - row, min(w.columns, p.nj - w.b_row), p.fp32, p.add,
+        : Store{static_cast<uint8_t*>(p.dw) + (w.end * p.e_stride + w.b_row * p.j_stride + row) * (FP32 ? 4 : 2),
+                p.j_stride, p.add && w.blocks == 0 ? 0 : p.ni - row, min(w.columns, p.nj - w.b_row), FP32, p.add,
                 p.vectors, &p.dw_map, row, w.b_row, w.end, staging} {}
   };
 };
@@ -349,7 +371,7 @@ bool direct(const ExpertMatrix& m) {
 }
 
 // The map of an operand; where it cannot be read as it is, of a copy in the workspace.
-cudaError_t operand(ExpertMatrix m, bool depth, uint8_t*& workspace, int sms, cudaStream_t stream, CUtensorMap* map,
+cudaError_t operand(ExpertMatrix m, bool depth, uint32_t box, uint8_t*& workspace, int sms, cudaStream_t stream, CUtensorMap* map,
                     mma::Kind* kind, CUtensorMap* few = nullptr) {
   if (!m.nx || !m.ny || !m.nz) return cudaSuccess;  // no tile reads it
   if (!direct(m)) {
@@ -364,28 +386,64 @@ cudaError_t operand(ExpertMatrix m, bool depth, uint8_t*& workspace, int sms, cu
     if (e != cudaSuccess) return e;
     m = ExpertMatrix{to, m.nx, m.ny, m.nz, pitch, m.ny * pitch};
   }
-  const cudaError_t e = mma::make_map(map, kind, true, m.at, m.nx, m.ny, m.nz, m.y_stride, m.z_stride, depth, 128);
+  const cudaError_t e = mma::make_map(map, kind, true, m.at, m.nx, m.ny, m.nz, m.y_stride, m.z_stride, depth, box);
   if (e != cudaSuccess || !few) return e;
   return mma::make_map(few, kind, true, m.at, m.nx, m.ny, m.nz, m.y_stride, m.z_stride, depth, 32);
 }
 
 // Whether rows of results can be stored 16 bytes at a time.
-bool vectors(const void* at, size_t stride, size_t matrix_stride = 0) {
-  return ((uintptr_t)at & 15) == 0 && stride % 8 == 0 && matrix_stride % 8 == 0;
+bool vectors(bool fp32, const void* at, size_t stride, size_t matrix_stride = 0) {
+  const size_t whole = fp32 ? 4 : 8;
+  return ((uintptr_t)at & 15) == 0 && stride % whole == 0 && matrix_stride % whole == 0;
 }
 
-template <int CG>
-cudaError_t forward(const ExpertsCall& c, const ForwardParams& p) {
-  const long long f = ((long long)c.out + mma::kRows * CG - 1) / (mma::kRows * CG);
-  const long long groups = (long long)std::min<size_t>(c.experts, c.rows) + 2 + (long long)(c.rows / (128 * CG));
-  return mma::launch_product<CG, Forward<CG>>(p, f * groups, c.sms, c.stream);
+template <int CG, bool FP32>
+cudaError_t forward(const ExpertsCall& c) {
+  using Policy = Forward<CG, FP32>;
+  ForwardParams p = {};
+  uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+  mma::Kind kind;
+  cudaError_t e = operand(c.w, c.w_in_contiguous, 128, ws, c.sms, c.stream, &p.weights, &p.w_kind);
+  if (e == cudaSuccess) e = operand(c.x, true, Policy::kWide / CG, ws, c.sms, c.stream, &p.x, &kind, &p.x_few);
+  p.vectors = vectors(FP32, c.y, c.y_stride);
+  if (e == cudaSuccess && p.vectors)
+    e = mma::make_store_map(&p.y_map, FP32, c.y, c.out, c.rows, 1, c.y_stride, 0);
+  if (e != cudaSuccess) return e;
+  p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
+  p.out = (int)c.out;
+  p.in = (int)c.in;
+  p.y = c.y;
+  p.y_stride = (long long)c.y_stride;
+  p.zero_rest = c.zero_rest;
+  const long long f = ((long long)c.out + Policy::kRowsOfTile - 1) / Policy::kRowsOfTile;
+  const long long groups = (long long)std::min<size_t>(c.experts, c.rows) + 2 + (long long)(c.rows / Policy::kWide);
+  return mma::launch_product<CG, Policy>(p, f * groups, c.sms, c.stream);
 }
 
-template <int CG>
-cudaError_t weight_gradient(const ExpertsCall& c, const GradientParams& p) {
-  const long long w = 128 * CG;
-  const long long tiles = (p.ni + w - 1) / w * ((p.nj + w - 1) / w) * (long long)c.experts;
-  return mma::launch_product<CG, WeightGradient<CG>>(p, tiles, c.sms, c.stream);
+template <int CG, bool FP32>
+cudaError_t weight_gradient(const ExpertsCall& c) {
+  using Policy = WeightGradient<CG, FP32>;
+  GradientParams p = {};
+  uint8_t* ws = static_cast<uint8_t*>(c.workspace);
+  // the contiguous side of dW is the lanes'
+  const bool lanes_in = c.w_in_contiguous;
+  cudaError_t e = operand(lanes_in ? c.x : c.dy, false, 128, ws, c.sms, c.stream, &p.a, &p.a_kind);
+  if (e == cudaSuccess)
+    e = operand(lanes_in ? c.dy : c.x, false, Policy::kWide / CG, ws, c.sms, c.stream, &p.b, &p.b_kind);
+  p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
+  p.ni = (int)(lanes_in ? c.in : c.out);
+  p.nj = (int)(lanes_in ? c.out : c.in);
+  p.dw = c.y;
+  p.e_stride = (long long)c.w.z_stride;
+  p.j_stride = (long long)c.w.y_stride;
+  p.add = c.accumulate;
+  p.vectors = vectors(FP32, c.y, c.w.y_stride, c.w.z_stride);
+  if (e == cudaSuccess && p.vectors)
+    e = mma::make_store_map(&p.dw_map, FP32, c.y, p.ni, p.nj, c.experts, c.w.y_stride, c.w.z_stride);
+  if (e != cudaSuccess) return e;
+  const auto over = [](long long n, long long d) { return (n + d - 1) / d; };
+  const long long tiles = over(p.ni, Policy::kRowsOfTile) * over(p.nj, Policy::kWide) * (long long)c.experts;
+  return mma::launch_product<CG, Policy>(p, tiles, c.sms, c.stream);
 }
 
 }  // namespace
@@ -395,56 +453,29 @@ size_t expert_matrix_workspace(const ExpertMatrix& m) {
 }
 
 cudaError_t launch_expert_product(const ExpertsCall& c) {
-  ForwardParams p = {};
-  uint8_t* ws = static_cast<uint8_t*>(c.workspace);
-  mma::Kind kind;
-  cudaError_t e = operand(c.w, c.w_in_contiguous, ws, c.sms, c.stream, &p.weights, &p.w_kind);
-  if (e == cudaSuccess) e = operand(c.x, true, ws, c.sms, c.stream, &p.x, &kind, &p.x_few);
-  if (e != cudaSuccess) return e;
-  p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
-  p.out = (int)c.out;
-  p.in = (int)c.in;
-  p.y = c.y;
-  p.y_stride = (long long)c.y_stride;
-  p.fp32 = c.dtype == AR_FLOAT32;
-  p.vectors = vectors(c.y, c.y_stride);
-  if (p.vectors && !p.fp32) {
-    e = mma::make_store_map(&p.y_map, true, c.y, c.out, c.rows, 1, c.y_stride, 0);
-    if (e != cudaSuccess) return e;
-  }
-  p.zero_rest = c.zero_rest;
   // the offsets are on the device: as if all experts had the same number of rows
-  const double some = (double)std::max<size_t>(1, std::min(c.experts, c.rows));
-  const auto tiles = [&](double side) { return std::ceil(c.out / side) * some * std::ceil(c.rows / some / side); };
-  return mma::better_in_pairs(tiles(256), tiles(128), std::ceil(c.in / 64.0), c.sms) ? forward<2>(c, p)
-                                                                                      : forward<1>(c, p);
+  const double some = (double)std::max<size_t>(1, std::min(c.experts, c.rows)), slices = std::ceil(c.in / 64.0);
+  const auto tiles = [&](double side, double wide) {
+    return std::ceil(c.out / side) * some * std::ceil(c.rows / some / wide);
+  };
+  if (c.dtype == AR_FLOAT32)
+    return mma::better_in_pairs(0.5 * tiles(256, 128), tiles(128, 128), slices, c.sms) ? forward<2, true>(c)
+                                                                                        : forward<1, true>(c);
+  return mma::better_in_pairs(tiles(256, 256), tiles(128, 128), slices, c.sms) ? forward<2, false>(c)
+                                                                                : forward<1, false>(c);
 }
 
 cudaError_t launch_expert_weight_gradient(const ExpertsCall& c) {
-  GradientParams p = {};
-  uint8_t* ws = static_cast<uint8_t*>(c.workspace);
-  // the contiguous side of dW is the lanes'
-  const bool lanes_in = c.w_in_contiguous;
-  cudaError_t e = operand(lanes_in ? c.x : c.dy, false, ws, c.sms, c.stream, &p.a, &p.a_kind);
-  if (e == cudaSuccess) e = operand(lanes_in ? c.dy : c.x, false, ws, c.sms, c.stream, &p.b, &p.b_kind);
-  if (e != cudaSuccess) return e;
-  p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
-  p.ni = (int)(lanes_in ? c.in : c.out);
-  p.nj = (int)(lanes_in ? c.out : c.in);
-  p.dw = c.y;
-  p.e_stride = (long long)c.w.z_stride;
-  p.j_stride = (long long)c.w.y_stride;
-  p.fp32 = c.dtype == AR_FLOAT32;
-  p.add = c.accumulate;
-  p.vectors = vectors(c.y, c.w.y_stride, c.w.z_stride);
-  if (p.vectors && !p.fp32) {
-    e = mma::make_store_map(&p.dw_map, true, c.y, p.ni, p.nj, c.experts, c.w.y_stride, c.w.z_stride);
-    if (e != cudaSuccess) return e;
-  }
-  const auto tiles = [&](double side) { return std::ceil(c.out / side) * std::ceil(c.in / side) * c.experts; };
   const double slices = std::ceil((double)c.rows / c.experts / 64.0);
-  return mma::better_in_pairs(tiles(256), tiles(128), slices, c.sms) ? weight_gradient<2>(c, p)
-                                                                      : weight_gradient<1>(c, p);
+  const auto tiles = [&](double side, double wide) {
+    const double lanes = c.w_in_contiguous ? c.in : c.out, columns = c.w_in_contiguous ? c.out : c.in;
+    return std::ceil(lanes / side) * std::ceil(columns / wide) * c.experts;
+  };
+  if (c.dtype == AR_FLOAT32)
+    return mma::better_in_pairs(0.5 * tiles(256, 128), tiles(128, 128), slices, c.sms) ? weight_gradient<2, true>(c)
+                                                                                        : weight_gradient<1, true>(c);
+  return mma::better_in_pairs(tiles(256, 256), tiles(128, 128), slices, c.sms) ? weight_gradient<2, false>(c)
+                                                                                : weight_gradient<1, false>(c);
 }
 
 }  // namespace ar

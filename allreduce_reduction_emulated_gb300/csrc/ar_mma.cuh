@@ -33,13 +33,12 @@ namespace mma {
 constexpr int kRows = 128;                 // i per block
 constexpr int kDepth = 64;                 // k per stage: 128 bytes, one swizzled row
 constexpr int kBoxBytes = 64 * kDepth * 2; // 64 x 64 elements, 128-byte rows
-constexpr int kStageBytes = 4 * kBoxBytes; // A: two of them, B: up to two
 constexpr int kAhead = 8;                  // tiles worked out ahead
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr uint32_t kPolls = 1u << 16;
 constexpr int kChunkStep = 32 * (kEpilogueWarps / 4);  // from one chunk of a warp to its next
-constexpr int kStaging = 2048;             // 32 x 32 16-bit results
+constexpr int kRunChunks = 2;              // of a warp, where sums are taken in runs: tiles of 128 columns
 
 // ------------------------------------------------------------------ PTX
 
@@ -121,7 +120,7 @@ __device__ __forceinline__ void tma_load(uint32_t to, const CUtensorMap* map, in
         : "memory");
 }
 
-// 32 x 32 16-bit values from shared memory to (x, y, z) of `map`; what lies outside the map is not stored.
+// 32 x 32 values from shared memory to (x, y, z) of `map`; what lies outside the map is not stored.
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t from, int x, int y, int z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
                "r"(y), "r"(z), "r"(from)
@@ -233,13 +232,13 @@ __device__ __forceinline__ void stage_columns(uint32_t staging, const uint32_t (
 // An epilogue warp's two staging areas in turn.  Every use ends in a commit, of stores or of nothing, so
 // that "all but the last" are those from the area that comes next.
 struct Staging {
-  uint32_t base;
+  uint32_t base, bytes;          // of the first, of each
   uint32_t used = 0;
-  __device__ __forceinline__ explicit Staging(uint32_t base) : base(base) {}
+  __device__ __forceinline__ Staging(uint32_t base, uint32_t bytes) : base(base), bytes(bytes) {}
   __device__ __forceinline__ uint32_t next() {
     if ((threadIdx.x & 31) == 0) bulk_wait_read<1>();
     __syncwarp();
-    return base + (used++ & 1) * kStaging;
+    return base + (used++ & 1) * bytes;
   }
   // What the warp has staged at `from` to (x, y, z) of map, where that is inside.
   __device__ __forceinline__ void store(uint32_t from, const CUtensorMap* map, int x, int y, int z, bool inside) const {
@@ -332,10 +331,10 @@ struct Tile {
 // What a chunk of a tile's epilogue is made of.
 enum Source : int { kZeros, kSums, kLate };
 
-template <int kStages, int kAreas>
+template <int kStages, int kStageBytes, int kStaging>
 struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
-  alignas(1024) uint8_t staging[kEpilogueWarps][kAreas * kStaging];
+  alignas(1024) uint8_t staging[kEpilogueWarps][kStaging];
   alignas(8) uint64_t full[kStages], empty[kStages], ready[2], drained[2], tail, done;
   // Tiles that have been worked out, with their epilogue's factors (columns 0: there are no more).
   uint64_t filled[kAhead], taken[kAhead], stored[kAhead];
@@ -343,6 +342,9 @@ struct Shared {
   float factors[kAhead][2];
   uint32_t tmem, late;
 };
+
+template <class Policy>
+using SharedOf = Shared<Policy::kStages, 2 * kBoxBytes + Policy::kBytesB, Policy::kAreas * Policy::kArea>;
 
 // Where the next slice of an operand is, and how far the one behind it.
 struct Boxes {
@@ -369,14 +371,14 @@ struct Boxes {
 
 template <int CG, class Policy>
 constexpr int shared_bytes() {
-  return (int)sizeof(Shared<Policy::kStages, Policy::kAreas>) + (int)sizeof(typename Policy::Local) + 1024;
+  return (int)sizeof(SharedOf<Policy>) + (int)sizeof(typename Policy::Local) + 1024;
 }
 
 template <int CG, class Policy>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ typename Policy::Params p) {
   extern __shared__ uint8_t raw[];
-  constexpr int kStages = Policy::kStages;
-  auto& s = *reinterpret_cast<Shared<kStages, Policy::kAreas>*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
+  constexpr int kStages = Policy::kStages, kStageBytes = 2 * kBoxBytes + Policy::kBytesB;
+  auto& s = *reinterpret_cast<SharedOf<Policy>*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
   auto& local = *reinterpret_cast<typename Policy::Local*>(&s + 1);
   constexpr uint32_t kColumns = 2 * 128 * CG;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -508,27 +510,35 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (lane == 0) bar_arrive(saddr(&s.taken[place]));
       if (w.columns == 0) break;
       if (w.blocks == 0) continue;
-      const uint32_t buffer = n & 1, d = tmem + buffer * (kColumns / 2);
-      bool ok = bar_wait(saddr(&s.drained[buffer]), ((n >> 1) & 1) ^ 1, late);
-      ++n;
-      fence_after();
       const uint32_t idesc = instruction<CG>(Policy::kBf16, w.a_kind == kDepthRows, w.b_kind == kDepthRows, w.columns);
       const uint32_t a_step = depth_step(w.a_kind == kDepthRows), b_step = depth_step(w.b_kind == kDepthRows);
-      for (int i = 0; ok && i < w.blocks; ++i) {
-        ok = bar_wait(saddr(&s.full[slot]), phase, late);
-        if (!ok) break;
+      bool ok = true;
+      for (int begin = 0; ok && begin < w.blocks;) {
+        const int end = Policy::kRun ? min(begin + Policy::kRun, w.blocks) : w.blocks;
+        const uint32_t buffer = n & 1, d = tmem + buffer * (kColumns / 2);
+        ok = bar_wait(saddr(&s.drained[buffer]), ((n >> 1) & 1) ^ 1, late);
+        ++n;
         fence_after();
-        if (one) {
-          const uint32_t at = saddr(s.stage[slot]);
-          const uint64_t a = operand_desc(at, w.a_kind == kDepthRows),
-                         b = operand_desc(at + 2 * kBoxBytes, w.b_kind == kDepthRows);
+        for (int i = begin; ok && i < end; ++i) {
+          ok = bar_wait(saddr(&s.full[slot]), phase, late);
+          if (!ok) break;
+          // zeros that the other block's threads have stored
+          if (CG == 2 && w.last < kDepth && i == w.blocks - 1) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          fence_after();
+          if (one) {
+            const uint32_t at = saddr(s.stage[slot]);
+            const uint64_t a = operand_desc(at, w.a_kind == kDepthRows),
+                           b = operand_desc(at + 2 * kBoxBytes, w.b_kind == kDepthRows);
 #pragma unroll
-          for (int k = 0; k < kDepth / 16; ++k) mma_f16<CG>(d, a + k * a_step, b + k * b_step, idesc, i + k > 0);
-          mma_commit<CG>(saddr(&s.empty[slot]));
-          if (i == w.blocks - 1) mma_commit<CG>(saddr(&s.ready[buffer]));
+            for (int k = 0; k < kDepth / 16; ++k)
+              mma_f16<CG>(d, a + k * a_step, b + k * b_step, idesc, i > begin || k > 0);
+            mma_commit<CG>(saddr(&s.empty[slot]));
+            if (i == end - 1) mma_commit<CG>(saddr(&s.ready[buffer]));
+          }
+          __syncwarp();
+          if (++slot == kStages) slot = 0, phase ^= 1;
         }
-        __syncwarp();
-        if (++slot == kStages) slot = 0, phase ^= 1;
+        begin = end;
       }
       if (!ok) break;
     }
@@ -541,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int e = warp - 4;
     uint32_t n = 0;
     bool ok = true;
-    Staging staging(saddr(s.staging[e]));
+    Staging staging(saddr(s.staging[e]), Policy::kArea);
     for (uint32_t t = 0;; ++t) {
       const uint32_t place = t % kAhead;
       Tile w;
@@ -557,23 +567,55 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       } else if (!Policy::tile(p, local, first + (int)t * pairs, w)) {
         break;
       }
-      const uint32_t buffer = n & 1, at = tmem + buffer * (kColumns / 2) + ((uint32_t)(e & 3) * 32 << 16);
-      const int row = w.a_row + (int)rank * kRows + (e & 3) * 32;
-      typename Policy::Epilogue out(p, local, w, row, (e >> 2) * 32, staging, factors);
-      if (w.blocks) {
-        ok = ok && bar_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
-        fence_after();
-      }
-      for (int c = (e >> 2) * 32; c < w.columns; c += kChunkStep)
-        out.chunk(at + c, c, !w.blocks ? kZeros : ok ? kSums : kLate);
-      if (w.blocks) {
-        ++n;
-        fence_before();
-        __syncwarp();
-        if (lane == 0 && ok) {
-          if constexpr (CG == 2) bar_free_cluster(of_rank(saddr(&s.drained[buffer]), 0));
-          else bar_arrive(saddr(&s.drained[buffer]));
+      const int row = w.a_row + (int)rank * kRows + (e & 3) * 32, first_column = (e >> 2) * 32;
+      // The accumulators of one run are ready: `use` reads them, then they are handed back.
+      const auto run = [&](auto use) {
+        const uint32_t buffer = n & 1, at = tmem + buffer * (kColumns / 2) + ((uint32_t)(e & 3) * 32 << 16);
+        if (w.blocks) {
+          ok = ok && bar_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
+          fence_after();
         }
+        use(at);
+        if (w.blocks) {
+          ++n;
+          fence_before();
+          __syncwarp();
+          if (lane == 0 && ok) {
+            if constexpr (CG == 2) bar_free_cluster(of_rank(saddr(&s.drained[buffer]), 0));
+            else bar_arrive(saddr(&s.drained[buffer]));
+          }
+        }
+      };
+      typename Policy::Epilogue out(p, local, w, row, first_column, staging, factors);
+      if constexpr (Policy::kRun == 0) {
+        run([&](uint32_t at) {
+          for (int c = first_column; c < w.columns; c += kChunkStep)
+            out.chunk(at + c, c, !w.blocks ? kZeros : ok ? kSums : kLate);
+        });
+      } else {
+        // The tensor cores cut what an addition to the accumulators loses: over 1000 k a sum is off by 1e-6 of itself,
+        // over 16000 by 2e-5.  So a run of 512 k is the longest that they add up; runs are added here, rounded.
+        float sum[kRunChunks][32];
+        const int runs = max(1, (w.blocks + Policy::kRun - 1) / Policy::kRun);
+        for (int r = 0; r < runs; ++r)
+          run([&](uint32_t at) {
+#pragma unroll
+            for (int i = 0; i < kRunChunks; ++i) {
+              const int c = first_column + i * kChunkStep;
+              float v[32];
+              if (w.blocks && ok && c < w.columns) {
+                tmem_rows(at + c, v);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = w.blocks && !ok ? __int_as_float(0x7fc00000) : 0.0f;
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum[i][j] = r == 0 ? v[j] : sum[i][j] + v[j];
+            }
+          });
+#pragma unroll
+        for (int i = 0; i < kRunChunks; ++i)
+          if (first_column + i * kChunkStep < w.columns) out.put(first_column + i * kChunkStep, sum[i]);
       }
       if constexpr (Policy::kOrdered) {  // warp 3 says so once all warps have stored their parts
         __syncwarp();
@@ -623,8 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
                      uint64_t y_stride, uint64_t z_stride, bool depth, uint32_t box);
 
-// The same for results stored in boxes of 32 x 32, 64-byte swizzle (as staged() lays them out).
-cudaError_t make_store_map(CUtensorMap* map, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
+// The same for results stored in boxes of 32 x 32: bf16 with 64-byte swizzle, as staged() lays them out, or fp32 as
+// they are.
+cudaError_t make_store_map(CUtensorMap* map, bool fp32, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
                            uint64_t y_stride, uint64_t z_stride);
 
 // Whether `in_pairs` tiles of pairs of blocks (256 x 256) take less time than `alone` tiles of blocks (128 x

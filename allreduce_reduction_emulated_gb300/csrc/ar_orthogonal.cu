@@ -475,7 +475,7 @@ struct StepsParams {
 template <int CG>
 struct Steps {
   static constexpr bool kBf16 = false, kOrdered = true;
-  static constexpr int kStages = 6, kAreas = 1;
+  static constexpr int kStages = 6, kBytesB = 2 * mma::kBoxBytes, kAreas = 1, kArea = 2048, kRun = 0;
   static constexpr int kSide = 128 * CG;
   using Params = StepsParams;
   struct Local {};
