@@ -11,8 +11,8 @@
 // Roles of a block's 12 warps: warp 2 works out the tiles, warp 0 issues the TMA loads of a
 // tile's 64-deep slices into a ring of shared-memory stages, warp 1 issues the matrix
 // instructions (of a pair only the even block's), warps 4 to 11 read finished accumulators and
-// hand them to the policy's epilogue, in chunks of 32 columns; warp 3 tells of stored tiles where
-// others wait for them.  There are two accumulators, so that
+// hand them to the policy's epilogue, in chunks of 32 columns; warp 3 clears what does not belong to a
+// last slice, or tells of stored tiles where others wait for them.  There are two accumulators, so that
 // one tile's epilogue overlaps the next tile's products.
 //
 // Every wait is bounded (about a second).  A block that gives up tells its other warps;
@@ -335,7 +335,7 @@ template <int kStages, int kStageBytes, int kStaging>
 struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
   alignas(1024) uint8_t staging[kEpilogueWarps][kStaging];
-  alignas(8) uint64_t full[kStages], empty[kStages], ready[2], drained[2], tail, done;
+  alignas(8) uint64_t full[kStages], empty[kStages], tail[kStages], ready[2], drained[2], done;
   // Tiles that have been worked out, with their epilogue's factors (columns 0: there are no more).
   uint64_t filled[kAhead], taken[kAhead], stored[kAhead];
   Tile tiles[kAhead];
@@ -388,16 +388,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int i = 0; i < kStages; ++i) {
       bar_init(saddr(&s.full[i]), CG);
       bar_init(saddr(&s.empty[i]), 1);
+      bar_init(saddr(&s.tail[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(saddr(&s.ready[i]), 1);
       bar_init(saddr(&s.drained[i]), CG * kEpilogueWarps);
     }
-    bar_init(saddr(&s.tail), 1);
     bar_init(saddr(&s.done), 1);
     for (int i = 0; i < kAhead; ++i) {
       bar_init(saddr(&s.filled[i]), 1);
-      bar_init(saddr(&s.taken[i]), kEpilogueWarps + 1 + (rank == 0 ? 1 : 0) + (Policy::kOrdered ? 1 : 0));
+      bar_init(saddr(&s.taken[i]), kEpilogueWarps + 2 + (rank == 0 ? 1 : 0));
       bar_init(saddr(&s.stored[i]), kEpilogueWarps);
     }
     s.late = 0;
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const bool one = elect();
     const uint32_t empty = saddr(&s.empty[0]), stages = saddr(s.stage[0]);
     const uint32_t full = CG == 2 ? of_rank(saddr(&s.full[0]), 0) : saddr(&s.full[0]);
-    uint32_t slot = 0, phase = 0, tails = 0;
+    uint32_t slot = 0, phase = 0;
     for (uint32_t t = 0;; ++t) {
       const uint32_t place = t % kAhead;
       if (!bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) break;
@@ -450,53 +450,27 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const uint32_t bytes = 2 * kBoxBytes + w.b_bytes;
       Boxes a(w.a, w.a_kind, w.a_row + (int)rank * kRows, w.k, w.a_z, 2 * kBoxBytes);
       Boxes b(w.b, w.b_kind, w.b_row + (int)rank * (w.columns / CG), w.k, w.b_z, w.b_bytes);
-      // One thread issues all whole slices.
-      const bool tail = w.last < kDepth;
-      const int whole = w.blocks - (tail ? 1 : 0);
       bool ok = true;
-      if (one) {
-        for (int i = 0; i < whole; ++i) {
+      if (one) {  // one thread issues them all
+        for (int i = 0; i < w.blocks; ++i) {
           ok = bar_wait(empty + 8 * slot, phase ^ 1, late);
           if (!ok) break;
-          if constexpr (CG == 2) bar_expect_cluster(full + 8 * slot, bytes);
-          else bar_expect(full + 8 * slot, bytes);
+          const bool tail = w.last < kDepth && i == w.blocks - 1;  // warp 3 passes it on
+          const uint32_t bar = tail ? saddr(&s.tail[slot]) : full + 8 * slot;
+          if (CG == 2 && !tail) bar_expect_cluster(bar, bytes);
+          else bar_expect(bar, bytes);
           const uint32_t at = stages + slot * kStageBytes;
-          a.load<CG>(at, full + 8 * slot);
-          b.load<CG>(at + 2 * kBoxBytes, full + 8 * slot);
+          a.load<CG>(at, bar);
+          b.load<CG>(at + 2 * kBoxBytes, bar);
           if (++slot == kStages) slot = 0, phase ^= 1;
         }
       }
       __syncwarp();
       if (!__all_sync(~0u, ok)) break;
       if (!one) {  // the others keep count
-        const uint32_t n = slot + whole;
+        const uint32_t n = slot + w.blocks;
         phase ^= n / kStages & 1;
         slot = n % kStages;
-      }
-      if (tail) {
-        // Rows of the next expert, or of none, come along: both operands' become 0 (the other
-        // operand's could be infinite).  k is a box's outer side here: whole 128-byte rows.
-        ok = bar_wait(empty + 8 * slot, phase ^ 1, late);
-        if (ok && one) {
-          bar_expect(saddr(&s.tail), bytes);
-          a.load<CG>(stages + slot * kStageBytes, saddr(&s.tail));
-          b.load<CG>(stages + slot * kStageBytes + 2 * kBoxBytes, saddr(&s.tail));
-        }
-        __syncwarp();
-        ok = ok && bar_wait(saddr(&s.tail), tails++ & 1, late);
-        if (!__all_sync(~0u, ok)) break;
-        const int rows = kDepth - w.last;
-        for (int v = lane; v < (int)bytes / kBoxBytes * rows * 8; v += 32) {
-          const int box = v / (rows * 8), rest = v % (rows * 8);
-          *reinterpret_cast<uint4*>(s.stage[slot] + box * kBoxBytes + (w.last * 8 + rest) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (one) {
-          if constexpr (CG == 2) bar_arrive_cluster(full + 8 * slot);
-          else bar_arrive(full + 8 * slot);
-        }
-        if (++slot == kStages) slot = 0, phase ^= 1;
       }
     }
   } else if (warp == 1 && rank == 0) {
@@ -624,6 +598,36 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     if (lane == 0) bulk_wait();
   } else if (warp == 3) {
+    if constexpr (!Policy::kOrdered) {
+      // The last slice of an expert's rows: those of the next expert, or of none, come along, and both operands'
+      // become 0 (the other operand's could be infinite).  k is a box's outer side there: whole 128-byte rows.
+      const uint32_t full = CG == 2 ? of_rank(saddr(&s.full[0]), 0) : saddr(&s.full[0]);
+      uint32_t slices = 0, phases = 0;
+      for (uint32_t t = 0;; ++t) {
+        const uint32_t place = t % kAhead;
+        if (!bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) break;
+        const Tile w = s.tiles[place];
+        __syncwarp();
+        if (lane == 0) bar_arrive(saddr(&s.taken[place]));
+        if (w.columns == 0) break;
+        slices += w.blocks;
+        if (w.blocks == 0 || w.last == kDepth) continue;
+        const uint32_t slot = (slices - 1) % kStages;
+        if (!bar_wait(saddr(&s.tail[slot]), phases >> slot & 1, late)) break;
+        phases ^= 1u << slot;
+        const int rows = kDepth - w.last, boxes = (2 * kBoxBytes + w.b_bytes) / kBoxBytes;
+        for (int v = lane; v < boxes * rows * 8; v += 32) {
+          const int box = v / (rows * 8), rest = v % (rows * 8);
+          *reinterpret_cast<uint4*>(s.stage[slot] + box * kBoxBytes + (w.last * 8 + rest) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (CG == 2) bar_arrive_cluster(full + 8 * slot);
+          else bar_arrive(full + 8 * slot);
+        }
+      }
+    }
     if constexpr (Policy::kOrdered) {
       for (uint32_t t = 0;; ++t) {
         const uint32_t place = t % kAhead;
