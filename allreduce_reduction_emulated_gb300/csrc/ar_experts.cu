@@ -60,17 +60,16 @@ cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_store_map(CUtensorMap* map, bool fp32, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
-                           uint64_t y_stride, uint64_t z_stride) {
+cudaError_t make_store_map(CUtensorMap* map, const void* base, uint64_t nx, uint64_t ny, uint64_t nz, uint64_t y_stride,
+                           uint64_t z_stride) {
   const Encode encode = encoder();
   if (!encode) return cudaErrorNotSupported;
-  const cuuint64_t size = fp32 ? 4 : 2, y = ny > 1 ? y_stride * size : (nx * size + 15) / 16 * 16;
-  const cuuint64_t dims[3] = {nx, ny, nz}, strides[2] = {y, nz > 1 ? z_stride * size : y};
+  const cuuint64_t y = ny > 1 ? y_stride * 2 : (nx * 2 + 15) / 16 * 16;
+  const cuuint64_t dims[3] = {nx, ny, nz}, strides[2] = {y, nz > 1 ? z_stride * 2 : y};
   const cuuint32_t box[3] = {32, 32, 1}, step[3] = {1, 1, 1};
-  const CUresult r = encode(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                            const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            fp32 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_64B,
-                            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -154,25 +153,23 @@ struct Store {
   int x, y, z;              // in it
   mma::Staging& staging;
 
-  // A lane's 32 columns as they are: a warp stores whole 128-byte runs of fp32.
-  __device__ __forceinline__ void put(int c, const float (&v)[32]) const {
+  // A lane's 32 columns as they are: a warp stores whole 128-byte runs of fp32.  `add`: to what is there.
+  __device__ __forceinline__ void put(int c, const float (&v)[32], bool add) const {
     const int lane = threadIdx.x & 31;
-    if (fp32 && vectors && !add && c + 32 <= columns) {
-      // whole chunks by TMA: 32 stores to shared memory, a column's 128 bytes each, and one to memory
-      const uint32_t area = staging.next() + lane * 4;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) asm volatile("st.shared.f32 [%0], %1;" ::"r"(area + i * 128), "f"(v[i]) : "memory");
-      staging.store(area - lane * 4, map, x, y + c, z, lanes > 0);
-      return;
-    }
     if (lane >= lanes) return;
     if (fp32) {
       float* y = static_cast<float*>(to) + lane + c * stride;
       if (add) {
+        // eight loads before the first store: a store before them would have them wait for it
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          if (c + i < columns) y[i * stride] += v[i];
-          if (i % 8 == 7) asm volatile("" ::: "memory");  // eight old values at a time: registers
+        for (int h = 0; h < 32; h += 8) {
+          float old[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) old[i] = c + h + i < columns ? y[(h + i) * stride] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + h + i < columns) y[(h + i) * stride] = old[i] + v[h + i];
+          asm volatile("" ::: "memory");
         }
       } else {
 #pragma unroll
@@ -182,20 +179,28 @@ struct Store {
     } else {
       uint16_t* y = static_cast<uint16_t*>(to) + lane + c * stride;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (c + i < columns) y[i * stride] = bf16_bits(add ? bf16_lo(y[i * stride]) + v[i] : v[i]);
+      for (int h = 0; h < 32; h += 8) {
+        float old[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) old[i] = add && c + h + i < columns ? bf16_lo(y[(h + i) * stride]) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + h + i < columns) y[(h + i) * stride] = bf16_bits(add ? old[i] + v[h + i] : v[h + i]);
+        asm volatile("" ::: "memory");
+      }
     }
   }
-  __device__ __forceinline__ void chunk(uint32_t at, int c, mma::Source source) const {
+  // `more`: a later run of a tile, added to the ones before.
+  __device__ __forceinline__ void chunk(uint32_t at, int c, mma::Source source, bool more) const {
     float v[32];
-    if (add || source != mma::kSums) {
+    if (fp32 || add || source != mma::kSums) {
       if (source == mma::kSums) {
         mma::tmem_rows(at, v);
       } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = source == mma::kZeros ? 0.0f : __int_as_float(0x7fc00000);
       }
-      put(c, v);
+      put(c, v, add || more);
       return;
     }
     // bf16: 8 x 8 matrices are transposed on their way through shared memory, 64 bytes a column
@@ -225,13 +230,15 @@ struct ForwardParams {
   bool vectors, zero_rest;
 };
 
-// FP32: of the results, whose sums over a long k are taken in runs, in tiles of half the columns.
+// FP32: of the results.  The tensor cores cut what an addition to the accumulators loses: over 1000 k a sum
+// is off by 1e-6 of itself, over 16000 by 2e-5.  So 960 k are the longest run that they add up; a later run is
+// added, rounded, to what the runs before have stored.  A bf16 result's own rounding is larger than all that.
 template <int CG, bool FP32>
 struct Forward {
   static constexpr bool kBf16 = true, kOrdered = false;
-  static constexpr int kStages = !FP32 ? 5 : CG == 2 ? 6 : 4, kAreas = 2, kArea = FP32 ? 4096 : 2048, kRun = FP32 ? 8 : 0;
-  static constexpr int kBytesB = (FP32 ? 128 / CG : 128) * 128;
-  static constexpr int kWide = FP32 ? 128 : 128 * CG, kUnit = 16 * CG;  // most columns of a tile, and what they are a multiple of
+  static constexpr int kStages = FP32 ? 6 : 5, kBytesB = 2 * mma::kBoxBytes;
+  static constexpr int kAreas = FP32 ? 0 : 2, kArea = 2048, kRun = FP32 ? 15 : 0;
+  static constexpr int kWide = 128 * CG, kUnit = 16 * CG;  // most columns of a tile, and what they are a multiple of
   using Params = ForwardParams;
   struct Local {
     Ranges r;
@@ -275,7 +282,7 @@ struct Forward {
     w.b_kind = mma::kDepthRows;
     const bool few = w.columns <= 32 * CG;
     w.b = few ? &p.x_few : &p.x;
-    w.b_bytes = few ? mma::kBoxBytes / 2 : kWide / CG * 128;
+    w.b_bytes = few ? mma::kBoxBytes / 2 : 2 * mma::kBoxBytes;
     w.end = end;
     return true;
   }
@@ -300,9 +307,9 @@ struct GradientParams {
 template <int CG, bool FP32>
 struct WeightGradient {
   static constexpr bool kBf16 = true, kOrdered = false;
-  static constexpr int kStages = !FP32 ? 5 : CG == 2 ? 6 : 4, kAreas = 2, kArea = FP32 ? 4096 : 2048, kRun = FP32 ? 8 : 0;
-  static constexpr int kBytesB = (FP32 ? 128 / CG : 128) * 128;
-  static constexpr int kWide = FP32 ? 128 : 128 * CG, kUnit = 64 * CG, kRowsOfTile = mma::kRows * CG;
+  static constexpr int kStages = FP32 ? 6 : 5, kBytesB = 2 * mma::kBoxBytes;
+  static constexpr int kAreas = FP32 ? 0 : 2, kArea = 2048, kRun = FP32 ? 15 : 0;
+  static constexpr int kWide = 128 * CG, kUnit = 64 * CG, kRowsOfTile = mma::kRows * CG;
   using Params = GradientParams;
   struct Local {
     Ranges r;
@@ -326,7 +333,7 @@ struct WeightGradient {
     w.columns = min(kWide, (p.nj - w.b_row + kUnit - 1) / kUnit * kUnit);
     w.a_kind = p.a_kind;
     w.b_kind = p.b_kind;
-    w.b_bytes = p.b_kind == mma::kNarrowRows && w.columns <= 64 * CG ? mma::kBoxBytes : kWide / CG * 128;
+    w.b_bytes = p.b_kind == mma::kNarrowRows && w.columns <= 64 * CG ? mma::kBoxBytes : 2 * mma::kBoxBytes;
     w.end = e;
     return true;
   }
@@ -371,7 +378,7 @@ bool direct(const ExpertMatrix& m) {
 }
 
 // The map of an operand; where it cannot be read as it is, of a copy in the workspace.
-cudaError_t operand(ExpertMatrix m, bool depth, uint32_t box, uint8_t*& workspace, int sms, cudaStream_t stream, CUtensorMap* map,
+cudaError_t operand(ExpertMatrix m, bool depth, uint8_t*& workspace, int sms, cudaStream_t stream, CUtensorMap* map,
                     mma::Kind* kind, CUtensorMap* few = nullptr) {
   if (!m.nx || !m.ny || !m.nz) return cudaSuccess;  // no tile reads it
   if (!direct(m)) {
@@ -386,15 +393,14 @@ cudaError_t operand(ExpertMatrix m, bool depth, uint32_t box, uint8_t*& workspac
     if (e != cudaSuccess) return e;
     m = ExpertMatrix{to, m.nx, m.ny, m.nz, pitch, m.ny * pitch};
   }
-  const cudaError_t e = mma::make_map(map, kind, true, m.at, m.nx, m.ny, m.nz, m.y_stride, m.z_stride, depth, box);
+  const cudaError_t e = mma::make_map(map, kind, true, m.at, m.nx, m.ny, m.nz, m.y_stride, m.z_stride, depth, 128);
   if (e != cudaSuccess || !few) return e;
   return mma::make_map(few, kind, true, m.at, m.nx, m.ny, m.nz, m.y_stride, m.z_stride, depth, 32);
 }
 
 // Whether rows of results can be stored 16 bytes at a time.
-bool vectors(bool fp32, const void* at, size_t stride, size_t matrix_stride = 0) {
-  const size_t whole = fp32 ? 4 : 8;
-  return ((uintptr_t)at & 15) == 0 && stride % whole == 0 && matrix_stride % whole == 0;
+bool vectors(const void* at, size_t stride, size_t matrix_stride = 0) {
+  return ((uintptr_t)at & 15) == 0 && stride % 8 == 0 && matrix_stride % 8 == 0;
 }
 
 template <int CG, bool FP32>
@@ -403,11 +409,11 @@ cudaError_t forward(const ExpertsCall& c) {
   ForwardParams p = {};
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   mma::Kind kind;
-  cudaError_t e = operand(c.w, c.w_in_contiguous, 128, ws, c.sms, c.stream, &p.weights, &p.w_kind);
-  if (e == cudaSuccess) e = operand(c.x, true, Policy::kWide / CG, ws, c.sms, c.stream, &p.x, &kind, &p.x_few);
-  p.vectors = vectors(FP32, c.y, c.y_stride);
+  cudaError_t e = operand(c.w, c.w_in_contiguous, ws, c.sms, c.stream, &p.weights, &p.w_kind);
+  if (e == cudaSuccess) e = operand(c.x, true, ws, c.sms, c.stream, &p.x, &kind, &p.x_few);
+  p.vectors = !FP32 && vectors(c.y, c.y_stride);
   if (e == cudaSuccess && p.vectors)
-    e = mma::make_store_map(&p.y_map, FP32, c.y, c.out, c.rows, 1, c.y_stride, 0);
+    e = mma::make_store_map(&p.y_map, c.y, c.out, c.rows, 1, c.y_stride, 0);
   if (e != cudaSuccess) return e;
   p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
   p.out = (int)c.out;
@@ -427,9 +433,9 @@ cudaError_t weight_gradient(const ExpertsCall& c) {
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   // the contiguous side of dW is the lanes'
   const bool lanes_in = c.w_in_contiguous;
-  cudaError_t e = operand(lanes_in ? c.x : c.dy, false, 128, ws, c.sms, c.stream, &p.a, &p.a_kind);
+  cudaError_t e = operand(lanes_in ? c.x : c.dy, false, ws, c.sms, c.stream, &p.a, &p.a_kind);
   if (e == cudaSuccess)
-    e = operand(lanes_in ? c.dy : c.x, false, Policy::kWide / CG, ws, c.sms, c.stream, &p.b, &p.b_kind);
+    e = operand(lanes_in ? c.dy : c.x, false, ws, c.sms, c.stream, &p.b, &p.b_kind);
   p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
   p.ni = (int)(lanes_in ? c.in : c.out);
   p.nj = (int)(lanes_in ? c.out : c.in);
@@ -437,9 +443,9 @@ cudaError_t weight_gradient(const ExpertsCall& c) {
   p.e_stride = (long long)c.w.z_stride;
   p.j_stride = (long long)c.w.y_stride;
   p.add = c.accumulate;
-  p.vectors = vectors(FP32, c.y, c.w.y_stride, c.w.z_stride);
+  p.vectors = !FP32 && vectors(c.y, c.w.y_stride, c.w.z_stride);
   if (e == cudaSuccess && p.vectors)
-    e = mma::make_store_map(&p.dw_map, FP32, c.y, p.ni, p.nj, c.experts, c.w.y_stride, c.w.z_stride);
+    e = mma::make_store_map(&p.dw_map, c.y, p.ni, p.nj, c.experts, c.w.y_stride, c.w.z_stride);
   if (e != cudaSuccess) return e;
   const auto over = [](long long n, long long d) { return (n + d - 1) / d; };
   const long long tiles = over(p.ni, Policy::kRowsOfTile) * over(p.nj, Policy::kWide) * (long long)c.experts;
@@ -454,28 +460,19 @@ size_t expert_matrix_workspace(const ExpertMatrix& m) {
 
 cudaError_t launch_expert_product(const ExpertsCall& c) {
   // the offsets are on the device: as if all experts had the same number of rows
-  const double some = (double)std::max<size_t>(1, std::min(c.experts, c.rows)), slices = std::ceil(c.in / 64.0);
-  const auto tiles = [&](double side, double wide) {
-    return std::ceil(c.out / side) * some * std::ceil(c.rows / some / wide);
-  };
-  if (c.dtype == AR_FLOAT32)
-    return mma::better_in_pairs(0.5 * tiles(256, 128), tiles(128, 128), slices, c.sms) ? forward<2, true>(c)
-                                                                                        : forward<1, true>(c);
-  return mma::better_in_pairs(tiles(256, 256), tiles(128, 128), slices, c.sms) ? forward<2, false>(c)
-                                                                                : forward<1, false>(c);
+  const double some = (double)std::max<size_t>(1, std::min(c.experts, c.rows));
+  const auto tiles = [&](double side) { return std::ceil(c.out / side) * some * std::ceil(c.rows / some / side); };
+  const bool pairs = mma::better_in_pairs(tiles(256), tiles(128), std::ceil(c.in / 64.0), c.sms);
+  if (c.dtype == AR_FLOAT32) return pairs ? forward<2, true>(c) : forward<1, true>(c);
+  return pairs ? forward<2, false>(c) : forward<1, false>(c);
 }
 
 cudaError_t launch_expert_weight_gradient(const ExpertsCall& c) {
-  const double slices = std::ceil((double)c.rows / c.experts / 64.0);
-  const auto tiles = [&](double side, double wide) {
-    const double lanes = c.w_in_contiguous ? c.in : c.out, columns = c.w_in_contiguous ? c.out : c.in;
-    return std::ceil(lanes / side) * std::ceil(columns / wide) * c.experts;
-  };
-  if (c.dtype == AR_FLOAT32)
-    return mma::better_in_pairs(0.5 * tiles(256, 128), tiles(128, 128), slices, c.sms) ? weight_gradient<2, true>(c)
-                                                                                        : weight_gradient<1, true>(c);
-  return mma::better_in_pairs(tiles(256, 256), tiles(128, 128), slices, c.sms) ? weight_gradient<2, false>(c)
-                                                                                : weight_gradient<1, false>(c);
+  const auto tiles = [&](double side) { return std::ceil(c.out / side) * std::ceil(c.in / side) * c.experts; };
+  const bool pairs =
+      mma::better_in_pairs(tiles(256), tiles(128), std::ceil((double)c.rows / c.experts / 64.0), c.sms);
+  if (c.dtype == AR_FLOAT32) return pairs ? weight_gradient<2, true>(c) : weight_gradient<1, true>(c);
+  return pairs ? weight_gradient<2, false>(c) : weight_gradient<1, false>(c);
 }
 
 }  // namespace ar

@@ -38,7 +38,6 @@ constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr uint32_t kPolls = 1u << 16;
 constexpr int kChunkStep = 32 * (kEpilogueWarps / 4);  // from one chunk of a warp to its next
-constexpr int kRunChunks = 2;              // of a warp, where sums are taken in runs: tiles of 128 columns
 
 // ------------------------------------------------------------------ PTX
 
@@ -322,7 +321,7 @@ struct Tile {
   int a_row, b_row;        // first i of the pair, first j
   int a_z, b_z;            // which matrix of the map
   int k, blocks;           // first k, number of 64-deep slices (0: the sum is 0)
-  int last;                // rows of the last slice that count: the others are made 0 (64: all count)
+  int last;                // k of the last slice that count (64: all)
   int columns;             // j of the tile, a multiple of 16 * CG (kWideRows: 64 * CG), at most 128 * CG
   int b_bytes;             // of B's box(es) per block and slice
   int end, shape, stage, step;  // the policy's own
@@ -334,7 +333,7 @@ enum Source : int { kZeros, kSums, kLate };
 template <int kStages, int kStageBytes, int kStaging>
 struct Shared {
   alignas(1024) uint8_t stage[kStages][kStageBytes];
-  alignas(1024) uint8_t staging[kEpilogueWarps][kStaging];
+  alignas(1024) uint8_t staging[kEpilogueWarps][kStaging ? kStaging : 16];
   alignas(8) uint64_t full[kStages], empty[kStages], tail[kStages], ready[2], drained[2], done;
   // Tiles that have been worked out, with their epilogue's factors (columns 0: there are no more).
   uint64_t filled[kAhead], taken[kAhead], stored[kAhead];
@@ -503,9 +502,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const uint32_t at = saddr(s.stage[slot]);
             const uint64_t a = operand_desc(at, w.a_kind == kDepthRows),
                            b = operand_desc(at + 2 * kBoxBytes, w.b_kind == kDepthRows);
+            if (i < w.blocks - 1 || w.last == kDepth) {
 #pragma unroll
-            for (int k = 0; k < kDepth / 16; ++k)
-              mma_f16<CG>(d, a + k * a_step, b + k * b_step, idesc, i > begin || k > 0);
+              for (int k = 0; k < kDepth / 16; ++k)
+                mma_f16<CG>(d, a + k * a_step, b + k * b_step, idesc, i > begin || k > 0);
+            } else {
+              for (int k = 0; k < (w.last + 15) / 16; ++k)
+                mma_f16<CG>(d, a + k * a_step, b + k * b_step, idesc, i > begin || k > 0);
+            }
             mma_commit<CG>(saddr(&s.empty[slot]));
             if (i == end - 1) mma_commit<CG>(saddr(&s.ready[buffer]));
           }
@@ -561,36 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
       };
       typename Policy::Epilogue out(p, local, w, row, first_column, staging, factors);
-      if constexpr (Policy::kRun == 0) {
+      const int runs = Policy::kRun ? max(1, (w.blocks + Policy::kRun - 1) / Policy::kRun) : 1;
+      for (int r = 0; r < runs; ++r)
         run([&](uint32_t at) {
           for (int c = first_column; c < w.columns; c += kChunkStep)
-            out.chunk(at + c, c, !w.blocks ? kZeros : ok ? kSums : kLate);
+            out.chunk(at + c, c, !w.blocks ? kZeros : ok ? kSums : kLate, r > 0);
         });
-      } else {
-        // The tensor cores cut what an addition to the accumulators loses: over 1000 k a sum is off by 1e-6 of itself,
-        // over 16000 by 2e-5.  So a run of 512 k is the longest that they add up; runs are added here, rounded.
-        float sum[kRunChunks][32];
-        const int runs = max(1, (w.blocks + Policy::kRun - 1) / Policy::kRun);
-        for (int r = 0; r < runs; ++r)
-          run([&](uint32_t at) {
-#pragma unroll
-            for (int i = 0; i < kRunChunks; ++i) {
-              const int c = first_column + i * kChunkStep;
-              float v[32];
-              if (w.blocks && ok && c < w.columns) {
-                tmem_rows(at + c, v);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = w.blocks && !ok ? __int_as_float(0x7fc00000) : 0.0f;
-              }
-#pragma unroll
-              for (int j = 0; j < 32; ++j) sum[i][j] = r == 0 ? v[j] : sum[i][j] + v[j];
-            }
-          });
-#pragma unroll
-        for (int i = 0; i < kRunChunks; ++i)
-          if (first_column + i * kChunkStep < w.columns) out.put(first_column + i * kChunkStep, sum[i]);
-      }
       if constexpr (Policy::kOrdered) {  // warp 3 says so once all warps have stored their parts
         __syncwarp();
         if (lane == 0) bar_arrive(saddr(&s.stored[place]));
@@ -615,11 +595,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const uint32_t slot = (slices - 1) % kStages;
         if (!bar_wait(saddr(&s.tail[slot]), phases >> slot & 1, late)) break;
         phases ^= 1u << slot;
-        const int rows = kDepth - w.last, boxes = (2 * kBoxBytes + w.b_bytes) / kBoxBytes;
-        for (int v = lane; v < boxes * rows * 8; v += 32) {
-          const int box = v / (rows * 8), rest = v % (rows * 8);
-          *reinterpret_cast<uint4*>(s.stage[slot] + box * kBoxBytes + (w.last * 8 + rest) * 16) = make_uint4(0, 0, 0, 0);
-        }
+        // up to whole sixteens, the rest is not multiplied
+        const int end = (w.last + 15) & ~15, boxes = (2 * kBoxBytes + w.b_bytes) / kBoxBytes;
+        for (int box = 0; box < boxes; ++box)
+          for (int row = w.last + (lane >> 3); row < end; row += 4)
+            *reinterpret_cast<uint4*>(s.stage[slot] + box * kBoxBytes + row * 128 + (lane & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
@@ -669,10 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 cudaError_t make_map(CUtensorMap* map, Kind* kind, bool bf16, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
                      uint64_t y_stride, uint64_t z_stride, bool depth, uint32_t box);
 
-// The same for results stored in boxes of 32 x 32: bf16 with 64-byte swizzle, as staged() lays them out, or fp32 as
-// they are.
-cudaError_t make_store_map(CUtensorMap* map, bool fp32, const void* base, uint64_t nx, uint64_t ny, uint64_t nz,
-                           uint64_t y_stride, uint64_t z_stride);
+// The same for bf16 results stored in boxes of 32 x 32, 64-byte swizzle, as staged() lays them out.
+cudaError_t make_store_map(CUtensorMap* map, const void* base, uint64_t nx, uint64_t ny, uint64_t nz, uint64_t y_stride,
+                           uint64_t z_stride);
 
 // Whether `in_pairs` tiles of pairs of blocks (256 x 256) take less time than `alone` tiles of blocks (128 x
 // 128, a quarter of the work): both in whole waves over the multiprocessors, a slice at 0.27 us (the matrix

@@ -628,7 +628,7 @@ struct Steps {
       }
     }
 
-    __device__ __forceinline__ void chunk(uint32_t at, int c, mma::Source source) {
+    __device__ __forceinline__ void chunk(uint32_t at, int c, mma::Source source, bool) {
       const int lane = threadIdx.x & 31;
       uint32_t o[16] = {};
       if (old) {
