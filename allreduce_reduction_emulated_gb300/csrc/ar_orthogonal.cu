@@ -13,9 +13,10 @@
 // tensor cores are as fast.  fp16's range is met by powers of two: all singular values of
 // X have a bound that follows from the coefficients, so that every element's has, and each
 // matrix is held times the power of two that brings the bound to 2^13.  Sums are fp32, and
-// a I + b A is added in fp32 before B's one rounding.  (With a I in B the last product needs no
-// X but its operand; B's diagonal is rounded once more than with a X added apart, and the result is no
-// less exact: 1.3e-3 instead of 1.4e-3 before the last rounding.)
+// a I + b A is added in fp32 before B's one rounding.  B's diagonal is most of it, and where the singular
+// values are alike (a short matrix) its roundings do not average out: what each element of it
+// loses is kept in fp32, as a factor of its row.  30 x 512: 2.9e-3 of the 2-norm before the last
+// rounding without, 1.4e-3 with it; 300 x 310: 1.3e-3 and 1.0e-3.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -239,6 +240,12 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// What B's diagonal loses when it is rounded: the factor of B's rows (or, as B is symmetric, columns) in the last
+// product's epilogue that makes up for it.
+__device__ __forceinline__ float rounding_rest(float exact, float rounded) {
+  return rounded == 0.0f ? 1.0f : __fdividef(exact, rounded);
+}
+
 // ------------------------------------------------------------------ small matrices, whole in one block
 
 // Up to 128 by 512 a matrix stays in one block's shared memory through all steps, and so do A and B: what
@@ -255,7 +262,7 @@ constexpr int kSquareBytes = 2 * kBox;
 struct SmallShared {
   uint64_t done;
   uint32_t tmem, late;
-  float coefs[kMaxSteps * kCoefs];
+  float coefs[kMaxSteps * kCoefs], rest[kSmallSide];
 };
 
 constexpr int small_bytes(int boxes) { return 1024 + 2 * kSquareBytes + boxes * kBox + (int)sizeof(SmallShared); }
@@ -397,6 +404,17 @@ __global__ void __launch_bounds__(kSmallThreads, COLUMNS == 128 ? 2 : 1) small_k
     for (int i = 0; i < 32; ++i) v[i] = f[2] * v[i] + (group * 32 + i == row ? f[3] : 0.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) put16(swizzled(sb, row, group * 32 + 8 * i), combine8(f[1], a[i], 1.0f, v + 8 * i, false));
+    if ((warp & 3) == group) {  // lane l has row and column l of a block on the diagonal
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum = i == lane ? v[i] : sum;
+      const auto at = [&](uint32_t base) {
+        uint16_t h;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(swizzled(base, row, row) + (row & 7) * 2) : "memory");
+        return __half2float(__ushort_as_half(h));
+      };
+      s.rest[row] = rounding_rest(f[1] * at(sa) + sum, at(sb));
+    }
     hand_over();
     if (warp == 0 && one) {
       // X with its columns contiguous: the next 64 of them are a box away
@@ -422,7 +440,7 @@ __global__ void __launch_bounds__(kSmallThreads, COLUMNS == 128 ? 2 : 1) small_k
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t x = swizzled(sx, row, col + 8 * i);
-        const uint4 r = combine8(0.0f, make_uint4(0, 0, 0, 0), f[4], v + 8 * i, last);
+        const uint4 r = combine8(0.0f, make_uint4(0, 0, 0, 0), f[4] * s.rest[row], v + 8 * i, last);
         if (!last) put16(x, r);
         else if (wide && k.out_vectors && row < side && col + 8 * i + 8 <= length) *reinterpret_cast<uint4*>(out + 8 * i) = r;
         w[4 * i] = r.x, w[4 * i + 1] = r.y, w[4 * i + 2] = r.z, w[4 * i + 3] = r.w;
@@ -456,6 +474,7 @@ struct Shape {
   int count, matrix;             // matrices, and the number of the first
   int first[3], tiles[3];        // of each stage: first tile in it, tiles of a matrix
   __half *x[2], *to_a, *to_b;
+  float* rest;                   // of B's diagonal, a_pitch apart
   bool vectors;                  // the results' rows are whole 16 bytes
 };
 
@@ -576,9 +595,11 @@ struct Steps {
     uint16_t *to, *mirror;       // likewise; a block above the diagonal is stored a second time, lanes as rows
     long long stride, stride_in; // of the results' columns; of A's, and of the mirrored rows
     int lanes, columns, pads, pad_columns;  // of the sides, and with what lies behind a row's end
-    bool last, vectors;
+    bool last, vectors, on_diagonal, tall;
     uint32_t staging;
-    uint4 next[4];               // the old values of the next chunk, loaded ahead
+    float* rest;                 // of the second product: where to keep the diagonal's; of the third: its columns'
+    float rows[4];               // of the third: of a lane's rows
+    uint4 next[4];               // of the next chunk, loaded ahead: A, or the columns' factors
 
     __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int c,
                                         mma::Staging& area, const float* factors)
@@ -590,10 +611,23 @@ struct Steps {
       const long long at = (long long)z * nj * pitch, here = at + (long long)w.b_row * pitch + row;
       last = w.stage == kApply && w.step + 1 == p.steps;
       vectors = true;
+      on_diagonal = false;
       stride = stride_in = pitch;
       old = nullptr;
       mirror = nullptr;
+      rest = nullptr;
+      tall = w.stage == kApply && s.rows > s.cols;
       if (w.stage == kApply) {
+        const float* factors = s.rest + (long long)z * s.a_pitch;
+        if (!tall) {
+          rest = const_cast<float*>(factors);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = row + (threadIdx.x & 31) / 4 + 8 * i;
+            rows[i] = at < ni ? __ldcg(factors + at) : 1.0f;
+          }
+        }
         to = reinterpret_cast<uint16_t*>(s.x[(w.step + 1) & 1]) + here;
         if (last) {
           stride = ni;
@@ -606,7 +640,9 @@ struct Steps {
         if (w.b_row >= w.a_row + kSide) mirror = result + at + (long long)row * pitch + w.b_row;
         if (w.stage == kSquare) {
           old = s.to_a + here;
-          if (!mirror) diagonal = __ldcg(p.coefs + ((long long)matrix * p.steps + w.step) * kCoefs + 3);
+          rest = s.rest + (long long)z * s.a_pitch;
+          on_diagonal = !mirror;
+          if (on_diagonal) diagonal = __ldcg(p.coefs + ((long long)matrix * p.steps + w.step) * kCoefs + 3);
         }
       }
       lanes = ni - row;
@@ -617,7 +653,17 @@ struct Steps {
     }
 
     __device__ __forceinline__ void load_next(int c) {
-      if (!old) return;
+      if (!old) {
+        if (!rest) return;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // whole pairs: `rest` is as long as a padded row
+          const int at = c + 8 * q + 2 * (threadIdx.x & 3);
+          const float2 f = at < columns ? __ldcg(reinterpret_cast<const float2*>(rest + column + at)) : make_float2(1.0f, 1.0f);
+          next[q].x = __float_as_uint(f.x);
+          next[q].y = __float_as_uint(f.y);
+        }
+        return;
+      }
       const int lane = threadIdx.x & 31, part = lane & 3, column = c + (lane >> 2);
       const __half* from = old + column * stride_in + part * 8;
 #pragma unroll
@@ -648,8 +694,11 @@ struct Steps {
                        : "r"(mma::staged(staging, 8 * q + (lane & 7), lane >> 3))
                        : "memory");
         __syncwarp();
-        load_next(c + mma::kChunkStep);
+      } else if (rest) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[2 * q] = next[q].x, o[2 * q + 1] = next[q].y;
       }
+      load_next(c + mma::kChunkStep);
       float v[32];
       if (source == mma::kSums) {
         mma::tmem_fragments(at, v);
@@ -658,17 +707,36 @@ struct Steps {
         for (int i = 0; i < 32; ++i) v[i] = source == mma::kZeros ? 0.0f : __int_as_float(0x7fc00000);
       }
       uint32_t w[16];
+      // A 32 x 32 block lies on the diagonal or off it.  On it a lane's rows lane / 4 + 8 k meet the columns 8 k +
+      // 2 (lane % 4) and the next: four elements of every fourth lane are the diagonal's.
+      const bool mine = on_diagonal && row == column + c && lane >> 3 == (lane & 3), upper = lane >> 2 & 1;
+      if (old) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
-        float lo = y * v[2 * i], hi = y * v[2 * i + 1];
-        if (old) lo += x * b.x, hi += x * b.y;
-        if (diagonal != 0.0f) {
-          const int off = row + (lane >> 2) + 8 * (i & 1) + 16 * (i >> 3) - (column + c + 8 * (i >> 1 & 3) + 2 * (lane & 3));
-          if (off == 0) lo += diagonal;
-          if (off == 1) hi += diagonal;
+        for (int i = 0; i < 16; ++i) {
+          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
+          float lo = y * v[2 * i] + x * b.x, hi = y * v[2 * i + 1] + x * b.y;
+          const int k = (i & 1) + 2 * (i >> 3);
+          if ((i >> 1 & 3) == k && mine) {
+            if (upper) hi += diagonal;
+            else lo += diagonal;
+            if ((lane >> 2) + 8 * k < lanes)
+              rest[row + (lane >> 2) + 8 * k] =
+                  rounding_rest(upper ? hi : lo, __half2float(__float2half_rn(upper ? hi : lo)));
+          }
+          w[i] = half2_bits(lo, hi);
         }
-        w[i] = last ? pack_bf16x2(lo, hi) : half2_bits(lo, hi);
+      } else {
+        // the columns' factors, or the lane's rows'
+        float f[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] = rest ? y * __uint_as_float(o[q]) : y;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int q = i >> 1 & 3;
+          float lo = f[2 * q] * v[2 * i], hi = f[2 * q + 1] * v[2 * i + 1];
+          if (tall) lo *= rows[(i & 1) + 2 * (i >> 3)], hi *= rows[(i & 1) + 2 * (i >> 3)];
+          w[i] = last ? pack_bf16x2(lo, hi) : half2_bits(lo, hi);
+        }
       }
       mma::stage_columns(staging, w);
       __syncwarp();
@@ -786,6 +854,7 @@ struct Class {
   size_t rows, cols, count;
   unsigned int matrix;           // number of the first
   __half *x[2], *a, *b;
+  float* rest;
   bool vectors;
 };
 
@@ -822,7 +891,7 @@ void gather(const OrthogonalCall& c, size_t first, bool whole, uint8_t* base, Gr
       for (k = 0; k < g.classes && !(g.cls[k].rows == c.rows[i] && g.cls[k].cols == c.cols[i]); ++k) {}
       if (k == g.classes) {
         if (g.classes == kMaxShapes) break;
-        g.cls[g.classes++] = Class{c.rows[i], c.cols[i], 0, 0, {}, nullptr, nullptr, true};
+        g.cls[g.classes++] = Class{c.rows[i], c.cols[i], 0, 0, {}, nullptr, nullptr, nullptr, true};
       }
       g.cls[k].count += c.counts[i];
       g.cls[k].vectors &= c.cols[i] % 8 == 0 && (c.outs == nullptr || ((uintptr_t)c.outs[i] & 15) == 0);
@@ -848,6 +917,7 @@ void gather(const OrthogonalCall& c, size_t first, bool whole, uint8_t* base, Gr
     for (int j = 0; j < 2; ++j) l.x[j] = reinterpret_cast<__half*>(take(l.count * x));
     l.a = reinterpret_cast<__half*>(take(l.count * a));
     l.b = reinterpret_cast<__half*>(take(l.count * a));
+    l.rest = reinterpret_cast<float*>(take(l.count * up(side, 64) * 4));
     l.matrix = (unsigned int)matrix;
     matrix += l.count;
   }
@@ -976,7 +1046,7 @@ cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const flo
     s.rows = (int)l.rows, s.cols = (int)l.cols, s.side = (int)side;
     s.x_pitch = (int)px, s.a_pitch = (int)pa;
     s.count = (int)l.count, s.matrix = (int)l.matrix;
-    s.to_a = l.a, s.to_b = l.b;
+    s.to_a = l.a, s.to_b = l.b, s.rest = l.rest;
     s.vectors = l.vectors;
     mma::Kind depth;
     const auto map = [&](CUtensorMap* to, mma::Kind* kind, const __half* at, size_t rows, size_t cols, size_t pitch,
