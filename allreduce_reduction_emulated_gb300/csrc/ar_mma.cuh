@@ -15,12 +15,13 @@
 // last slice, or tells of stored tiles where others wait for them.  There are two accumulators, so that
 // one tile's epilogue overlaps the next tile's products.
 //
-// Every wait is bounded (about a second).  A block that gives up tells its other warps;
+// Every wait is bounded (two seconds).  A block that gives up tells its other warps;
 // what they have not computed by then becomes NaN in the output, copies and matrix
 // instructions on their way are let finish, tensor memory is freed and the block ends.
 #pragma once
 
 #include <cstdint>
+#include <cstdlib>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -36,7 +37,7 @@ constexpr int kBoxBytes = 64 * kDepth * 2; // 64 x 64 elements, 128-byte rows
 constexpr int kAhead = 8;                  // tiles worked out ahead
 constexpr int kEpilogueWarps = 8;
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
-constexpr uint32_t kPolls = 1u << 16;
+constexpr uint64_t kLimit = 2000000000;    // ns that anything may be waited for
 constexpr int kChunkStep = 32 * (kEpilogueWarps / 4);  // from one chunk of a warp to its next
 
 // ------------------------------------------------------------------ PTX
@@ -75,14 +76,27 @@ __device__ __forceinline__ bool bar_try(uint32_t b, uint32_t parity) {
                : "memory");
   return done != 0;
 }
+__device__ __forceinline__ uint64_t nanoseconds() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
 // False where the phase did not end in time, or another warp of the block has given up.
 __device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity, volatile uint32_t* late) {
-  for (uint32_t n = 0; n < kPolls; ++n) {
+  if (bar_try(b, parity)) return true;
+  const uint64_t begin = nanoseconds();
+  for (uint32_t n = 1;; ++n) {
     if (bar_try(b, parity)) return true;
     if (*late) return false;
+    if (n % 256 == 0 && nanoseconds() - begin > kLimit) {
+      *late = 1;
+      return false;
+    }
   }
-  *late = 1;
-  return false;
+}
+// The same for a whole warp: all its lanes get one answer.
+__device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile uint32_t* late) {
+  return __all_sync(~0u, bar_wait(b, parity, late));
 }
 __device__ __forceinline__ uint32_t of_rank(uint32_t a, uint32_t rank) {
   uint32_t r;
@@ -374,7 +388,7 @@ constexpr int shared_bytes() {
 }
 
 template <int CG, class Policy>
-__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ typename Policy::Params p) {
+__global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ typename Policy::Params p, int late_block) {
   extern __shared__ uint8_t raw[];
   constexpr int kStages = Policy::kStages, kStageBytes = 2 * kBoxBytes + Policy::kBytesB;
   auto& s = *reinterpret_cast<SharedOf<Policy>*>(raw + ((1024 - (saddr(raw) & 1023)) & 1023));
@@ -421,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       Tile w;
       const bool more = Policy::tile(p, local, first + (int)t * pairs, w);
       const uint32_t place = t % kAhead;
-      if (!bar_wait(saddr(&s.taken[place]), (t / kAhead & 1) ^ 1, late)) break;
+      if (!warp_wait(saddr(&s.taken[place]), (t / kAhead & 1) ^ 1, late)) break;
       if constexpr (Policy::kOrdered) {
         if (more && !Policy::wait(p, w, late)) break;
         // what other blocks have stored is read by TMA from here on (in the loading warp the fence holds the loads up)
@@ -435,13 +449,16 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (!more) break;
     }
   } else if (warp == 0) {
+    const bool gives_up = (int)blockIdx.x == late_block;
+    if (gives_up) *late = 1;
     const bool one = elect();
     const uint32_t empty = saddr(&s.empty[0]), stages = saddr(s.stage[0]);
     const uint32_t full = CG == 2 ? of_rank(saddr(&s.full[0]), 0) : saddr(&s.full[0]);
     uint32_t slot = 0, phase = 0;
-    for (uint32_t t = 0;; ++t) {
+    // (Whether a warp goes on is decided by votes alone: its lanes may read `late` at different times.)
+    for (uint32_t t = 0; !gives_up; ++t) {
       const uint32_t place = t % kAhead;
-      if (!bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) break;
+      if (!warp_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) break;
       const Tile w = s.tiles[place];
       __syncwarp();
       if (lane == 0) bar_arrive(saddr(&s.taken[place]));
@@ -477,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     uint32_t slot = 0, phase = 0, n = 0;
     for (uint32_t t = 0;; ++t) {
       const uint32_t place = t % kAhead;
-      if (!bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) break;
+      if (!warp_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) break;
       const Tile w = s.tiles[place];
       __syncwarp();
       if (lane == 0) bar_arrive(saddr(&s.taken[place]));
@@ -489,11 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       for (int begin = 0; ok && begin < w.blocks;) {
         const int end = Policy::kRun ? min(begin + Policy::kRun, w.blocks) : w.blocks;
         const uint32_t buffer = n & 1, d = tmem + buffer * (kColumns / 2);
-        ok = bar_wait(saddr(&s.drained[buffer]), ((n >> 1) & 1) ^ 1, late);
+        ok = warp_wait(saddr(&s.drained[buffer]), ((n >> 1) & 1) ^ 1, late);
         ++n;
         fence_after();
         for (int i = begin; ok && i < end; ++i) {
-          ok = bar_wait(saddr(&s.full[slot]), phase, late);
+          ok = warp_wait(saddr(&s.full[slot]), phase, late);
           if (!ok) break;
           // zeros that the other block's threads have stored
           if (CG == 2 && w.last < kDepth && i == w.blocks - 1) asm volatile("fence.acq_rel.cluster;" ::: "memory");
@@ -520,10 +537,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       }
       if (!ok) break;
     }
-    if (*late) {  // let what was issued finish
+    if (__any_sync(~0u, *late)) {  // let what was issued finish
       if (one) mma_commit<CG>(saddr(&s.done));
       __syncwarp();
-      for (uint32_t i = 0; i < kPolls && !bar_try(saddr(&s.done), 0); ++i) {}
+      for (const uint64_t begin = nanoseconds(); !bar_try(saddr(&s.done), 0) && nanoseconds() - begin < kLimit;) {}
     }
   } else if (warp >= 4) {
     const int e = warp - 4;
@@ -534,23 +551,26 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const uint32_t place = t % kAhead;
       Tile w;
       float factors[2] = {0.0f, 0.0f};
-      ok = ok && bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late);
-      ok = __all_sync(~0u, ok);
+      ok = ok && warp_wait(saddr(&s.filled[place]), t / kAhead & 1, late);
       if (ok) {
         w = s.tiles[place];
         if constexpr (Policy::kOrdered) factors[0] = s.factors[place][0], factors[1] = s.factors[place][1];
         __syncwarp();
         if (lane == 0) bar_arrive(saddr(&s.taken[place]));
         if (w.columns == 0) break;
-      } else if (!Policy::tile(p, local, first + (int)t * pairs, w)) {
-        break;
+      } else {
+        // The block has given up: from here on its tiles' results are NaN.  (The ring is not asked again: a barrier
+        // that nothing arrives on any more lets every other round through.)
+        if (!Policy::tile(p, local, first + (int)t * pairs, w)) break;
+        if constexpr (Policy::kOrdered)
+          if (!Policy::result(p, w)) continue;
       }
       const int row = w.a_row + (int)rank * kRows + (e & 3) * 32, first_column = (e >> 2) * 32;
       // The accumulators of one run are ready: `use` reads them, then they are handed back.
       const auto run = [&](auto use) {
         const uint32_t buffer = n & 1, at = tmem + buffer * (kColumns / 2) + ((uint32_t)(e & 3) * 32 << 16);
         if (w.blocks) {
-          ok = ok && bar_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
+          ok = ok && warp_wait(saddr(&s.ready[buffer]), (n >> 1) & 1, late);
           fence_after();
         }
         use(at);
@@ -585,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       uint32_t slices = 0, phases = 0;
       for (uint32_t t = 0;; ++t) {
         const uint32_t place = t % kAhead;
-        if (!bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) break;
+        if (!warp_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) break;
         const Tile w = s.tiles[place];
         __syncwarp();
         if (lane == 0) bar_arrive(saddr(&s.taken[place]));
@@ -593,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         slices += w.blocks;
         if (w.blocks == 0 || w.last == kDepth) continue;
         const uint32_t slot = (slices - 1) % kStages;
-        if (!bar_wait(saddr(&s.tail[slot]), phases >> slot & 1, late)) break;
+        if (!warp_wait(saddr(&s.tail[slot]), phases >> slot & 1, late)) break;
         phases ^= 1u << slot;
         // up to whole sixteens, the rest is not multiplied
         const int end = (w.last + 15) & ~15, boxes = (2 * kBoxBytes + w.b_bytes) / kBoxBytes;
@@ -610,21 +630,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       }
     }
     if constexpr (Policy::kOrdered) {
+      bool ok = true;
       for (uint32_t t = 0;; ++t) {
         const uint32_t place = t % kAhead;
         Tile w;
-        if (bar_wait(saddr(&s.filled[place]), t / kAhead & 1, late)) {
+        ok = ok && warp_wait(saddr(&s.filled[place]), t / kAhead & 1, late);
+        if (ok) {
           w = s.tiles[place];
           __syncwarp();
           if (lane == 0) bar_arrive(saddr(&s.taken[place]));
           if (w.columns == 0) break;
+          ok = warp_wait(saddr(&s.stored[place]), t / kAhead & 1, late);
         } else if (!Policy::tile(p, local, first + (int)t * pairs, w)) {
           break;
         }
-        // in a block that has given up too: its NaN are to be there before others read on
-        for (uint32_t i = 0; i < 2 * kPolls && !bar_try(saddr(&s.stored[place]), t / kAhead & 1); ++i) {}
-        // the fence covers what the epilogue's warps stored before they arrived
-        if (lane == 0) Policy::done(p, w);
+        // the fence covers what the epilogue's warps stored before they arrived; who waits for a tile of a
+        // block that has given up gives up too
+        if (lane == 0) Policy::done(p, w, ok);
       }
     }
   }
@@ -663,6 +685,15 @@ inline bool better_in_pairs(double in_pairs, double alone, double slices, int sm
   return whole(in_pairs / pairs) * (0.27 * slices + 3.0) <= whole(alone / sms) * (0.20 * slices + 2.0);
 }
 
+// AR_LATE_BLOCK=<number> in the environment: a block that gives up at once, for tests; -1: none.
+inline int late_block() {
+  static const int block = [] {
+    const char* s = std::getenv("AR_LATE_BLOCK");
+    return s ? std::atoi(s) : -1;
+  }();
+  return block;
+}
+
 // `together`: the blocks wait for one another, so all of them have to be on the GPU at once.
 template <int CG, class Policy>
 cudaError_t launch_product(const typename Policy::Params& p, long long tiles, int sms, cudaStream_t stream,
@@ -691,7 +722,7 @@ cudaError_t launch_product(const typename Policy::Params& p, long long tiles, in
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, product_kernel<CG, Policy>, p);
+  return cudaLaunchKernelEx(&cfg, product_kernel<CG, Policy>, p, late_block());
 }
 
 }  // namespace mma

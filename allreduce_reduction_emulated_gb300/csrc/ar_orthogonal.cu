@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kSmallThreads, COLUMNS == 128 ? 2 : 1) small_k
   const bool one = mma::elect();
   bool ok = true;
   const auto wait = [&] {  // for the matrix instructions
-    ok = mma::bar_wait(mma::saddr(&s.done), phase, late) && ok;
+    ok = mma::warp_wait(mma::saddr(&s.done), phase, late) && ok;
     phase ^= 1;
     mma::fence_after();
   };
@@ -496,6 +496,7 @@ struct Steps {
   static constexpr bool kBf16 = false, kOrdered = true;
   static constexpr int kStages = 6, kBytesB = 2 * mma::kBoxBytes, kAreas = 1, kArea = 2048, kRun = 0;
   static constexpr int kSide = 128 * CG;
+  static constexpr unsigned int kFailed = 1u << 31;  // in a matrix' count: a block that had tiles of it has given up
   using Params = StepsParams;
   struct Local {};
   static __device__ __forceinline__ void begin(const Params&, Local&) {}
@@ -567,18 +568,25 @@ struct Steps {
     if (before == 0) return true;
     const unsigned int* at = p.done + s.matrix + w.a_z;
     bool ok = false;
-    for (uint32_t n = 0; n < 16 * mma::kPolls; ++n) {  // about 0.7 us each
+    const uint64_t begin = mma::nanoseconds();
+    for (uint32_t n = 1;; ++n) {
       unsigned int v;
       asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
-      ok = v >= before;
-      if (ok || *late) break;
+      ok = v >= before && !(v & kFailed);
+      if (ok || *late || (v & kFailed) || (n % 256 == 0 && mma::nanoseconds() - begin > mma::kLimit)) break;
     }
     if (!ok) *late = 1;
     return __all_sync(~0u, ok);
   }
-  static __device__ __forceinline__ void done(const Params& p, const Tile& w) {
+  static __device__ __forceinline__ void done(const Params& p, const Tile& w, bool ok) {
+    unsigned int* at = p.done + p.shape[w.shape].matrix + w.a_z;
     __threadfence();
-    atomicAdd(p.done + p.shape[w.shape].matrix + w.a_z, 1u);
+    if (ok) atomicAdd(at, 1u);
+    else atomicOr(at, kFailed);
+  }
+  // Whether the tile is of the results, not of what goes between the products.
+  static __device__ __forceinline__ bool result(const Params& p, const Tile& w) {
+    return w.stage == kApply && w.step + 1 == p.steps;
   }
 
   // Of the sum (0) and, of the second product, of A (1) in the epilogue.

@@ -274,10 +274,10 @@ ar_status_t ar_expert_product(const void* x, size_t rows, size_t x_stride, const
   c.y = y, c.y_stride = rows > 1 ? y_stride : out, c.dtype = (int)y_dtype;
   c.zero_rest = zero_rest != 0;
   c.workspace = workspace, c.stream = static_cast<cudaStream_t>(stream);
+  if (too_many_tiles(out, rows, experts + 2)) return AR_ERR_UNSUPPORTED;
   ar_status_t st = check_experts(c, weights, 2, expert_stride, out_stride, in_stride);
   if (st == AR_SUCCESS) st = check_rows(c.x);
   if (st != AR_SUCCESS) return st;
-  if (too_many_tiles(out, rows, experts + 2)) return AR_ERR_UNSUPPORTED;
   if (rows == 0 || out == 0) return AR_SUCCESS;
   const size_t es = ar::elem_bytes(c.dtype);
   const size_t there = c.y_stride < out ? 0 : span(rows, out, c.y_stride, es);

@@ -24,7 +24,8 @@
  * about a second.  Where one ran out, the cluster's rows, of which there are at most
  * 32, would give NaN in gradient and log-probability, and so would the statistics.
  * AR_LATE_BLOCK=<rank> in the environment of the process lets that block of
- * every cluster give up its first wait: for tests.)
+ * every cluster give up its first wait, and the block of that number of the
+ * products below give up at once: for tests.)
  *
  * Logits.  A matrix of `rows` tokens by `vocab` columns, AR_FLOAT32 or
  * AR_BFLOAT16; row t starts at logits + t * row_stride elements
@@ -193,7 +194,7 @@ ar_status_t ar_clip_grads(size_t ntensors, const void* const* grads, void* const
  * Errors: AR_ERR_INVALID_ARG (NULL or misaligned pointer, strides, enum, workspace
  * too small, overlap of y with x), AR_ERR_UNSUPPORTED (another data type, more than
  * AR_MAX_TOKENS rows, AR_MAX_EXPERTS experts, AR_MAX_FEATURES columns or 2^30 tiles
- * of 128 x 128), AR_ERR_CUDA.  Waits inside the kernel are bounded (about a second);
+ * of 128 x 128), AR_ERR_CUDA.  Waits inside the kernel are bounded (two seconds);
  * what a block has not computed when one runs out is NaN.
  */
 #define AR_MAX_EXPERTS 1024
@@ -248,7 +249,7 @@ ar_status_t ar_expert_weight_gradient(const void* dy, size_t dy_stride, const vo
  * The host arrays are read during the call only.  Errors: AR_ERR_INVALID_ARG (NULL or misaligned pointer, enum,
  * steps, a parameter that is not finite, eps < 0, coefficients under which the singular values of a matrix of
  * norm 1 exceed 10^6, workspace too small), AR_ERR_UNSUPPORTED (AR_INT32, a side above AR_MAX_SIDE, more than
- * AR_MAX_MATRICES matrices in a stack), AR_ERR_CUDA.  Waits inside the kernels are bounded (about a second);
+ * AR_MAX_MATRICES matrices in a stack), AR_ERR_CUDA.  Waits inside the kernels are bounded (two seconds);
  * what a block has not computed when one runs out is NaN.
  */
 #define AR_MAX_ORTHOGONAL_STEPS 16
