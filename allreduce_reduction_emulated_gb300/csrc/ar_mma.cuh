@@ -20,6 +20,7 @@
 // instructions on their way are let finish, tensor memory is freed and the block ends.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cstdlib>
 
@@ -703,9 +704,7 @@ cudaError_t launch_product(const typename Policy::Params& p, long long tiles, in
   const cudaError_t e =
       cudaFuncSetAttribute(product_kernel<CG, Policy>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  const long long most = sms / CG;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * CG));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
@@ -722,6 +721,22 @@ cudaError_t launch_product(const typename Policy::Params& p, long long tiles, in
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  long long most = sms / CG;
+  if (together) {  // as many as fit at once, asked once per device
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n <= 0) {
+      cfg.gridDim = dim3((unsigned)(most * CG));
+      const cudaError_t q = cudaOccupancyMaxActiveClusters(&n, product_kernel<CG, Policy>, &cfg);
+      if (q != cudaSuccess) return q;
+      if (n <= 0) return cudaErrorCooperativeLaunchTooLarge;
+      known[dev].store(n, std::memory_order_relaxed);
+    }
+    if (n < most) most = n;
+  }
+  cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * CG));
   return cudaLaunchKernelEx(&cfg, product_kernel<CG, Policy>, p, late_block());
 }
 
