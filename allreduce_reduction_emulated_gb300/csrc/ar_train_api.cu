@@ -128,6 +128,21 @@ ar_status_t check_rows(const ar::ExpertMatrix& m) {
   return span(m.ny, m.nx, m.ny > 1 ? m.y_stride : m.nx, 2) ? AR_SUCCESS : AR_ERR_INVALID_ARG;
 }
 
+// Bytes from the first to past the last element of matrices of any size above 0.
+size_t span_of(const ar::ExpertMatrix& m, size_t es) {
+  return ((m.nz - 1) * m.z_stride + (m.ny - 1) * m.y_stride + m.nx) * es;
+}
+
+// Whether two matrices of `rows` > 0 rows share memory; columns and strides in bytes.  Columns of one
+// wider matrix do not.
+bool rows_overlap(const void* a, size_t a_cols, size_t a_stride, const void* b, size_t b_cols, size_t b_stride, size_t rows) {
+  if (!overlap(a, (rows - 1) * a_stride + a_cols, b, (rows - 1) * b_stride + b_cols)) return false;
+  if (a_stride != b_stride) return true;
+  const bool behind = (uintptr_t)b > (uintptr_t)a;
+  const size_t way = (behind ? (uintptr_t)b - (uintptr_t)a : (uintptr_t)a - (uintptr_t)b) % a_stride;
+  return behind ? way < a_cols || way + b_cols > a_stride : way < b_cols || way + a_cols > a_stride;
+}
+
 // Sizes, offsets, the layout of the weights (or of their gradient) and the workspace of the expert products.
 // Fills in c.w and c.w_in_contiguous.
 ar_status_t check_experts(ar::ExpertsCall& c, const void* w, size_t es, size_t expert_stride, size_t out_stride,
@@ -282,7 +297,8 @@ ar_status_t ar_expert_product(const void* x, size_t rows, size_t x_stride, const
   const size_t es = ar::elem_bytes(c.dtype);
   const size_t there = c.y_stride < out ? 0 : span(rows, out, c.y_stride, es);
   if (!aligned(y, es) || !there) return AR_ERR_INVALID_ARG;
-  if (in && overlap(x, span(rows, in, c.x.y_stride, 2), y, there)) return AR_ERR_INVALID_ARG;
+  if (in && rows_overlap(x, in * 2, c.x.y_stride * 2, y, out * es, c.y_stride * es, rows)) return AR_ERR_INVALID_ARG;
+  if (in && experts && overlap(weights, span_of(c.w, 2), y, there)) return AR_ERR_INVALID_ARG;
   const size_t need = ar::expert_matrix_workspace(c.x) + ar::expert_matrix_workspace(c.w);
   if (workspace_bytes < need || (need && !aligned(workspace, 16))) return AR_ERR_INVALID_ARG;
   if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
@@ -309,6 +325,9 @@ ar_status_t ar_expert_weight_gradient(const void* dy, size_t dy_stride, const vo
   if (st != AR_SUCCESS) return st;
   if ((double)experts * ((double)in / 128 + 1) * ((double)out / 128 + 1) > (double)(1 << 30)) return AR_ERR_UNSUPPORTED;
   if (experts == 0 || in == 0 || out == 0) return AR_SUCCESS;
+  const size_t there = span_of(c.w, ar::elem_bytes(c.dtype));
+  if (rows && (overlap(x, span_of(c.x, 2), dw, there) || overlap(dy, span_of(c.dy, 2), dw, there)))
+    return AR_ERR_INVALID_ARG;
   const size_t need = ar::expert_matrix_workspace(c.x) + ar::expert_matrix_workspace(c.dy);
   if (workspace_bytes < need || (need && !aligned(workspace, 16))) return AR_ERR_INVALID_ARG;
   if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;

@@ -84,6 +84,24 @@ def _weights(what: str, name: str, w, device: int, dtypes=(torch.bfloat16,)):
     return E, N, K, e, n, k
 
 
+def _shared(a, b) -> bool:
+    """Whether two tensors share memory.  Columns of one wider matrix do not."""
+    def span(t):
+        return sum((n - 1) * s for n, s in zip(t.shape, t.stride())) * t.element_size() + t.element_size()
+
+    if not a.numel() or not b.numel():
+        return False
+    if b.data_ptr() < a.data_ptr():
+        a, b = b, a
+    way = b.data_ptr() - a.data_ptr()
+    if way >= span(a):
+        return False
+    row = a.stride(0) * a.element_size()
+    if a.dim() == b.dim() == 2 and row == b.stride(0) * b.element_size():
+        return way % row < a.shape[1] * a.element_size() or way % row + b.shape[1] * b.element_size() > row
+    return True
+
+
 def _space(lib, device, *operands) -> tuple:
     """(tensor or None, address, bytes) of the workspace of (address, columns, rows, count, row stride, matrix
     stride) operands; none where all of them are aligned, which needs no call to know."""
@@ -159,7 +177,7 @@ def expert_gradients(dy, x, weights, offsets, dx=None, dw=None, dw_dtype=None, a
 
     dx, dw      where they go; None makes dx in bfloat16 and dw in dw_dtype (bfloat16
                 by default, or float32), laid out as the weights are.  A given dw may be a view
-                of a flat gradient buffer
+                of a flat gradient buffer.  None of it may be part of an input
     accumulate  add to the dw that is given (an expert without rows keeps its own)
     need_dx, need_dw   False leaves one out (None in its place)"""
     what = "expert_gradients"
@@ -188,6 +206,10 @@ def expert_gradients(dy, x, weights, offsets, dx=None, dw=None, dw_dtype=None, a
         dx = None
     if not need_dw:
         dw = None
+    if dx is not None and need_dw:  # dx is written before x is read again
+        for name, t in ("x", x), ("dw", dw):
+            if t is not None and _shared(dx, t):
+                raise _bad(what, f"dx and {name} share memory")
     if stream is not None:
         context, handle = _on(stream)
         with context:

@@ -192,7 +192,7 @@ ar_status_t ar_clip_grads(size_t ntensors, const void* const* grads, void* const
  * `in` and `out` and their strides exchanged).  Sums are fp32, rounded once.
  * rows == 0 or out == 0 is a no-op; in == 0 gives zeros for the experts' rows.
  * Errors: AR_ERR_INVALID_ARG (NULL or misaligned pointer, strides, enum, workspace
- * too small, overlap of y with x), AR_ERR_UNSUPPORTED (another data type, more than
+ * too small, overlap of y with x or weights), AR_ERR_UNSUPPORTED (another data type, more than
  * AR_MAX_TOKENS rows, AR_MAX_EXPERTS experts, AR_MAX_FEATURES columns or 2^30 tiles
  * of 128 x 128), AR_ERR_CUDA.  Waits inside the kernel are bounded (two seconds);
  * what a block has not computed when one runs out is NaN.
@@ -214,7 +214,7 @@ ar_status_t ar_expert_product(const void* x, size_t rows, size_t x_stride, const
  * 0 for an expert without rows; with accumulate != 0 added to what dW holds.
  *   dy        rows by `out`, x rows by `in`, AR_BFLOAT16
  *   dw        dw_dtype (AR_FLOAT32 or AR_BFLOAT16), laid out by its three strides as
- *             the weights are
+ *             the weights are; no part of dy or x
  *   workspace the sum of ar_expert_workspace() of dy and of x
  * Everything else as for ar_expert_product.
  */

@@ -153,3 +153,46 @@ def test_orthogonalizer_refusals(lib):
     refused(lambda: make([c(x)], coefficients=(1.0, 2.0)), "three coefficients")
     refused(lambda: make([c(x)], scale="rows"), "'shape'")
     refused(lambda: make([c(x)], scale=[1.0, 2.0]), "2 scales")
+
+
+def test_results_in_their_inputs(lib, monkeypatch):
+    """What a product writes may not be what it reads; columns of one wider matrix are apart."""
+    def product(y, y_stride=16, x_stride=8, w=64 * P):
+        return lib.ar_expert_product(P, 4, x_stride, w, 2, 16, 8, 128, 8, 1, P, 8, y, y_stride, ar.AR_BFLOAT16, 0, None, 0,
+                                     None)
+
+    def gradient(dw, dtype=ar.AR_BFLOAT16):
+        return lib.ar_expert_weight_gradient(64 * P, 16, P, 8, 4, 2, 16, 8, P, 8, dw, 128, 8, 1, dtype, 0, None, 0, None)
+
+    launched = (ar.AR_SUCCESS, ar.AR_ERR_CUDA)  # what a call answers that is not refused, without a GPU
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are stand-ins")
+    # the weights span (128 + 15 * 8 + 8) * 2 bytes, y 4 * 16 * 2
+    for y in (64 * P, 64 * P + 510, 64 * P - 126, P, P + 62, P - 126):
+        assert product(y) == BAD, y
+    for y in (64 * P + 512, 64 * P - 128, P + 64, P - 128):
+        assert product(y) in launched, y
+    # x in the first 8 of 24 columns, y in the others; then one column too far to the left, or too wide a row
+    assert product(P + 16, 24, 24) in launched and product(P + 16 + 48, 24, 24) in launched
+    assert product(P - 32, 24, 24) in launched
+    for y, stride in ((P + 14, 24), (P + 16, 23), (P - 30, 24), (P + 18, 24)):
+        assert product(y, stride, 24) == BAD, (y, stride)
+    for dw in (P, P + 62, P - 510, 64 * P, 64 * P + 126, 64 * P - 510):
+        assert gradient(dw) == BAD, dw
+    assert gradient(P - 1022 + 2, ar.AR_FLOAT32) == BAD
+    for dw in (P + 64, P - 512, 64 * P + 128, 64 * P - 512):
+        assert gradient(dw) in launched, dw
+
+    for m in (losses, experts):
+        monkeypatch.setattr(m, "_current_device", lambda: 0)
+    g, h = OnGpu.of, experts.expert_gradients
+    both = torch.zeros(6, 24, dtype=torch.bfloat16)
+    x, dy, w = g(both[:, :8]), g(torch.zeros(6, 16, dtype=torch.bfloat16)), g(torch.zeros(3, 16, 8, dtype=torch.bfloat16))
+    off = g(torch.tensor([0, 2, 4, 6]))
+    refused(lambda: h(dy, x, w, off, dx=x), "dx and x share")
+    refused(lambda: h(dy, x, w, off, dx=g(both[:, 7:15])), "dx and x share")
+    refused(lambda: h(dy, x, w, off, dx=g(both.view(-1)[3:99].view(6, 16)[:, :8])), "dx and x share")
+    flat = torch.zeros(3 * 16 * 8, dtype=torch.bfloat16)
+    refused(lambda: h(dy, x, w, off, dx=g(flat[336:].view(6, 8)), dw=g(flat.view(3, 16, 8))), "dx and dw share")
+    assert not experts._shared(both[:, :8], both[:, 8:]) and not experts._shared(both[:, 8:], both[:, :8])
+    assert experts._shared(both[:, :9], both[:, 8:]) and experts._shared(both[:, 20:], both[1:, :3]) is False
