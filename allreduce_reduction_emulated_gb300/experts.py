@@ -19,6 +19,7 @@ stream        a torch stream or a cudaStream_t (default: the current stream).  W
 Rows of no expert (in front of offsets[0], behind offsets[-1]) are left as they are in
 a result that is given, and 0 in one that the call makes.  Operands whose address or
 strides are not whole 16 bytes are copied to a workspace first, which takes longer.
+bfloat16 results of sums over more than 2^18 products go by way of float32 ones.
 Nothing waits for the GPU and nothing is kept between calls.
 """
 from __future__ import annotations
@@ -29,6 +30,10 @@ from . import AR_BFLOAT16, AR_ERR_UNSUPPORTED, AR_FLOAT32, library
 from .losses import _bad, _check, _current_device, _indices, _on
 
 _DTYPES = {torch.float32: AR_FLOAT32, torch.bfloat16: AR_BFLOAT16}
+
+# The tensor cores cut what an addition loses, on average 2^-25 of the sum for every 16 products: over so many it is an
+# eighth of bfloat16's half step.  Longer sums of a bfloat16 result are made in float32, which adds them up in runs.
+_LONGEST = 1 << 18
 
 
 def _rows(what: str, name: str, x, device: int | None = None, rows: int | None = None, dtypes=(torch.bfloat16,)):
@@ -134,6 +139,15 @@ def _of(x, shape, dtype):
     return torch.empty(shape, dtype=dtype, device=x.device)
 
 
+def _rounded(what, lib, x, at_x, w, at_w, offsets, off_size, out, fresh, handle):
+    """_product, by way of float32 where its sums are too long to be rounded once."""
+    if at_x[2] <= _LONGEST or out.dtype == torch.float32:
+        return _product(what, lib, x, at_x, w, at_w, offsets, off_size, out, fresh, handle)
+    wide = _of(x, out.shape, torch.float32) if fresh else out.float()
+    _product(what, lib, x, at_x, w, at_w, offsets, off_size, wide, fresh, handle)
+    out.copy_(wide)
+
+
 def expert_product(x, weights, offsets, out=None, dtype=None, stream=None):
     """y[t] = weights[e] @ x[t] for the rows t of each expert e: (rows, out).
 
@@ -165,7 +179,7 @@ def _into(what, x, at_x, weights, at_w, off, size, out, dtype, handle):
     fresh = out is None
     if fresh:
         out = _of(x, (at_x[1], at_w[1]), torch.bfloat16 if dtype is None else dtype)
-    _product(what, library(), x, at_x, weights, at_w, off, size, out, fresh, handle)
+    _rounded(what, library(), x, at_x, weights, at_w, off, size, out, fresh, handle)
     return out
 
 
@@ -229,16 +243,24 @@ def _both(what, dy, at_y, x, at_x, weights, at_w, off, size, dx, dw, at_dw, dw_d
         fresh = dx is None
         if fresh:
             dx = _of(x, (rows, K), torch.bfloat16)
-        _product(what, lib, dy, at_y, weights, (E, K, N, e, k, n), off, size, dx, fresh, handle)
+        _rounded(what, lib, dy, at_y, weights, (E, K, N, e, k, n), off, size, dx, fresh, handle)
     if need_dw:
-        if dw is None:
-            dtype = torch.bfloat16 if dw_dtype is None else dw_dtype
+        def new(dtype):
             if k == 1:
-                dw, at_dw = _of(x, (E, N, K), dtype), (E, N, K, N * K, K, 1)
-            else:
-                dw, at_dw = _of(x, (E, K, N), dtype).transpose(1, 2), (E, N, K, N * K, 1, N)
+                return _of(x, (E, N, K), dtype), (E, N, K, N * K, K, 1)
+            return _of(x, (E, K, N), dtype).transpose(1, 2), (E, N, K, N * K, 1, N)
+
+        if dw is None:
+            dw, at_dw = new(torch.bfloat16 if dw_dtype is None else dw_dtype)
+        to = dw
+        if rows > _LONGEST and dw.dtype == torch.bfloat16:
+            to, at_dw = new(torch.float32)
+            if accumulate:
+                to.copy_(dw)
         dy_at, x_at = dy.data_ptr(), x.data_ptr()
         space, at, bytes_ = _space(lib, x.device, (dy_at, N, rows, 1, dy_stride, 0), (x_at, K, rows, 1, x_stride, 0))
-        _check(lib.ar_expert_weight_gradient(dy_at, dy_stride, x_at, x_stride, rows, E, N, K, off, size, dw.data_ptr(),
-                                             *at_dw[3:], _DTYPES[dw.dtype], accumulate, at, bytes_, handle), what)
+        _check(lib.ar_expert_weight_gradient(dy_at, dy_stride, x_at, x_stride, rows, E, N, K, off, size, to.data_ptr(),
+                                             *at_dw[3:], _DTYPES[to.dtype], accumulate, at, bytes_, handle), what)
+        if to is not dw:
+            dw.copy_(to)
     return dx, dw
