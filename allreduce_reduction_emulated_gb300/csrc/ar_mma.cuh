@@ -15,6 +15,11 @@
 // last slice, or tells of stored tiles where others wait for them.  There are two accumulators, so that
 // one tile's epilogue overlaps the next tile's products.
 //
+// What bounds it: with 256 columns or so the matrix instructions (a pair's slice takes them 0.27 us; 4096 rows of 8
+// even experts, 2048 -> 8192: 98 us, 1.40 PFLOP/s), with few columns the loads (16 rows of 8 experts: 47 us, 5.7 TB/s of
+// weights).  Five or six stages keep 160 to 192 KB a block on their way; one thread issues all loads without a
+// branch, as a slice's instructions in a whole warp took longer (0.36 us) than its products.
+//
 // Every wait is bounded (two seconds).  A block that gives up tells its other warps;
 // what they have not computed by then becomes NaN in the output, copies and matrix
 // instructions on their way are let finish, tensor memory is freed and the block ends.
@@ -273,6 +278,18 @@ struct Staging {
 __device__ __forceinline__ void put_columns(uint32_t staging, uint16_t* to, long long stride, int rows, int columns,
                                             bool vectors) {
   const int lane = threadIdx.x & 31, part = lane & 3;
+  if (!vectors) {
+    // a column at a time, a lane an element: 64 bytes in one store instruction (as 8 elements a lane, a sector each:
+    // 700 x 700 x 700 18.0 us, now 12.1; dW of 7 x 1431 x 1001 67, now 28)
+    columns = min(columns, 32);
+#pragma unroll 8
+    for (int c = 0; c < columns; ++c) {
+      uint16_t v;
+      asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(staged(staging, c, lane >> 3) + (lane & 7) * 2));
+      if (lane < rows) to[c * stride + lane] = v;
+    }
+    return;
+  }
   uint4 o[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q)
@@ -280,7 +297,7 @@ __device__ __forceinline__ void put_columns(uint32_t staging, uint16_t* to, long
                  : "=r"(o[q].x), "=r"(o[q].y), "=r"(o[q].z), "=r"(o[q].w)
                  : "r"(staged(staging, 8 * q + (lane >> 2), part)));
   uint16_t* d = to + (lane >> 2) * stride + part * 8;
-  if (vectors && rows >= 32 && columns >= 32) {  // of the whole warp: no branches between the stores
+  if (rows >= 32 && columns >= 32) {  // of the whole warp: no branches between the stores
 #pragma unroll
     for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(d + q * (8 * stride)) = o[q];
     return;
@@ -288,7 +305,7 @@ __device__ __forceinline__ void put_columns(uint32_t staging, uint16_t* to, long
   for (int q = 0; q < 4; ++q, d += 8 * stride) {
     if (8 * q + (lane >> 2) >= columns) break;
     const uint4 v = q == 0 ? o[0] : q == 1 ? o[1] : q == 2 ? o[2] : o[3];
-    if (vectors && part * 8 + 8 <= rows) {
+    if (part * 8 + 8 <= rows) {
       *reinterpret_cast<uint4*>(d) = v;
     } else {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};

@@ -169,6 +169,9 @@ __device__ __forceinline__ void walk_chunk(const PrepareParams& p, const Place& 
   walk<WRITE>(p, *at.s, at.matrix, begin, min(begin + p.chunk, total), kThreads, use);
 }
 
+// Momentum, and a chunk's sum of squares.  Bound by HBM: momentum is read and written, the gradient read (2 layers of 101M
+// fp32 elements: 6.6 to 6.8 TB/s).  A second pass has to follow, as the norm needs all chunks; both read 8 elements at once,
+// four times before the first is used.
 __global__ void __launch_bounds__(kThreads) norm_sum_kernel(const __grid_constant__ PrepareParams p) {
   pdl_enter();
   const Place at = place(p, blockIdx.x);
@@ -208,6 +211,8 @@ __device__ __forceinline__ void coefficients(const PrepareParams& p, float norm,
   to[4] = s * r / sb;
 }
 
+// The norm from its parts (every block for itself, in one order), the factors of all steps, and u times a power of two
+// in fp16.  Bound by HBM, but for what the kernel before has left in L2.
 __global__ void __launch_bounds__(kThreads) halve_kernel(const __grid_constant__ PrepareParams p) {
   pdl_enter();
   // from the last chunk to the first: it begins with what the kernel before has left in L2
@@ -490,7 +495,10 @@ struct StepsParams {
 // All tiles of all steps in one launch: those of the first product of all matrices, of the second, of the
 // third, then the next step's.  A tile waits until all tiles of its matrix before it are stored, which
 // with several matrices they mostly are: nobody waits for the last tile of a launch, and a step of a small
-// matrix costs three times the way through the chip, not three launches (8.4 us each).
+// matrix costs three times the way through the chip, not three launches (256 x 256, five steps: 144 us
+// so, 98 in one launch, 74 with tiles of half the width).  16 x 1024 x 2048: 590 us, 2 layers of 101M elements
+// 2670 us, of which 320 are the passes over the gradients: bound by the matrix instructions, at 1.65 PFLOP/s of what is
+// executed.
 template <int CG>
 struct Steps {
   static constexpr bool kBf16 = false, kOrdered = true;
@@ -820,8 +828,8 @@ int whole_columns(size_t rows, size_t cols) {
 }
 
 // The small matrices go whole where that is faster.  Alone they nearly always do; beside others, whose tiles
-// leave room for theirs, it is the time of a launch more.  Times in us, measured: 128 x 128 24, 128 x 512
-// 50, in tiles 256 x 256 75.
+// leave room for theirs, it is the time of a launch more.  Times in us, measured: 128 x 128 27, 128 x 512
+// 50, in tiles 256 x 256 74.
 bool take_whole(const OrthogonalCall& c) {
   double alone = 0.0;
   Sizes rest[kMaxShapes], all[kMaxShapes];
