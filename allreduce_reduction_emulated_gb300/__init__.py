@@ -15,7 +15,9 @@ call with dtype / count taken from the tensors and a cached communicator.
 
 The operators at the two ends of the data-parallel step (include/ar_train.h)
 are in ``losses`` (token log-probabilities, policy and preference losses with
-the gradient of the logits) and ``clipping`` (global gradient norm, clipping).
+the gradient of the logits), ``experts`` (products of expert layers and their
+gradients), ``clipping`` (global gradient norm, clipping) and ``orthogonal``
+(updates of matrices orthogonalised by Newton-Schulz products).
 """
 from __future__ import annotations
 
