@@ -110,6 +110,7 @@ def library() -> ctypes.CDLL:
                     fn.restype = i
                 for fn, args in ((L.ar_policy_loss_workspace, [sz]), (L.ar_preference_loss_workspace, [sz, sz]),
                                  (L.ar_grad_norm_workspace, []), (L.ar_expert_workspace, [vp, sz, sz, sz, sz, sz]),
+                                 (L.ar_expert_parts_workspace, [sz, sz, sz, sz, i]),
                                  (L.ar_orthogonalize_workspace, [sz, vp, vp, vp, i])):
                     fn.argtypes, fn.restype = args, sz
                 _lib = L

@@ -220,6 +220,14 @@ struct Store {
   }
 };
 
+// Of a tile's slices those of one of `parts` parts.
+__device__ __forceinline__ void cut(Tile& w, int part, int parts) {
+  const int begin = (int)((long long)w.blocks * part / parts), end = (int)((long long)w.blocks * (part + 1) / parts);
+  if (end < w.blocks) w.last = mma::kDepth;
+  w.k += begin * mma::kDepth;
+  w.blocks = end - begin;
+}
+
 struct ForwardParams {
   CUtensorMap weights, x, x_few, y_map;  // x_few: boxes of 32 rows
   mma::Kind w_kind;
@@ -228,6 +236,8 @@ struct ForwardParams {
   void* y;
   long long y_stride;
   bool vectors, zero_rest;
+  int splits;              // parts of the sums, fp32, each with results of its own
+  long long split_stride;
 };
 
 // The experts' weights are read once for every 128 CG rows of theirs, x once for every 128 CG outputs, both
@@ -265,8 +275,18 @@ struct Forward {
   }
   static constexpr int kRowsOfTile = mma::kRows * CG;
   static __device__ __forceinline__ bool tile(const Params& p, const Local& l, int t, Tile& w) {
-    const int E = p.offsets.experts;
-    if (t >= l.r.first[E + 2]) return false;
+    const int E = p.offsets.experts, total = l.r.first[E + 2];
+    int part = 0;
+    if constexpr (FP32) {
+      if (p.splits > 1 && t >= total) {
+        if (total == 0) return false;
+        part = t / total;
+        if (part >= p.splits) return false;
+        t -= part * total;
+      }
+      w.shape = part;
+    }
+    if (t >= total) return false;
     const int e = find(l.r.first, E + 2, t), j = t - l.r.first[e];
     const int begin = e < E ? l.r.start[e] : e == E ? 0 : l.r.start[E];
     const int end = e < E ? l.r.start[e + 1] : e == E ? l.r.start[0] : (int)p.offsets.rows;
@@ -280,6 +300,8 @@ struct Forward {
     w.k = 0;
     w.blocks = e < E ? (p.in + mma::kDepth - 1) / mma::kDepth : 0;
     w.last = mma::kDepth;
+    if constexpr (FP32)
+      if (p.splits > 1) cut(w, part, p.splits);
     // the tiles before may have taken all rows (rounding up to whole units)
     const int left = end - w.b_row;
     w.columns = left < width ? max(kUnit, (left + kUnit - 1) / kUnit * kUnit) : width;
@@ -294,7 +316,8 @@ struct Forward {
   struct Epilogue : Store {
     __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, mma::Staging& staging,
                                         const float*)
-        : Store{static_cast<uint8_t*>(p.y) + (w.b_row * p.y_stride + row) * (FP32 ? 4 : 2), p.y_stride, p.out - row,
+        : Store{static_cast<uint8_t*>(p.y) + (w.b_row * p.y_stride + row) * (FP32 ? 4 : 2) +
+                    (FP32 ? w.shape * p.split_stride * 4 : 0), p.y_stride, p.out - row,
                 min(w.columns, w.end - w.b_row), FP32, false, p.vectors, &p.y_map, row, w.b_row, 0, staging} {}
   };
 };
@@ -307,6 +330,8 @@ struct GradientParams {
   void* dw;                // dW_e[j, i] at e * e_stride + j * j_stride + i
   long long e_stride, j_stride;
   bool add, vectors;
+  int splits;              // as above
+  long long split_stride;
 };
 
 // Sums over an expert's rows, which are k here: of both operands the outer side, so a slice is whole rows of
@@ -329,6 +354,16 @@ struct WeightGradient {
   }
   static __device__ __forceinline__ bool tile(const Params& p, const Local& l, int t, Tile& w) {
     const int fi = (p.ni + kRowsOfTile - 1) / kRowsOfTile, fj = (p.nj + kWide - 1) / kWide;
+    int part = 0;
+    if constexpr (FP32) {
+      const long long total = (long long)fi * fj * p.offsets.experts;
+      if (p.splits > 1 && t >= total) {
+        part = (int)(t / total);
+        if (part >= p.splits) return false;
+        t -= (int)(part * total);
+      }
+      w.shape = part;
+    }
     const int e = t / (fi * fj), rest = t % (fi * fj);
     if (e >= p.offsets.experts) return false;
     const int begin = l.r.start[e], n = l.r.start[e + 1] - begin;
@@ -340,6 +375,8 @@ struct WeightGradient {
     w.k = begin;
     w.blocks = (n + mma::kDepth - 1) / mma::kDepth;
     w.last = n - (w.blocks - 1) * mma::kDepth;
+    if constexpr (FP32)
+      if (p.splits > 1) cut(w, part, p.splits);
     w.columns = min(kWide, (p.nj - w.b_row + kUnit - 1) / kUnit * kUnit);
     w.a_kind = p.a_kind;
     w.b_kind = p.b_kind;
@@ -350,7 +387,8 @@ struct WeightGradient {
   struct Epilogue : Store {
     __device__ __forceinline__ Epilogue(const Params& p, const Local&, const Tile& w, int row, int, mma::Staging& staging,
                                         const float*)
-        : Store{static_cast<uint8_t*>(p.dw) + (w.end * p.e_stride + w.b_row * p.j_stride + row) * (FP32 ? 4 : 2),
+        : Store{static_cast<uint8_t*>(p.dw) + (w.end * p.e_stride + w.b_row * p.j_stride + row) * (FP32 ? 4 : 2) +
+                    (FP32 ? w.shape * p.split_stride * 4 : 0),
                 p.j_stride, p.add && w.blocks == 0 ? 0 : p.ni - row, min(w.columns, p.nj - w.b_row), FP32, p.add,
                 p.vectors, &p.dw_map, row, w.b_row, w.end, staging} {}
   };
@@ -358,27 +396,114 @@ struct WeightGradient {
 
 // ------------------------------------------------------------------ operands that TMA cannot read
 
-// nz x ny rows of nx bf16 each, at any alignment and strides, into rows of `pitch`
-// elements one behind the other.  A pass over memory more, by single elements, as any alignment has to do: 1000 rows of
-// 1001 by 7 experts' weights of 1431 x 1001 take 26 us with it in a captured graph, of 1008 by 1432 x 1008 without it 15.
-__global__ void __launch_bounds__(256) pack_kernel(const uint16_t* from, long long nx, long long ny, long long rows,
-                                                   long long y_stride, long long z_stride, uint16_t* to,
-                                                   long long pitch) {
+// nz x ny rows of nx bf16 each, at any alignment and strides, into rows of whole slots of eight elements one behind the
+// other; of the weights only experts that may have rows.  Bound by HBM, a pass over the operand more: 57 matrices of
+// 240 x 5549 are laid out and multiplied with 2000 rows in 91 us (by single elements and 64-bit divisions 99), with 30
+// rows, which half of the experts have, in 58 (85).  A slot takes two aligned loads, the second of which is the next
+// thread's first, and is shifted in registers.  More slots of a thread at once are slower (16336 x 163: 14 us of
+// the call, one 12.6).
+struct PackParams {
+  const uint16_t* from;
+  uint16_t* to;
+  unsigned int nx, ny, slots;   // slots: of a row
+  long long total;              // slots in all
+  long long y_stride, z_stride;
+  Offsets offsets;              // experts 0: not the weights
+};
+constexpr int kPackThreads = 256;
+
+template <class I>  // of slots: 32 bits where they fit
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constant__ PackParams p) {
+  __shared__ uint32_t has_rows[(kMaxExperts + 31) / 32];
   pdl_enter();
-  const long long slots = pitch / 8;
-  for (long long v = blockIdx.x * 256ll + threadIdx.x; v < rows * slots; v += gridDim.x * 256ll) {
-    const long long r = v / slots, x = v % slots * 8;
-    const uint16_t* p = from + r / ny * z_stride + r % ny * y_stride + x;
-    uint16_t e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = x + i < nx ? p[i] : 0;
-    uint4 o;
-    o.x = e[0] | (uint32_t)e[1] << 16;
-    o.y = e[2] | (uint32_t)e[3] << 16;
-    o.z = e[4] | (uint32_t)e[5] << 16;
-    o.w = e[6] | (uint32_t)e[7] << 16;
-    *reinterpret_cast<uint4*>(to + r * pitch + x) = o;
+  const bool some = p.offsets.experts > 0;
+  if (some) {
+    for (int e = threadIdx.x; e - (int)(threadIdx.x & 31) < p.offsets.experts; e += kPackThreads) {
+      const bool has = e < p.offsets.experts && p.offsets.get(e + 1) > p.offsets.get(e);
+      const uint32_t bits = __ballot_sync(~0u, has);
+      if ((threadIdx.x & 31) == 0) has_rows[e >> 5] = bits;
+    }
+    __syncthreads();
   }
+  const I total = (I)p.total, step = (I)gridDim.x * kPackThreads;
+  for (I v = (I)blockIdx.x * kPackThreads + threadIdx.x; v < total; v += step) {
+    const I row = v / p.slots;
+    const unsigned int x = (unsigned int)(v - row * p.slots) * 8, z = (unsigned int)(row / p.ny);
+    if (some && !(has_rows[z >> 5] >> (z & 31) & 1)) continue;
+    const uint16_t* from = p.from + z * p.z_stride + (long long)(row - (I)z * p.ny) * p.y_stride + x;
+    const int left = (int)(p.nx - x);                      // of the row
+    const int before = (int)((uintptr_t)from & 15) >> 1;   // elements in front of the slot in its first 16 bytes
+    const uint4* aligned = reinterpret_cast<const uint4*>(from - before);
+    const uint4 lo = __ldg(aligned);
+    uint4 hi = make_uint4(0, 0, 0, 0);
+    if (before && before + left > 8) hi = __ldg(aligned + 1);  // (it has elements of the row)
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int j = 0; j < 6; ++j) w[j] = before & 4 ? w[j + 2] : w[j];
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = before & 2 ? w[j + 1] : w[j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (before & 1) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+      if (left < 8) w[j] = 2 * j >= left ? 0 : 2 * j + 1 >= left ? w[j] & 0xffff : w[j];  // zeros behind the row's end
+    }
+    reinterpret_cast<uint4*>(p.to)[v] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ------------------------------------------------------------------ sums in parts
+
+// Few tiles of long sums leave multiprocessors idle: their slices are split into parts, each a tile of its own with
+// fp32 results in the workspace, and this adds them up, in their order.  Bound by a launch, the parts are in L2 mostly.
+// 5 rows of 4 experts, 8192 -> 1024: 31.8 us whole, 14.4 in parts; dx and dW of 16336 rows of 2 experts, 163 -> 264: 63.5,
+// 28.3; dx and dW of 1355 rows of 19, 93 -> 7512: 78, 50.
+struct JoinParams {
+  const float* parts;
+  long long split_stride;
+  int splits;
+  unsigned int count, cols, per;   // values, of a row, rows of a matrix
+  void* to;
+  long long z_stride, y_stride;
+  bool fp32, add, zero_rest;
+  Offsets offsets;                 // experts 0: all rows are somebody's
+};
+
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinParams p) {
+  __shared__ int most;
+  pdl_enter();
+  int begin = 0, end = 0;
+  if (p.offsets.experts) {
+    if (threadIdx.x == 0) most = 0;
+    __syncthreads();
+    int last = 0;
+    for (int i = threadIdx.x; i <= p.offsets.experts; i += 256) last = max(last, p.offsets.get(i));
+    atomicMax(&most, last);
+    __syncthreads();
+    begin = p.offsets.get(0), end = most;
+  }
+  for (unsigned int i = blockIdx.x * 256 + threadIdx.x; i < p.count; i += gridDim.x * 256) {
+    const unsigned int row = i / p.cols, z = row / p.per;
+    const long long at = z * p.z_stride + (row - z * p.per) * p.y_stride + (i - row * p.cols);
+    float sum = 0.0f;
+    if (!p.offsets.experts || ((int)row >= begin && (int)row < end)) {
+#pragma unroll 4
+      for (int s = 0; s < p.splits; ++s) sum += __ldcg(p.parts + s * p.split_stride + i);
+    } else if (!p.zero_rest) {
+      continue;
+    }
+    if (p.fp32) {
+      float* y = static_cast<float*>(p.to) + at;
+      *y = p.add ? *y + sum : sum;
+    } else {
+      uint16_t* y = static_cast<uint16_t*>(p.to) + at;
+      *y = bf16_bits(p.add ? bf16_lo(*y) + sum : sum);
+    }
+  }
+}
+
+cudaError_t join(const JoinParams& p, int sms, cudaStream_t stream) {
+  const unsigned int blocks = std::min<unsigned int>((p.count + 255) / 256, (unsigned int)sms * 8);
+  return launch_kernel(join_kernel, dim3(blocks), dim3(256), 0, stream, true, p);
 }
 
 constexpr size_t whole(size_t n) { return (n + 7) / 8 * 8; }
@@ -389,18 +514,20 @@ bool direct(const ExpertMatrix& m) {
 }
 
 // The map of an operand; where it cannot be read as it is, of a copy in the workspace.
-cudaError_t operand(ExpertMatrix m, bool depth, uint8_t*& workspace, int sms, cudaStream_t stream, CUtensorMap* map,
-                    mma::Kind* kind, CUtensorMap* few = nullptr) {
+cudaError_t operand(ExpertMatrix m, bool depth, uint8_t*& workspace, const Offsets& offsets, int sms,
+                    cudaStream_t stream, CUtensorMap* map, mma::Kind* kind, CUtensorMap* few = nullptr) {
   if (!m.nx || !m.ny || !m.nz) return cudaSuccess;  // no tile reads it
   if (!direct(m)) {
     const size_t pitch = whole(m.nx), rows = m.ny * m.nz;
     uint16_t* to = reinterpret_cast<uint16_t*>(workspace);
     workspace += expert_matrix_workspace(m);
-    const size_t blocks = std::min<size_t>((rows * (pitch / 8) + 255) / 256, (size_t)sms * 8);
-    const cudaError_t e =
-        launch_kernel(pack_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, true, static_cast<const uint16_t*>(m.at),
-                      (long long)m.nx, (long long)m.ny, (long long)rows, (long long)m.y_stride, (long long)m.z_stride, to,
-                      (long long)pitch);
+    PackParams p = {static_cast<const uint16_t*>(m.at), to, (unsigned)m.nx, (unsigned)m.ny, (unsigned)(pitch / 8),
+                    (long long)(rows * (pitch / 8)), (long long)m.y_stride, (long long)m.z_stride, offsets};
+    if (m.nz != (size_t)offsets.experts) p.offsets.experts = 0;
+    const long long blocks = std::min<long long>((p.total + kPackThreads - 1) / kPackThreads, sms * 8);
+    const bool few = p.total + blocks * kPackThreads < 1ll << 32;
+    const cudaError_t e = launch_kernel(few ? pack_kernel<unsigned int> : pack_kernel<unsigned long long>,
+                                        dim3((unsigned)blocks), dim3(kPackThreads), 0, stream, true, p);
     if (e != cudaSuccess) return e;
     m = ExpertMatrix{to, m.nx, m.ny, m.nz, pitch, m.ny * pitch};
   }
@@ -414,19 +541,20 @@ bool vectors(const void* at, size_t stride, size_t matrix_stride = 0) {
   return ((uintptr_t)at & 15) == 0 && stride % 8 == 0 && matrix_stride % 8 == 0;
 }
 
+// splits > 1: the sums in so many parts, joined from the workspace behind the operands'.
 template <int CG, bool FP32>
-cudaError_t forward(const ExpertsCall& c) {
+cudaError_t forward(const ExpertsCall& c, int splits = 1) {
   using Policy = Forward<CG, FP32>;
   ForwardParams p = {};
+  p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   mma::Kind kind;
-  cudaError_t e = operand(c.w, c.w_in_contiguous, ws, c.sms, c.stream, &p.weights, &p.w_kind);
-  if (e == cudaSuccess) e = operand(c.x, true, ws, c.sms, c.stream, &p.x, &kind, &p.x_few);
+  cudaError_t e = operand(c.w, c.w_in_contiguous, ws, p.offsets, c.sms, c.stream, &p.weights, &p.w_kind);
+  if (e == cudaSuccess) e = operand(c.x, true, ws, p.offsets, c.sms, c.stream, &p.x, &kind, &p.x_few);
   p.vectors = !FP32 && vectors(c.y, c.y_stride);
   if (e == cudaSuccess && p.vectors)
     e = mma::make_store_map(&p.y_map, c.y, c.out, c.rows, 1, c.y_stride, 0);
   if (e != cudaSuccess) return e;
-  p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
   p.out = (int)c.out;
   p.in = (int)c.in;
   p.y = c.y;
@@ -434,20 +562,29 @@ cudaError_t forward(const ExpertsCall& c) {
   p.zero_rest = c.zero_rest;
   const long long f = ((long long)c.out + Policy::kRowsOfTile - 1) / Policy::kRowsOfTile;
   const long long groups = (long long)std::min<size_t>(c.experts, c.rows) + 2 + (long long)(c.rows / Policy::kWide);
-  return mma::launch_product<CG, Policy>(p, f * groups, c.sms, c.stream);
+  p.splits = splits;
+  if (splits > 1) {
+    p.y = ws, p.y_stride = p.out, p.zero_rest = false;
+    p.split_stride = (long long)c.rows * p.out;
+  }
+  e = mma::launch_product<CG, Policy>(p, f * groups * splits, c.sms, c.stream);
+  if (e != cudaSuccess || splits == 1) return e;
+  return join(JoinParams{static_cast<const float*>(p.y), p.split_stride, splits, (unsigned)p.split_stride, (unsigned)p.out,
+                         (unsigned)c.rows, c.y, 0, (long long)c.y_stride, c.dtype == AR_FLOAT32, false, c.zero_rest,
+                         p.offsets}, c.sms, c.stream);
 }
 
 template <int CG, bool FP32>
-cudaError_t weight_gradient(const ExpertsCall& c) {
+cudaError_t weight_gradient(const ExpertsCall& c, int splits = 1) {
   using Policy = WeightGradient<CG, FP32>;
   GradientParams p = {};
+  p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
   uint8_t* ws = static_cast<uint8_t*>(c.workspace);
   // the contiguous side of dW is the lanes'
   const bool lanes_in = c.w_in_contiguous;
-  cudaError_t e = operand(lanes_in ? c.x : c.dy, false, ws, c.sms, c.stream, &p.a, &p.a_kind);
+  cudaError_t e = operand(lanes_in ? c.x : c.dy, false, ws, p.offsets, c.sms, c.stream, &p.a, &p.a_kind);
   if (e == cudaSuccess)
-    e = operand(lanes_in ? c.dy : c.x, false, ws, c.sms, c.stream, &p.b, &p.b_kind);
-  p.offsets = Offsets{c.offsets, c.offset_bytes, (int)c.experts, (long long)c.rows};
+    e = operand(lanes_in ? c.dy : c.x, false, ws, p.offsets, c.sms, c.stream, &p.b, &p.b_kind);
   p.ni = (int)(lanes_in ? c.in : c.out);
   p.nj = (int)(lanes_in ? c.out : c.in);
   p.dw = c.y;
@@ -460,7 +597,17 @@ cudaError_t weight_gradient(const ExpertsCall& c) {
   if (e != cudaSuccess) return e;
   const auto over = [](long long n, long long d) { return (n + d - 1) / d; };
   const long long tiles = over(p.ni, Policy::kRowsOfTile) * over(p.nj, Policy::kWide) * (long long)c.experts;
-  return mma::launch_product<CG, Policy>(p, tiles, c.sms, c.stream);
+  p.splits = splits;
+  if (splits > 1) {
+    p.dw = ws, p.add = false;
+    p.j_stride = p.ni, p.e_stride = (long long)p.nj * p.ni;
+    p.split_stride = p.e_stride * (long long)c.experts;
+  }
+  e = mma::launch_product<CG, Policy>(p, tiles * splits, c.sms, c.stream);
+  if (e != cudaSuccess || splits == 1) return e;
+  return join(JoinParams{static_cast<const float*>(p.dw), p.split_stride, splits, (unsigned)p.split_stride, (unsigned)p.ni,
+                         (unsigned)p.nj, c.y, (long long)c.w.z_stride, (long long)c.w.y_stride, c.dtype == AR_FLOAT32,
+                         c.accumulate, false, Offsets{}}, c.sms, c.stream);
 }
 
 }  // namespace
@@ -469,21 +616,57 @@ size_t expert_matrix_workspace(const ExpertMatrix& m) {
   return direct(m) ? 0 : (whole(m.nx) * m.ny * m.nz * 2 + 127) / 128 * 128;
 }
 
-cudaError_t launch_expert_product(const ExpertsCall& c) {
-  // the offsets are on the device: as if all experts had the same number of rows
+// What the choice between pairs, blocks alone and sums in parts goes by.  The offsets are on the device: as if all experts
+// had the same number of rows.
+struct Work {
+  double in_pairs, alone, slices, values;   // tiles, 64-deep slices of a tile, results
+};
+static Work product_work(const ExpertsCall& c) {
   const double some = (double)std::max<size_t>(1, std::min(c.experts, c.rows));
   const auto tiles = [&](double side) { return std::ceil(c.out / side) * some * std::ceil(c.rows / some / side); };
-  const bool pairs = mma::better_in_pairs(tiles(256), tiles(128), std::ceil(c.in / 64.0), c.sms);
-  if (c.dtype == AR_FLOAT32) return pairs ? forward<2, true>(c) : forward<1, true>(c);
-  return pairs ? forward<2, false>(c) : forward<1, false>(c);
+  return Work{tiles(256), tiles(128), std::ceil(c.in / 64.0), (double)c.rows * (double)c.out};
+}
+static Work gradient_work(const ExpertsCall& c) {
+  const auto tiles = [&](double side) { return std::ceil(c.out / side) * std::ceil(c.in / side) * (double)c.experts; };
+  return Work{tiles(256), tiles(128), std::ceil((double)c.rows / std::max<size_t>(1, c.experts) / 64.0),
+              (double)c.experts * (double)c.out * (double)c.in};
+}
+static bool pairs(const Work& w, int sms) { return mma::better_in_pairs(w.in_pairs, w.alone, w.slices, sms); }
+
+// Into how many parts the sums are split: where the blocks' tiles take less time so, with a launch that adds the
+// parts up (about 3 us, and what it reads and writes, from L2 mostly).
+static int best_splits(const Work& w, int sms) {
+  const auto time = [&](int n) {
+    return std::ceil(w.alone * n / sms) * (0.20 * std::ceil(w.slices / n) + 2.0) +
+           (n > 1 ? 3.0 + w.values * 4 * (2 * n + 1) / 4e6 : 0.0);
+  };
+  if (w.alone > sms || w.values > 1 << 26) return 1;
+  int best = 1;
+  for (int n : {2, 3, 4, 6, 8, 12, 16})
+    if (time(n) < time(best)) best = n;
+  return time(best) < 0.9 * time(1) ? best : 1;
+}
+static size_t parts_bytes(const Work& w, int splits) { return splits > 1 ? (size_t)w.values * 4 * splits : 0; }
+
+size_t expert_parts_workspace(const ExpertsCall& c, bool of_weights) {
+  const Work w = of_weights ? gradient_work(c) : product_work(c);
+  return parts_bytes(w, best_splits(w, c.sms));
+}
+
+cudaError_t launch_expert_product(const ExpertsCall& c) {
+  const Work w = product_work(c);
+  const int splits = best_splits(w, c.sms);
+  if (splits > 1 && c.spare >= parts_bytes(w, splits)) return forward<1, true>(c, splits);
+  if (c.dtype == AR_FLOAT32) return pairs(w, c.sms) ? forward<2, true>(c) : forward<1, true>(c);
+  return pairs(w, c.sms) ? forward<2, false>(c) : forward<1, false>(c);
 }
 
 cudaError_t launch_expert_weight_gradient(const ExpertsCall& c) {
-  const auto tiles = [&](double side) { return std::ceil(c.out / side) * std::ceil(c.in / side) * c.experts; };
-  const bool pairs =
-      mma::better_in_pairs(tiles(256), tiles(128), std::ceil((double)c.rows / c.experts / 64.0), c.sms);
-  if (c.dtype == AR_FLOAT32) return pairs ? weight_gradient<2, true>(c) : weight_gradient<1, true>(c);
-  return pairs ? weight_gradient<2, false>(c) : weight_gradient<1, false>(c);
+  const Work w = gradient_work(c);
+  const int splits = best_splits(w, c.sms);
+  if (splits > 1 && c.spare >= parts_bytes(w, splits)) return weight_gradient<1, true>(c, splits);
+  if (c.dtype == AR_FLOAT32) return pairs(w, c.sms) ? weight_gradient<2, true>(c) : weight_gradient<1, true>(c);
+  return pairs(w, c.sms) ? weight_gradient<2, false>(c) : weight_gradient<1, false>(c);
 }
 
 }  // namespace ar

@@ -278,6 +278,14 @@ size_t ar_expert_workspace(const void* at, size_t cols, size_t rows, size_t coun
   return ar::expert_matrix_workspace(ar::ExpertMatrix{at, cols, rows, count, row_stride, matrix_stride});
 }
 
+size_t ar_expert_parts_workspace(size_t rows, size_t experts, size_t out, size_t in, int of_weights) {
+  if (rows > AR_MAX_TOKENS || experts > AR_MAX_EXPERTS || in > AR_MAX_FEATURES || out > AR_MAX_FEATURES) return SIZE_MAX;
+  ar::ExpertsCall c = {};
+  c.rows = rows, c.experts = experts, c.in = in, c.out = out;
+  if (!rows || !experts || !in || !out || !multiprocessors(&c.sms)) return 0;
+  return ar::expert_parts_workspace(c, of_weights != 0);
+}
+
 ar_status_t ar_expert_product(const void* x, size_t rows, size_t x_stride, const void* weights, size_t experts,
                               size_t out, size_t in, size_t expert_stride, size_t out_stride, size_t in_stride,
                               const void* offsets, int offset_bytes, void* y, size_t y_stride, ar_dtype_t y_dtype,
@@ -301,6 +309,7 @@ ar_status_t ar_expert_product(const void* x, size_t rows, size_t x_stride, const
   if (in && experts && overlap(weights, span_of(c.w, 2), y, there)) return AR_ERR_INVALID_ARG;
   const size_t need = ar::expert_matrix_workspace(c.x) + ar::expert_matrix_workspace(c.w);
   if (workspace_bytes < need || (need && !aligned(workspace, 16))) return AR_ERR_INVALID_ARG;
+  c.spare = aligned(workspace, 16) ? workspace_bytes - need : 0;
   if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
   Range range("ar_expert_product");
   return finish(ar::launch_expert_product(c), "expert_product", rows, out);
@@ -330,6 +339,7 @@ ar_status_t ar_expert_weight_gradient(const void* dy, size_t dy_stride, const vo
     return AR_ERR_INVALID_ARG;
   const size_t need = ar::expert_matrix_workspace(c.x) + ar::expert_matrix_workspace(c.dy);
   if (workspace_bytes < need || (need && !aligned(workspace, 16))) return AR_ERR_INVALID_ARG;
+  c.spare = aligned(workspace, 16) ? workspace_bytes - need : 0;
   if (!multiprocessors(&c.sms)) return AR_ERR_CUDA;
   Range range("ar_expert_weight_gradient");
   return finish(ar::launch_expert_weight_gradient(c), "expert_weight_gradient", out, in);

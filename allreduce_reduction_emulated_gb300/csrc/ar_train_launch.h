@@ -90,6 +90,7 @@ struct ExpertsCall {
   int dtype;                       // of y: fp32 or bf16
   bool zero_rest, accumulate;
   void* workspace;
+  size_t spare;                    // bytes of it behind the operands'
   int sms;
   cudaStream_t stream;
 };
@@ -117,6 +118,7 @@ bool orthogonal_bounded(const OrthogonalCall& c);
 cudaError_t launch_orthogonal(const OrthogonalCall& c);
 
 size_t expert_matrix_workspace(const ExpertMatrix& m);
+size_t expert_parts_workspace(const ExpertsCall& c, bool of_weights);  // of c its sizes and sms
 cudaError_t launch_expert_product(const ExpertsCall& c);
 cudaError_t launch_expert_weight_gradient(const ExpertsCall& c);
 

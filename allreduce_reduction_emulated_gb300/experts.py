@@ -35,6 +35,9 @@ _DTYPES = {torch.float32: AR_FLOAT32, torch.bfloat16: AR_BFLOAT16}
 # eighth of bfloat16's half step.  Longer sums of a bfloat16 result are made in float32, which adds them up in runs.
 _LONGEST = 1 << 18
 
+# Shorter sums, or more tiles of 128 x 128, are never split into parts: no call to ask.
+_LONG, _FEW = 1024, 256
+
 
 def _rows(what: str, name: str, x, device: int | None = None, rows: int | None = None, dtypes=(torch.bfloat16,)):
     """(device, rows, columns, row stride) of a matrix that the kernels can walk."""
@@ -107,15 +110,13 @@ def _shared(a, b) -> bool:
     return True
 
 
-def _space(lib, device, *operands) -> tuple:
+def _space(lib, device, parts, *operands) -> tuple:
     """(tensor or None, address, bytes) of the workspace of (address, columns, rows, count, row stride, matrix
-    stride) operands; none where all of them are aligned, which needs no call to know."""
+    stride) operands; none where all of them are aligned, which needs no call to know.  parts: bytes more."""
     bits = 0
     for at, _, _, _, row, matrix in operands:
         bits |= at | row << 1 | matrix << 1
-    if not bits & 15:
-        return None, None, 0
-    n = sum(lib.ar_expert_workspace(*o) for o in operands)
+    n = parts + sum(lib.ar_expert_workspace(*o) for o in operands) if bits & 15 else parts
     if not n:
         return None, None, 0
     t = torch.empty(n, dtype=torch.uint8, device=device)
@@ -128,7 +129,10 @@ def _product(what, lib, x, at_x, w, at_w, offsets, off_size, out, zero_rest, han
     E, N, _, e, n, k = at_w
     x_at, w_at = x.data_ptr(), w.data_ptr()
     by_weights = (w_at, K, N, E, n, e) if k == 1 else (w_at, N, K, E, k, e)
-    space, at, bytes_ = _space(lib, x.device, (x_at, K, rows, 1, x_stride, 0), by_weights)
+    parts = 0
+    if K >= _LONG and -(-N // 128) * (min(E, rows) + rows // 128) <= _FEW:
+        parts = lib.ar_expert_parts_workspace(rows, E, N, K, 0)
+    space, at, bytes_ = _space(lib, x.device, parts, (x_at, K, rows, 1, x_stride, 0), by_weights)
     _check(lib.ar_expert_product(x_at, rows, x_stride, w_at, E, N, K, e, n, k, offsets, off_size, out.data_ptr(),
                                  out.stride(0) if rows > 1 else N, _DTYPES[out.dtype], zero_rest, at, bytes_, handle),
            what)
@@ -258,7 +262,11 @@ def _both(what, dy, at_y, x, at_x, weights, at_w, off, size, dx, dw, at_dw, dw_d
             if accumulate:
                 to.copy_(dw)
         dy_at, x_at = dy.data_ptr(), x.data_ptr()
-        space, at, bytes_ = _space(lib, x.device, (dy_at, N, rows, 1, dy_stride, 0), (x_at, K, rows, 1, x_stride, 0))
+        parts = 0
+        if rows >= _LONG * E and -(-N // 128) * -(-K // 128) * E <= _FEW:
+            parts = lib.ar_expert_parts_workspace(rows, E, N, K, 1)
+        space, at, bytes_ = _space(lib, x.device, parts, (dy_at, N, rows, 1, dy_stride, 0),
+                                   (x_at, K, rows, 1, x_stride, 0))
         _check(lib.ar_expert_weight_gradient(dy_at, dy_stride, x_at, x_stride, rows, E, N, K, off, size, to.data_ptr(),
                                              *at_dw[3:], _DTYPES[to.dtype], accumulate, at, bytes_, handle), what)
         if to is not dw:

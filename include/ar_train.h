@@ -187,7 +187,9 @@ ar_status_t ar_clip_grads(size_t ntensors, const void* const* grads, void* const
  *   workspace 16-byte aligned, at least the sum of ar_expert_workspace() of x and
  *             of weights bytes: operands that are not 16-byte aligned, or whose
  *             strides are not whole 16 bytes, are laid out there first.  NULL when
- *             that is 0
+ *             that is 0.  With ar_expert_parts_workspace() bytes more, where that is not 0, long
+ *             sums that make few tiles are split into parts, which takes less time; they are
+ *             added up in a fixed order, but another one than without
  * The same call gives the gradient of x: dx = ar_expert_product(dy, weights with
  * `in` and `out` and their strides exchanged).  Sums are fp32, rounded once.
  * (The tensor cores cut what an addition loses: 960 products lose up to 2e-6 of their sum.  fp32 results add
@@ -207,6 +209,9 @@ ar_status_t ar_clip_grads(size_t ntensors, const void* const* grads, void* const
  * bf16 elements, with the rows and the matrices at these strides (elements). */
 size_t ar_expert_workspace(const void* at, size_t cols, size_t rows, size_t count, size_t row_stride,
                            size_t matrix_stride);
+/* What the products of these sizes can use besides; 0 where nothing is won.  of_weights: of the gradient of the
+ * weights.  Asks the current device for its number of multiprocessors. */
+size_t ar_expert_parts_workspace(size_t rows, size_t experts, size_t out, size_t in, int of_weights);
 ar_status_t ar_expert_product(const void* x, size_t rows, size_t x_stride, const void* weights, size_t experts,
                               size_t out, size_t in, size_t expert_stride, size_t out_stride, size_t in_stride,
                               const void* offsets, int offset_bytes, void* y, size_t y_stride, ar_dtype_t y_dtype,
@@ -218,7 +223,7 @@ ar_status_t ar_expert_product(const void* x, size_t rows, size_t x_stride, const
  *   dy        rows by `out`, x rows by `in`, AR_BFLOAT16
  *   dw        dw_dtype (AR_FLOAT32 or AR_BFLOAT16), laid out by its three strides as
  *             the weights are; no part of dy or x
- *   workspace the sum of ar_expert_workspace() of dy and of x
+ *   workspace the sum of ar_expert_workspace() of dy and of x, or more, as above
  * Everything else as for ar_expert_product.
  */
 ar_status_t ar_expert_weight_gradient(const void* dy, size_t dy_stride, const void* x, size_t x_stride, size_t rows,

@@ -61,6 +61,14 @@ def test_expert_workspace(lib):
     assert f(P, 1 << 25, 1, 1, 0, 0) == ctypes.c_size_t(-1).value
 
 
+def test_expert_parts_workspace(lib):
+    f = lib.ar_expert_parts_workspace
+    for sizes in ((0, 1, 8, 8), (8, 0, 8, 8), (8, 1, 0, 8), (8, 1, 8, 0)):
+        assert f(*sizes, 0) == 0 and f(*sizes, 1) == 0
+    for sizes in (((1 << 28) + 1, 1, 8, 8), (8, 1025, 8, 8), (8, 1, (1 << 24) + 1, 8), (8, 1, 8, (1 << 24) + 1)):
+        assert f(*sizes, 1) == ctypes.c_size_t(-1).value
+
+
 def test_orthogonalize_arguments(lib):
     def arrays(kind, values):
         return None if values is None else (kind * len(values))(*values)
