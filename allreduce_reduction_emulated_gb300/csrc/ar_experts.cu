@@ -241,9 +241,10 @@ struct ForwardParams {
 };
 
 // The experts' weights are read once for every 128 CG rows of theirs, x once for every 128 CG outputs, both
-// mostly from L2: what is on the GPU at once are neighbours.  4096 rows of 8 uneven experts, 2048 -> 8192: 106 us (1.3
-// PFLOP/s; what is left of the last wave costs the rest), 16384 rows of 64, 2048 -> 1024: 74 us (5.0 TB/s).
-// An expert's rows are cut into tiles of one width, rather than whole ones and a rest: the last wave is as wide as the first.
+// mostly from L2: what is on the GPU at once are neighbours.  4096 rows of 8 uneven experts, 2048 -> 8192: 104 us (1.3
+// PFLOP/s; what is left of the last wave costs the rest), 16384 rows of 64, 2048 -> 1024: 75 us (4.9 TB/s).
+// An expert's rows are cut into tiles of one width, rather than whole ones and a rest: the last wave is as wide as the
+// first.
 //
 // FP32: of the results.  The tensor cores cut what an addition to the accumulators loses: over 1000 k a sum
 // is off by 1e-6 of itself, over 16000 by 2e-5.  So 960 k are the longest run that they add up; a later run is
@@ -337,7 +338,7 @@ struct GradientParams {
 // Sums over an expert's rows, which are k here: of both operands the outer side, so a slice is whole rows of
 // boxes and the last one's rest is cleared in shared memory (warp 3; by the loading warp 64 rows of 8 experts, 2048 ->
 // 2048, took 47 us, now 38).  Bound by the matrix instructions where experts have many rows (dx and dW of 16384 rows of
-// 16 experts, 2048 -> 8192: 783 us, 1.40 PFLOP/s), by storing dW where they have few (4096 rows of 8, 8192 -> 2048, fp32:
+// 16 experts, 2048 -> 8192: 767 us, 1.43 PFLOP/s), by storing dW where they have few (4096 rows of 8, 8192 -> 2048, fp32:
 // 155 us for 537 MB and 137 GFLOP).
 template <int CG, bool FP32>
 struct WeightGradient {

@@ -255,7 +255,7 @@ __device__ __forceinline__ float rounding_rest(float exact, float rounded) {
 
 // Up to 128 by 512 a matrix stays in one block's shared memory through all steps, and so do A and B: what
 // a step costs is the matrix instructions' way and three turns through the registers (about 3 us), where the
-// tiles of the launch below go through L2 and wait for one another (14 us).
+// tiles of the launch below go through L2 and wait for one another (10 us).
 //
 // X lies as boxes of 128 rows (the short side) by 64 columns, 128-byte swizzle.  The first product reads
 // it with the columns as k, the third with the rows as k: the tensor cores take the same bytes both ways.
@@ -496,8 +496,8 @@ struct StepsParams {
 // third, then the next step's.  A tile waits until all tiles of its matrix before it are stored, which
 // with several matrices they mostly are: nobody waits for the last tile of a launch, and a step of a small
 // matrix costs three times the way through the chip, not three launches (256 x 256, five steps: 144 us
-// so, 98 in one launch, 74 with tiles of half the width).  16 x 1024 x 2048: 590 us, 2 layers of 101M elements
-// 2670 us, of which 320 are the passes over the gradients: bound by the matrix instructions, at 1.65 PFLOP/s of what is
+// so, 98 in one launch, 74 with tiles of half the width).  16 x 1024 x 2048: 585 us, 2 layers of 101M elements
+// 2590 us, of which 320 are the passes over the gradients: bound by the matrix instructions, at 1.65 PFLOP/s of what is
 // executed.
 template <int CG>
 struct Steps {
@@ -780,7 +780,8 @@ struct Cut {
   int pair, width;
 };
 // A tile's slice and its epilogue, in us: the loads of 16 KiB of A and 8 or 16 of B a block bound a slice but of the
-// whole pair's tile, which the matrix instructions do.
+// whole pair's tile, which the matrix instructions do.  Updates measured with each cut, us: 256 x 256 104, 83, 89, 75;
+// 1024 x 1024 170, 134, 137, 119; 4 x 1024 x 2048 214, 196, 206, 282; 16 of them 468, 609, 624, 1054.
 constexpr Cut kCuts[4] = {{2, 256}, {2, 128}, {1, 128}, {1, 64}};
 constexpr double kSlice[4] = {0.30, 0.17, 0.18, 0.14}, kEnd[4] = {1.5, 0.8, 0.8, 0.4};
 constexpr double kTurn = 3.0;  // of a stage, from its last tile's sums to the next stage's first
@@ -828,8 +829,8 @@ int whole_columns(size_t rows, size_t cols) {
 }
 
 // The small matrices go whole where that is faster.  Alone they nearly always do; beside others, whose tiles
-// leave room for theirs, it is the time of a launch more.  Times in us, measured: 128 x 128 27, 128 x 512
-// 50, in tiles 256 x 256 74.
+// leave room for theirs, it is the time of a launch more.  Times in us, measured,
+// whole and in the best tiles: 128 x 128 27 and 58, 400 of them 60 and 105, 128 x 512 50 and 70, 1000 of 16 x 16 95 and 191.
 bool take_whole(const OrthogonalCall& c) {
   double alone = 0.0;
   Sizes rest[kMaxShapes], all[kMaxShapes];

@@ -251,7 +251,10 @@ ar_status_t ar_expert_weight_gradient(const void* dy, size_t dy_stride, const vo
  *   workspace at least ar_orthogonalize_workspace() bytes, 16-byte aligned; its contents on
  *             entry do not matter
  * Momentum, norms and all sums are fp32; X, A and b A + c A^2 are held between the products in fp16 times
- * powers of two that follow from bounds of the singular values; the result is rounded once to bf16.
+ * powers of two that follow from bounds of the singular values; the result is rounded once to bf16.  So a
+ * direction whose singular value is s of the norm is known to about 3e-4 / (s sqrt(min(rows, cols))) of itself:
+ * next to nothing for a matrix of rank one in the directions that it lacks.  Elements whose squares are below fp32's
+ * range do not count in the norm.
  * A matrix of zeros gives zeros; one whose norm is not finite (a square above the fp32 range makes
  * it infinite) gives NaN.  Empty stacks are left out.  Pointers need element alignment only.
  * The host arrays are read during the call only.  Errors: AR_ERR_INVALID_ARG (NULL or misaligned pointer, enum,
