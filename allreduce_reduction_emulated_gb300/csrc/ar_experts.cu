@@ -632,42 +632,51 @@ static Work gradient_work(const ExpertsCall& c) {
   return Work{tiles(256), tiles(128), std::ceil((double)c.rows / std::max<size_t>(1, c.experts) / 64.0),
               (double)c.experts * (double)c.out * (double)c.in};
 }
-static bool pairs(const Work& w, int sms) { return mma::better_in_pairs(w.in_pairs, w.alone, w.slices, sms); }
-
-// Into how many parts the sums are split: where the blocks' tiles take less time so, with a launch that adds the
-// parts up (about 3 us, and what it reads and writes, from L2 mostly).
-static int best_splits(const Work& w, int sms) {
-  const auto time = [&](int n) {
-    return std::ceil(w.alone * n / sms) * (0.20 * std::ceil(w.slices / n) + 2.0) +
+// Pairs of blocks or blocks alone, and into how many parts the sums are split: where the tiles take less time so, with a
+// launch that adds the parts up (about 3 us, and what it reads and writes, from L2 mostly).  Without a workspace for
+// the parts, whole sums.
+struct Plan {
+  bool pairs;
+  int splits;
+  size_t bytes;
+};
+static Plan whole_sums(const Work& w, int sms) {
+  return Plan{mma::better_in_pairs(w.in_pairs, w.alone, w.slices, sms), 1, 0};
+}
+static Plan plan(const Work& w, int sms) {
+  const auto time = [&](bool pairs, int n) {
+    const double tiles = (pairs ? w.in_pairs : w.alone) * n, at_once = pairs ? sms / 2 : sms;
+    return std::ceil(tiles / at_once) * ((pairs ? 0.27 : 0.20) * std::ceil(w.slices / n) + (pairs ? 3.0 : 2.0)) +
            (n > 1 ? 3.0 + w.values * 4 * (2 * n + 1) / 4e6 : 0.0);
   };
-  if (w.alone > sms || w.values > 1 << 26) return 1;
-  int best = 1;
-  for (int n : {2, 3, 4, 6, 8, 12, 16})
-    if (time(n) < time(best)) best = n;
-  return time(best) < 0.9 * time(1) ? best : 1;
+  Plan best = whole_sums(w, sms);
+  if (w.values > 1 << 26 || sms < 2) return best;
+  double least = 0.9 * time(best.pairs, 1);
+  for (const bool pairs : {false, true})
+    for (int n = 2; n <= 16 && (pairs ? w.in_pairs : w.alone) <= (pairs ? sms / 2 : sms); ++n)
+      if (time(pairs, n) < least) least = time(pairs, n), best = Plan{pairs, n, (size_t)w.values * 4 * n};
+  return best;
 }
-static size_t parts_bytes(const Work& w, int splits) { return splits > 1 ? (size_t)w.values * 4 * splits : 0; }
 
 size_t expert_parts_workspace(const ExpertsCall& c, bool of_weights) {
-  const Work w = of_weights ? gradient_work(c) : product_work(c);
-  return parts_bytes(w, best_splits(w, c.sms));
+  return plan(of_weights ? gradient_work(c) : product_work(c), c.sms).bytes;
 }
 
 cudaError_t launch_expert_product(const ExpertsCall& c) {
   const Work w = product_work(c);
-  const int splits = best_splits(w, c.sms);
-  if (splits > 1 && c.spare >= parts_bytes(w, splits)) return forward<1, true>(c, splits);
-  if (c.dtype == AR_FLOAT32) return pairs(w, c.sms) ? forward<2, true>(c) : forward<1, true>(c);
-  return pairs(w, c.sms) ? forward<2, false>(c) : forward<1, false>(c);
+  Plan to = plan(w, c.sms);
+  if (to.bytes > c.spare) to = whole_sums(w, c.sms);
+  if (c.dtype == AR_FLOAT32 || to.splits > 1) return to.pairs ? forward<2, true>(c, to.splits) : forward<1, true>(c, to.splits);
+  return to.pairs ? forward<2, false>(c) : forward<1, false>(c);
 }
 
 cudaError_t launch_expert_weight_gradient(const ExpertsCall& c) {
   const Work w = gradient_work(c);
-  const int splits = best_splits(w, c.sms);
-  if (splits > 1 && c.spare >= parts_bytes(w, splits)) return weight_gradient<1, true>(c, splits);
-  if (c.dtype == AR_FLOAT32) return pairs(w, c.sms) ? weight_gradient<2, true>(c) : weight_gradient<1, true>(c);
-  return pairs(w, c.sms) ? weight_gradient<2, false>(c) : weight_gradient<1, false>(c);
+  Plan to = plan(w, c.sms);
+  if (to.bytes > c.spare) to = whole_sums(w, c.sms);
+  if (c.dtype == AR_FLOAT32 || to.splits > 1)
+    return to.pairs ? weight_gradient<2, true>(c, to.splits) : weight_gradient<1, true>(c, to.splits);
+  return to.pairs ? weight_gradient<2, false>(c) : weight_gradient<1, false>(c);
 }
 
 }  // namespace ar
