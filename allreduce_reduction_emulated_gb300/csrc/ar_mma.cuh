@@ -400,6 +400,15 @@ struct Boxes {
   }
 };
 
+// Into how many runs, of at most kRun slices, a tile's sums are cut, and the slices of one: all alike, so that an
+// epilogue has as many behind it as the next.  (So many slices a run make exactly so many runs: fewer would take r (r - 1) >=
+// blocks > most (r - 1), so r > most, and then a run has `most`.)
+__device__ __forceinline__ int runs_of(int blocks, int most) { return max(1, (blocks + most - 1) / most); }
+__device__ __forceinline__ int run_length(int blocks, int most) {
+  const int runs = runs_of(blocks, most);
+  return (blocks + runs - 1) / runs;
+}
+
 template <int CG, class Policy>
 constexpr int shared_bytes() {
   return (int)sizeof(SharedOf<Policy>) + (int)sizeof(typename Policy::Local) + 1024;
@@ -522,7 +531,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const uint32_t a_step = depth_step(w.a_kind == kDepthRows), b_step = depth_step(w.b_kind == kDepthRows);
       bool ok = true;
       for (int begin = 0; ok && begin < w.blocks;) {
-        const int end = Policy::kRun ? min(begin + Policy::kRun, w.blocks) : w.blocks;
+        int end = w.blocks;
+        if constexpr (Policy::kRun > 0) end = min(begin + run_length(w.blocks, Policy::kRun), end);
         const uint32_t buffer = n & 1, d = tmem + buffer * (kColumns / 2);
         ok = warp_wait(saddr(&s.drained[buffer]), ((n >> 1) & 1) ^ 1, late);
         ++n;
@@ -603,7 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
       };
       typename Policy::Epilogue out(p, local, w, row, first_column, staging, factors);
-      const int runs = Policy::kRun ? max(1, (w.blocks + Policy::kRun - 1) / Policy::kRun) : 1;
+      int runs = 1;
+      if constexpr (Policy::kRun > 0) runs = runs_of(w.blocks, Policy::kRun);
       for (int r = 0; r < runs; ++r)
         run([&](uint32_t at) {
           for (int c = first_column; c < w.columns; c += kChunkStep)
