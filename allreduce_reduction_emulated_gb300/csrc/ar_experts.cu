@@ -619,8 +619,8 @@ struct Work {
   double in_pairs, alone, slices, values;   // tiles, 64-deep slices of a tile, results
 };
 static Work product_work(const ExpertsCall& c) {
-  const double some = (double)std::max<size_t>(1, std::min(c.experts, c.rows));
-  const auto tiles = [&](double side) { return std::ceil(c.out / side) * some * std::ceil(c.rows / some / side); };
+  const double some = (double)std::min(c.experts, c.rows);   // 0: no tiles
+  const auto tiles = [&](double side) { return some ? std::ceil(c.out / side) * some * std::ceil(c.rows / some / side) : 0; };
   return Work{tiles(256), tiles(128), std::ceil(c.in / 64.0), (double)c.rows * (double)c.out};
 }
 static Work gradient_work(const ExpertsCall& c) {
@@ -646,7 +646,8 @@ static Plan plan(const Work& w, int sms) {
            (n > 1 ? 3.0 + w.values * 4 * (2 * n + 1) / 4e6 : 0.0);
   };
   Plan best = whole_sums(w, sms);
-  if (w.values > 1 << 26 || sms < 2) return best;
+  // (Without tiles nobody would write the parts that the join adds up.)
+  if (w.values > 1 << 26 || w.alone == 0 || sms < 2) return best;
   double least = 0.9 * time(best.pairs, 1);
   for (const bool pairs : {false, true})
     for (int n = 2; n <= 16 && (pairs ? w.in_pairs : w.alone) <= (pairs ? sms / 2 : sms); ++n)
