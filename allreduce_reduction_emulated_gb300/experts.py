@@ -35,6 +35,9 @@ _DTYPES = {torch.float32: AR_FLOAT32, torch.bfloat16: AR_BFLOAT16}
 # eighth of bfloat16's half step.  Longer sums of a bfloat16 result are made in float32, which adds them up in runs.
 _LONGEST = 1 << 18
 
+# More bytes than any workspace of sizes within the limits that fits a GPU.
+_LARGEST = 1 << 48
+
 # Shorter sums, or more tiles of 128 x 128, are never split into parts: no call to ask.
 _LONG, _FEW = 1024, 256
 
@@ -117,7 +120,7 @@ def _space(lib, device, parts, *operands) -> tuple:
     for at, _, _, _, row, matrix in operands:
         bits |= at | row << 1 | matrix << 1
     n = parts + sum(lib.ar_expert_workspace(*o) for o in operands) if bits & 15 else parts
-    if not n:
+    if not n or n > _LARGEST:   # (of sizes beyond the limits, which the library's call refuses)
         return None, None, 0
     t = torch.empty(n, dtype=torch.uint8, device=device)
     return t, t.data_ptr(), n
