@@ -231,6 +231,14 @@ def expert_gradients(dy, x, weights, offsets, dx=None, dw=None, dw_dtype=None, a
         for name, t in ("x", x), ("dw", dw):
             if t is not None and _shared(dx, t):
                 raise _bad(what, f"dx and {name} share memory")
+    if at_dw is not None and rows and dw.numel():  # before dx is launched
+        e, n, k = at_dw[3:]
+        begin = dw.data_ptr()
+        end = begin + ((E - 1) * e + (N - 1) * n + (K - 1) * k + 1) * dw.element_size()
+        for name, t, (_, _, columns, row) in ("x", x, at_x), ("dy", dy, at_y):
+            at = t.data_ptr()
+            if at < end and begin < at + ((rows - 1) * row + columns) * 2:
+                raise _bad(what, f"dw and {name} share memory")
     if stream is not None:
         context, handle = _on(stream)
         with context:

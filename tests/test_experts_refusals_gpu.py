@@ -44,3 +44,24 @@ def test_sizes_beyond_the_limits(shift):
     dy = bf(3, 8)
     refused(lambda: experts.expert_gradients(dy, x, w, off), AR_ERR_UNSUPPORTED)
     refused(lambda: experts.expert_gradients(dy, x, w, off, need_dx=False), AR_ERR_UNSUPPORTED)
+
+
+def test_a_refused_dw_leaves_dx_alone():
+    """dw in the memory of x or dy: nothing is launched, not dx either."""
+    from allreduce_reduction_emulated_gb300 import AR_ERR_INVALID_ARG, experts
+
+    rows, N, K = 40, 64, 64
+    w, off = bf(1, N, K), offsets(0, rows)
+    flat = bf(2 * N * K)
+    near, far = flat[:rows * K].view(rows, K), bf(rows, K)
+    dx = bf(rows, K, value=7.0)
+    for dy, x in ((near, far), (far, near)):
+        for dw in (flat[:N * K].view(1, N, K), flat[rows * K - 8:][:N * K].view(1, N, K)):
+            refused(lambda: experts.expert_gradients(dy, x, w, off, dx=dx, dw=dw), AR_ERR_INVALID_ARG, "share memory")
+            refused(lambda: experts.expert_gradients(dy, x, w, off, dw=dw, need_dx=False), AR_ERR_INVALID_ARG)
+    torch.cuda.synchronize()
+    assert bool((dx == 7.0).all()) and bool((flat == 1.0).all())
+    # right behind x
+    dw = flat[rows * K:][:N * K].view(1, N, K)
+    assert experts.expert_gradients(far, near, w, off, dx=dx, dw=dw)[1] is dw
+    assert bool((dw == float(rows)).all()) and bool((dx == float(N)).all())
