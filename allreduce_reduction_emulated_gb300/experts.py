@@ -150,6 +150,8 @@ def _rounded(what, lib, x, at_x, w, at_w, offsets, off_size, out, fresh, handle)
     """_product, by way of float32 where its sums are too long to be rounded once."""
     if at_x[2] <= _LONGEST or out.dtype == torch.float32:
         return _product(what, lib, x, at_x, w, at_w, offsets, off_size, out, fresh, handle)
+    if not fresh and (_shared(out, x) or _shared(out, w)):  # which the library cannot see
+        raise _bad(what, "the result shares memory with what it is made of")
     wide = _of(x, out.shape, torch.float32) if fresh else out.float()
     _product(what, lib, x, at_x, w, at_w, offsets, off_size, wide, fresh, handle)
     out.copy_(wide)

@@ -65,3 +65,21 @@ def test_a_refused_dw_leaves_dx_alone():
     dw = flat[rows * K:][:N * K].view(1, N, K)
     assert experts.expert_gradients(far, near, w, off, dx=dx, dw=dw)[1] is dw
     assert bool((dw == float(rows)).all()) and bool((dx == float(N)).all())
+
+
+def test_long_sums_in_their_inputs():
+    """Results that go by way of 32-bit ones are refused in their inputs' memory like any others."""
+    from allreduce_reduction_emulated_gb300 import AR_ERR_INVALID_ARG, experts
+
+    N, K = (1 << 18) + 64, 8
+    dy, x, w, off = bf(2, N), bf(2, K), bf(1, N, K), offsets(0, 2)
+    inside = dy.view(-1)[:2 * K].view(2, K)
+    refused(lambda: experts.expert_gradients(dy, x, w, off, dx=inside), AR_ERR_INVALID_ARG, "memory")
+    refused(lambda: experts.expert_gradients(dy, x, w, off, dx=inside, need_dw=False), AR_ERR_INVALID_ARG, "memory")
+    refused(lambda: experts.expert_product(dy, w.transpose(1, 2), off, out=inside), AR_ERR_INVALID_ARG, "memory")
+    inside = w.view(-1)[:2 * K].view(2, K)
+    refused(lambda: experts.expert_gradients(dy, x, w, off, dx=inside), AR_ERR_INVALID_ARG, "memory")
+    torch.cuda.synchronize()
+    assert bool((dy == 1.0).all()) and bool((w == 1.0).all())
+    dx, dw = experts.expert_gradients(dy, x, w, off, dx=bf(2, K))
+    assert bool((dx == 2.0 ** 18).all()) and bool((dw == 2.0).all())     # 2^18 + 64 rounds to 2^18
