@@ -246,9 +246,11 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
 }
 
 // What B's diagonal loses when it is rounded: the factor of B's rows (or, as B is symmetric, columns) in the last
-// product's epilogue that makes up for it.
+// product's epilogue that makes up for it.  It goes with the whole row, so it may only be a rounding's, 1 +- 2^-11: under
+// coefficients whose polynomial has a root the element can come below fp16's normal values, where a step is a larger part of
+// it than the row's other elements can bear, and what it loses is at most 2^-25 beside a bound of 2^12 or more.
 __device__ __forceinline__ float rounding_rest(float exact, float rounded) {
-  return rounded == 0.0f ? 1.0f : __fdividef(exact, rounded);
+  return fabsf(rounded) < 0x1p-14f ? 1.0f : __fdividef(exact, rounded);  // (NaN stays)
 }
 
 // ------------------------------------------------------------------ small matrices, whole in one block
