@@ -39,8 +39,8 @@ class Orthogonalizer:
     The list is checked and its addresses are laid out once; every call reads the gradients anew.  The
     object keeps the tensors' memory, and a workspace of a bit more than 4 bytes for each element and 4 for
     each of the smaller sides' squares.  Its calls share both: they may be on any stream and from any thread
-    but must not overlap on the GPU, captured ones among them.  A captured call needs its object for as
-    long as it is replayed.
+    but must not overlap on the GPU, captured ones among them; one on another stream than the object was made on
+    waits for what that one had to do then.  A captured call needs its object for as long as it is replayed.
     """
 
     def __init__(self, grads, out=None, momentum=None, beta: float = 0.95, nesterov: bool = True, steps: int = 5,
@@ -95,6 +95,8 @@ class Orthogonalizer:
             self._home = torch.cuda.current_stream().cuda_stream
             self._workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
             self.out = [torch.empty(s, dtype=torch.bfloat16, device=self.device) for s in shapes] if out is None else out
+            # Kernels on their way on this stream may still use what this memory was before.
+            self._free = None if torch.cuda.is_current_stream_capturing() else torch.cuda.current_stream().record_event()
         self._made = out is None
         pointers = ctypes.c_void_p * n
         self._grads = pointers(*[g.data_ptr() for g in self.grads])
@@ -155,6 +157,10 @@ class Orthogonalizer:
                 handle = _on(stream)[1]
             if handle != self._home:
                 s = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+                # (A captured call cannot wait for it, and need not: torch.cuda.graph waits for the GPU before it begins.)
+                with torch.cuda.stream(s):
+                    if self._free is not None and not torch.cuda.is_current_stream_capturing():
+                        s.wait_event(self._free)
                 self._workspace.record_stream(s)
                 if self._made:
                     for o in self.out:
