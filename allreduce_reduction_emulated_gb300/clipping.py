@@ -34,8 +34,9 @@ class GradClipper:
     the gradients anew.  The clipper keeps their memory: tensors that are made anew
     (zero_grad(set_to_none=True)) or get another storage need a new clipper, which
     goes best with gradients in flat buffers.  Calls of one clipper share a workspace of 32 KiB: they
-    may be on any stream and from any thread but must not overlap on the GPU.  A captured call needs
-    its clipper, like its gradients, for as long as it is replayed.
+    may be on any stream and from any thread but must not overlap on the GPU; one on another stream than the clipper
+    was made on waits for what that one had to do then.  A captured call needs its clipper, like its gradients, for as
+    long as it is replayed.
     """
 
     NORMS = 128   # results handed out of one block; each is written by one call only
@@ -76,6 +77,8 @@ class GradClipper:
         with torch.cuda.device(self.device):
             self._home = torch.cuda.current_stream().cuda_stream
             self._workspace = torch.empty(self._bytes, dtype=torch.uint8, device=self.device)
+            # Kernels on their way on this stream may still use what this memory was before.
+            self._free = None if _capturing() else torch.cuda.current_stream().record_event()
         self._at = self._workspace.data_ptr()
         self._norms, self._captured = [], []
         # A call's kernels follow one another on the stream, whatever other threads call meanwhile: the library's
@@ -119,6 +122,9 @@ class GradClipper:
                 norm = torch.empty((), dtype=torch.float32, device=self.device)
                 if _capturing():
                     self._captured.append(norm)
+                # (A captured call cannot wait for it, and need not: torch.cuda.graph waits for the GPU before it begins.)
+                elif handle != self._home and self._free is not None:
+                    s.wait_event(self._free)
                 return handle, norm
         if not self._norms:
             self._norms.extend(torch.empty(self.NORMS, dtype=torch.float32, device=self.device).unbind())

@@ -47,3 +47,16 @@ def test_orthogonalizer():
     del probe
     got = first_used_elsewhere(lambda: Orthogonalizer([g], out=out), lambda o, s: o.update(stream=s)[0], bytes_)
     assert torch.equal(got, want)
+
+
+def test_clipper():
+    from allreduce_reduction_emulated_gb300.clipping import GradClipper
+
+    g = [torch.ones(1 << 22, device="cuda")]
+    probe = GradClipper(g)
+    bytes_ = probe._workspace.numel()
+    probe.norm()                        # (a kernel's first launch may wait for the GPU)
+    del probe
+    assert float(first_used_elsewhere(lambda: GradClipper(g), lambda c, s: c.norm(stream=s), bytes_)) == 2048.0
+    got = first_used_elsewhere(lambda: GradClipper(g), lambda c, s: c.clip(1.0, stream=s), bytes_)
+    assert float(got) == 2048.0 and float(g[0][0]) == 1 / 2048
