@@ -138,6 +138,8 @@ def _on(stream):
     if isinstance(stream, int):
         s = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
         return torch.cuda.stream(s), stream
+    if stream.device_index != _current_device():  # its context would make that device the current one
+        raise _bad("stream", f"it is on cuda:{stream.device_index}, the current device is cuda:{_current_device()}")
     return torch.cuda.stream(stream), stream.cuda_stream
 
 
