@@ -34,6 +34,7 @@ namespace {
 using mma::Tile;
 
 constexpr int kMaxShapes = 16, kMaxStacks = 256;  // of one group of launches
+constexpr long long kMaxTiles = 1 << 24;          // and of each stage of one group
 constexpr int kMaxSteps = AR_MAX_ORTHOGONAL_STEPS;
 constexpr int kCoefs = 5;                          // of a matrix and step
 
@@ -898,15 +899,27 @@ unsigned int chunk_for(size_t slots) {
   return (unsigned int)std::min<size_t>(kMostChunk, std::max<size_t>(kThreads, slots / 1200 / kThreads * kThreads));
 }
 
-// `whole`: without the small matrices.
+// The tiles of a matrix in the stage that has most, cut as finely as any cut does.
+long long most_tiles(size_t rows, size_t cols) {
+  long long most = 0;
+  for (int stage = 0; stage < 3; ++stage)
+    most = std::max(most, stage_tiles(stage, (long long)rows, (long long)cols, kCuts[3]));
+  return most;
+}
+
+// `whole`: without the small matrices.  A group ends where its tiles would be too many, but has one stack at least.
 void gather(const OrthogonalCall& c, size_t first, bool whole, uint8_t* base, Group& g) {
   g.classes = 0;
   g.matrices = g.chunks = 0;
   size_t slots = 0;
+  long long tiles = 0;
   size_t i = first;
   for (; i < c.nstacks && i - first < kMaxStacks; ++i) {
     short k = -1;
     if (c.counts[i] && c.rows[i] && c.cols[i] && !(whole && whole_columns(c.rows[i], c.cols[i]))) {
+      const long long more = most_tiles(c.rows[i], c.cols[i]) * (long long)c.counts[i];
+      if (tiles && tiles + more > kMaxTiles) break;
+      tiles += more;
       for (k = 0; k < g.classes && !(g.cls[k].rows == c.rows[i] && g.cls[k].cols == c.cols[i]); ++k) {}
       if (k == g.classes) {
         if (g.classes == kMaxShapes) break;
@@ -1085,7 +1098,7 @@ cudaError_t run(const OrthogonalCall& c, const Group& g, size_t first, const flo
     map(&s.b, &depth, l.b, side, side, pa, true, wide ? half : 128);
     for (int stage = 0; stage < 3; ++stage) {
       const long long one = stage_tiles(stage, sizes[k].rows, sizes[k].cols, cut);
-      if (total[stage] + one * sizes[k].count > 1 << 24) return cudaErrorInvalidValue;
+      if (total[stage] + one * sizes[k].count > kMaxTiles) return cudaErrorInvalidValue;  // (one stack of 275 GB or more)
       s.first[stage] = (int)total[stage];
       s.tiles[stage] = (int)one;
       total[stage] += one * sizes[k].count;
