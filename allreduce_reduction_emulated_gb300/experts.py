@@ -108,7 +108,7 @@ def _shared(a, b) -> bool:
     if way >= span(a):
         return False
     row = a.stride(0) * a.element_size()
-    if a.dim() == b.dim() == 2 and row == b.stride(0) * b.element_size():
+    if a.dim() == b.dim() == 2 and len(a) > 1 and row == b.stride(0) * b.element_size():
         return way % row < a.shape[1] * a.element_size() or way % row + b.shape[1] * b.element_size() > row
     return True
 
