@@ -15,7 +15,8 @@
 // last slice, or tells of stored tiles where others wait for them.  There are two accumulators, so that
 // one tile's epilogue overlaps the next tile's products.
 //
-// What bounds it: with 256 columns or so the matrix instructions (a pair's slice takes them 0.27 us; 4096 rows of 8
+// What bounds it: with 256 columns or so the matrix instructions (a pair's slice takes them 0.27 us at full clocks, 0.37
+// in loops long enough for the power cap, which is cuBLAS's sustained rate; 4096 rows of 8
 // even experts, 2048 -> 8192: 85 us in a captured graph, 1.6 PFLOP/s), with few columns the loads (16 rows of 8 experts: 47 us, 5.7 TB/s of
 // weights).  Five or six stages keep 160 to 192 KB a block on their way; one thread issues all loads without a
 // branch, as a slice's instructions in a whole warp took longer (0.36 us) than its products.
@@ -707,7 +708,7 @@ cudaError_t make_store_map(CUtensorMap* map, const void* base, uint64_t nx, uint
 
 // Whether `in_pairs` tiles of pairs of blocks (256 x 256) take less time than `alone` tiles of blocks (128 x
 // 128, a quarter of the work): both in whole waves over the multiprocessors, a slice at 0.27 us (the matrix
-// instructions) against 0.20 (its loads), and what a tile takes besides.  Measured, us, in pairs and alone: 4096 rows of 8
+// instructions at full clocks) against 0.20 (its loads), and what a tile takes besides.  Measured, us, in pairs and alone: 4096 rows of 8
 // experts, 2048 -> 8192, 85 and 125; 16384 of 64, 2048 -> 1024, 69 and 75; 700 x 700 x 700 26 and 17; 5 rows of 4, 512
 // -> 1024, 6.7 and 5.9.
 inline bool better_in_pairs(double in_pairs, double alone, double slices, int sms) {

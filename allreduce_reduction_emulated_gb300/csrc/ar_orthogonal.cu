@@ -8,9 +8,12 @@
 // products of all steps and shapes.  A and B are symmetric: only their blocks on one
 // side of the diagonal are computed, and stored to both.
 //
-// Between products X, A and B are held in fp16, not in bf16: its 11 bits keep the result within
-// 2^-9 (2-norm) of fp32 arithmetic where bf16's 8 would be off by 2% after five steps, and the
-// tensor cores are as fast.  fp16's range is met by powers of two: all singular values of
+// Between products X, A and B are held in fp16, not in bf16: its 11 bits keep the result of a matrix of normal values
+// within 2^-9 (2-norm) of fp32 arithmetic from sides of about 16 on where bf16's 8 would be off by 2% after five steps, and the
+// tensor cores are as fast.  A direction whose singular value is a small part s of the norm is known to 3e-4 / (s
+// sqrt(side)), so matrices of two or three directions, or square ones, have a tail: of 4096 each, 99% (and the worst) are off
+// by, bf16's 1.7e-3 included, 2 x 2 6.4e-3 (7e-2), 13 x 2 4.8e-3 (6.8e-3), 3 x 300 3.8e-3 (4.5e-3), 8 x 8 5.5e-3 (1.6e-2),
+// 16 x 16 3.8e-3 (5.6e-3), 16 x 40 2.4e-3 (2.6e-3), 128 x 128 2.1e-3, 1024 x 2048 1.8e-3.  fp16's range is met by powers of two: all singular values of
 // X have a bound that follows from the coefficients, so that every element's has, and each
 // matrix is held times the power of two that brings the bound to 2^13.  Sums are fp32, and
 // a I + b A is added in fp32 before B's one rounding.  B's diagonal is most of it, and where the singular
@@ -213,7 +216,9 @@ __device__ __forceinline__ void coefficients(const PrepareParams& p, float norm,
 }
 
 // The norm from its parts (every block for itself, in one order), the factors of all steps, and u times a power of two
-// in fp16.  Bound by HBM, but for what the kernel before has left in L2.
+// in fp16.  Bound by HBM, but for what the kernel before has left in L2; of one matrix of very many chunks by their
+// sums, which every block reads: 8192 x 28672 (14336 chunks) fp32 takes 217 us, 6.5 TB/s, 65536 x 16384 (65536) 1500 to 2100,
+// 4.3 to 3.1 TB/s.
 __global__ void __launch_bounds__(kThreads) halve_kernel(const __grid_constant__ PrepareParams p) {
   pdl_enter();
   // from the last chunk to the first: it begins with what the kernel before has left in L2
@@ -499,9 +504,12 @@ struct StepsParams {
 // third, then the next step's.  A tile waits until all tiles of its matrix before it are stored, which
 // with several matrices they mostly are: nobody waits for the last tile of a launch, and a step of a small
 // matrix costs three times the way through the chip, not three launches (256 x 256, five steps: 144 us
-// so, 98 in one launch, 74 with tiles of half the width).  16 x 1024 x 2048: 585 us, 2 layers of 101M elements
-// 2590 us, of which 320 are the passes over the gradients: bound by the matrix instructions, at 1.65 PFLOP/s of what is
-// executed.
+// so, 98 in one launch, 74 with tiles of half the width).  16 x 1024 x 2048: 590 us, of which 93 are the passes over the
+// gradients; a further step takes 84 us for 133 GFLOP executed, 1.58 PFLOP/s.  2 layers of 101M elements: 2590 to 2730 us,
+// passes 316, a step 462 us for 721 GFLOP, 1.56 PFLOP/s.  Bound by the matrix instructions under the power cap (cuBLAS's
+// sustained rate is 1.72) and, at 1024 x 2048, by epilogues of 5 us beside products of 6.5 us a tile.  Not so far: a short
+// side's A is one tile or two whose sum runs over the whole long side (16 of 64 x 8192: 260 us, 48 a step), and many of a
+// middle size are bound by the epilogues of their short sums (300 of 200 x 300: 465 us, 200 of 256 x 256 211).
 template <int CG>
 struct Steps {
   static constexpr bool kBf16 = false, kOrdered = true;
@@ -784,7 +792,9 @@ struct Cut {
 };
 // A tile's slice and its epilogue, in us: the loads of 16 KiB of A and 8 or 16 of B a block bound a slice but of the
 // whole pair's tile, which the matrix instructions do.  Updates measured with each cut, us: 256 x 256 104, 83, 89, 75;
-// 1024 x 1024 170, 134, 137, 119; 4 x 1024 x 2048 214, 196, 206, 282; 16 of them 468, 609, 624, 1054.
+// 1024 x 1024 170, 134, 137, 119; 4 x 1024 x 2048 214, 196, 206, 282; 16 of them 468, 609, 624, 1054.  Not always the
+// best: 2048 x 8192 527, 544, 595, 989 (takes the second), and many short sums take longer than estimated, as kEnd is less than
+// half of their epilogue (300 x 200 x 300: 447, 571, 422, 594, estimated 240 for the third).
 constexpr Cut kCuts[4] = {{2, 256}, {2, 128}, {1, 128}, {1, 64}};
 constexpr double kSlice[4] = {0.30, 0.17, 0.18, 0.14}, kEnd[4] = {1.5, 0.8, 0.8, 0.4};
 constexpr double kTurn = 3.0;  // of a stage, from its last tile's sums to the next stage's first

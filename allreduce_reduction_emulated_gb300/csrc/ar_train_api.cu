@@ -1,6 +1,7 @@
 // ar_train_api.cu -- the C ABI of the training operators (declared in
 // include/ar_train.h): argument checks and dispatch.  Host code only; the
-// kernels live in ar_logits.cu and ar_clip.cu.  Nothing here allocates or throws.
+// kernels live in ar_logits.cu, ar_clip.cu, ar_experts.cu and ar_orthogonal.cu.
+// Nothing here allocates or throws.
 #include <atomic>
 #include <cstdint>
 #include <cstdio>

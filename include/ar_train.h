@@ -194,7 +194,8 @@ ar_status_t ar_clip_grads(size_t ntensors, const void* const* grads, void* const
  * `in` and `out` and their strides exchanged).  Sums are fp32, rounded once.
  * (The tensor cores cut what an addition loses: 960 products lose up to 2e-6 of their sum.  fp32 results add
  * such runs up, rounded; of a bf16 result a sum over k products is short by about k * 2e-9 of it, an eighth
- * of a half step at 2^18.  For longer ones ask for fp32.)
+ * of a half step at 2^18.  For longer ones ask for fp32.  Where fp32 runs are added up, values below 2^-126 may
+ * become 0.)
  * rows == 0 or out == 0 is a no-op; in == 0 gives zeros for the experts' rows.
  * Errors: AR_ERR_INVALID_ARG (NULL or misaligned pointer, strides, enum, workspace
  * too small, overlap of y with x or weights), AR_ERR_UNSUPPORTED (another data type, more than
@@ -219,7 +220,8 @@ ar_status_t ar_expert_product(const void* x, size_t rows, size_t x_stride, const
 
 /*
  * Gradient of the weights: dW_e[f, k] = sum over expert e's rows of dy[t, f] x[t, k],
- * 0 for an expert without rows; with accumulate != 0 added to what dW holds.
+ * 0 for an expert without rows; with accumulate != 0 added to what dW holds (of an expert that has rows; in fp32
+ * what lies below 2^-126, of dW or of the sum, may become 0).
  *   dy        rows by `out`, x rows by `in`, AR_BFLOAT16
  *   dw        dw_dtype (AR_FLOAT32 or AR_BFLOAT16), laid out by its three strides as
  *             the weights are; no part of dy or x
@@ -252,8 +254,9 @@ ar_status_t ar_expert_weight_gradient(const void* dy, size_t dy_stride, const vo
  *             entry do not matter
  * Momentum, norms and all sums are fp32; X, A and b A + c A^2 are held between the products in fp16 times
  * powers of two that follow from bounds of the singular values; the result is rounded once to bf16.  So a
- * direction whose singular value is s of the norm is known to about 3e-4 / (s sqrt(min(rows, cols))) of itself:
- * next to nothing for a matrix of rank one in the directions that it lacks.  Elements whose squares are below fp32's
+ * direction whose singular value is s of the norm is known to about 3e-4 / (s sqrt(min(rows, cols))) of itself
+ * (of 4096 matrices of 2 x 2 normal values 99% are off by less than 0.65% of their 2-norm, the worst by 7%): next to
+ * nothing for a matrix of rank one in the directions that it lacks.  Elements whose squares are below fp32's
  * range do not count in the norm.
  * A matrix of zeros gives zeros; one whose norm is not finite (a square above the fp32 range makes
  * it infinite) gives NaN.  Empty stacks are left out.  Pointers need element alignment only.
